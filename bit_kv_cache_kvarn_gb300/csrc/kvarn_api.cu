@@ -320,7 +320,14 @@ kvarn_status kvarn_device_error(uint32_t* code_out) {
     unsigned int y = 0;
     e = kvarn::read_and_clear_selftest_error(&y);
     if (e != cudaSuccess) return cuda_fail(e, "device error word");
-    *code_out = v | (w << 1) | (x << 2) | (y << 3);
+    unsigned int serving[3] = {0, 0, 0};
+    e = kvarn::read_and_clear_tables_error(&serving[0]);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = kvarn::read_and_clear_rope_error(&serving[1]);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    e = kvarn::read_and_clear_paged_attn_error(&serving[2]);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    *code_out = v | (w << 1) | (x << 2) | (y << 3) | (serving[0] << 4) | (serving[1] << 5) | (serving[2] << 6);
     if (*code_out & KVARN_DEVICE_TIMEOUT_BITS)
         return fail(KVARN_ERR_TIMEOUT, "a bounded device wait gave up (device error bits 0x%x)", *code_out);
     return ok();
@@ -443,6 +450,322 @@ kvarn_status kvarn_decode_attention_static_ws(
                                   v_params, v_scale, block_table, max_tiles, seq_lens, seq_lens_host,
                                   k_tail_bf16, v_tail_bf16, softmax_scale, ws,
                                   (size_t)KVARN_STATIC_WS_BYTES, out, stream);
+}
+
+// ---- a serving step around the caches ----
+
+kvarn_status kvarn_step_tables(int B, int max_pages, int page_size, const int32_t* seq_lens,
+                               const int32_t* n_new, const int32_t* page_counts, int32_t* page_table,
+                               int32_t* free_pages, const int32_t* free_count, int free_capacity,
+                               int32_t* kv_lens, int32_t* page_counts_out, int32_t* free_count_out,
+                               int32_t* cu_tokens, int32_t* positions, int32_t* slot_map, int n_rows,
+                               int32_t* block_table, int Hkv, int32_t* status, kvarn_stream_t stream) {
+    if (B < 0 || B > kvarn::kMaxTableSeqs)
+        return fail(KVARN_ERR_INVALID_ARG, "B = %d outside 0..%d", B, kvarn::kMaxTableSeqs);
+    if (page_size < 1 || page_size > 65536) return fail(KVARN_ERR_INVALID_ARG, "page_size = %d outside 1..65536", page_size);
+    if (max_pages < 1 || (int64_t)B * max_pages > (1LL << 30))
+        return fail(KVARN_ERR_INVALID_ARG, "max_pages = %d: need at least 1 and B * max_pages <= 2^30", max_pages);
+    if (n_rows < 0 || n_rows > (1 << 30)) return fail(KVARN_ERR_INVALID_ARG, "n_rows = %d outside 0..2^30", n_rows);
+    if (free_capacity < 0 || free_capacity > (1 << 30))
+        return fail(KVARN_ERR_INVALID_ARG, "free_capacity = %d outside 0..2^30", free_capacity);
+    if (Hkv < 0 || Hkv > 1024) return fail(KVARN_ERR_INVALID_ARG, "Hkv = %d outside 0..1024", Hkv);
+    if ((Hkv > 0) != (block_table != nullptr))
+        return fail(KVARN_ERR_INVALID_ARG, "Hkv = %d: block_table goes with Hkv > 0, and only with it", Hkv);
+    if (B == 0) return ok();
+    const struct {
+        const void* p;
+        const char* name;
+    } arrays[] = {{seq_lens, "seq_lens"},     {n_new, "n_new"},
+                  {page_counts, "page_counts"}, {page_table, "page_table"},
+                  {free_count, "free_count"}, {kv_lens, "kv_lens"},
+                  {page_counts_out, "page_counts_out"}, {free_count_out, "free_count_out"},
+                  {cu_tokens, "cu_tokens"},   {status, "status"}};
+    for (const auto& x : arrays) KV_TRY(check_ptr(x.p, 4, x.name));
+    if (free_capacity > 0) KV_TRY(check_ptr(free_pages, 4, "free_pages"));
+    if (n_rows > 0) {
+        KV_TRY(check_ptr(positions, 4, "positions"));
+        KV_TRY(check_ptr(slot_map, 4, "slot_map"));
+    }
+    if (block_table) KV_TRY(check_ptr(block_table, 4, "block_table"));
+    kvarn::StepTablesArgs a;
+    a.B = B;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.free_capacity = free_capacity;
+    a.n_rows = n_rows;
+    a.Hkv = Hkv;
+    a.seq_lens = seq_lens;
+    a.n_new = n_new;
+    a.page_counts = page_counts;
+    a.page_table = page_table;
+    a.free_pages = free_pages;
+    a.free_count = free_count;
+    a.kv_lens = kv_lens;
+    a.page_counts_out = page_counts_out;
+    a.free_count_out = free_count_out;
+    a.cu_tokens = cu_tokens;
+    a.positions = positions;
+    a.slot_map = slot_map;
+    a.block_table = block_table;
+    a.status = status;
+    cudaError_t e = kvarn::launch_step_tables(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "step tables launch");
+    return ok();
+}
+
+kvarn_status kvarn_rope_frequencies(const kvarn_rope_config* cfg, double* freqs, float* rope_scale) {
+    if (!cfg || !freqs || !rope_scale) return fail(KVARN_ERR_INVALID_ARG, "cfg, freqs or rope_scale is NULL");
+    const int R = cfg->rot_dim;
+    if (R < 16 || R > KVARN_HEAD_DIM || R % 16 != 0)
+        return fail(KVARN_ERR_INVALID_ARG, "rot_dim = %d; need a multiple of 16, 16..128", R);
+    if (cfg->scaling < KVARN_ROPE_PLAIN || cfg->scaling > KVARN_ROPE_YARN)
+        return fail(KVARN_ERR_INVALID_ARG, "scaling = %d; expected 0..4", cfg->scaling);
+    if (!(cfg->base > 1.0) || !isfinite(cfg->base)) return fail(KVARN_ERR_INVALID_ARG, "base = %g; need a finite base > 1", cfg->base);
+    const double s = cfg->scaling == KVARN_ROPE_PLAIN ? 1.0 : cfg->factor;
+    if (!(s >= 1.0) || !isfinite(s)) return fail(KVARN_ERR_INVALID_ARG, "factor = %g; need a finite factor >= 1", s);
+    const bool mixed = cfg->scaling == KVARN_ROPE_BANDS || cfg->scaling == KVARN_ROPE_YARN;
+    if (mixed && (!(cfg->original_len > 0.0) || !isfinite(cfg->original_len)))
+        return fail(KVARN_ERR_INVALID_ARG, "original_len = %g; need a finite length > 0", cfg->original_len);
+    if (mixed && !(cfg->low > 0.0 && cfg->low < cfg->high && isfinite(cfg->high)))
+        return fail(KVARN_ERR_INVALID_ARG, "low = %g, high = %g; need 0 < low < high", cfg->low, cfg->high);
+    const double two_pi = 6.28318530717958647692;
+    const double base = cfg->scaling == KVARN_ROPE_NTK ? cfg->base * pow(s, R / (R - 2.0)) : cfg->base;
+    // YaRN: the (fractional) channel pair that makes n turns over the trained context
+    auto pair_of = [&](double turns) { return R * log(cfg->original_len / (turns * two_pi)) / (2.0 * log(base)); };
+    double first = 0.0, last = 0.0;
+    if (cfg->scaling == KVARN_ROPE_YARN) {
+        first = fmax(floor(pair_of(cfg->high)), 0.0);
+        last = fmin(ceil(pair_of(cfg->low)), R - 1.0);
+        if (!(last > first)) last = first + 0.001;
+    }
+    for (int i = 0; i < R / 2; ++i) {
+        const double f = pow(base, -2.0 * i / R);
+        double keep = 1.0;  // share of the unstretched frequency
+        if (cfg->scaling == KVARN_ROPE_LINEAR) {
+            keep = 0.0;
+        } else if (cfg->scaling == KVARN_ROPE_BANDS) {
+            keep = fmin(fmax((cfg->original_len * f / two_pi - cfg->low) / (cfg->high - cfg->low), 0.0), 1.0);
+        } else if (cfg->scaling == KVARN_ROPE_YARN) {
+            keep = 1.0 - fmin(fmax((i - first) / (last - first), 0.0), 1.0);
+        }
+        freqs[i] = keep * f + (1.0 - keep) * (f / s);
+    }
+    *rope_scale = cfg->scaling == KVARN_ROPE_YARN ? (float)(0.1 * log(s) + 1.0) : 1.0f;
+    return ok();
+}
+
+namespace {
+
+bool is_16bit(int t) { return t == KVARN_DTYPE_BF16 || t == KVARN_DTYPE_FP16; }
+
+kvarn_status check_strides(const char* name, int64_t token, int64_t head, int multiple) {
+    if (token < 0 || head < 0 || token % multiple != 0 || head % multiple != 0)
+        return fail(KVARN_ERR_INVALID_ARG, "%s strides %lld, %lld: need non-negative multiples of %d", name,
+                    (long long)token, (long long)head, multiple);
+    return KVARN_OK;
+}
+
+kvarn_status check_cache(const void* k, const void* v, int64_t n_pages, int Hkv, int page_size, int64_t page_stride,
+                         int64_t head_stride, int64_t token_stride) {
+    if (page_size < 1 || n_pages < 1 || n_pages > 0x7fffffffLL / page_size)
+        return fail(KVARN_ERR_INVALID_ARG, "n_pages = %lld, page_size = %d: need positive sizes and n_pages * page_size <= 2^31 - 1",
+                    (long long)n_pages, page_size);
+    KV_TRY(check_ptr(k, 16, "k_cache"));
+    KV_TRY(check_ptr(v, 16, "v_cache"));
+    // sorted by stride, each axis has to step over the whole of the axes below it
+    struct Axis {
+        int64_t stride, size;
+    } ax[3] = {{page_stride, n_pages}, {head_stride, Hkv}, {token_stride, page_size}};
+    for (int i = 0; i < 3; ++i)  // the stride of a single entry is never used
+        if (ax[i].size > 1 && (ax[i].stride <= 0 || ax[i].stride % 8 != 0 || ax[i].stride > (1LL << 40)))
+            return fail(KVARN_ERR_INVALID_ARG, "cache strides %lld, %lld, %lld: need positive multiples of 8 up to 2^40",
+                        (long long)page_stride, (long long)head_stride, (long long)token_stride);
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (ax[j].stride > ax[j + 1].stride || (ax[j].stride == ax[j + 1].stride && ax[j].size > ax[j + 1].size)) {
+                const Axis t = ax[j];
+                ax[j] = ax[j + 1];
+                ax[j + 1] = t;
+            }
+    int64_t extent = KVARN_HEAD_DIM;
+    for (int i = 0; i < 3; ++i) {
+        if (ax[i].size == 1) continue;
+        if (ax[i].stride < extent)
+            return fail(KVARN_ERR_INVALID_ARG, "cache strides %lld, %lld, %lld: elements would coincide",
+                        (long long)page_stride, (long long)head_stride, (long long)token_stride);
+        if (ax[i].size - 1 > (1LL << 48) / ax[i].stride)
+            return fail(KVARN_ERR_INVALID_ARG, "the cache spans more than 2^48 elements");
+        extent += (ax[i].size - 1) * ax[i].stride;
+    }
+    return KVARN_OK;
+}
+
+}  // namespace
+
+kvarn_status kvarn_rope_qkv(kvarn_dtype x_dtype, kvarn_dtype out_dtype, int n_tokens, int Hq, int Hkv,
+                            const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                            const void* v, int64_t kv_token_stride, int64_t kv_head_stride,
+                            const int32_t* positions, const double* inv_freq, int rot_dim,
+                            int interleaved, float rope_scale, const float* q_weight,
+                            const float* k_weight, float eps, void* q_out, int64_t qo_token_stride,
+                            int64_t qo_head_stride, void* k_cache, void* v_cache, int64_t n_pages,
+                            int page_size, int64_t page_stride, int64_t head_stride,
+                            int64_t token_stride, const int32_t* slot_map, kvarn_stream_t stream) {
+    if (!is_16bit(out_dtype)) return fail(KVARN_ERR_INVALID_ARG, "out_dtype = %d; expected bf16 or fp16", (int)out_dtype);
+    if (x_dtype != out_dtype && x_dtype != KVARN_DTYPE_FP32)
+        return fail(KVARN_ERR_INVALID_ARG, "x_dtype = %d; expected out_dtype (%d) or fp32", (int)x_dtype, (int)out_dtype);
+    if (n_tokens < 0) return fail(KVARN_ERR_INVALID_ARG, "n_tokens = %d < 0", n_tokens);
+    if (Hq < 0 || Hq > 65535 || Hkv < 0 || Hkv > 65535)
+        return fail(KVARN_ERR_INVALID_ARG, "Hq = %d, Hkv = %d: allowed 0..65535", Hq, Hkv);
+    if (rot_dim < 0 || rot_dim > KVARN_HEAD_DIM || rot_dim % 16 != 0)
+        return fail(KVARN_ERR_INVALID_ARG, "rot_dim = %d; need a multiple of 16, 0..128", rot_dim);
+    if (interleaved != 0 && interleaved != 1)
+        return fail(KVARN_ERR_INVALID_ARG, "interleaved = %d; expected 0 or 1", interleaved);
+    if (!isfinite(rope_scale)) return fail(KVARN_ERR_INVALID_ARG, "rope_scale is not finite");
+    if (!(eps >= 0.f) || !isfinite(eps)) return fail(KVARN_ERR_INVALID_ARG, "eps = %g; need a finite eps >= 0", eps);
+    if (n_tokens == 0 || (Hq == 0 && Hkv == 0)) return ok();
+    KV_TRY(check_ptr(positions, 4, "positions"));
+    if (rot_dim > 0) KV_TRY(check_ptr(inv_freq, 8, "inv_freq"));
+    const int x_step = x_dtype == KVARN_DTYPE_FP32 ? 4 : 8;
+    if (Hq > 0) {
+        KV_TRY(check_ptr(q, 16, "q"));
+        KV_TRY(check_ptr(q_out, 16, "q_out"));
+        KV_TRY(check_strides("q", q_token_stride, q_head_stride, x_step));
+        KV_TRY(check_strides("q_out", qo_token_stride, qo_head_stride, 8));
+        if (q_weight) KV_TRY(check_ptr(q_weight, 16, "q_weight"));
+        const int64_t lo = qo_token_stride < qo_head_stride ? qo_token_stride : qo_head_stride;
+        const int64_t hi = qo_token_stride < qo_head_stride ? qo_head_stride : qo_token_stride;
+        const int64_t n_lo = qo_token_stride < qo_head_stride ? n_tokens : Hq;
+        const int64_t n_hi = qo_token_stride < qo_head_stride ? Hq : n_tokens;
+        if ((n_lo > 1 && lo < KVARN_HEAD_DIM) || (n_hi > 1 && hi < (n_lo > 1 ? (n_lo - 1) * lo : 0) + KVARN_HEAD_DIM))
+            return fail(KVARN_ERR_INVALID_ARG, "q_out strides %lld, %lld: rows would coincide",
+                        (long long)qo_token_stride, (long long)qo_head_stride);
+        if (q == q_out && (x_dtype != out_dtype || q_token_stride != qo_token_stride || q_head_stride != qo_head_stride))
+            return fail(KVARN_ERR_INVALID_ARG, "q_out may be q only with its type and strides");
+    }
+    if (Hkv > 0) {
+        KV_TRY(check_ptr(k, 16, "k"));
+        KV_TRY(check_ptr(v, 16, "v"));
+        KV_TRY(check_strides("k, v", kv_token_stride, kv_head_stride, x_step));
+        KV_TRY(check_cache(k_cache, v_cache, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
+        if (k_weight) KV_TRY(check_ptr(k_weight, 16, "k_weight"));
+        if (slot_map) KV_TRY(check_ptr(slot_map, 4, "slot_map"));
+        else if (n_tokens > n_pages * page_size)
+            return fail(KVARN_ERR_INVALID_ARG, "n_tokens = %d rows without a slot_map; the cache has %lld slots", n_tokens,
+                        (long long)(n_pages * page_size));
+    }
+    kvarn::RopeArgs a;
+    a.n_tokens = n_tokens;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.rot_dim = rot_dim;
+    a.interleaved = interleaved;
+    a.page_size = Hkv > 0 ? page_size : 1;
+    a.n_slots = Hkv > 0 ? (int)(n_pages * page_size) : 0;
+    a.rows_per_cta = 0;
+    a.rope_scale = rope_scale;
+    a.eps = eps;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_token_stride = q_token_stride;
+    a.q_head_stride = q_head_stride;
+    a.kv_token_stride = kv_token_stride;
+    a.kv_head_stride = kv_head_stride;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.q_out = q_out;
+    a.qo_token_stride = qo_token_stride;
+    a.qo_head_stride = qo_head_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.page_stride = page_stride;
+    a.head_stride = head_stride;
+    a.token_stride = token_stride;
+    a.slot_map = slot_map;
+    cudaError_t e = kvarn::launch_rope_qkv(a, (int)x_dtype, (int)out_dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+    return ok();
+}
+
+static kvarn_status check_paged_shape(int B, int Hq, int Hkv) {
+    if (B < 0 || B > 65535) return fail(KVARN_ERR_INVALID_ARG, "B = %d outside 0..65535", B);
+    if (Hq <= 0 || Hkv <= 0 || Hq > 65535 || Hq % Hkv != 0)
+        return fail(KVARN_ERR_INVALID_ARG, "Hq = %d, Hkv = %d: need Hq a positive multiple of Hkv, up to 65535", Hq, Hkv);
+    return KVARN_OK;
+}
+
+size_t kvarn_paged_attention_workspace_size(int B, int Hq, int Hkv) {
+    if (check_paged_shape(B, Hq, Hkv) != KVARN_OK) return 0;
+    return kvarn::paged_attention_workspace_bytes(B, Hq, Hkv);
+}
+
+kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, const void* q,
+                                   int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+                                   const void* v_cache, int64_t n_pages, int page_size,
+                                   int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                   const int32_t* page_table, int max_pages, const int32_t* kv_lens,
+                                   const int32_t* kv_starts, int window, float softmax_scale,
+                                   float softcap, const float* slopes, void* workspace,
+                                   size_t workspace_bytes, kvarn_dtype out_dtype, void* out, float* lse,
+                                   kvarn_stream_t stream) {
+    KV_TRY(check_paged_shape(B, Hq, Hkv));
+    if (!is_16bit(dtype)) return fail(KVARN_ERR_INVALID_ARG, "dtype = %d; expected bf16 or fp16", (int)dtype);
+    if (out_dtype != KVARN_DTYPE_FP32 && out_dtype != dtype)
+        return fail(KVARN_ERR_INVALID_ARG, "out_dtype = %d; expected fp32 or dtype (%d)", (int)out_dtype, (int)dtype);
+    if (!isfinite(softmax_scale)) return fail(KVARN_ERR_INVALID_ARG, "softmax_scale is not finite");
+    if (!(softcap >= 0.f) || !isfinite(softcap)) return fail(KVARN_ERR_INVALID_ARG, "softcap = %g; need a finite cap >= 0", softcap);
+    if (window < 0) return fail(KVARN_ERR_INVALID_ARG, "window = %d < 0", window);
+    if (page_size < 16 || page_size % 16 != 0)
+        return fail(KVARN_ERR_INVALID_ARG, "page_size = %d; need a positive multiple of 16", page_size);
+    if (max_pages < 1 || (int64_t)max_pages * page_size > 0x7fffffffLL - 63)
+        return fail(KVARN_ERR_INVALID_ARG, "max_pages = %d: need at least 1 and max_pages * page_size <= 2^31 - 64", max_pages);
+    if (B == 0) return ok();
+    KV_TRY(check_ptr(q, 16, "q"));
+    KV_TRY(check_strides("q", q_token_stride, q_head_stride, 8));
+    KV_TRY(check_cache(k_cache, v_cache, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
+    KV_TRY(check_ptr(page_table, 4, "page_table"));
+    KV_TRY(check_ptr(kv_lens, 4, "kv_lens"));
+    if (kv_starts) KV_TRY(check_ptr(kv_starts, 4, "kv_starts"));
+    if (slopes) KV_TRY(check_ptr(slopes, 4, "slopes"));
+    KV_TRY(check_ptr(out, 16, "out"));
+    if (lse) KV_TRY(check_ptr(lse, 4, "lse"));
+    KV_TRY(check_ptr(workspace, 16, "workspace"));
+    const size_t need = kvarn::paged_attention_workspace_bytes(B, Hq, Hkv);
+    if (workspace_bytes < need)
+        return fail(KVARN_ERR_WORKSPACE, "workspace_bytes = %zu < required %zu", workspace_bytes, need);
+    kvarn::PagedAttnArgs a = {};
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.max_len = max_pages * page_size;
+    a.window = window;
+    a.out_dtype = (int)out_dtype;
+    a.n_pages = n_pages;
+    a.scale = softmax_scale;
+    a.softcap = softcap;
+    a.q = q;
+    a.q_token_stride = q_token_stride;
+    a.q_head_stride = q_head_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.page_stride = page_stride;
+    a.head_stride = head_stride;
+    a.token_stride = token_stride;
+    a.page_table = page_table;
+    a.kv_lens = kv_lens;
+    a.kv_starts = kv_starts;
+    a.slopes = slopes;
+    a.workspace = workspace;
+    a.out = out;
+    a.lse = lse;
+    cudaError_t e = kvarn::launch_paged_attention(a, (int)dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+    return ok();
 }
 
 const char* kvarn_status_string(kvarn_status status) {

@@ -81,6 +81,91 @@ cudaError_t launch_append(const AppendArgs& a, int B, int k_bits, int v_bits, in
                           void* v_params, float* v_scale, cudaStream_t stream);
 cudaError_t read_and_clear_append_error(unsigned int* out);
 
+// Launch with programmatic stream serialisation: the grid may start before the previous kernel in the
+// stream completes; the kernel executes griddepcontrol.wait before it reads or writes global memory.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kern, args...);
+}
+
+// A step's tables: see kvarn_step_tables for the arrays.
+constexpr int kMaxTableSeqs = 16384;  // three prefix sums per sequence in shared memory
+struct StepTablesArgs {
+    int B, max_pages, page_size, free_capacity, n_rows, Hkv;
+    const int32_t* seq_lens;
+    const int32_t* n_new;
+    const int32_t* page_counts;
+    int32_t* page_table;
+    int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* kv_lens;
+    int32_t* page_counts_out;
+    int32_t* free_count_out;
+    int32_t* cu_tokens;
+    int32_t* positions;
+    int32_t* slot_map;
+    int32_t* block_table;
+    int32_t* status;
+};
+cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream);
+cudaError_t read_and_clear_tables_error(unsigned int* out);
+
+// Norm, rotation and cache write: see kvarn_rope_qkv.  Strides in elements.
+struct RopeArgs {
+    int n_tokens, Hq, Hkv, rot_dim, interleaved, page_size, n_slots;
+    int rows_per_cta;  // set by the launcher
+    float rope_scale, eps;
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_token_stride, q_head_stride, kv_token_stride, kv_head_stride;
+    const int32_t* positions;
+    const double* inv_freq;
+    const float* q_weight;
+    const float* k_weight;
+    void* q_out;
+    int64_t qo_token_stride, qo_head_stride;
+    void* k_cache;
+    void* v_cache;
+    int64_t page_stride, head_stride, token_stride;
+    const int32_t* slot_map;
+};
+cudaError_t launch_rope_qkv(const RopeArgs& a, int x_dtype, int out_dtype, cudaStream_t stream);
+cudaError_t read_and_clear_rope_error(unsigned int* out);
+
+// Attention over a paged 16-bit cache: see kvarn_paged_attention.  Strides in elements.
+struct PagedAttnArgs {
+    int B, Hq, Hkv, page_size, max_pages, max_len, window, out_dtype;
+    int64_t n_pages;
+    int group, rows, row_blocks, units;  // set by the launcher: query heads per kv head, per unit; units per sequence
+    float scale, softcap, inv_softcap;
+    const void* q;
+    int64_t q_token_stride, q_head_stride;
+    const void* k_cache;
+    const void* v_cache;
+    int64_t page_stride, head_stride, token_stride;
+    const int32_t* page_table;
+    const int32_t* kv_lens;
+    const int32_t* kv_starts;
+    const float* slopes;
+    void* workspace;
+    void* out;
+    float* lse;
+};
+size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv);
+cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stream);
+cudaError_t read_and_clear_paged_attn_error(unsigned int* out);
+
 // Self-check: one kernel whose bounded mbarrier wait runs out after limit_us (see bounded_wait.cu).
 cudaError_t launch_bounded_wait_check(uint32_t limit_us, cudaStream_t stream);
 cudaError_t read_and_clear_selftest_error(unsigned int* out);

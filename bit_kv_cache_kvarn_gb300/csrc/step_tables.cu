@@ -1,0 +1,226 @@
+// A serving step's page tables and slot maps, built on the device from the requests' lengths.
+//
+// Mathematics: three exclusive prefix sums over the sequences (tokens added, pages taken, pages given
+// back) turn every output into a lookup.  Token t belongs to the last sequence whose prefix is <= t;
+// the k-th page taken, counted over the sequences in order, is entry top - 1 - k of the page stack,
+// whose part at and above the caller's count is the pages given back in the same order.  So no thread
+// waits for another's allotment, and the result does not depend on the schedule.
+//
+// What bounds it: latency.  A step moves a few words per token and per new page (at most some MB for a
+// long prefill) and is a chain of three dependent round trips (lengths, the page or stack entry, the
+// store) around one block-wide scan.  One launch, one cluster: every CTA scans all sequences itself,
+// which is cheaper than handing prefixes over, and the one cluster barrier only keeps the lengths,
+// counts and stack size, which may be updated in place, unwritten until every CTA has read them.
+#include <cooperative_groups.h>
+
+#include "kvarn_common.cuh"
+#include "kvarn_internal.h"
+
+namespace kvarn {
+
+// Set when a step's tables could not be built (status word non-zero).  Read by kvarn_device_error.
+__device__ unsigned int g_tables_error = 0;
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+
+struct Sums {
+    long long add, fresh, given;
+};
+
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) {
+    return {a.add + b.add, a.fresh + b.fresh, a.given + b.given};
+}
+
+struct Seq {
+    int len, n_new, count;
+};
+
+__device__ __forceinline__ Seq load_seq(const StepTablesArgs& a, int b) {
+    return {a.seq_lens[b], a.n_new[b], a.page_counts[b]};
+}
+
+// pages held after the step; new length (both 0 for a finished sequence)
+__device__ __forceinline__ Sums seq_sums(const StepTablesArgs& a, Seq s, unsigned& bad) {
+    if (s.len < 0 || s.count < 0 || s.count > a.max_pages) {
+        bad |= KVARN_TABLES_INVALID;
+        return {0, 0, 0};
+    }
+    if (s.n_new < 0) return {0, 0, s.count};
+    const long long kv = (long long)s.len + s.n_new;
+    const long long pages = (kv + a.page_size - 1) / a.page_size;
+    if (kv > 0x7fffffffLL) bad |= KVARN_TABLES_INVALID;
+    if (pages > a.max_pages) bad |= KVARN_TABLES_ROW_FULL;
+    return {s.n_new, pages > s.count ? pages - s.count : 0, 0};
+}
+
+// last i in [0, n) with pre[i] <= x; pre[0] = 0 <= x
+__device__ __forceinline__ int last_at_most(const int* pre, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) step_tables_kernel(StepTablesArgs a) {
+    extern __shared__ int dsm[];
+    __shared__ Sums s_warp[kWarps];
+    __shared__ unsigned s_bad;
+    int* pre_add = dsm;             // [B] tokens of the sequences before b
+    int* pre_fresh = dsm + a.B;     // [B] pages they take
+    int* pre_given = dsm + 2 * a.B; // [B] pages they give back
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) s_bad = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int F = *a.free_count;
+    __syncthreads();
+
+    // prefix sums in 64 bits, kThreads sequences at a time; stored in 32 (used only if totals fit)
+    Sums carry = {0, 0, 0};
+    unsigned bad = 0;
+    for (int base = 0; base < a.B; base += kThreads) {
+        const int b = base + tid;
+        Sums own = {0, 0, 0};
+        if (b < a.B) own = seq_sums(a, load_seq(a, b), bad);
+        Sums inc = own;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            Sums o;
+            o.add = __shfl_up_sync(0xffffffffu, inc.add, s);
+            o.fresh = __shfl_up_sync(0xffffffffu, inc.fresh, s);
+            o.given = __shfl_up_sync(0xffffffffu, inc.given, s);
+            if (lane >= s) inc = inc + o;
+        }
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        Sums before = carry, total = carry;
+        for (int w = 0; w < kWarps; ++w) {
+            const Sums v = s_warp[w];
+            if (w < warp) before = before + v;
+            total = total + v;
+        }
+        if (b < a.B) {
+            pre_add[b] = (int)(before.add + inc.add - own.add);
+            pre_fresh[b] = (int)(before.fresh + inc.fresh - own.fresh);
+            pre_given[b] = (int)(before.given + inc.given - own.given);
+        }
+        carry = total;
+        __syncthreads();  // s_warp is reused
+    }
+    if (bad) atomicOr(&s_bad, bad);
+    __syncthreads();
+    unsigned status = s_bad;
+    const long long left = (long long)F + carry.given - carry.fresh;
+    if (F < 0 || F > a.free_capacity) status |= KVARN_TABLES_INVALID;
+    if (left < 0) status |= KVARN_TABLES_NO_PAGES;
+    if (left > a.free_capacity) status |= KVARN_TABLES_FREE_FULL;
+    if (carry.add > a.n_rows) status |= KVARN_TABLES_ROWS;
+    const bool ok = status == 0;
+    const int total = ok ? (int)carry.add : 0, fresh = ok ? (int)carry.fresh : 0;
+    const long long top = (long long)F + carry.given;
+
+    // entry j of the page stack: the caller's, then the pages given back in order
+    auto stack = [&](long long j) {
+        if (j < F) return a.free_pages[j];
+        const int r = (int)(j - F);
+        const int b = last_at_most(pre_given, a.B, r);
+        return a.page_table[(size_t)b * a.max_pages + (r - pre_given[b])];
+    };
+
+    const int n_ctas = gridDim.x;
+    const int first = blockIdx.x * kThreads + tid, step = n_ctas * kThreads;
+    for (int t = first; t < a.n_rows; t += step) {
+        int pos = -1, slot = -1;
+        if (t < total) {
+            const int b = last_at_most(pre_add, a.B, t);
+            pos = a.seq_lens[b] + (t - pre_add[b]);
+            const int count = a.page_counts[b], pi = pos / a.page_size;
+            const int page = pi < count ? a.page_table[(size_t)b * a.max_pages + pi]
+                                        : stack(top - 1 - pre_fresh[b] - (pi - count));
+            slot = (int)((unsigned)page * (unsigned)a.page_size + (unsigned)(pos - pi * a.page_size));
+        }
+        a.positions[t] = pos;
+        a.slot_map[t] = slot;
+    }
+    for (int k = first; k < fresh; k += step) {
+        const int b = last_at_most(pre_fresh, a.B, k);
+        const int i = a.page_counts[b] + (k - pre_fresh[b]);
+        const int page = stack(top - 1 - k);
+        a.page_table[(size_t)b * a.max_pages + i] = page;
+        for (int h = 0; h < a.Hkv; ++h)
+            a.block_table[((size_t)b * a.Hkv + h) * a.max_pages + i] = page * a.Hkv + h;
+    }
+    if (ok)
+        for (long long j = (long long)F + first; j < left; j += step) a.free_pages[j] = stack(j);
+    for (int b = first; b <= a.B; b += step)
+        a.cu_tokens[b] = !ok ? 0 : b < a.B ? pre_add[b] : total;
+
+    // everything that may alias an input, once every CTA has read it
+    if (n_ctas > 1) cg::this_cluster().sync();
+    else __syncthreads();
+    for (int b = first; b < a.B; b += step) {
+        const Seq s = load_seq(a, b);
+        int kv = s.len, held = s.count;
+        if (ok) {
+            if (s.n_new < 0) kv = held = 0;
+            else {
+                kv = s.len + s.n_new;
+                held = max(held, (int)(((long long)kv + a.page_size - 1) / a.page_size));
+            }
+        }
+        a.kv_lens[b] = kv;
+        a.page_counts_out[b] = held;
+    }
+    if (first == 0) {
+        *a.free_count_out = ok ? (int)left : F;
+        *a.status = (int)status;
+        if (!ok) atomicOr(&g_tables_error, 1u);
+    }
+}
+
+}  // namespace
+
+cudaError_t read_and_clear_tables_error(unsigned int* out) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_tables_error, sizeof(v));
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyToSymbol(g_tables_error, &zero, sizeof(zero));
+    *out = v;
+    return e;
+}
+
+cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = current_device(&dev, &sms);
+    if (e != cudaSuccess) return e;
+    const size_t smem = (size_t)3 * a.B * sizeof(int);
+    e = set_smem_limit_once(step_tables_kernel, 3 * kMaxTableSeqs * (int)sizeof(int), false, dev);
+    if (e != cudaSuccess) return e;
+    const int ctas = a.n_rows > 2 * kThreads || a.B > 2 * kThreads ? kCluster : 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(ctas);
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    return cudaLaunchKernelEx(&lc, step_tables_kernel, a);
+}
+
+}  // namespace kvarn

@@ -273,15 +273,179 @@ kvarn_status kvarn_append_tokens(const kvarn_config* cfg, int B, int Hkv, const 
                                  float* v_scale, const int32_t* block_table, int max_tiles, void* workspace,
                                  size_t workspace_bytes, kvarn_stream_t stream);
 
+/* ---- a serving step around the caches: tables, queries and keys, 16-bit paged attention ----------
+ *
+ * The three calls below make what the calls above take, and serve layers whose cache stays in 16 bit:
+ * kvarn_step_tables turns the requests' lengths into page tables, tile ids (block_table of
+ * kvarn_decode_attention and kvarn_append_tokens), positions and slots; kvarn_rope_qkv normalises and
+ * rotates the projected queries and keys ("post-RoPE K" of kvarn_encode_blocks) and writes keys and
+ * values into a paged cache or into kvarn_append_tokens' layout; kvarn_paged_attention attends over
+ * the paged cache.  The pages have no counterpart for them: their caches are "FP16" where they are not
+ * quantised [paperlayer, "D Experimental details"], which here is any 16-bit type.
+ *
+ * A paged cache is two arrays (K and V) of n_pages x Hkv x page_size x 128 elements of one 16-bit
+ * type, with the same strides for both, in elements: page_stride, head_stride and token_stride
+ * (channels are contiguous).  Both [pages][heads][tokens][128] and [pages][tokens][heads][128] fit, and
+ * K and V in one array.  Strides are positive multiples of 8 under which no two elements coincide;
+ * pointers are 16-byte aligned.  Slot s is token s mod page_size of page s / page_size;
+ * n_pages * page_size is at most 2^31 - 1. */
+typedef enum {
+    KVARN_DTYPE_BF16 = 0,
+    KVARN_DTYPE_FP16 = 1,
+    KVARN_DTYPE_FP32 = 2
+} kvarn_dtype;
+
+/* Bits of kvarn_step_tables' status word. */
+#define KVARN_TABLES_NO_PAGES 1u  /* the free pages do not suffice */
+#define KVARN_TABLES_ROW_FULL 2u  /* a sequence needs more than max_pages pages */
+#define KVARN_TABLES_ROWS 4u      /* more new tokens than n_rows */
+#define KVARN_TABLES_FREE_FULL 8u /* the pages given back do not fit free_pages */
+#define KVARN_TABLES_INVALID 16u  /* a negative length, a page count outside 0..max_pages, a free count
+                                     outside 0..free_capacity, or a length past 2^31 - 1 */
+
+/* Build one step's tables on the device.  Sequence b holds seq_lens[b] tokens in page_counts[b] pages
+ * (the first entries of row b of page_table) and takes n_new[b] >= 0 new tokens this step; n_new[b] < 0
+ * says that it is finished: its pages go back and its length becomes 0.  Sequences stand in order:
+ *   pages given back are pushed on the stack free_pages in (sequence, page) order, then the pages that
+ *   the new tokens need beyond page_counts[b] are popped in (sequence, page) order; a sequence that
+ *   holds more pages than it needs (a rejected draft) keeps them.
+ * Inputs: seq_lens, n_new, page_counts : [B]; page_table : [B][max_pages]; free_pages :
+ * [free_capacity], its first *free_count entries valid.  Page ids are not checked; a slot
+ * (page * page_size + offset) has to fit 31 bits.
+ * Outputs
+ *   kv_lens, page_counts_out : [B], free_count_out : [1]: the state after the step; each may be the
+ *                 array it replaces (seq_lens, page_counts, free_count) itself, else they are apart.
+ *   page_table, free_pages : new entries are written, all others stay as they were.
+ *   cu_tokens   : [B + 1] first row of each sequence's new tokens, then their number.
+ *   positions, slot_map : [n_rows] position and slot of each new token, sequence after sequence; -1
+ *                 in the rows after the last.  May be NULL when n_rows = 0.
+ *   block_table : [B][Hkv][max_pages] or NULL (Hkv = 0): tile id page * Hkv + h of each new page, for
+ *                 the packed pools; other entries stay as they were.
+ *   status      : [1] 0, or KVARN_TABLES_* bits.  With any bit set nothing of the state changes:
+ *                 kv_lens, page_counts_out and free_count_out repeat the inputs, cu_tokens is 0,
+ *                 positions and slot_map are -1, and value 16 of kvarn_device_error is set.
+ * All arrays are int32 on the device.  0 <= B <= 16384, page_size 1..65536, 1 <= max_pages,
+ * B * max_pages <= 2^30 (times Hkv: <= 2^40), 0 <= n_rows, free_capacity <= 2^30.  B = 0 is a no-op.
+ * One launch. */
+kvarn_status kvarn_step_tables(int B, int max_pages, int page_size, const int32_t* seq_lens,
+                               const int32_t* n_new, const int32_t* page_counts, int32_t* page_table,
+                               int32_t* free_pages, const int32_t* free_count, int free_capacity,
+                               int32_t* kv_lens, int32_t* page_counts_out, int32_t* free_count_out,
+                               int32_t* cu_tokens, int32_t* positions, int32_t* slot_map, int n_rows,
+                               int32_t* block_table, int Hkv, int32_t* status, kvarn_stream_t stream);
+
+/* How the rotation's frequencies are stretched for contexts longer than the trained one. */
+typedef enum {
+    KVARN_ROPE_PLAIN = 0,  /* f_i = base^(-2i/R) */
+    KVARN_ROPE_LINEAR = 1, /* f_i / factor (positions interpolated) */
+    KVARN_ROPE_NTK = 2,    /* base' = base * factor^(R / (R - 2)) */
+    KVARN_ROPE_BANDS = 3,  /* by the turns t_i = original_len f_i / 2 pi over the trained context: f_i for
+                              t_i > high, f_i / factor for t_i < low, between them the mean weighted
+                              with (t_i - low) / (high - low) */
+    KVARN_ROPE_YARN = 4    /* YaRN (arXiv:2309.00071): the same mean with a weight linear in i between
+                              the channels that make `high` and `low` turns, and rope_scale
+                              0.1 ln(factor) + 1 */
+} kvarn_rope_scaling;
+
+typedef struct {
+    int32_t rot_dim;     /* R: multiple of 16, 16..128 */
+    int32_t scaling;     /* kvarn_rope_scaling */
+    double base;         /* > 1 */
+    double factor;       /* >= 1; unused by PLAIN */
+    double original_len; /* > 0; BANDS, YARN */
+    double low, high;    /* 0 < low < high; BANDS (usual: 1, 4), YARN (usual: 1, 32) */
+} kvarn_rope_config;
+
+/* Frequencies of a rotation, on the host: freqs[R/2] (radians per position) and the factor of cos and
+ * sin.  Errors: NULL pointers, values out of the ranges above. */
+kvarn_status kvarn_rope_frequencies(const kvarn_rope_config* cfg, double* freqs, float* rope_scale);
+
+/* Norm and rotation of a step's queries and keys, and the write of keys and values into a paged cache.
+ * Row t of q ([n_tokens][Hq][128]), k and v ([n_tokens][Hkv][128]) belongs to position positions[t]:
+ *   y = x w / sqrt(mean(x^2) + eps)   per head, when that norm's weight is given, else y = x
+ *   (y_a, y_b) -> rope_scale (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = positions[t] f_i,
+ * over the pairs i < rot_dim / 2: (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved; the
+ * channels from rot_dim on are not rotated.  Values are only converted.  All in fp32 (angles exactly
+ * reduced at any position), rounded once.
+ *   x_dtype     : type of q, k, v: out_dtype or KVARN_DTYPE_FP32.  out_dtype : KVARN_DTYPE_BF16 or
+ *                 _FP16, the type of q_out and the cache.
+ *   q, k, v     : element (t, h, c) at t * token_stride + h * head_stride + c, so that slices of one
+ *                 fused projection can be given; k and v share their strides.  Strides are
+ *                 non-negative multiples of 16 bytes, pointers 16-byte aligned.
+ *   positions   : [n_tokens] int32.  A negative position marks a padding row: nothing of it is read
+ *                 further or written.
+ *   inv_freq    : [rot_dim / 2] double, device (kvarn_rope_frequencies); rot_dim 0 or a multiple of 16
+ *                 up to 128 (0: no rotation, inv_freq may be NULL).
+ *   q_weight, k_weight : [128] float32, device, 16-byte aligned, or NULL for no norm.
+ *   q_out       : [n_tokens][Hq][128] with its strides; may be q itself (same type and strides).
+ *   k_cache, v_cache and their sizes and strides: the paged cache; rows go to slot slot_map[t].
+ *   slot_map    : [n_tokens] int32 or NULL (slot t).  -1: the row's key and value are not written; one
+ *                 past the cache is not written either and sets value 32 of kvarn_device_error.  Slots
+ *                 are distinct.
+ * With page_size = n_new, NULL slot_map and n_tokens = B * n_new the cache layout is
+ * kvarn_append_tokens' [B][Hkv][n_new][128].  Hq = 0 (no queries) or Hkv = 0 (no keys and values)
+ * leaves the pointers of that side unused.  Outputs do not overlap inputs otherwise.
+ * n_tokens = 0 is a no-op.  0 <= Hq, Hkv <= 65535, page_size >= 1.  One launch. */
+kvarn_status kvarn_rope_qkv(kvarn_dtype x_dtype, kvarn_dtype out_dtype, int n_tokens, int Hq, int Hkv,
+                            const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                            const void* v, int64_t kv_token_stride, int64_t kv_head_stride,
+                            const int32_t* positions, const double* inv_freq, int rot_dim,
+                            int interleaved, float rope_scale, const float* q_weight,
+                            const float* k_weight, float eps, void* q_out, int64_t qo_token_stride,
+                            int64_t qo_head_stride, void* k_cache, void* v_cache, int64_t n_pages,
+                            int page_size, int64_t page_stride, int64_t head_stride,
+                            int64_t token_stride, const int32_t* slot_map, kvarn_stream_t stream);
+
+/* Bytes of device workspace kvarn_paged_attention needs for these heads, whatever the lengths; 0 for
+ * an invalid shape. */
+size_t kvarn_paged_attention_workspace_size(int B, int Hq, int Hkv);
+
+/* Attention of one query per sequence over a paged 16-bit cache, grouped-query heads.  The query is the
+ * sequence's last token, at position L - 1 (its key is in the cache); with L = kv_lens[b] clamped to
+ * 0..max_pages * page_size the visible keys are j in [max(kv_starts[b], L - window, 0), L), and
+ *   s_j = softmax_scale q.k_j;  s_j = softcap tanh(s_j / softcap) if softcap > 0;
+ *   s_j += slopes[h] (j - (L - 1)) if slopes are given;  out = sum_j softmax(s)_j v_j.
+ *   dtype       : type of q and the cache, KVARN_DTYPE_BF16 or _FP16.
+ *   q           : [B][Hq][128], element (b, h, c) at b * q_token_stride + h * q_head_stride + c; strides
+ *                 non-negative multiples of 8.
+ *   cache       : as described above; page_size a multiple of 16.  Nothing outside the visible tokens
+ *                 is read: unwritten slots may hold anything, NaN and infinities included.
+ *   page_table  : [B][max_pages] int32; entry i of row b is the page of tokens [i P, (i + 1) P).  Only
+ *                 entries of visible tokens are read; one outside 0..n_pages - 1 is not followed: its
+ *                 keys and values count as zeros and value 64 of kvarn_device_error is set.
+ *   kv_lens     : [B] int32 (kvarn_step_tables' kv_lens); kv_starts : [B] int32 or NULL: first visible
+ *                 token (left padding, or another document before it); negative counts as 0.
+ *   window      : 0, or the number of last tokens that are visible, the query's own among them.
+ *   softcap     : 0 (none) or positive; slopes : [Hq] float32 or NULL.
+ *   out         : [B][Hq][128] of out_dtype (KVARN_DTYPE_FP32 or dtype).
+ *   lse         : [B][Hq] float32 or NULL: natural log of sum_j exp(s_j).
+ *   workspace   : >= kvarn_paged_attention_workspace_size(B, Hq, Hkv) bytes, 16-byte aligned; needs no
+ *                 clearing.  Calls that may overlap on the GPU need one each.
+ * Sequences without a visible key (and rows whose scores are all -inf) get zeros and lse -inf.
+ * Hq a positive multiple of Hkv, Hq <= 65535, B <= 65535, 1 <= max_pages, max_pages * page_size <=
+ * 2^31 - 64.  B = 0 is a no-op.  The query heads of a kv head are taken 16 at a time; each block
+ * reads the kv head's tokens once.  Launches: one split and one join kernel. */
+kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, const void* q,
+                                   int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+                                   const void* v_cache, int64_t n_pages, int page_size,
+                                   int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                   const int32_t* page_table, int max_pages, const int32_t* kv_lens,
+                                   const int32_t* kv_starts, int window, float softmax_scale,
+                                   float softcap, const float* slopes, void* workspace,
+                                   size_t workspace_bytes, kvarn_dtype out_dtype, void* out, float* lse,
+                                   kvarn_stream_t stream);
+
 /* Reads and clears the device-side error words of the current device, after synchronising it.
  * Bit 1 (value 1): an encoder TMA bulk copy did not complete within its bounded wait (the affected
  * tiles are left unwritten).  Bit 2 (value 2): a decode wait gave up.  Bit 3 (value 4): an append
  * found no block-table slot for a completed block.  Bit 4 (value 8): the wait of
- * kvarn_check_bounded_wait gave up.  *code_out = 0 means no such event.
+ * kvarn_check_bounded_wait gave up.  Bits 5, 6 and 7 (values 16, 32, 64): a step's tables could not be
+ * built, a slot lay outside its cache, a page table entry lay outside its cache.  *code_out = 0 means no
+ * such event.
  * Kernels cannot return a status to the call that enqueued them (that call has returned long
  * before they run), so a device wait that gives up sets its bit, ends its kernel normally -- the
  * CUDA context stays usable -- and is reported here: the call returns KVARN_ERR_TIMEOUT when any
- * timeout bit (KVARN_DEVICE_TIMEOUT_BITS) was set, KVARN_OK otherwise (bit 3 alone is reported in
+ * timeout bit (KVARN_DEVICE_TIMEOUT_BITS) was set, KVARN_OK otherwise (the other bits are reported in
  * *code_out with KVARN_OK); *code_out is filled in both cases.  The bits stay set until read: until
  * then every bounded wait of the kernel family that set one gives up at once.
  * (A library diagnostic; the pages have no counterpart.) */
