@@ -17,12 +17,15 @@
 //     units, and never waits for another warp until its piece is done;
 //   - the query heads of a kv head are the 16 rows of m16n8k16 products: scores from K as it lies
 //     (ldmatrix), then P V with the probabilities taken from the score registers.  A group of 8 KB is
-//     48 such products, a quarter of what an SM's warps can issue in the time HBM needs to bring it, so
-//     the warp-level products, which need no hand-over between warps, fit better than 128-row
-//     tensor-memory tiles that would be at most one eighth full.
+//     48 or 64 such products, at most a third of what an SM's warps can issue in the time HBM needs to
+//     bring it, so the warp-level products, which need no hand-over between warps, fit better than
+//     128-row tensor-memory tiles that would be at most one eighth full;
+//   - units that cross warps of a CTA are joined in shared memory at its end, units that cross CTAs by
+//     a second launch of one CTA per boundary.
 // Rounding: the products take the cache's type exactly; scores, maximum, sums and outputs are fp32.
-// A probability enters the second product as two 16-bit pieces (p = hi + lo, error 2^-18 for bf16 and
-// 2^-22 for fp16), because one piece alone (2^-9) would be the largest error of an fp32 result.  Each
+// A probability enters the second product in 16-bit pieces that add up to it.  bf16: two pieces are off
+// by up to 2^-18, 2.3e-6 of an output whose other errors are 4e-7, so an fp32 output takes three
+// pieces (2^-26) and a bf16 output, which rounds by 2^-9 itself, two.  fp16: two pieces (2^-22).  Each
 // group's P V is added to the running output by an fp32 addition, rounded to nearest.
 #include <math_constants.h>
 
@@ -45,14 +48,15 @@ constexpr int kRows = 16;                              // query heads per unit
 constexpr int kHalfBytes = kGroup * kTile * 2;         // K or V of a group
 constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kMaxCtas = 160;                          // CTAs of a grid, at most
-constexpr int kMergeThreads = 128;
+constexpr int kJoinWarps = 16;
 
-// Workspace: partial slots [worker][2], each o[rows][128] then m[rows] and l[rows] (fp32; a slot is a
-// multiple of 16 bytes, the join reads four channels at a time), then one Join per worker.  A worker (warp) writes slot 0 for a unit that began before its piece, slot 1 for
-// one that begins in its piece and goes on after it.
+// Workspace: partial slots, each o[rows][128] then m[rows] and l[rows] (fp32; a slot is a multiple of 16
+// bytes, joins read four channels at a time): one per warp (the unit that began before its piece and ends
+// inside it), then two per CTA (slot 0: the unit that began before the CTA's pieces, slot 1: the one
+// that begins in them and goes on after them); then one Join per CTA.
 struct Join {
-    int unit_b, unit_u;  // sequence and unit to join, -1: none
-    int last;            // the last worker that holds a part
+    int b, u;  // sequence and unit that slot 1 begins; b = -1: none
+    int last;  // the last CTA that holds a part
     int pad;
 };
 
@@ -92,21 +96,21 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// (x, y) as two 16-bit pieces each: hi + lo
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo, __nv_bfloat16) {
+// (x, y) to 16 bits; x and y become what is left
+__device__ __forceinline__ uint32_t take2(float& x, float& y, __nv_bfloat16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
-    lo = *reinterpret_cast<const uint32_t*>(&l);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+    x -= __uint_as_float(u << 16);
+    y -= __uint_as_float(u & 0xffff0000u);
+    return u;
 }
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo, __half) {
+__device__ __forceinline__ uint32_t take2(float& x, float& y, __half) {
     const __half2 h = __floats2half2_rn(x, y);
     const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
+    x -= f.x;
+    y -= f.y;
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
-
 __device__ __forceinline__ void store2(const PagedAttnArgs& a, int64_t at, float x, float y) {
     if (a.out_dtype == KVARN_DTYPE_FP32) {
         *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(x, y);
@@ -152,106 +156,167 @@ struct Cursor {
 __device__ __forceinline__ float score(const PagedAttnArgs& a, float dot, float slope, float dist) {
     // in the log2 domain
     float s = dot * a.scale;
-    if (a.softcap > 0.f) {
-        // tanh(x) = 1 - 2 / (1 + e^{2x}); saturates to +-1 through e^{2x} = 0 or inf
-        const float x = s * a.inv_softcap;
-        s = a.softcap * (1.f - 2.f / (1.f + exp2f(x * (2.f * kLog2e))));
-    }
+    if (a.softcap > 0.f) s = a.softcap * tanhf(s * a.inv_softcap);
     return fmaf(slope, dist, s) * kLog2e;
 }
 
-template <typename T>
+// Joins `parts` partials of one row: part(i) points at o[row][0], at_m(i) at m and l of that row.  Lane j
+// holds channels 4j..4j+3.  The sum runs over the parts first, first + step, ...; m over all of them.
+struct RowSum {
+    float m, l;  // m: the reference subtracted (0 where every part's maximum is -inf)
+    float4 o;
+};
+template <typename Slot>
+__device__ __forceinline__ RowSum join_row(Slot slot, int rows, int r, int parts, int first, int step, int lane) {
+    float mx = -CUDART_INF_F;
+    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, slot(i)[rows * kTile + r]);
+    mx = warp_max(mx);
+    RowSum s = {mx == -CUDART_INF_F ? 0.f : mx, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+    for (int i = first; i < parts; i += step) {
+        const float* p = slot(i);
+        const float4 v = *reinterpret_cast<const float4*>(p + r * kTile + 4 * lane);
+        const float w = exp2f(p[rows * kTile + r] - s.m);
+        s.l = fmaf(w, p[rows * kTile + rows + r], s.l);
+        s.o.x = fmaf(w, v.x, s.o.x);
+        s.o.y = fmaf(w, v.y, s.o.y);
+        s.o.z = fmaf(w, v.z, s.o.z);
+        s.o.w = fmaf(w, v.w, s.o.w);
+    }
+    return s;
+}
+__device__ __forceinline__ float lse_of(float m, float l) {  // l = 0: no key, or only scores of -inf
+    return l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+}
+__device__ __forceinline__ void store_row(const PagedAttnArgs& a, int64_t row, const RowSum& s, int lane) {
+    const float inv = s.l != 0.f ? 1.f / s.l : 0.f;
+    store2(a, row * kTile + 4 * lane, s.o.x * inv, s.o.y * inv);
+    store2(a, row * kTile + 4 * lane + 2, s.o.z * inv, s.o.w * inv);
+    if (a.lse != nullptr && lane == 0) a.lse[row] = lse_of(s.m, s.l);
+}
+
+// Query heads of a unit: the first one and how many (the last block of a kv head's may be short).
+struct Heads {
+    int kvh, first, rows;
+};
+__device__ __forceinline__ Heads heads_of(const PagedAttnArgs& a, int u) {
+    Heads h;
+    h.kvh = u / a.row_blocks;
+    const int rb = u - h.kvh * a.row_blocks;
+    h.first = h.kvh * a.group + rb * kRows;
+    h.rows = min(a.group - rb * kRows, kRows);
+    return h;
+}
+
+struct Workspace {
+    float* base;
+    size_t stride;
+    int ctas;
+    __device__ __forceinline__ float* warp_slot(int worker) const { return base + worker * stride; }
+    __device__ __forceinline__ float* cta_slot(int cta, int which) const {
+        return base + ((size_t)ctas * kWarps + 2 * cta + which) * stride;
+    }
+    __device__ __forceinline__ Join* joins() const { return reinterpret_cast<Join*>(cta_slot(ctas, 0)); }
+};
+
+// What a warp leaves for the join at its CTA's end.
+struct Left {
+    int b, u;
+    bool open;    // the warp's last unit is in its shared slot:
+    bool starts;  //   it begins in this warp's piece
+    bool ends;    //   it ends with this warp's piece
+    bool head;    // its first unit began before its piece, ended inside it, and is in its workspace slot
+    long long end;  // stream position of the last group of the open unit (where it starts here)
+};
+
+// T: type of q and the cache; PIECES: 16-bit pieces of a probability.
+template <typename T, int PIECES>
 __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ long long s_scan[kWarps];
     __shared__ long long s_pre[kThreads];
+    __shared__ Left s_left[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- this warp's piece of the stream ----
-    long long sum = 0;
-    for (int b = tid; b < a.B; b += kThreads) sum += load_span(a, b).groups();
+    const int worker = blockIdx.x * kWarps + warp, workers = gridDim.x * kWarps;
+    long long total = -1;
+    if (a.B > kThreads) {  // else the one chunk below gives it
+        long long sum = 0;
+        for (int b = tid; b < a.B; b += kThreads) sum += load_span(a, b).groups();
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    if (lane == 0) s_scan[warp] = sum;
-    __syncthreads();
-    long long total = 0;
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        if (lane == 0) s_scan[warp] = sum;
+        __syncthreads();
+        total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_scan[w];
-    total *= a.units;
-    const int workers = gridDim.x * kWarps;
-    const long long piece = max((total + workers - 1) / workers, 1LL);
-    const int worker = blockIdx.x * kWarps + warp;
-    const long long begin = min(total, piece * worker);
-    const int len = (int)(min(total, begin + piece) - begin);
-
+        for (int w = 0; w < kWarps; ++w) total += s_scan[w];
+        total *= a.units;
+        __syncthreads();
+    }
     Cursor at = {};
-    long long seq_begin = 0;  // stream position of the sequence the piece begins in
-    {
-        long long carry = 0;
-        bool found = false;
-        for (int base = 0; base < a.B; base += kThreads) {
-            const int b = base + tid;
-            long long own = b < a.B ? (long long)load_span(a, b).groups() * a.units : 0, inc = own;
+    long long piece = 1, begin = 0, seq_begin = 0, carry = 0;
+    int len = 0;
+    for (int base = 0; base < a.B; base += kThreads) {
+        const int b = base + tid;
+        long long inc = b < a.B ? (long long)load_span(a, b).groups() * a.units : 0;
 #pragma unroll
-            for (int s = 1; s < 32; s <<= 1) {
-                const long long o = __shfl_up_sync(0xffffffffu, inc, s);
-                if (lane >= s) inc += o;
-            }
-            __syncthreads();  // s_scan and s_pre are reused
-            if (lane == 31) s_scan[warp] = inc;
-            __syncthreads();
-            long long before = carry;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) before += s_scan[w];
-                carry += s_scan[w];
-            }
-            s_pre[tid] = before + inc;  // end of sequence base + tid
-            __syncthreads();
-            if (!found && begin < carry) {
-                found = true;
-                int skip = 0;  // sequences of this chunk that end at or before the piece's begin
+        for (int s = 1; s < 32; s <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, inc, s);
+            if (lane >= s) inc += o;
+        }
+        if (base > 0) __syncthreads();  // s_scan and s_pre are reused
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        const long long chunk_begin = carry;
 #pragma unroll
-                for (int i = 0; i < kThreads / 32; ++i)
-                    skip += __popc(__ballot_sync(0xffffffffu, s_pre[32 * i + lane] <= begin));
-                at.b = base + skip;
-                at.s = load_span(a, at.b);
-                at.n = at.s.groups();
-                seq_begin = s_pre[skip] - (long long)at.n * a.units;
-            }
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) inc += s_scan[w];
+            carry += s_scan[w];
+        }
+        s_pre[tid] = chunk_begin + inc;  // end of sequence b in the stream
+        __syncthreads();
+        if (base == 0) {
+            if (total < 0) total = carry;
+            piece = max((total + workers - 1) / workers, 1LL);
+            begin = min(total, piece * worker);
+            len = (int)(min(total, begin + piece) - begin);
+        }
+        if (begin >= chunk_begin && begin < carry) {
+            int skip = 0;  // sequences of this chunk that end at or before the piece's begin
+#pragma unroll
+            for (int i = 0; i < kThreads / 32; ++i)
+                skip += __popc(__ballot_sync(0xffffffffu, s_pre[32 * i + lane] <= begin));
+            at.b = base + skip;
+            at.s = load_span(a, at.b);
+            at.n = at.s.groups();
+            seq_begin = s_pre[skip] - (long long)at.n * a.units;
         }
     }
-    // sequences with nothing visible: zeros, log-sum-exp -inf
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (load_span(a, b).groups() > 0) continue;
-        for (int i = tid; i < a.Hq * kTile / 2; i += kThreads) store2(a, (int64_t)b * a.Hq * kTile + 2 * i, 0.f, 0.f);
-        if (a.lse != nullptr)
-            for (int h = tid; h < a.Hq; h += kThreads) a.lse[(int64_t)b * a.Hq + h] = -CUDART_INF_F;
-    }
-    float* slots = static_cast<float*>(a.workspace);
-    Join* joins = reinterpret_cast<Join*>(slots + 2 * (size_t)workers * slot_floats(a.rows));
-    if (lane == 0) joins[worker].unit_b = -1;
-    if (len == 0) return;
-    {
+    const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.rows), (int)gridDim.x};
+    if (len > 0) {
         const long long in_seq = begin - seq_begin;
         at.u = (int)(in_seq / at.n);
         at.g = (int)(in_seq - (long long)at.u * at.n);
     }
 
     // ---- fetching ----
-    const uint32_t ring = smem_addr(dsm) + warp * kStages * kStageBytes;
+    uint8_t* own = dsm + warp * kStages * kStageBytes;
+    const uint32_t ring = smem_addr(own);
     const int c_row = lane >> 4, c_chunk = lane & 15;  // a copy instruction covers two rows
     const T* kbase = static_cast<const T*>(a.k_cache) + 8 * c_chunk;
     const T* vbase = static_cast<const T*>(a.v_cache) + 8 * c_chunk;
     Cursor in = at;  // next group to fetch, and its page
     auto page_of = [&](const Cursor& c) { return a.page_table[(int64_t)c.b * a.max_pages + c.token() / a.page_size]; };
-    int page = page_of(in);
-    int fetched = 0;
+    int page = len > 0 ? page_of(in) : 0;
+    int fetched = 0, in_stage = 0;
     auto fetch = [&]() {
         if (fetched < len) {
             const int t0 = in.token();
-            const uint32_t dst = ring + (fetched % kStages) * kStageBytes;
+            const uint32_t dst = ring + in_stage * kStageBytes;
+            in_stage = in_stage + 1 < kStages ? in_stage + 1 : 0;
             const bool bad = page < 0 || page >= a.n_pages;
             if (bad && lane == 0) atomicOr(&g_paged_attn_error, 1u);
             const int64_t o = (int64_t)(bad ? 0 : page) * a.page_stride + (int64_t)(in.u / a.row_blocks) * a.head_stride +
@@ -275,24 +340,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
 
+    // sequences with nothing visible: zeros, log-sum-exp -inf
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (load_span(a, b).groups() > 0) continue;
+        for (int i = tid; i < a.Hq * kTile / 2; i += kThreads) store2(a, (int64_t)b * a.Hq * kTile + 2 * i, 0.f, 0.f);
+        if (a.lse != nullptr)
+            for (int h = tid; h < a.Hq; h += kThreads) a.lse[(int64_t)b * a.Hq + h] = -CUDART_INF_F;
+    }
+
     // ---- consuming ----
     const int row0 = lane >> 2, col0 = 2 * (lane & 3);
     const int k_row = ((lane >> 4) << 3) + (lane & 7), k_sel = (lane >> 3) & 1;  // ldmatrix rows of K
     const int v_row = (((lane >> 3) & 1) << 3) + (lane & 7), v_sel = lane >> 4;  // and of V
-    int done = 0;
-    bool first_unit = true;
+    int done = 0, stage = 0;
+    Left left = {};
     while (done < len) {
         const int b = at.b, u = at.u, g_begin = at.g, n = at.n;
         const Span span = at.s;
         const int steps = min(n - g_begin, len - done);
-        const int kvh = u / a.row_blocks, head0 = kvh * a.group + (u - kvh * a.row_blocks) * kRows;
-        const int rows = min(a.group - (u - kvh * a.row_blocks) * kRows, kRows);
+        const Heads hd = heads_of(a, u);
+        const int rows = hd.rows;
         // the unit's queries as the products' left operand, zero rows below
         uint32_t qf[8][4];
         {
             const T* q = static_cast<const T*>(a.q) + (int64_t)b * a.q_token_stride + col0;
-            const T* q0 = q + (int64_t)(head0 + row0) * a.q_head_stride;
-            const T* q1 = q + (int64_t)(head0 + row0 + 8) * a.q_head_stride;
+            const T* q0 = q + (int64_t)(hd.first + row0) * a.q_head_stride;
+            const T* q1 = q + (int64_t)(hd.first + row0 + 8) * a.q_head_stride;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 qf[kk][0] = row0 < rows ? *reinterpret_cast<const uint32_t*>(q0 + 16 * kk) : 0u;
@@ -303,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
         }
         float slope[2] = {0.f, 0.f};
         if (a.slopes != nullptr) {
-            if (row0 < rows) slope[0] = a.slopes[head0 + row0];
-            if (row0 + 8 < rows) slope[1] = a.slopes[head0 + row0 + 8];
+            if (row0 < rows) slope[0] = a.slopes[hd.first + row0];
+            if (row0 + 8 < rows) slope[1] = a.slopes[hd.first + row0 + 8];
         }
         float o[16][4];
 #pragma unroll
@@ -313,11 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
             for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
         float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
 
-        for (int st = 0; st < steps; ++st, ++done) {
+        for (int st = 0; st < steps; ++st) {
             cp_wait<kStages - 2>();
             __syncwarp();
             fetch();  // into the stage consumed in the step before
-            const uint32_t kb = ring + (done % kStages) * kStageBytes, vb = kb + kHalfBytes;
+            const uint32_t kb = ring + stage * kStageBytes, vb = kb + kHalfBytes;
+            stage = stage + 1 < kStages ? stage + 1 : 0;
             float s[2][2][4] = {};  // [chain][token half]
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
@@ -358,30 +432,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
             }
             // a row whose scores are all -inf so far has no maximum to subtract
             const float ref[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0], m[1] == -CUDART_INF_F ? 0.f : m[1]};
-            uint32_t hi[4], lo[4];
+            uint32_t p[PIECES][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float p0 = exp2f(s[0][j][2 * h] - ref[h]), p1 = exp2f(s[0][j][2 * h + 1] - ref[h]);
+                    float p0 = exp2f(s[0][j][2 * h] - ref[h]), p1 = exp2f(s[0][j][2 * h + 1] - ref[h]);
                     l[h] += p0 + p1;
-                    split2(p0, p1, hi[2 * j + h], lo[2 * j + h], T());
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i) p[i][2 * j + h] = take2(p0, p1, T());
                 }
 #pragma unroll
             for (int cc = 0; cc < 8; ++cc) {
                 uint32_t f[4];
                 ldm4t(f, vb + v_row * (kTile * 2) + (((2 * cc + v_sel) ^ (v_row & 7)) << 4));
                 float d0[4] = {}, d1[4] = {};
-                mma(d0, lo, f[0], f[1], T());
-                mma(d1, lo, f[2], f[3], T());
-                mma(d0, hi, f[0], f[1], T());
-                mma(d1, hi, f[2], f[3], T());
+#pragma unroll
+                for (int i = PIECES - 1; i >= 0; --i) {  // the small pieces first
+                    mma(d0, p[i], f[0], f[1], T());
+                    mma(d1, p[i], f[2], f[3], T());
+                }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[2 * cc][c] += d0[c], o[2 * cc + 1][c] += d1[c];
             }
             __syncwarp();  // the stage is read before a later step fetches into it
             at.next(a);
         }
+        done += steps;
 
         // ---- end of the unit, or of this warp's part of it ----
 #pragma unroll
@@ -389,22 +466,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
         }
-        const bool starts_here = g_begin == 0, ends_here = g_begin + steps == n;
-        if (starts_here && ends_here) {
+        const bool starts = g_begin == 0, ends = g_begin + steps == n;
+        if (starts && ends) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = row0 + 8 * h;
                 if (r >= rows) continue;
-                const int64_t row = (int64_t)b * a.Hq + head0 + r;
-                const float inv = l[h] != 0.f ? 1.f / l[h] : 0.f;  // 0: no key, or only scores of -inf
+                const int64_t row = (int64_t)b * a.Hq + hd.first + r;
+                const float inv = l[h] != 0.f ? 1.f / l[h] : 0.f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) store2(a, row * kTile + 8 * i + col0, o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
-                if (a.lse != nullptr && (lane & 3) == 0)
-                    a.lse[row] = l[h] != 0.f ? (m[h] + log2f(l[h])) * 0.69314718055994531f : -CUDART_INF_F;
+                if (a.lse != nullptr && (lane & 3) == 0) a.lse[row] = lse_of(m[h], l[h]);
             }
         } else {
-            const int which = first_unit && !starts_here ? 0 : 1;
-            float* slot = slots + (2 * (size_t)worker + which) * slot_floats(a.rows);
+            // the last unit of the piece waits in shared memory (this warp's ring is read out) for the
+            // join at the CTA's end; one that ended before goes to the workspace
+            const bool last = done == len;
+            if (last) cp_wait<0>();
+            float* slot = last ? reinterpret_cast<float*>(own) : warp == 0 ? ws.cta_slot(blockIdx.x, 0) : ws.warp_slot(worker);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = row0 + 8 * h;
@@ -417,57 +496,78 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
                     slot[a.rows * kTile + a.rows + r] = l[h];
                 }
             }
-            if (which == 1 && lane == 0) {
-                // the unit's last group, in the stream, tells the last worker that holds a part
-                const long long end = begin + done - steps + n - 1;
-                joins[worker] = Join{b, u, (int)(end / piece), 0};
+            if (last) {
+                left.b = b, left.u = u, left.open = true, left.starts = starts, left.ends = ends;
+                left.end = begin + done - steps + n - 1;
+            } else {
+                left.head = true;
             }
         }
-        first_unit = false;
+    }
+
+    // ---- join of the units that cross warps of this CTA: chains of warps, a row at a time ----
+    if (lane == 0) s_left[warp] = left;
+    __syncthreads();
+    const int cta = blockIdx.x;
+    if (tid == 0) ws.joins()[cta].b = -1;
+    int task = 0;
+    for (int w0 = 0; w0 < kWarps; ++w0) {
+        if (!s_left[w0].open || (w0 > 0 && !s_left[w0].starts)) continue;
+        // members: the shared slots of w0 .. w1, and the workspace slot of w1 + 1 where the unit ends in it
+        int w1 = w0;
+        while (!s_left[w1].ends && w1 + 1 < kWarps && s_left[w1 + 1].open && !s_left[w1 + 1].starts && !s_left[w1 + 1].head) ++w1;
+        const bool tail = !s_left[w1].ends && w1 + 1 < kWarps && s_left[w1 + 1].head;
+        const bool starts = s_left[w0].starts, ends = s_left[w1].ends || tail;
+        const Heads hd = heads_of(a, s_left[w0].u);
+        const int64_t row = (int64_t)s_left[w0].b * a.Hq + hd.first;
+        const int parts = w1 - w0 + 1 + (tail ? 1 : 0);
+        const float* beyond = ws.warp_slot(cta * kWarps + w1 + 1);
+        auto part = [&](int i) -> const float* {
+            return w0 + i <= w1 ? reinterpret_cast<const float*>(dsm + (w0 + i) * kStages * kStageBytes) : beyond;
+        };
+        for (int r = 0; r < hd.rows; ++r, ++task) {
+            if (task % kWarps != warp) continue;
+            const RowSum s = join_row(part, a.rows, r, parts, 0, 1, lane);
+            if (starts && ends) {
+                store_row(a, row + r, s, lane);
+            } else {
+                float* slot = ws.cta_slot(cta, starts ? 1 : 0);
+                *reinterpret_cast<float4*>(slot + r * kTile + 4 * lane) = s.o;
+                if (lane == 0) {
+                    slot[a.rows * kTile + r] = s.l != 0.f ? s.m : -CUDART_INF_F;
+                    slot[a.rows * kTile + a.rows + r] = s.l;
+                }
+            }
+        }
+        if (starts && !ends && tid == 0)
+            ws.joins()[cta] = Join{s_left[w0].b, s_left[w0].u, (int)(s_left[w0].end / (piece * kWarps)), 0};
     }
 }
 
-// One CTA per worker whose last unit goes on in other pieces: a warp takes a query head, a lane four
-// channels.
-__global__ void __launch_bounds__(kMergeThreads) paged_join_kernel(PagedAttnArgs a, int workers) {
+// One CTA per CTA of the split whose last unit goes on in others: kJoinWarps warps share the unit's rows.
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(PagedAttnArgs a) {
+    __shared__ RowSum s_sum[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float* slots = static_cast<const float*>(a.workspace);
-    const size_t stride = slot_floats(a.rows);
-    const Join* joins = reinterpret_cast<const Join*>(slots + 2 * (size_t)workers * stride);
-    const int w0 = blockIdx.x;
-    const Join jn = joins[w0];
-    if (jn.unit_b < 0) return;
-    const int kvh = jn.unit_u / a.row_blocks, rb = jn.unit_u - kvh * a.row_blocks;
-    const int head0 = kvh * a.group + rb * kRows, rows = min(a.group - rb * kRows, kRows);
-    const int parts = jn.last - w0 + 1;
-    // part 0 is slot 1 of w0, part i slot 0 of w0 + i
-    auto part = [&](int i) { return slots + (2 * (size_t)(w0 + i) + (i == 0 ? 1 : 0)) * stride; };
-    for (int r = blockIdx.y * (kMergeThreads / 32) + warp; r < rows; r += gridDim.y * (kMergeThreads / 32)) {
-        float mx = -CUDART_INF_F;
-        for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, part(i)[a.rows * kTile + r]);
-        mx = warp_max(mx);
-        const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const float* p = part(i);
-            const float wgt = exp2f(p[a.rows * kTile + r] - ref);
-            const float4 v = *reinterpret_cast<const float4*>(p + r * kTile + 4 * lane);
-            l = fmaf(wgt, p[a.rows * kTile + a.rows + r], l);
-            acc.x = fmaf(wgt, v.x, acc.x);
-            acc.y = fmaf(wgt, v.y, acc.y);
-            acc.z = fmaf(wgt, v.z, acc.z);
-            acc.w = fmaf(wgt, v.w, acc.w);
-        }
-        const int64_t row = (int64_t)jn.unit_b * a.Hq + head0 + r;
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        store2(a, row * kTile + 4 * lane, acc.x * inv, acc.y * inv);
-        store2(a, row * kTile + 4 * lane + 2, acc.z * inv, acc.w * inv);
-        if (a.lse != nullptr && lane == 0) a.lse[row] = l != 0.f ? (ref + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+    const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.rows), (int)gridDim.x};
+    const int c0 = blockIdx.x;
+    const Join jn = ws.joins()[c0];
+    if (jn.b < 0) return;
+    const Heads hd = heads_of(a, jn.u);
+    const int share = kJoinWarps / hd.rows;  // warps of a row, rows <= kRows <= kJoinWarps
+    const int r = warp / share, sub = warp % share;
+    auto part = [&](int i) -> const float* { return ws.cta_slot(c0 + i, i == 0 ? 1 : 0); };
+    if (r < hd.rows) s_sum[warp][lane] = join_row(part, a.rows, r, jn.last - c0 + 1, sub, share, lane);
+    __syncthreads();
+    if (r >= hd.rows || sub != 0) return;
+    RowSum s = s_sum[warp][lane];
+    for (int i = 1; i < share; ++i) {  // the same m in all of them
+        const RowSum t = s_sum[warp + i][lane];
+        s.l += t.l;
+        s.o.x += t.o.x, s.o.y += t.o.y, s.o.z += t.o.z, s.o.w += t.o.w;
     }
+    store_row(a, (int64_t)jn.b * a.Hq + hd.first + r, s, lane);
 }
 
 int grid_ctas(int64_t max_groups, int sms) {
@@ -481,8 +581,8 @@ int grid_ctas(int64_t max_groups, int sms) {
 size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv) {
     (void)B;
     const int group = Hq / Hkv, rows = group < kRows ? group : kRows;
-    const size_t workers = (size_t)kMaxCtas * kWarps;
-    const size_t bytes = 2 * workers * slot_floats(rows) * sizeof(float) + workers * sizeof(Join);
+    const size_t slots = (size_t)kMaxCtas * (kWarps + 2);
+    const size_t bytes = slots * slot_floats(rows) * sizeof(float) + kMaxCtas * sizeof(Join);
     return (bytes + 255) & ~(size_t)255;
 }
 
@@ -507,13 +607,14 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stre
     const int64_t cap = a.window > 0 && a.window < a.max_len ? (int64_t)a.window + kGroup : a.max_len;
     const int ctas = grid_ctas((int64_t)a.B * a.units * ((cap + kGroup - 1) / kGroup), sms);
     const size_t smem = (size_t)kWarps * kStages * kStageBytes;
-    auto kern = dtype == KVARN_DTYPE_BF16 ? paged_split_kernel<__nv_bfloat16> : paged_split_kernel<__half>;
+    auto kern = dtype == KVARN_DTYPE_FP16             ? paged_split_kernel<__half, 2>
+                : a.out_dtype == KVARN_DTYPE_FP32 ? paged_split_kernel<__nv_bfloat16, 3>
+                                                  : paged_split_kernel<__nv_bfloat16, 2>;
     e = set_smem_limit_once(kern, (int)smem, false, dev);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, a);
     if (e != cudaSuccess) return e;
-    const int workers = ctas * kWarps;
-    return launch_pdl(paged_join_kernel, dim3(workers, (a.rows + 3) / 4), dim3(kMergeThreads), 0, stream, a, workers);
+    return launch_pdl(paged_join_kernel, dim3(ctas), dim3(32 * kJoinWarps), 0, stream, a);
 }
 
 }  // namespace kvarn
