@@ -2,8 +2,9 @@
 
 Argument marshalling only: every step of the codec runs in the CUDA kernels of libkvarn.so.  The
 functions keep the C names and order of arguments; tensors are torch CUDA tensors (their
-data_ptr() is passed) and the stream defaults to torch's current stream.  There is no fallback:
-if the shared library is missing or fails to load, every call raises.
+data_ptr() is passed) and the stream defaults to torch's current stream.  The calls of the serving
+step check and pass their arguments in compiled code (csrc/serving_binding.cpp), the others through
+ctypes.  There is no fallback: if a shared library is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
@@ -130,6 +131,32 @@ def _check(status: int):
     if status != 0:
         lib = load()
         raise KvarnError(status, lib.kvarn_last_error().decode() or lib.kvarn_status_string(status).decode())
+
+
+_compiled = None
+
+
+def _native():
+    """The compiled calls of the serving step (csrc/serving_binding.cpp)."""
+    global _compiled
+    if _compiled is None:
+        load()
+        path = os.path.join(_PKG, "_serving.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_serving.so not found at {path}: run __graft_entry__.build() first")
+        from . import _serving
+        _compiled = _serving
+    return _compiled
+
+
+def _call(status: int):
+    if status:
+        _check(status)
+
+
+def _raw(stream):
+    """A stream as the compiled calls take it: None is torch's current stream."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def _ptr(t) -> int | None:
@@ -316,53 +343,6 @@ def kvarn_decode_attention_static_ws(cfg: kvarn_config, q, Hkv: int, k_codes, k_
         host, _ptr(k_tail), _ptr(v_tail), float(softmax_scale), _ptr(out), _stream(stream)))
 
 
-_DTYPES = {torch.bfloat16: KVARN_DTYPE_BF16, torch.float16: KVARN_DTYPE_FP16, torch.float32: KVARN_DTYPE_FP32}
-
-
-def _dev_ptr(t, device, dtype, shape, name):
-    """data_ptr() of a contiguous tensor of that device, type and shape (None: any size)."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be a tensor of the current CUDA device")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    got = t.shape
-    if len(got) != len(shape) or any(w is not None and w != g for g, w in zip(got, shape)):
-        raise ValueError(f"{name} has shape {tuple(got)}, needs {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows(t, device, dtype, tokens, heads, name):
-    """(data_ptr(), token stride, head stride) of a [tokens, heads, 128] view; channels contiguous.  The
-    stride of an axis of one entry is never used and given as 0."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be a tensor of the current CUDA device")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (tokens, heads, TILE):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {(tokens, heads, TILE)}")
-    ts, hs, cs = t.stride()
-    if cs != 1:
-        raise ValueError(f"{name}: the channels must be contiguous")
-    return t.data_ptr(), (ts if tokens > 1 else 0), (hs if heads > 1 else 0)
-
-
-def _cache(k_cache, v_cache, device, dtype):
-    """(k, v, n_pages, page_size, page, head and token stride) of [n_pages, Hkv, page_size, 128] views."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.get_device() != device:
-            raise ValueError(f"{name} must be a tensor of the current CUDA device")
-        if t.dtype is not dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape, stride = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or shape[3] != TILE or stride[3] != 1:
-        raise ValueError("k_cache must be [n_pages, Hkv, page_size, 128] with contiguous channels")
-    if v_cache.shape != shape or v_cache.stride() != stride:
-        raise ValueError("v_cache must have k_cache's shape and strides")
-    return k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[2], stride[0], stride[1], stride[2]
-
-
 def kvarn_step_tables(seq_lens, n_new, page_counts, page_table, free_pages, free_count, page_size: int, kv_lens,
                       page_counts_out, free_count_out, cu_tokens, positions, slot_map, status, block_table=None,
                       stream=None):
@@ -371,24 +351,9 @@ def kvarn_step_tables(seq_lens, n_new, page_counts, page_table, free_pages, free
     free_count [1] valid entries -> kv_lens, page_counts_out [B], free_count_out [1] (may be the inputs
     they replace), cu_tokens [B + 1], positions, slot_map [n_rows] (-1 after the last new token),
     status [1] and, with block_table [B, Hkv, max_pages], the new pages' tile ids."""
-    dev, i32 = torch.cuda.current_device(), torch.int32
-    if len(page_table.shape) != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    B, max_pages = page_table.shape
-    n_rows, cap = positions.shape[0], free_pages.shape[0]
-    hkv = 0 if block_table is None else block_table.shape[1]
-    seqs, one = (B,), (1,)
-    _check(load().kvarn_step_tables(
-        B, max_pages, page_size, _dev_ptr(seq_lens, dev, i32, seqs, "seq_lens"), _dev_ptr(n_new, dev, i32, seqs, "n_new"),
-        _dev_ptr(page_counts, dev, i32, seqs, "page_counts"),
-        _dev_ptr(page_table, dev, i32, (B, max_pages), "page_table"),
-        _dev_ptr(free_pages, dev, i32, (cap,), "free_pages"), _dev_ptr(free_count, dev, i32, one, "free_count"), cap,
-        _dev_ptr(kv_lens, dev, i32, seqs, "kv_lens"), _dev_ptr(page_counts_out, dev, i32, seqs, "page_counts_out"),
-        _dev_ptr(free_count_out, dev, i32, one, "free_count_out"), _dev_ptr(cu_tokens, dev, i32, (B + 1,), "cu_tokens"),
-        _dev_ptr(positions, dev, i32, (n_rows,), "positions"), _dev_ptr(slot_map, dev, i32, (n_rows,), "slot_map"),
-        n_rows,
-        None if block_table is None else _dev_ptr(block_table, dev, i32, (B, hkv, max_pages), "block_table"), hkv,
-        _dev_ptr(status, dev, i32, one, "status"), _stream(stream)))
+    _call(_native().step_tables(seq_lens, n_new, page_counts, page_table, free_pages, free_count, page_size, kv_lens,
+                                page_counts_out, free_count_out, cu_tokens, positions, slot_map, status, block_table,
+                                _raw(stream)))
 
 
 def kvarn_rope_frequencies(rot_dim: int = TILE, base: float = 10000.0, scaling: int = KVARN_ROPE_PLAIN,
@@ -409,39 +374,8 @@ def kvarn_rope_qkv(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slot_m
     [T, Hq, 128] bf16 or fp16 (may be q); k_cache, v_cache [n_pages, Hkv, page_size, 128] views of one
     layout; slot_map [T] int32 or None (slot t); weights [128] float32 or None.  q and q_out, or k, v
     and the caches, may be None together."""
-    dev = torch.cuda.current_device()
-    if (q is None) != (q_out is None) or len({x is None for x in (k, v, k_cache, v_cache)}) != 1:
-        raise ValueError("q goes with q_out, and k with v, k_cache and v_cache")
-    if q is None and k is None:
-        raise ValueError("neither queries nor keys are given")
-    T = positions.shape[0]
-    qs, qo, ks, cache = (None, 0, 0), (None, 0, 0), (None, None, 0, 0), (None, None, 0, 1, 0, 0, 0)
-    hq = hkv = 0
-    if q is not None:
-        hq, xt, ot = q.shape[1], q.dtype, q_out.dtype
-        qs = _rows(q, dev, xt, T, hq, "q")
-        qo = _rows(q_out, dev, ot, T, hq, "q_out")
-    if k is not None:
-        hkv = k.shape[1]
-        if q is None:
-            xt, ot = k.dtype, k_cache.dtype
-        kp, kts, khs = _rows(k, dev, xt, T, hkv, "k")
-        vp, vts, vhs = _rows(v, dev, xt, T, hkv, "v")
-        if (kts, khs) != (vts, vhs):
-            raise ValueError("k and v must have the same strides")
-        ks = (kp, vp, kts, khs)
-        cache = _cache(k_cache, v_cache, dev, ot)
-        if k_cache.shape[1] != hkv:
-            raise ValueError(f"the cache has {k_cache.shape[1]} heads, k has {hkv}")
-    if xt not in _DTYPES or ot not in _DTYPES:
-        raise ValueError(f"unsupported types {xt} -> {ot}")
-    _check(load().kvarn_rope_qkv(
-        _DTYPES[xt], _DTYPES[ot], T, hq, hkv, *qs, *ks, _dev_ptr(positions, dev, torch.int32, (T,), "positions"),
-        None if inv_freq is None else _dev_ptr(inv_freq, dev, torch.float64, (None,), "inv_freq"),
-        0 if inv_freq is None else 2 * inv_freq.shape[0], 1 if interleaved else 0, rope_scale,
-        None if q_weight is None else _dev_ptr(q_weight, dev, torch.float32, (TILE,), "q_weight"),
-        None if k_weight is None else _dev_ptr(k_weight, dev, torch.float32, (TILE,), "k_weight"), eps, *qo, *cache,
-        None if slot_map is None else _dev_ptr(slot_map, dev, torch.int32, (T,), "slot_map"), _stream(stream)))
+    _call(_native().rope_qkv(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slot_map, q_weight, k_weight, eps,
+                             rope_scale, interleaved, _raw(stream)))
 
 
 def kvarn_paged_attention_workspace_size(B: int, Hq: int, Hkv: int) -> int:
@@ -458,24 +392,8 @@ def kvarn_paged_attention(q, k_cache, v_cache, page_table, kv_lens, out, softmax
     tanh, slopes [Hq] float32 adds slope * (key position - query position), window > 0 leaves the last
     `window` tokens, kv_starts [B] int32 hides the tokens before it; lse [B, Hq] float32 receives the
     log-sum-exp.  A sequence without visible keys gets zeros and -inf."""
-    dev = torch.cuda.current_device()
-    B, hq = q.shape[0], q.shape[1]
-    dt = q.dtype
-    if dt not in _DTYPES or out.dtype not in _DTYPES:
-        raise ValueError(f"unsupported types {dt} -> {out.dtype}")
-    cache = _cache(k_cache, v_cache, dev, dt)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor of the current CUDA device")
-    max_pages = page_table.shape[-1]
-    _check(load().kvarn_paged_attention(
-        _DTYPES[dt], B, hq, k_cache.shape[1], *_rows(q, dev, dt, B, hq, "q"), *cache,
-        _dev_ptr(page_table, dev, torch.int32, (B, max_pages), "page_table"), max_pages,
-        _dev_ptr(kv_lens, dev, torch.int32, (B,), "kv_lens"),
-        None if kv_starts is None else _dev_ptr(kv_starts, dev, torch.int32, (B,), "kv_starts"), window, softmax_scale,
-        softcap, None if slopes is None else _dev_ptr(slopes, dev, torch.float32, (hq,), "slopes"),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _DTYPES[out.dtype],
-        _dev_ptr(out, dev, out.dtype, (B, hq, TILE), "out"),
-        None if lse is None else _dev_ptr(lse, dev, torch.float32, (B, hq), "lse"), _stream(stream)))
+    _call(_native().paged_attention(q, k_cache, v_cache, page_table, kv_lens, out, softmax_scale, workspace, softcap,
+                                    slopes, window, kv_starts, lse, _raw(stream)))
 
 
 def kvarn_device_error() -> int:

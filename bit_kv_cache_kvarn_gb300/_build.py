@@ -1,15 +1,18 @@
-"""Build libkvarn.so in-tree with nvcc for sm_103a (one -gencode, translation units in parallel)."""
+"""Build libkvarn.so in-tree with nvcc for sm_103a (one -gencode, translation units in parallel), and the
+compiled part of the Python binding, _serving.so, with the host compiler."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvarn.so")
+BINDING = os.path.join(PKG, "_serving.so")
 SOURCES = ["kvarn_api.cu", "encode.cu", "dequant.cu", "decode_attn.cu", "append.cu", "bounded_wait.cu",
            "step_tables.cu", "rope_qkv.cu", "paged_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -24,6 +27,35 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: libkvarn needs the CUDA toolkit to build")
 
 
+def compile_binding() -> str:
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    obj = os.path.join(BUILD, "serving_binding.o")
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{inc}",
+           f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-I{cuda}",
+           f"-I{sysconfig.get_paths()['include']}", "-c", os.path.join(CSRC, "serving_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling the binding failed:\n{r.stderr}")
+    return obj
+
+
+def link_binding(obj: str) -> None:
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB, "-Wl,-rpath,$ORIGIN", f"-L{libs}", "-ltorch_python",
+           "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking the binding failed:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -36,8 +68,10 @@ def build(verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, SOURCES))
+        binding_obj = binding.result()
     log = "".join(err for _, err in results)
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         f.write(log)
@@ -45,10 +79,12 @@ def build(verbose: bool = False) -> str:
         print(log)
     objs = [o for o, _ in results]
     tmp = LIB + ".tmp"
-    r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+    r = subprocess.run([cc, *ARCH, "-shared", "-Xlinker", "-soname=libkvarn.so", "-o", tmp, *objs], capture_output=True,
+                       text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    link_binding(binding_obj)
     return LIB
 
 

@@ -393,7 +393,7 @@ def attn_check(c, out, lse, scale=1 / math.sqrt(128), softcap=0.0, slopes=None):
     bad = np.abs(got - want) > tol
     assert not bad.any(), (np.argwhere(bad)[:4], np.abs(got - want)[bad][:4], tol[bad][:4])
     fin = np.isfinite(want_lse)
-    assert np.all(np.abs(got_lse - want_lse)[fin] <= (err + 2.0 ** -22 * np.abs(want_lse) + 2.0 ** -17)[fin])
+    assert np.all(np.abs(got_lse[fin] - want_lse[fin]) <= err[fin] + 2.0 ** -22 * np.abs(want_lse[fin]) + 2.0 ** -17)
 
 
 LENS = [0, 1, 15, 16, 17, 127, 128, 129, 500, 0, 1000, 33]

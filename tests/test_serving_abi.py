@@ -58,14 +58,20 @@ def test_rope_refusals(lib):
     assert b"q_out" in lib.kvarn_last_error()
 
 
-def test_rope_python_refusals_name_the_argument():
+def test_python_calls_refuse_what_is_no_device_tensor(lib):
+    # without a GPU the current device cannot be asked for, with one the tensors are on another device
     import torch
 
     import bit_kv_cache_kvarn_gb300 as kv
 
-    t = torch.zeros(2, 1, 128, dtype=torch.bfloat16)
-    with pytest.raises(Exception):  # CPU tensors are refused (or no device to ask)
-        kv.kvarn_rope_qkv(t, None, None, torch.zeros(2, dtype=torch.int32), None, t, None, None)
+    t, i = torch.zeros(2, 1, 128, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    c = torch.zeros(4, 1, 16, 128, dtype=torch.bfloat16)
+    with pytest.raises((ValueError, RuntimeError)):
+        kv.kvarn_rope_qkv(t, None, None, i, None, t, None, None)
+    with pytest.raises((ValueError, RuntimeError)):
+        kv.kvarn_paged_attention(t, c, c, torch.zeros(2, 2, dtype=torch.int32), i, t, 0.1, i)
+    with pytest.raises((ValueError, RuntimeError)):
+        kv.kvarn_step_tables(i, i, i, torch.zeros(2, 2, dtype=torch.int32), i, i[:1], 16, i, i, i[:1], i, i, i, i[:1])
 
 
 def _attn(lib, dt=0, B=2, hq=4, hkv=2, q=FAKE, qs=(512, 128), kc=FAKE, vc=FAKE, pages=4, page=16, cs=(4096, 2048, 128),
