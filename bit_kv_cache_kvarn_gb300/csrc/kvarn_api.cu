@@ -487,7 +487,7 @@ kvarn_status kvarn_step_tables(int B, int max_pages, int page_size, const int32_
         KV_TRY(check_ptr(slot_map, 4, "slot_map"));
     }
     if (block_table) KV_TRY(check_ptr(block_table, 4, "block_table"));
-    kvarn::StepTablesArgs a;
+    kvarn::StepTablesArgs a = {};
     a.B = B;
     a.max_pages = max_pages;
     a.page_size = page_size;
@@ -662,7 +662,7 @@ kvarn_status kvarn_rope_qkv(kvarn_dtype x_dtype, kvarn_dtype out_dtype, int n_to
     a.interleaved = interleaved;
     a.page_size = Hkv > 0 ? page_size : 1;
     a.n_slots = Hkv > 0 ? (int)(n_pages * page_size) : 0;
-    a.rows_per_cta = 0;
+    a.slices = a.passes = 0;
     a.rope_scale = rope_scale;
     a.eps = eps;
     a.q = q;

@@ -102,6 +102,7 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, c
 constexpr int kMaxTableSeqs = 16384;  // three prefix sums per sequence in shared memory
 struct StepTablesArgs {
     int B, max_pages, page_size, free_capacity, n_rows, Hkv;
+    int page_shift;  // set by the launcher: log2 of a page size that is a power of two, else -1
     const int32_t* seq_lens;
     const int32_t* n_new;
     const int32_t* page_counts;
@@ -123,7 +124,7 @@ cudaError_t read_and_clear_tables_error(unsigned int* out);
 // Norm, rotation and cache write: see kvarn_rope_qkv.  Strides in elements.
 struct RopeArgs {
     int n_tokens, Hq, Hkv, rot_dim, interleaved, page_size, n_slots;
-    int rows_per_cta;  // set by the launcher
+    int slices, passes;  // set by the launcher: warps of a token, times four rows of a warp
     float rope_scale, eps;
     const void* q;
     const void* k;

@@ -78,102 +78,84 @@ __device__ __forceinline__ void store8(O* p, const float (&f)[8]) {
                                               pack2(f[4], f[5], O()), pack2(f[6], f[7], O()));
 }
 
-// X: type of q, k, v; O: type of q_out and the cache; grid.x over blocks of TOK tokens, grid.y over
-// slices of a.rows_per_cta of the Hq + 2 Hkv rows of a token; kWarps / TOK warps share a token.
-template <typename X, typename O, int TOK, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_qkv_kernel(RopeArgs a) {
-    __shared__ float2 s_turn[TOK][kHalf];  // (cos, sin) * rope_scale of the CTA's tokens
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kShare = kWarps / TOK;
-    const int pairs = a.rot_dim >> 1;
-    const int64_t token0 = (int64_t)blockIdx.x * TOK;
+// X: type of q, k, v; O: type of q_out and the cache.  A warp takes a.passes times four of the
+// Hq + 2 Hkv rows of a token and works alone; a token is a.slices warps.
+template <typename X, typename O, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, 7) rope_qkv_kernel(RopeArgs a) {
+    __shared__ float2 s_turn[kWarps][kHalf];  // (cos, sin) * rope_scale of the warp's token
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned id = blockIdx.x * kWarps + warp;
+    const int t = (int)(id / (unsigned)a.slices), slice = (int)(id - (unsigned)t * (unsigned)a.slices);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = tid; i < TOK * kHalf; i += kThreads) {
-        const int64_t t = token0 + i / kHalf;
-        const int p = i % kHalf;
-        if (p < pairs && t < a.n_tokens) {
-            const int pos = a.positions[t];
-            // 2^64 f / 2 pi modulo 2^64: whole turns per position drop out
-            const double turns = a.inv_freq[p] * 0.15915494309189533577;
-            const double frac = turns - floor(turns);
-            const unsigned long long F = __double2ull_rn(frac * 18446744073709551616.0);
-            const unsigned long long at = F * (unsigned long long)(unsigned)max(pos, 0);
-            // nearest fraction of a turn in [-1/2, 1/2), as half turns for sincospif
-            const float half_turns = (float)(int)((at + 0x80000000ull) >> 32) * 4.656612873077393e-10f;
-            float sn, cs;
-            sincospif(half_turns, &sn, &cs);
-            s_turn[i / kHalf][p] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
-        }
-    }
-    __syncthreads();
-    const int tok = warp / kShare;
-    const int64_t t = token0 + tok;
-    if (t >= a.n_tokens || a.positions[t] < 0) return;  // a padding row: nothing of it is written
-
+    if (t >= a.n_tokens) return;
+    const int rows = a.Hq + 2 * a.Hkv, pairs = a.rot_dim >> 1;
     const int sub = lane >> 3, j = lane & 7;
     const bool turned = j < (a.rot_dim >> 4);
     const int ca = 8 * (INTERLEAVED || !turned ? 2 * j : j);
     const int cb = INTERLEAVED || !turned ? ca + 8 : ca + pairs;
-    const int r_begin = blockIdx.y * a.rows_per_cta;
-    const int r_end = min(r_begin + a.rows_per_cta, a.Hq + 2 * a.Hkv);
-
-    O* kdst = nullptr;
-    O* vdst = nullptr;
-    if (a.Hkv > 0) {
-        const int slot = a.slot_map != nullptr ? a.slot_map[t] : (int)t;
-        if (slot >= 0 && slot < a.n_slots) {
-            const int page = slot / a.page_size, off = slot - page * a.page_size;
-            const int64_t o = (int64_t)page * a.page_stride + (int64_t)off * a.token_stride;
-            kdst = static_cast<O*>(a.k_cache) + o;
-            vdst = static_cast<O*>(a.v_cache) + o;
-        } else if (slot >= 0 && lane == 0) {
-            atomicOr(&g_rope_error, 1u);
-        }
-    }
-
     const X* q = static_cast<const X*>(a.q) + t * a.q_token_stride;
     const X* k = static_cast<const X*>(a.k) + t * a.kv_token_stride;
     const X* v = static_cast<const X*>(a.v) + t * a.kv_token_stride;
     O* qo = static_cast<O*>(a.q_out) + t * a.qo_token_stride;
 
-    // whole warps walk the rows, so that every lane takes part in the shuffles
-    for (int r0 = r_begin + 4 * (warp % kShare); r0 < r_end; r0 += 4 * kShare) {
-        const int r = r0 + sub;
-        const X* src = nullptr;
-        O* dst = nullptr;
-        const float* w = nullptr;
-        bool turn = true;
-        if (r < r_end) {
-            if (r < a.Hq) {
-                src = q + (int64_t)r * a.q_head_stride;
-                dst = qo + (int64_t)r * a.qo_head_stride;
-                w = a.q_weight;
-            } else if (r < a.Hq + a.Hkv) {
-                const int h = r - a.Hq;
-                src = k + (int64_t)h * a.kv_head_stride;
-                dst = kdst != nullptr ? kdst + (int64_t)h * a.head_stride : nullptr;
-                w = a.k_weight;
-            } else {
-                const int h = r - a.Hq - a.Hkv;
-                src = v + (int64_t)h * a.kv_head_stride;
-                dst = vdst != nullptr ? vdst + (int64_t)h * a.head_stride : nullptr;
-                turn = false;
-            }
-        }
-        Raw8<X> ra = {}, rb = {};
-        if (dst != nullptr) {
-            ra.load(src + ca);
-            rb.load(src + cb);
-        }
+    auto load = [&](int r, Raw8<X>& ra, Raw8<X>& rb) {
+        if (r >= rows) return;
+        const X* src = r < a.Hq           ? q + r * a.q_head_stride
+                       : r < a.Hq + a.Hkv ? k + (r - a.Hq) * a.kv_head_stride
+                                          : v + (r - a.Hq - a.Hkv) * a.kv_head_stride;
+        ra.load(src + ca);
+        rb.load(src + cb);
+    };
+    // the first rows are on their way while the angles are made
+    int r = 4 * slice * a.passes + sub;
+    Raw8<X> ra = {}, rb = {};
+    load(r, ra, rb);
+    const int pos = a.positions[t];
+    const int slot = a.Hkv == 0 ? -1 : a.slot_map != nullptr ? a.slot_map[t] : t;
+    if (pos < 0) return;  // a padding row: nothing of it is written
+    for (int p = lane; p < pairs; p += 32) {
+        // 2^64 f / 2 pi modulo 2^64: whole turns per position drop out
+        const double turns = a.inv_freq[p] * 0.15915494309189533577;
+        const double frac = turns - floor(turns);
+        const unsigned long long F = __double2ull_rn(frac * 18446744073709551616.0);
+        const unsigned long long at = F * (unsigned long long)(unsigned)pos;
+        // nearest fraction of a turn in [-1/2, 1/2), as half turns for sincospif
+        const float half_turns = (float)(int)((at + 0x80000000ull) >> 32) * 4.656612873077393e-10f;
+        float sn, cs;
+        sincospif(half_turns, &sn, &cs);
+        s_turn[warp][p] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
+    }
+    O* kdst = nullptr;
+    O* vdst = nullptr;
+    if (slot >= 0 && slot < a.n_slots) {
+        const int page = slot / a.page_size, off = slot - page * a.page_size;
+        const int64_t o = page * a.page_stride + off * a.token_stride;
+        kdst = static_cast<O*>(a.k_cache) + o;
+        vdst = static_cast<O*>(a.v_cache) + o;
+    } else if (slot >= 0 && lane == 0) {
+        atomicOr(&g_rope_error, 1u);
+    }
+    __syncwarp();
+
+    for (int pass = 0; pass < a.passes; ++pass, r += 4) {
+        Raw8<X> na = {}, nb = {};  // the next four rows
+        if (pass + 1 < a.passes) load(r + 4, na, nb);
         float fa[8], fb[8];
         ra.get(fa);
         rb.get(fb);
+        ra = na, rb = nb;
+        const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv;
+        const float* w = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) sq = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], sq));
 #pragma unroll
         for (int s = 1; s < 8; s <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, s);
+        O* dst = nullptr;
+        if (is_q) dst = qo + r * a.qo_head_stride;
+        else if (is_k) dst = kdst != nullptr ? kdst + (r - a.Hq) * a.head_stride : nullptr;
+        else if (r < rows) dst = vdst != nullptr ? vdst + (r - a.Hq - a.Hkv) * a.head_stride : nullptr;
         if (dst == nullptr) continue;
         if (w != nullptr) {
             const float inv = 1.0f / sqrtf(sq * (1.0f / kTile) + a.eps);
@@ -186,8 +168,8 @@ __global__ void __launch_bounds__(kThreads) rope_qkv_kernel(RopeArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) fa[i] *= inv * wa[i], fb[i] *= inv * wb[i];
         }
-        if (turn && turned) {
-            const float2* cs = &s_turn[tok][8 * j];
+        if (turned && (is_q || is_k)) {
+            const float2* cs = &s_turn[warp][8 * j];
             if (INTERLEAVED) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -213,22 +195,22 @@ __global__ void __launch_bounds__(kThreads) rope_qkv_kernel(RopeArgs a) {
     }
 }
 
-template <typename X, typename O, int TOK>
-cudaError_t launch(const RopeArgs& a, dim3 grid, cudaStream_t stream) {
-    return a.interleaved ? launch_pdl(rope_qkv_kernel<X, O, TOK, true>, grid, kThreads, 0, stream, a)
-                         : launch_pdl(rope_qkv_kernel<X, O, TOK, false>, grid, kThreads, 0, stream, a);
-}
-
 template <typename X, typename O>
 cudaError_t launch(RopeArgs a, cudaStream_t stream) {
-    const int rows = a.Hq + 2 * a.Hkv;
-    if (a.n_tokens < 1024) {
-        // one token's rows over several CTAs, one pass of 16 rows each: latency counts
-        a.rows_per_cta = 4 * kWarps;
-        return launch<X, O, 1>(a, dim3((unsigned)a.n_tokens, (rows + a.rows_per_cta - 1) / a.rows_per_cta), stream);
-    }
-    a.rows_per_cta = rows;
-    return launch<X, O, kWarps>(a, dim3((unsigned)((a.n_tokens + kWarps - 1) / kWarps)), stream);
+    int dev = 0, sms = 0;
+    const cudaError_t e = current_device(&dev, &sms);
+    if (e != cudaSuccess) return e;
+    // a warp takes the whole token once there are tokens enough for 28 warps on every SM, so that the
+    // angles are made once; with fewer, a token is spread over more warps
+    const int quads = (a.Hq + 2 * a.Hkv + 3) / 4;
+    const int64_t passes = (int64_t)a.n_tokens * quads / (28 * (int64_t)sms);
+    a.passes = (int)(passes < 1 ? 1 : passes < quads ? passes : quads);
+    a.slices = (quads + a.passes - 1) / a.passes;
+    a.passes = (quads + a.slices - 1) / a.slices;
+    const int64_t warps = (int64_t)a.n_tokens * a.slices;
+    const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps));
+    return a.interleaved ? launch_pdl(rope_qkv_kernel<X, O, true>, grid, dim3(kThreads), 0, stream, a)
+                         : launch_pdl(rope_qkv_kernel<X, O, false>, grid, dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace

@@ -25,16 +25,31 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 1024;
 constexpr int kCluster = 8;
+constexpr int kPerThread = 4;                // rows in flight per thread
+constexpr unsigned kMost = 0x7fffffffu;
 
+// Sums over sequences: new tokens and pages taken (both saturating, beyond every allowed total), pages
+// given back (<= B * max_pages <= 2^30).
 struct Sums {
-    long long add, fresh, given;
+    int add, fresh, given;
 };
-
 __device__ __forceinline__ Sums operator+(Sums a, Sums b) {
-    return {a.add + b.add, a.fresh + b.fresh, a.given + b.given};
+    return {(int)min((unsigned)a.add + (unsigned)b.add, kMost), (int)min((unsigned)a.fresh + (unsigned)b.fresh, kMost),
+            a.given + b.given};
+}
+__device__ __forceinline__ Sums shfl_up(Sums v, int s) {
+    return {__shfl_up_sync(0xffffffffu, v.add, s), __shfl_up_sync(0xffffffffu, v.fresh, s),
+            __shfl_up_sync(0xffffffffu, v.given, s)};
+}
+__device__ __forceinline__ Sums warp_inclusive(Sums v, int lane) {
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const Sums o = shfl_up(v, s);
+        if (lane >= s) v = v + o;
+    }
+    return v;
 }
 
 struct Seq {
@@ -45,7 +60,9 @@ __device__ __forceinline__ Seq load_seq(const StepTablesArgs& a, int b) {
     return {a.seq_lens[b], a.n_new[b], a.page_counts[b]};
 }
 
-// pages held after the step; new length (both 0 for a finished sequence)
+__device__ __forceinline__ int page_of(const StepTablesArgs& a, int pos) {
+    return a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+}
 __device__ __forceinline__ Sums seq_sums(const StepTablesArgs& a, Seq s, unsigned& bad) {
     if (s.len < 0 || s.count < 0 || s.count > a.max_pages) {
         bad |= KVARN_TABLES_INVALID;
@@ -53,10 +70,15 @@ __device__ __forceinline__ Sums seq_sums(const StepTablesArgs& a, Seq s, unsigne
     }
     if (s.n_new < 0) return {0, 0, s.count};
     const long long kv = (long long)s.len + s.n_new;
-    const long long pages = (kv + a.page_size - 1) / a.page_size;
-    if (kv > 0x7fffffffLL) bad |= KVARN_TABLES_INVALID;
+    int pages;
+    if (kv > (long long)kMost) {
+        bad |= KVARN_TABLES_INVALID;
+        pages = (int)min((kv + a.page_size - 1) / a.page_size, (long long)kMost);
+    } else {
+        pages = kv > 0 ? page_of(a, (int)kv - 1) + 1 : 0;
+    }
     if (pages > a.max_pages) bad |= KVARN_TABLES_ROW_FULL;
-    return {s.n_new, pages > s.count ? pages - s.count : 0, 0};
+    return {s.n_new, max(pages - s.count, 0), 0};
 }
 
 // last i in [0, n) with pre[i] <= x; pre[0] = 0 <= x
@@ -70,51 +92,47 @@ __device__ __forceinline__ int last_at_most(const int* pre, int n, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) step_tables_kernel(StepTablesArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) step_tables_kernel(StepTablesArgs a) {
     extern __shared__ int dsm[];
-    __shared__ Sums s_warp[kWarps];
+    __shared__ Sums s_warp[32];
     __shared__ unsigned s_bad;
     int* pre_add = dsm;             // [B] tokens of the sequences before b
     int* pre_fresh = dsm + a.B;     // [B] pages they take
     int* pre_given = dsm + 2 * a.B; // [B] pages they give back
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) s_bad = 0;
+    if (tid < 32) s_warp[tid] = Sums{0, 0, 0};
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int F = *a.free_count;
     __syncthreads();
 
-    // prefix sums in 64 bits, kThreads sequences at a time; stored in 32 (used only if totals fit)
+    // prefix sums, one sequence per thread at a time
     Sums carry = {0, 0, 0};
     unsigned bad = 0;
-    for (int base = 0; base < a.B; base += kThreads) {
+    for (int base = 0; base < a.B; base += threads) {
         const int b = base + tid;
         Sums own = {0, 0, 0};
         if (b < a.B) own = seq_sums(a, load_seq(a, b), bad);
-        Sums inc = own;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            Sums o;
-            o.add = __shfl_up_sync(0xffffffffu, inc.add, s);
-            o.fresh = __shfl_up_sync(0xffffffffu, inc.fresh, s);
-            o.given = __shfl_up_sync(0xffffffffu, inc.given, s);
-            if (lane >= s) inc = inc + o;
-        }
+        const Sums inc = warp_inclusive(own, lane);
         if (lane == 31) s_warp[warp] = inc;
         __syncthreads();
-        Sums before = carry, total = carry;
-        for (int w = 0; w < kWarps; ++w) {
-            const Sums v = s_warp[w];
-            if (w < warp) before = before + v;
-            total = total + v;
-        }
-        if (b < a.B) {
-            pre_add[b] = (int)(before.add + inc.add - own.add);
-            pre_fresh[b] = (int)(before.fresh + inc.fresh - own.fresh);
-            pre_given[b] = (int)(before.given + inc.given - own.given);
-        }
-        carry = total;
-        __syncthreads();  // s_warp is reused
+        const Sums all = warp_inclusive(s_warp[lane], lane);
+        Sums before;
+        before.add = __shfl_sync(0xffffffffu, all.add, max(warp - 1, 0));
+        before.fresh = __shfl_sync(0xffffffffu, all.fresh, max(warp - 1, 0));
+        before.given = __shfl_sync(0xffffffffu, all.given, max(warp - 1, 0));
+        if (warp == 0) before = Sums{0, 0, 0};
+        before = carry + before;
+        const Sums prev = shfl_up(inc, 1);
+        if (lane > 0) before = before + prev;
+        if (b < a.B) pre_add[b] = before.add, pre_fresh[b] = before.fresh, pre_given[b] = before.given;
+        Sums total;
+        total.add = __shfl_sync(0xffffffffu, all.add, 31);
+        total.fresh = __shfl_sync(0xffffffffu, all.fresh, 31);
+        total.given = __shfl_sync(0xffffffffu, all.given, 31);
+        carry = carry + total;
+        if (base + threads < a.B) __syncthreads();  // s_warp is reused
     }
     if (bad) atomicOr(&s_bad, bad);
     __syncthreads();
@@ -137,19 +155,43 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(StepTablesArgs a)
     };
 
     const int n_ctas = gridDim.x;
-    const int first = blockIdx.x * kThreads + tid, step = n_ctas * kThreads;
-    for (int t = first; t < a.n_rows; t += step) {
-        int pos = -1, slot = -1;
-        if (t < total) {
-            const int b = last_at_most(pre_add, a.B, t);
-            pos = a.seq_lens[b] + (t - pre_add[b]);
-            const int count = a.page_counts[b], pi = pos / a.page_size;
-            const int page = pi < count ? a.page_table[(size_t)b * a.max_pages + pi]
-                                        : stack(top - 1 - pre_fresh[b] - (pi - count));
-            slot = (int)((unsigned)page * (unsigned)a.page_size + (unsigned)(pos - pi * a.page_size));
+    const int first = blockIdx.x * threads + tid, step = n_ctas * threads;
+    // a thread's rows are taken kPerThread at a time, so that their lookups overlap
+    for (int t0 = first; t0 < a.n_rows; t0 += kPerThread * step) {
+        int b[kPerThread], pos[kPerThread], count[kPerThread], page[kPerThread];
+        long long entry[kPerThread];  // of the page stack, -1: an old page
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int t = t0 + i * step;
+            b[i] = t < total ? last_at_most(pre_add, a.B, t) : -1;
         }
-        a.positions[t] = pos;
-        a.slot_map[t] = slot;
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int seq = max(b[i], 0);
+            pos[i] = b[i] >= 0 ? a.seq_lens[seq] + (t0 + i * step - pre_add[seq]) : -1;
+            count[i] = b[i] >= 0 ? a.page_counts[seq] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int seq = max(b[i], 0), pi = page_of(a, max(pos[i], 0));
+            const bool old = pi < count[i];
+            entry[i] = old ? -1 : top - 1 - pre_fresh[seq] - (pi - count[i]);
+            const int32_t* src = old ? a.page_table + (size_t)seq * a.max_pages + pi : a.free_pages + max(entry[i], 0LL);
+            page[i] = b[i] >= 0 && entry[i] < F ? *src : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int t = t0 + i * step;
+            if (t >= a.n_rows) continue;
+            int slot = -1;
+            if (b[i] >= 0) {
+                if (entry[i] >= F) page[i] = stack(entry[i]);  // a page given back in this step
+                slot = (int)((unsigned)page[i] * (unsigned)a.page_size +
+                             (unsigned)(pos[i] - page_of(a, pos[i]) * a.page_size));
+            }
+            a.positions[t] = pos[i];
+            a.slot_map[t] = slot;
+        }
     }
     for (int k = first; k < fresh; k += step) {
         const int b = last_at_most(pre_fresh, a.B, k);
@@ -205,7 +247,12 @@ cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
     const size_t smem = (size_t)3 * a.B * sizeof(int);
     e = set_smem_limit_once(step_tables_kernel, 3 * kMaxTableSeqs * (int)sizeof(int), false, dev);
     if (e != cudaSuccess) return e;
-    const int ctas = a.n_rows > 2 * kThreads || a.B > 2 * kThreads ? kCluster : 1;
+    // one CTA, as small as the step is, until it would make more than two rounds
+    const int most = a.n_rows > a.B ? a.n_rows : a.B;
+    const int ctas = most > 2 * kMaxThreads ? kCluster : 1;
+    const int threads = most > kMaxThreads / 2 ? kMaxThreads : most > 128 ? kMaxThreads / 2 : 128;
+    StepTablesArgs args = a;
+    args.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -215,12 +262,12 @@ cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(ctas);
-    lc.blockDim = dim3(kThreads);
+    lc.blockDim = dim3(threads);
     lc.dynamicSmemBytes = smem;
     lc.stream = stream;
     lc.attrs = attr;
     lc.numAttrs = 2;
-    return cudaLaunchKernelEx(&lc, step_tables_kernel, a);
+    return cudaLaunchKernelEx(&lc, step_tables_kernel, args);
 }
 
 }  // namespace kvarn

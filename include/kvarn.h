@@ -372,8 +372,8 @@ kvarn_status kvarn_rope_frequencies(const kvarn_rope_config* cfg, double* freqs,
  *   q, k, v     : element (t, h, c) at t * token_stride + h * head_stride + c, so that slices of one
  *                 fused projection can be given; k and v share their strides.  Strides are
  *                 non-negative multiples of 16 bytes, pointers 16-byte aligned.
- *   positions   : [n_tokens] int32.  A negative position marks a padding row: nothing of it is read
- *                 further or written.
+ *   positions   : [n_tokens] int32.  A negative position marks a padding row: nothing of it is
+ *                 written, whatever it holds.
  *   inv_freq    : [rot_dim / 2] double, device (kvarn_rope_frequencies); rot_dim 0 or a multiple of 16
  *                 up to 128 (0: no rotation, inv_freq may be NULL).
  *   q_weight, k_weight : [128] float32, device, 16-byte aligned, or NULL for no norm.
