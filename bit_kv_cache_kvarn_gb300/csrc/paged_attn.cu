@@ -11,15 +11,17 @@
 // operations per query head: HBM.  So the work is arranged around keeping bytes in flight:
 //   - the visible tokens of all (sequence, kv head, block of 16 query heads) units, in groups of 16,
 //     form one stream that is cut into equal contiguous pieces, one per warp of a persistent grid
-//     (one CTA of 8 warps per SM), so the load is even whatever the lengths;
+//     (one CTA per SM), so the load is even whatever the lengths;
 //   - a warp is on its own: it fetches its next groups into its own 3-stage ring in shared memory
 //     (16-byte asynchronous copies, 8 KB per group, 128 to 192 KB in flight per SM) across the ends of
 //     units, and never waits for another warp until its piece is done;
-//   - the query heads of a kv head are the 16 rows of m16n8k16 products: scores from K as it lies
-//     (ldmatrix), then P V with the probabilities taken from the score registers.  A group of 8 KB is
-//     48 or 64 such products, at most a third of what an SM's warps can issue in the time HBM needs to
-//     bring it, so the warp-level products, which need no hand-over between warps, fit better than
-//     128-row tensor-memory tiles that would be at most one eighth full;
+//   - both products are taken transposed, m16n8k16: scores^T = K Q^T with the group's 16 tokens as rows
+//     (K as it lies, ldmatrix) and 8 query heads as columns, out^T = V^T P^T with 16 channels as rows
+//     (V through the transposing ldmatrix) and the probabilities turned in registers (movmatrix).  With
+//     query heads as the 16 rows instead, half of every product, exponential and addition was padding
+//     for groups of up to 8 heads.  A group of 8 KB is 24 or 32 such products per 8 heads, a small part
+//     of what an SM's warps can issue while HBM brings it, so these products, which need no hand-over
+//     between warps, fit better than 128-row tensor-memory tiles;
 //   - units that cross warps of a CTA are joined in shared memory at its end, units that cross CTAs by
 //     a second launch of one CTA per boundary.
 // Rounding: the products take the cache's type exactly; scores, maximum, sums and outputs are fp32.
@@ -44,7 +46,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kGroup = 16;                             // tokens per step
-constexpr int kRows = 16;                              // query heads per unit
+constexpr int kRows = 16;                              // query heads per unit, at most
 constexpr int kHalfBytes = kGroup * kTile * 2;         // K or V of a group
 constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kMaxCtas = 160;                          // CTAs of a grid, at most
@@ -82,6 +84,12 @@ __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+// the 8 x 8 matrix of 16-bit pairs that the warp holds (row lane / 4), transposed
+__device__ __forceinline__ uint32_t turn8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 // d += a (16 x 16) b (16 x 8)
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16) {
@@ -153,10 +161,11 @@ struct Cursor {
     __device__ __forceinline__ int token() const { return (s.first() + g) * kGroup; }
 };
 
+template <bool CAP>
 __device__ __forceinline__ float score(const PagedAttnArgs& a, float dot, float slope, float dist) {
     // in the log2 domain
     float s = dot * a.scale;
-    if (a.softcap > 0.f) s = a.softcap * tanhf(s * a.inv_softcap);
+    if (CAP) s = a.softcap * tanhf(s * a.inv_softcap);
     return fmaf(slope, dist, s) * kLog2e;
 }
 
@@ -229,8 +238,15 @@ struct Left {
     long long end;  // stream position of the last group of the open unit (where it starts here)
 };
 
-// T: type of q and the cache; PIECES: 16-bit pieces of a probability.
-template <typename T, int PIECES>
+__device__ __forceinline__ void store1(const PagedAttnArgs& a, int64_t at, float x) {
+    if (a.out_dtype == KVARN_DTYPE_FP32) static_cast<float*>(a.out)[at] = x;
+    else if (a.out_dtype == KVARN_DTYPE_BF16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(x);
+    else static_cast<__half*>(a.out)[at] = __float2half_rn(x);
+}
+
+// T: type of q and the cache; PIECES: 16-bit pieces of a probability; NT: eights of query heads in a
+// unit; CAP: scores are capped.
+template <typename T, int PIECES, int NT, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ long long s_scan[kWarps];
@@ -306,30 +322,48 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
     uint8_t* own = dsm + warp * kStages * kStageBytes;
     const uint32_t ring = smem_addr(own);
     const int c_row = lane >> 4, c_chunk = lane & 15;  // a copy instruction covers two rows
-    const T* kbase = static_cast<const T*>(a.k_cache) + 8 * c_chunk;
-    const T* vbase = static_cast<const T*>(a.v_cache) + 8 * c_chunk;
+    const int64_t c_off = c_row * a.token_stride + 8 * c_chunk;
+    const T* kbase = static_cast<const T*>(a.k_cache) + c_off;
+    const T* vbase = static_cast<const T*>(a.v_cache) + c_off;
+    uint32_t c_dst[4];  // row r of a copy: 256 r + 16 (chunk ^ (r mod 8)), r = 2 i + c_row
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c_dst[i] = ring + (2 * i + c_row) * (kTile * 2) + ((c_chunk ^ (2 * i + c_row)) << 4);
     Cursor in = at;  // next group to fetch, and its page
     auto page_of = [&](const Cursor& c) { return a.page_table[(int64_t)c.b * a.max_pages + c.token() / a.page_size]; };
     int page = len > 0 ? page_of(in) : 0;
-    int fetched = 0, in_stage = 0;
+    int fetched = 0;
+    uint32_t in_stage = 0;
     auto fetch = [&]() {
         if (fetched < len) {
             const int t0 = in.token();
-            const uint32_t dst = ring + in_stage * kStageBytes;
-            in_stage = in_stage + 1 < kStages ? in_stage + 1 : 0;
             const bool bad = page < 0 || page >= a.n_pages;
             if (bad && lane == 0) atomicOr(&g_paged_attn_error, 1u);
             const int64_t o = (int64_t)(bad ? 0 : page) * a.page_stride + (int64_t)(in.u / a.row_blocks) * a.head_stride +
                               (int64_t)(t0 % a.page_size) * a.token_stride;
+            const T* ks = kbase + o;
+            const T* vs = vbase + o;
+            if (!bad && t0 >= in.s.lo && t0 + kGroup <= in.s.len) {
 #pragma unroll
-            for (int i = 0; i < kGroup / 2; ++i) {
-                const int r = 2 * i + c_row, t = t0 + r;
-                const bool read = !bad && t >= in.s.lo && t < in.s.len;
-                const uint32_t d = dst + r * (kTile * 2) + ((c_chunk ^ (r & 7)) << 4);
-                const int64_t src = o + (int64_t)r * a.token_stride;
-                cp_async16(d, read ? kbase + src : kbase, read);
-                cp_async16(d + kHalfBytes, read ? vbase + src : vbase, read);
+                for (int i = 0; i < kGroup / 2; ++i) {
+                    const uint32_t d = c_dst[i & 3] + in_stage + (i >> 2) * 8 * kTile * 2;
+                    cp_async16(d, ks, true);
+                    cp_async16(d + kHalfBytes, vs, true);
+                    ks += 2 * a.token_stride;
+                    vs += 2 * a.token_stride;
+                }
+            } else {  // rows that are not visible are not read but zero
+#pragma unroll 1
+                for (int i = 0; i < kGroup / 2; ++i) {
+                    const int r = 2 * i + c_row, t = t0 + r;
+                    const bool read = !bad && t >= in.s.lo && t < in.s.len;
+                    const uint32_t d = ring + in_stage + r * (kTile * 2) + ((c_chunk ^ (r & 7)) << 4);
+                    cp_async16(d, read ? ks : kbase, read);
+                    cp_async16(d + kHalfBytes, read ? vs : vbase, read);
+                    ks += 2 * a.token_stride;
+                    vs += 2 * a.token_stride;
+                }
             }
+            in_stage = in_stage + kStageBytes < kStages * kStageBytes ? in_stage + kStageBytes : 0;
             if (++fetched < len) {
                 in.next(a);
                 page = page_of(in);
@@ -349,10 +383,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
     }
 
     // ---- consuming ----
+    // products' layout: a lane holds tokens lane / 4 and lane / 4 + 8 (scores) or those channels (output)
+    // of the query heads 2 (lane mod 4) and + 1 of each eight
     const int row0 = lane >> 2, col0 = 2 * (lane & 3);
-    const int k_row = ((lane >> 4) << 3) + (lane & 7), k_sel = (lane >> 3) & 1;  // ldmatrix rows of K
-    const int v_row = (((lane >> 3) & 1) << 3) + (lane & 7), v_sel = lane >> 4;  // and of V
-    int done = 0, stage = 0;
+    const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row that this lane addresses
+    const int k_row = ((mi & 1) << 3) + mr, k_sel = mi >> 1;
+    const int v_row = ((mi >> 1) << 3) + mr, v_sel = mi & 1;
+    int done = 0;
+    uint32_t stage = 0;
     Left left = {};
     while (done < len) {
         const int b = at.b, u = at.u, g_begin = at.g, n = at.n;
@@ -360,100 +398,111 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
         const int steps = min(n - g_begin, len - done);
         const Heads hd = heads_of(a, u);
         const int rows = hd.rows;
-        // the unit's queries as the products' left operand, zero rows below
-        uint32_t qf[8][4];
-        {
-            const T* q = static_cast<const T*>(a.q) + (int64_t)b * a.q_token_stride + col0;
-            const T* q0 = q + (int64_t)(hd.first + row0) * a.q_head_stride;
-            const T* q1 = q + (int64_t)(hd.first + row0 + 8) * a.q_head_stride;
+        // the unit's queries as the products' right operand, zeros past the last head
+        uint32_t qf[NT][8][2];
+        float slope[NT][2];
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-                qf[kk][0] = row0 < rows ? *reinterpret_cast<const uint32_t*>(q0 + 16 * kk) : 0u;
-                qf[kk][1] = row0 + 8 < rows ? *reinterpret_cast<const uint32_t*>(q1 + 16 * kk) : 0u;
-                qf[kk][2] = row0 < rows ? *reinterpret_cast<const uint32_t*>(q0 + 16 * kk + 8) : 0u;
-                qf[kk][3] = row0 + 8 < rows ? *reinterpret_cast<const uint32_t*>(q1 + 16 * kk + 8) : 0u;
-            }
+        for (int e = 0; e < NT; ++e) {
+            const int r = 8 * e + row0;
+            const T* q = static_cast<const T*>(a.q) + (int64_t)b * a.q_token_stride +
+                         (int64_t)(hd.first + (r < rows ? r : 0)) * a.q_head_stride + col0;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    qf[e][kk][i] = r < rows ? *reinterpret_cast<const uint32_t*>(q + 16 * kk + 8 * i) : 0u;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                slope[e][i] = a.slopes != nullptr && 8 * e + col0 + i < rows ? a.slopes[hd.first + 8 * e + col0 + i] : 0.f;
         }
-        float slope[2] = {0.f, 0.f};
-        if (a.slopes != nullptr) {
-            if (row0 < rows) slope[0] = a.slopes[hd.first + row0];
-            if (row0 + 8 < rows) slope[1] = a.slopes[hd.first + row0 + 8];
+        float o[NT][8][4];
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int e = 0; e < NT; ++e) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[e][i][c] = 0.f;
+            m[e][0] = m[e][1] = -CUDART_INF_F;
+            l[e][0] = l[e][1] = 0.f;
         }
-        float o[16][4];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
-        float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
 
         for (int st = 0; st < steps; ++st) {
             cp_wait<kStages - 2>();
             __syncwarp();
             fetch();  // into the stage consumed in the step before
-            const uint32_t kb = ring + stage * kStageBytes, vb = kb + kHalfBytes;
-            stage = stage + 1 < kStages ? stage + 1 : 0;
-            float s[2][2][4] = {};  // [chain][token half]
+            const uint32_t kb = ring + stage, vb = kb + kHalfBytes;
+            stage = stage + kStageBytes < kStages * kStageBytes ? stage + kStageBytes : 0;
+            float s[NT][2][4] = {};  // [eight][chain]
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 uint32_t f[4];
-                ldm4(f, kb + k_row * (kTile * 2) + (((2 * kk + k_sel) ^ (k_row & 7)) << 4));
-                mma(s[kk & 1][0], qf[kk], f[0], f[1], T());
-                mma(s[kk & 1][1], qf[kk], f[2], f[3], T());
-            }
-            const int t0 = (span.first() + g_begin + st) * kGroup;
-            float mx[2] = {m[0], m[1]};
+                ldm4(f, kb + k_row * (kTile * 2) + (((2 * kk + k_sel) ^ mr) << 4));
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                for (int e = 0; e < NT; ++e) mma(s[e][kk & 1], f, qf[e][kk][0], qf[e][kk][1], T());
+            }
+            const int t0 = (span.first() + g_begin + st) * kGroup + row0;
+            const bool seen[2] = {t0 >= span.lo && t0 < span.len, t0 + 8 >= span.lo && t0 + 8 < span.len};
+            const float dist = (float)(t0 - (span.len - 1));
+            float mx[NT][2];
+            bool grew = false;
+#pragma unroll
+            for (int e = 0; e < NT; ++e) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int t = t0 + 8 * j + col0 + (c & 1);
-                    const float x = score(a, s[0][j][c] + s[1][j][c], slope[c >> 1], (float)(t - (span.len - 1)));
-                    s[0][j][c] = t >= span.lo && t < span.len ? x : -CUDART_INF_F;
-                    mx[c >> 1] = fmaxf(mx[c >> 1], s[0][j][c]);
+                    const float x = score<CAP>(a, s[e][0][c] + s[e][1][c], slope[e][c & 1], dist + 8 * (c >> 1));
+                    s[e][0][c] = seen[c >> 1] ? x : -CUDART_INF_F;
                 }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-            }
-            if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
-                float al[2];
+                for (int i = 0; i < 2; ++i) {
+                    mx[e][i] = fmaxf(fmaxf(s[e][0][i], s[e][0][i + 2]), m[e][i]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    al[h] = mx[h] > m[h] ? exp2f(m[h] - mx[h]) : 1.f;
-                    m[h] = mx[h];
-                    l[h] *= al[h];
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    o[i][0] *= al[0], o[i][1] *= al[0];
-                    o[i][2] *= al[1], o[i][3] *= al[1];
+                    for (int d = 4; d < 32; d <<= 1) mx[e][i] = fmaxf(mx[e][i], __shfl_xor_sync(0xffffffffu, mx[e][i], d));
+                    grew |= mx[e][i] > m[e][i];
                 }
             }
-            // a row whose scores are all -inf so far has no maximum to subtract
-            const float ref[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0], m[1] == -CUDART_INF_F ? 0.f : m[1]};
-            uint32_t p[PIECES][4];
+            if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                for (int e = 0; e < NT; ++e) {
+                    float al[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        al[i] = mx[e][i] > m[e][i] ? exp2f(m[e][i] - mx[e][i]) : 1.f;
+                        m[e][i] = mx[e][i];
+                        l[e][i] *= al[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[e][i][c] *= al[c & 1];
+                }
+            }
+            uint32_t p[NT][PIECES][2];
+#pragma unroll
+            for (int e = 0; e < NT; ++e) {
+                // a row whose scores are all -inf so far has no maximum to subtract
+                const float ref[2] = {m[e][0] == -CUDART_INF_F ? 0.f : m[e][0], m[e][1] == -CUDART_INF_F ? 0.f : m[e][1]};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float p0 = exp2f(s[0][j][2 * h] - ref[h]), p1 = exp2f(s[0][j][2 * h + 1] - ref[h]);
-                    l[h] += p0 + p1;
+                    float p0 = exp2f(s[e][0][2 * h] - ref[0]), p1 = exp2f(s[e][0][2 * h + 1] - ref[1]);
+                    l[e][0] += p0;
+                    l[e][1] += p1;
 #pragma unroll
-                    for (int i = 0; i < PIECES; ++i) p[i][2 * j + h] = take2(p0, p1, T());
+                    for (int i = 0; i < PIECES; ++i) p[e][i][h] = turn8(take2(p0, p1, T()));
                 }
+            }
 #pragma unroll
             for (int cc = 0; cc < 8; ++cc) {
                 uint32_t f[4];
-                ldm4t(f, vb + v_row * (kTile * 2) + (((2 * cc + v_sel) ^ (v_row & 7)) << 4));
-                float d0[4] = {}, d1[4] = {};
+                ldm4t(f, vb + v_row * (kTile * 2) + (((2 * cc + v_sel) ^ mr) << 4));
 #pragma unroll
-                for (int i = PIECES - 1; i >= 0; --i) {  // the small pieces first
-                    mma(d0, p[i], f[0], f[1], T());
-                    mma(d1, p[i], f[2], f[3], T());
+                for (int e = 0; e < NT; ++e) {
+                    float d[4] = {};
+#pragma unroll
+                    for (int i = PIECES - 1; i >= 0; --i) mma(d, f, p[e][i][0], p[e][i][1], T());  // the small pieces first
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[e][cc][c] += d[c];
                 }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) o[2 * cc][c] += d0[c], o[2 * cc + 1][c] += d1[c];
             }
             __syncwarp();  // the stage is read before a later step fetches into it
             at.next(a);
@@ -461,47 +510,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
         done += steps;
 
         // ---- end of the unit, or of this warp's part of it ----
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        }
         const bool starts = g_begin == 0, ends = g_begin + steps == n;
-        if (starts && ends) {
+        const bool whole = starts && ends, last = done == len;
+        // the last unit of the piece, if not whole, waits in shared memory (this warp's ring is read out) for
+        // the join at the CTA's end; one that ended before goes to the workspace
+        if (!whole && last) cp_wait<0>();
+        float* slot = last ? reinterpret_cast<float*>(own) : warp == 0 ? ws.cta_slot(blockIdx.x, 0) : ws.warp_slot(worker);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = row0 + 8 * h;
+        for (int e = 0; e < NT; ++e) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[e][i] += __shfl_xor_sync(0xffffffffu, l[e][i], d);
+                const int r = 8 * e + col0 + i;
                 if (r >= rows) continue;
-                const int64_t row = (int64_t)b * a.Hq + hd.first + r;
-                const float inv = l[h] != 0.f ? 1.f / l[h] : 0.f;
+                if (whole) {
+                    const int64_t row = (int64_t)b * a.Hq + hd.first + r;
+                    const float inv = l[e][i] != 0.f ? 1.f / l[e][i] : 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) store2(a, row * kTile + 8 * i + col0, o[i][2 * h] * inv, o[i][2 * h + 1] * inv);
-                if (a.lse != nullptr && (lane & 3) == 0) a.lse[row] = lse_of(m[h], l[h]);
-            }
-        } else {
-            // the last unit of the piece waits in shared memory (this warp's ring is read out) for the
-            // join at the CTA's end; one that ended before goes to the workspace
-            const bool last = done == len;
-            if (last) cp_wait<0>();
-            float* slot = last ? reinterpret_cast<float*>(own) : warp == 0 ? ws.cta_slot(blockIdx.x, 0) : ws.warp_slot(worker);
+                    for (int cc = 0; cc < 8; ++cc) {
+                        store1(a, row * kTile + 16 * cc + row0, o[e][cc][i] * inv);
+                        store1(a, row * kTile + 16 * cc + row0 + 8, o[e][cc][i + 2] * inv);
+                    }
+                    if (a.lse != nullptr && row0 == 0) a.lse[row] = lse_of(m[e][i], l[e][i]);
+                } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = row0 + 8 * h;
-                if (r >= rows) continue;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<float2*>(slot + r * kTile + 8 * i + col0) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
-                if ((lane & 3) == 0) {
-                    slot[a.rows * kTile + r] = m[h];
-                    slot[a.rows * kTile + a.rows + r] = l[h];
+                    for (int cc = 0; cc < 8; ++cc) {
+                        slot[r * kTile + 16 * cc + row0] = o[e][cc][i];
+                        slot[r * kTile + 16 * cc + row0 + 8] = o[e][cc][i + 2];
+                    }
+                    if (row0 == 0) {
+                        slot[a.rows * kTile + r] = m[e][i];
+                        slot[a.rows * kTile + a.rows + r] = l[e][i];
+                    }
                 }
             }
-            if (last) {
-                left.b = b, left.u = u, left.open = true, left.starts = starts, left.ends = ends;
-                left.end = begin + done - steps + n - 1;
-            } else {
-                left.head = true;
-            }
+        }
+        if (!whole && last) {
+            left.b = b, left.u = u, left.open = true, left.starts = starts, left.ends = ends;
+            left.end = begin + done - steps + n - 1;
+        } else if (!whole) {
+            left.head = true;
         }
     }
 
@@ -570,6 +619,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(PagedAttnAr
     store_row(a, (int64_t)jn.b * a.Hq + hd.first + r, s, lane);
 }
 
+using Kernel = void (*)(PagedAttnArgs);
+template <typename T, int PIECES>
+Kernel pick(const PagedAttnArgs& a) {
+    if (a.rows <= 8) return a.softcap > 0.f ? paged_split_kernel<T, PIECES, 1, true> : paged_split_kernel<T, PIECES, 1, false>;
+    return a.softcap > 0.f ? paged_split_kernel<T, PIECES, 2, true> : paged_split_kernel<T, PIECES, 2, false>;
+}
+
 int grid_ctas(int64_t max_groups, int sms) {
     const int64_t fill = (max_groups + kWarps - 1) / kWarps;
     const int most = sms < kMaxCtas ? sms : kMaxCtas;
@@ -607,9 +663,9 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stre
     const int64_t cap = a.window > 0 && a.window < a.max_len ? (int64_t)a.window + kGroup : a.max_len;
     const int ctas = grid_ctas((int64_t)a.B * a.units * ((cap + kGroup - 1) / kGroup), sms);
     const size_t smem = (size_t)kWarps * kStages * kStageBytes;
-    auto kern = dtype == KVARN_DTYPE_FP16             ? paged_split_kernel<__half, 2>
-                : a.out_dtype == KVARN_DTYPE_FP32 ? paged_split_kernel<__nv_bfloat16, 3>
-                                                  : paged_split_kernel<__nv_bfloat16, 2>;
+    const Kernel kern = dtype == KVARN_DTYPE_FP16             ? pick<__half, 2>(a)
+                        : a.out_dtype == KVARN_DTYPE_FP32 ? pick<__nv_bfloat16, 3>(a)
+                                                          : pick<__nv_bfloat16, 2>(a);
     e = set_smem_limit_once(kern, (int)smem, false, dev);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, a);

@@ -5,10 +5,11 @@
 //   y = x w / sqrt(mean(x^2) + eps) (only with a weight w), then over the first R channels, in pairs
 //   (a, b) = (i, i + R/2) or (2i, 2i + 1):  y_a' = s (y_a cos t - y_b sin t),
 //   y_b' = s (y_b cos t + y_a sin t),  t = position * f_i.
-// The angle is reduced exactly: F = round(2^64 f / 2 pi) is the frequency as a fraction of a turn, and
-// position * F mod 2^64 is the fraction of the turn that is left, off by at most 2^31 * 2^-65 turns
-// (plus the 2^-53 of the fp64 frequency itself) at any position; an fp32 product would be off by 0.06
-// radians at position 10^6.  cos and sin of that fraction are then taken in fp32.
+// The angle is reduced exactly: F = 2^64 f / 2 pi mod 2^64 is the frequency as a fraction of a turn, and
+// position * F mod 2^64 is the fraction of the turn that is left, off by at most 2^31 * 2^-63 turns at
+// any position; an fp32 product would be off by 0.06 radians at position 10^6.  F comes from the
+// frequency's bits by one 64 x 64 bit product (fp64 runs at 2 operations per SM and clock here: 1.3 us
+// for a step of 256 tokens).  cos and sin of that fraction are then taken in fp32.
 //
 // What bounds it: every element is read and written once and nothing is read again, so HBM for
 // chunks of thousands of tokens and launch latency for a decode step.  Eight lanes hold a head, two
@@ -29,34 +30,29 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHalf = kTile / 2;  // most pairs a head has
 
-// 8 consecutive channels of a row, as fp32
-__device__ __forceinline__ void unpack2(uint32_t u, float& a, float& b, __nv_bfloat16) {
-    a = __uint_as_float(u << 16);
-    b = __uint_as_float(u & 0xffff0000u);
+__device__ __forceinline__ float2 unpack2(uint32_t u, __nv_bfloat16) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
-__device__ __forceinline__ void unpack2(uint32_t u, float& a, float& b, __half) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-    a = f.x;
-    b = f.y;
-}
-__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ float2 unpack2(uint32_t u, __half) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+__device__ __forceinline__ uint32_t pack2(float2 v, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
-    const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint32_t pack2(float2 v, __half) {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 8 neighbouring channels of a row, as loaded
 template <typename X>
-struct Raw8 {  // 8 channels as loaded
+struct Raw8 {
     uint4 u;
     __device__ __forceinline__ void load(const X* p) { u = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        unpack2(u.x, f[0], f[1], X());
-        unpack2(u.y, f[2], f[3], X());
-        unpack2(u.z, f[4], f[5], X());
-        unpack2(u.w, f[6], f[7], X());
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+        f[0] = unpack2(u.x, X());
+        f[1] = unpack2(u.y, X());
+        f[2] = unpack2(u.z, X());
+        f[3] = unpack2(u.w, X());
     }
 };
 template <>
@@ -66,22 +62,35 @@ struct Raw8<float> {
         a = reinterpret_cast<const float4*>(p)[0];
         b = reinterpret_cast<const float4*>(p)[1];
     }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+        f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+        f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
     }
 };
 
 template <typename O>
-__device__ __forceinline__ void store8(O* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], f[1], O()), pack2(f[2], f[3], O()),
-                                              pack2(f[4], f[5], O()), pack2(f[6], f[7], O()));
+__device__ __forceinline__ void store8(O* p, const float2 (&f)[4]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], O()), pack2(f[1], O()), pack2(f[2], O()), pack2(f[3], O()));
+}
+
+// 2^64 f / 2 pi mod 2^64, truncated: f = m 2^e with a 53-bit m, and 1 / 2 pi = c 2^-66 with c = 2^64 (2 / pi).
+__device__ __forceinline__ unsigned long long turn_fraction(double f) {
+    const unsigned long long bits = (unsigned long long)__double_as_longlong(f), c = 0xa2f9836e4e44152aull;
+    const int ex = (int)(bits >> 52) & 0x7ff;
+    const unsigned long long m = (bits & ((1ull << 52) - 1)) | (ex > 0 ? 1ull << 52 : 0ull);
+    const unsigned long long hi = __umul64hi(m, c), lo = m * c;
+    const int down = 2 - ((ex > 0 ? ex : 1) - 1075);  // m c 2^(64 - 66 + e)
+    unsigned long long r;
+    if (down >= 64) r = down < 128 ? hi >> (down - 64) : 0ull;
+    else if (down > 0) r = (hi << (64 - down)) | (lo >> down);
+    else r = down > -64 ? lo << -down : 0ull;
+    return (long long)bits < 0 ? 0ull - r : r;
 }
 
 // X: type of q, k, v; O: type of q_out and the cache.  A warp takes a.passes times four of the
 // Hq + 2 Hkv rows of a token and works alone; a token is a.slices warps.
 template <typename X, typename O, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 7) rope_qkv_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kThreads) rope_qkv_kernel(RopeArgs a) {
     __shared__ float2 s_turn[kWarps][kHalf];  // (cos, sin) * rope_scale of the warp's token
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned id = blockIdx.x * kWarps + warp;
@@ -115,11 +124,7 @@ __global__ void __launch_bounds__(kThreads, 7) rope_qkv_kernel(RopeArgs a) {
     const int slot = a.Hkv == 0 ? -1 : a.slot_map != nullptr ? a.slot_map[t] : t;
     if (pos < 0) return;  // a padding row: nothing of it is written
     for (int p = lane; p < pairs; p += 32) {
-        // 2^64 f / 2 pi modulo 2^64: whole turns per position drop out
-        const double turns = a.inv_freq[p] * 0.15915494309189533577;
-        const double frac = turns - floor(turns);
-        const unsigned long long F = __double2ull_rn(frac * 18446744073709551616.0);
-        const unsigned long long at = F * (unsigned long long)(unsigned)pos;
+        const unsigned long long at = turn_fraction(a.inv_freq[p]) * (unsigned long long)(unsigned)pos;
         // nearest fraction of a turn in [-1/2, 1/2), as half turns for sincospif
         const float half_turns = (float)(int)((at + 0x80000000ull) >> 32) * 4.656612873077393e-10f;
         float sn, cs;
@@ -138,55 +143,74 @@ __global__ void __launch_bounds__(kThreads, 7) rope_qkv_kernel(RopeArgs a) {
     }
     __syncwarp();
 
+    // this lane's 8 pairs, kept in registers: from shared memory in every pass, 64 bytes apart, they
+    // were the bound (85% of the L1 rate, three quarters of it bank conflicts)
+    float2 cs[4], sn[4];  // of neighbouring pairs
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        cs[i] = sn[i] = make_float2(0.f, 0.f);
+        if (turned) {
+            const float2 c = s_turn[warp][8 * j + 2 * i], d = s_turn[warp][8 * j + 2 * i + 1];
+            cs[i] = make_float2(c.x, d.x);
+            sn[i] = make_float2(c.y, d.y);
+        }
+    }
+    float2 wa[4], wb[4];  // and its weights, of the queries' or the keys' norm
+    const float* held = nullptr;
+
     for (int pass = 0; pass < a.passes; ++pass, r += 4) {
         Raw8<X> na = {}, nb = {};  // the next four rows
         if (pass + 1 < a.passes) load(r + 4, na, nb);
-        float fa[8], fb[8];
+        float2 fa[4], fb[4];
         ra.get(fa);
         rb.get(fb);
         ra = na, rb = nb;
         const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv;
         const float* w = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
-        float sq = 0.f;
+        float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], sq));
+        for (int i = 0; i < 4; ++i) sq = ffma2(fa[i], fa[i], ffma2(fb[i], fb[i], sq));
+        float sum = sq.x + sq.y;
 #pragma unroll
-        for (int s = 1; s < 8; s <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, s);
+        for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
         O* dst = nullptr;
         if (is_q) dst = qo + r * a.qo_head_stride;
         else if (is_k) dst = kdst != nullptr ? kdst + (r - a.Hq) * a.head_stride : nullptr;
         else if (r < rows) dst = vdst != nullptr ? vdst + (r - a.Hq - a.Hkv) * a.head_stride : nullptr;
         if (dst == nullptr) continue;
         if (w != nullptr) {
-            const float inv = 1.0f / sqrtf(sq * (1.0f / kTile) + a.eps);
-            float wa[8], wb[8];
-            Raw8<float> t8;
-            t8.load(w + ca);
-            t8.get(wa);
-            t8.load(w + cb);
-            t8.get(wb);
+            if (w != held) {
+                held = w;
+                Raw8<float> t8;
+                t8.load(w + ca);
+                t8.get(wa);
+                t8.load(w + cb);
+                t8.get(wb);
+            }
+            const float inv = rsqrtf(sum * (1.0f / kTile) + a.eps);
+            const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) fa[i] *= inv * wa[i], fb[i] *= inv * wb[i];
+            for (int i = 0; i < 4; ++i) {
+                fa[i] = fmul2(fa[i], fmul2(inv2, wa[i]));
+                fb[i] = fmul2(fb[i], fmul2(inv2, wb[i]));
+            }
         }
         if (turned && (is_q || is_k)) {
-            const float2* cs = &s_turn[warp][8 * j];
             if (INTERLEAVED) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 c = cs[i], d = cs[i + 4];
-                    const float x = fa[2 * i], y = fa[2 * i + 1], z = fb[2 * i], u = fb[2 * i + 1];
-                    fa[2 * i] = x * c.x - y * c.y;
-                    fa[2 * i + 1] = y * c.x + x * c.y;
-                    fb[2 * i] = z * d.x - u * d.y;
-                    fb[2 * i + 1] = u * d.x + z * d.y;
+                    // pairs 8 j + i of the first piece and 8 j + 4 + i of the second
+                    const float c = i & 1 ? cs[i / 2].y : cs[i / 2].x, n = i & 1 ? sn[i / 2].y : sn[i / 2].x;
+                    const float d = i & 1 ? cs[i / 2 + 2].y : cs[i / 2 + 2].x, e = i & 1 ? sn[i / 2 + 2].y : sn[i / 2 + 2].x;
+                    fa[i] = make_float2(fa[i].x * c - fa[i].y * n, fa[i].y * c + fa[i].x * n);
+                    fb[i] = make_float2(fb[i].x * d - fb[i].y * e, fb[i].y * d + fb[i].x * e);
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 c = cs[i];
-                    const float x = fa[i], y = fb[i];
-                    fa[i] = x * c.x - y * c.y;
-                    fb[i] = y * c.x + x * c.y;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 x = fa[i], y = fb[i];
+                    fa[i] = ffma2(x, cs[i], fmul2(y, make_float2(-sn[i].x, -sn[i].y)));
+                    fb[i] = ffma2(y, cs[i], fmul2(x, sn[i]));
                 }
             }
         }

@@ -81,13 +81,25 @@ __device__ __forceinline__ Sums seq_sums(const StepTablesArgs& a, Seq s, unsigne
     return {s.n_new, max(pages - s.count, 0), 0};
 }
 
-// last i in [0, n) with pre[i] <= x; pre[0] = 0 <= x
-__device__ __forceinline__ int last_at_most(const int* pre, int n, int x) {
-    int lo = 0, hi = n;
+// last i in [lo, hi) with pre[i] <= x; pre[lo] <= x
+__device__ __forceinline__ int last_at_most(const int* pre, int lo, int hi, int x) {
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (pre[mid] <= x) lo = mid;
         else hi = mid;
+    }
+    return lo;
+}
+
+// The same for the whole warp at once, one x: 32 probes a round.  All lanes return it.
+__device__ __forceinline__ int warp_last_at_most(const int* pre, int n, int x, int lane) {
+    int lo = 0, width = n;  // the answer is in [lo, lo + width)
+    while (width > 1) {
+        const int step = (width + 31) >> 5, i = lo + lane * step;
+        const unsigned in = __ballot_sync(0xffffffffu, lane * step < width && pre[i] <= x);
+        const int k = 31 - __clz(in);  // pre rises, so the set lanes are the first ones; lane 0 is set
+        lo += k * step;
+        width = min(step, width - k * step);
     }
     return lo;
 }
@@ -144,65 +156,79 @@ __global__ void __launch_bounds__(kMaxThreads) step_tables_kernel(StepTablesArgs
     if (carry.add > a.n_rows) status |= KVARN_TABLES_ROWS;
     const bool ok = status == 0;
     const int total = ok ? (int)carry.add : 0, fresh = ok ? (int)carry.fresh : 0;
-    const long long top = (long long)F + carry.given;
+    // ok: top = left + fresh <= 2^31, and every index of the stack fits 32 bits
+    const unsigned top = (unsigned)F + (unsigned)carry.given, held = (unsigned)F;
 
     // entry j of the page stack: the caller's, then the pages given back in order
-    auto stack = [&](long long j) {
-        if (j < F) return a.free_pages[j];
-        const int r = (int)(j - F);
-        const int b = last_at_most(pre_given, a.B, r);
+    auto stack = [&](unsigned j) {
+        if (j < held) return a.free_pages[j];
+        const int r = (int)(j - held);
+        const int b = last_at_most(pre_given, 0, a.B, r);
         return a.page_table[(size_t)b * a.max_pages + (r - pre_given[b])];
     };
 
     const int n_ctas = gridDim.x;
     const int first = blockIdx.x * threads + tid, step = n_ctas * threads;
-    // a thread's rows are taken kPerThread at a time, so that their lookups overlap
-    for (int t0 = first; t0 < a.n_rows; t0 += kPerThread * step) {
-        int b[kPerThread], pos[kPerThread], count[kPerThread], page[kPerThread];
-        long long entry[kPerThread];  // of the page stack, -1: an old page
+    const int n_warps = step >> 5, warp_id = first >> 5;
+    // A warp takes 32 * kPerThread rows in a row: their sequences lie between those of the first and the
+    // last, found by the whole warp, and the lookups of a thread's rows overlap.
+    constexpr int kRun = 32 * kPerThread;
+    for (int run = warp_id * kRun; run < a.n_rows; run += n_warps * kRun) {
+        if (run >= total) {
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int t = t0 + i * step;
-            b[i] = t < total ? last_at_most(pre_add, a.B, t) : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int seq = max(b[i], 0);
-            pos[i] = b[i] >= 0 ? a.seq_lens[seq] + (t0 + i * step - pre_add[seq]) : -1;
-            count[i] = b[i] >= 0 ? a.page_counts[seq] : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int seq = max(b[i], 0), pi = page_of(a, max(pos[i], 0));
-            const bool old = pi < count[i];
-            entry[i] = old ? -1 : top - 1 - pre_fresh[seq] - (pi - count[i]);
-            const int32_t* src = old ? a.page_table + (size_t)seq * a.max_pages + pi : a.free_pages + max(entry[i], 0LL);
-            page[i] = b[i] >= 0 && entry[i] < F ? *src : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int t = t0 + i * step;
-            if (t >= a.n_rows) continue;
-            int slot = -1;
-            if (b[i] >= 0) {
-                if (entry[i] >= F) page[i] = stack(entry[i]);  // a page given back in this step
-                slot = (int)((unsigned)page[i] * (unsigned)a.page_size +
-                             (unsigned)(pos[i] - page_of(a, pos[i]) * a.page_size));
+            for (int i = 0; i < kPerThread; ++i) {
+                const int t = run + 32 * i + lane;
+                if (t < a.n_rows) a.positions[t] = a.slot_map[t] = -1;
             }
-            a.positions[t] = pos[i];
-            a.slot_map[t] = slot;
+            continue;
+        }
+        const int b_lo = warp_last_at_most(pre_add, a.B, run, lane);
+        const int b_hi = warp_last_at_most(pre_add, a.B, min(run + kRun, total) - 1, lane) + 1;
+        int b[kPerThread], pos[kPerThread], count[kPerThread], page[kPerThread];
+        unsigned entry[kPerThread];  // of the page stack
+        bool old[kPerThread];        // or a page that the sequence holds already
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int t = min(run + 32 * i + lane, total - 1);
+            b[i] = last_at_most(pre_add, b_lo, b_hi, t);
+            pos[i] = a.seq_lens[b[i]] + (t - pre_add[b[i]]);
+            count[i] = a.page_counts[b[i]];
+        }
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int pi = page_of(a, pos[i]);
+            old[i] = pi < count[i];
+            entry[i] = old[i] ? 0u : top - 1u - (unsigned)(pre_fresh[b[i]] + pi - count[i]);
+            page[i] = -1;
+            if (old[i] || entry[i] < held)
+                page[i] = *(old[i] ? a.page_table + (size_t)b[i] * a.max_pages + pi : a.free_pages + entry[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int t = run + 32 * i + lane;
+            if (!old[i] && entry[i] >= held) page[i] = stack(entry[i]);  // a page given back in this step
+            const int slot = (int)((unsigned)page[i] * (unsigned)a.page_size +
+                                   (unsigned)(pos[i] - page_of(a, pos[i]) * a.page_size));
+            if (t < a.n_rows) {
+                a.positions[t] = t < total ? pos[i] : -1;
+                a.slot_map[t] = t < total ? slot : -1;
+            }
         }
     }
-    for (int k = first; k < fresh; k += step) {
-        const int b = last_at_most(pre_fresh, a.B, k);
+    for (int run = warp_id * 32; run < fresh; run += n_warps * 32) {
+        const int b_lo = warp_last_at_most(pre_fresh, a.B, run, lane);
+        const int k = run + lane;
+        if (k >= fresh) continue;
+        const int b = last_at_most(pre_fresh, b_lo, a.B, k);
         const int i = a.page_counts[b] + (k - pre_fresh[b]);
-        const int page = stack(top - 1 - k);
+        const int page = stack(top - 1u - (unsigned)k);
         a.page_table[(size_t)b * a.max_pages + i] = page;
         for (int h = 0; h < a.Hkv; ++h)
             a.block_table[((size_t)b * a.Hkv + h) * a.max_pages + i] = page * a.Hkv + h;
     }
-    if (ok)
-        for (long long j = (long long)F + first; j < left; j += step) a.free_pages[j] = stack(j);
+    // the pages given back that stay on the stack
+    const int kept = ok && left > F ? (int)(left - F) : 0;
+    for (int r = first; r < kept; r += step) a.free_pages[F + r] = stack(held + (unsigned)r);
     for (int b = first; b <= a.B; b += step)
         a.cu_tokens[b] = !ok ? 0 : b < a.B ? pre_add[b] : total;
 
@@ -211,16 +237,16 @@ __global__ void __launch_bounds__(kMaxThreads) step_tables_kernel(StepTablesArgs
     else __syncthreads();
     for (int b = first; b < a.B; b += step) {
         const Seq s = load_seq(a, b);
-        int kv = s.len, held = s.count;
+        int kv = s.len, pages = s.count;
         if (ok) {
-            if (s.n_new < 0) kv = held = 0;
+            if (s.n_new < 0) kv = pages = 0;
             else {
                 kv = s.len + s.n_new;
-                held = max(held, (int)(((long long)kv + a.page_size - 1) / a.page_size));
+                pages = max(pages, kv > 0 ? page_of(a, kv - 1) + 1 : 0);
             }
         }
         a.kv_lens[b] = kv;
-        a.page_counts_out[b] = held;
+        a.page_counts_out[b] = pages;
     }
     if (first == 0) {
         *a.free_count_out = ok ? (int)left : F;
