@@ -64,15 +64,6 @@ struct Join {
 
 __host__ __device__ constexpr size_t slot_floats(int rows) { return ((size_t)rows * (kTile + 2) + 3) & ~(size_t)3; }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
-    const int n = read ? 16 : 0;  // 0: the 16 bytes are zero-filled
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -369,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
                 page = page_of(in);
             }
         }
-        cp_commit();
+        cp_async_commit();
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
@@ -428,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
         }
 
         for (int st = 0; st < steps; ++st) {
-            cp_wait<kStages - 2>();
+            cp_async_wait<kStages - 2>();
             __syncwarp();
             fetch();  // into the stage consumed in the step before
             const uint32_t kb = ring + stage, vb = kb + kHalfBytes;
@@ -514,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
         const bool whole = starts && ends, last = done == len;
         // the last unit of the piece, if not whole, waits in shared memory (this warp's ring is read out) for
         // the join at the CTA's end; one that ended before goes to the workspace
-        if (!whole && last) cp_wait<0>();
+        if (!whole && last) cp_async_wait<0>();
         float* slot = last ? reinterpret_cast<float*>(own) : warp == 0 ? ws.cta_slot(blockIdx.x, 0) : ws.warp_slot(worker);
 #pragma unroll
         for (int e = 0; e < NT; ++e) {

@@ -43,30 +43,29 @@ __device__ __forceinline__ uint32_t pack2(float2 v, __half) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 8 neighbouring channels of a row, as loaded
+// Channels c .. c + 7 of a row in shared memory, in the pieces' order above.
 template <typename X>
-struct Raw8 {
-    uint4 u;
-    __device__ __forceinline__ void load(const X* p) { u = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void get(float2 (&f)[4]) const {
+__device__ __forceinline__ void take8(const uint4* row, int c, float2 (&f)[4]) {
+    const int p = c * (int)sizeof(X) / 16;
+    const uint4 u = row[p ^ ((p >> 3) & 3)];
+    if constexpr (sizeof(X) == 2) {
         f[0] = unpack2(u.x, X());
         f[1] = unpack2(u.y, X());
         f[2] = unpack2(u.z, X());
         f[3] = unpack2(u.w, X());
+    } else {
+        const uint4 w = row[(p + 1) ^ ((p >> 3) & 3)];
+        f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+        f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+        f[2] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+        f[3] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
     }
-};
-template <>
-struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void get(float2 (&f)[4]) const {
-        f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
-        f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
-    }
-};
+}
+__device__ __forceinline__ void load8(const float* p, float2 (&f)[4]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
+}
 
 template <typename O>
 __device__ __forceinline__ void store8(O* p, const float2 (&f)[4]) {
@@ -87,106 +86,148 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f) {
     return (long long)bits < 0 ? 0ull - r : r;
 }
 
-// X: type of q, k, v; O: type of q_out and the cache.  A warp takes a.passes times four of the
-// Hq + 2 Hkv rows of a token and works alone; a token is a.slices warps.
-template <typename X, typename O, bool INTERLEAVED>
+// X: type of q, k, v; O: type of q_out and the cache; SHARE: warps that share a token and its angles.  A
+// warp takes a.passes times four of the token's Hq + 2 Hkv rows; grid.y: the slices of a token.
+template <typename X, typename O, int SHARE, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rope_qkv_kernel(RopeArgs a) {
-    __shared__ float2 s_turn[kWarps][kHalf];  // (cos, sin) * rope_scale of the warp's token
+    constexpr int kDepth = sizeof(X) == 4 ? 3 : 4;     // passes in flight per warp
+    constexpr int kPieces = kTile * sizeof(X) / 16;  // 16-byte pieces of a row; piece p lies at p ^ (p / 8 mod 4),
+                                                     // so that the lanes of a row never meet in a bank
+    __shared__ float2 s_turns[kWarps / SHARE][kHalf];  // (cos, sin) * rope_scale of the tokens
+    __shared__ uint4 s_raw[kWarps][kDepth][4][kPieces];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned id = blockIdx.x * kWarps + warp;
-    const int t = (int)(id / (unsigned)a.slices), slice = (int)(id - (unsigned)t * (unsigned)a.slices);
+    const int t = blockIdx.x * (kWarps / SHARE) + warp / SHARE;
+    const int row_base = 4 * (blockIdx.y * a.passes * SHARE + warp % SHARE);
+    float2* s_turn = s_turns[warp / SHARE];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (t >= a.n_tokens) return;
+    if (SHARE == 1 && t >= a.n_tokens) return;
     const int rows = a.Hq + 2 * a.Hkv, pairs = a.rot_dim >> 1;
     const int sub = lane >> 3, j = lane & 7;
     const bool turned = j < (a.rot_dim >> 4);
     const int ca = 8 * (INTERLEAVED || !turned ? 2 * j : j);
     const int cb = INTERLEAVED || !turned ? ca + 8 : ca + pairs;
-    const X* q = static_cast<const X*>(a.q) + t * a.q_token_stride;
-    const X* k = static_cast<const X*>(a.k) + t * a.kv_token_stride;
-    const X* v = static_cast<const X*>(a.v) + t * a.kv_token_stride;
-    O* qo = static_cast<O*>(a.q_out) + t * a.qo_token_stride;
+    constexpr int kStep = 4 * SHARE;  // rows from one pass to the next
 
-    auto load = [&](int r, Raw8<X>& ra, Raw8<X>& rb) {
-        if (r >= rows) return;
-        const X* src = r < a.Hq           ? q + r * a.q_head_stride
-                       : r < a.Hq + a.Hkv ? k + (r - a.Hq) * a.kv_head_stride
-                                          : v + (r - a.Hq - a.Hkv) * a.kv_head_stride;
-        ra.load(src + ca);
-        rb.load(src + cb);
+    // Rows come through a ring in shared memory that each warp fills and reads alone; kept in registers,
+    // passes ahead would cost the warps that the rate needs.  The copies go along the row: with each lane
+    // copying its own pieces, the interleaved layout and fp32 took half sectors, and twice the L2 traffic.
+    // Addresses are carried from pass to pass inside a section (queries, keys, values): made anew for
+    // each row they were half of the kernel's instructions.
+    constexpr uint32_t kEntry = sizeof(s_raw[0][0]);
+    const uint32_t ring = smem_addr(s_raw[warp][0][sub]);
+    const int last_row = min(rows, row_base + a.passes * kStep);  // of the warp, rounded up
+    int in_row = row_base + sub, in_end = 0;
+    const uint4* src = nullptr;
+    int64_t src_step = 0;
+    uint32_t in_at = 0;
+    auto load = [&]() {
+        if (in_row < last_row) {
+            if (in_row >= in_end) {  // the first row, or one of another section
+                const X* p;
+                int64_t stride;
+                if (in_row < a.Hq) {
+                    stride = a.q_head_stride, in_end = a.Hq;
+                    p = static_cast<const X*>(a.q) + t * a.q_token_stride + in_row * stride;
+                } else {
+                    const bool key = in_row < a.Hq + a.Hkv;
+                    const int h = in_row - (key ? a.Hq : a.Hq + a.Hkv);
+                    stride = a.kv_head_stride, in_end = key ? a.Hq + a.Hkv : rows;
+                    p = static_cast<const X*>(key ? a.k : a.v) + t * a.kv_token_stride + h * stride;
+                }
+                src = reinterpret_cast<const uint4*>(p) + j;
+                src_step = kStep * stride * (int64_t)sizeof(X) / 16;
+            }
+#pragma unroll
+            for (int i = 0; i < kPieces / 8; ++i)
+                cp_async16(ring + in_at + 16 * ((j + 8 * i) ^ (i & 3)), src + 8 * i, true);
+            src += src_step;
+            in_row += kStep;
+        }
+        in_at = in_at + kEntry < kDepth * kEntry ? in_at + kEntry : 0;
+        cp_async_commit();
     };
     // the first rows are on their way while the angles are made
-    int r = 4 * slice * a.passes + sub;
-    Raw8<X> ra = {}, rb = {};
-    load(r, ra, rb);
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) load();
     const int pos = a.positions[t];
     const int slot = a.Hkv == 0 ? -1 : a.slot_map != nullptr ? a.slot_map[t] : t;
-    if (pos < 0) return;  // a padding row: nothing of it is written
-    for (int p = lane; p < pairs; p += 32) {
+    if (pos < 0) {  // a padding row: nothing of it is written
+        cp_async_wait<0>();
+        return;
+    }
+    for (int p = lane + 32 * (warp % SHARE); p < pairs; p += 32 * SHARE) {
         const unsigned long long at = turn_fraction(a.inv_freq[p]) * (unsigned long long)(unsigned)pos;
         // nearest fraction of a turn in [-1/2, 1/2), as half turns for sincospif
         const float half_turns = (float)(int)((at + 0x80000000ull) >> 32) * 4.656612873077393e-10f;
         float sn, cs;
         sincospif(half_turns, &sn, &cs);
-        s_turn[warp][p] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
+        s_turn[p] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
     }
-    O* kdst = nullptr;
-    O* vdst = nullptr;
+    int64_t cache_at = -1;  // of the token's slot
     if (slot >= 0 && slot < a.n_slots) {
         const int page = slot / a.page_size, off = slot - page * a.page_size;
-        const int64_t o = page * a.page_stride + off * a.token_stride;
-        kdst = static_cast<O*>(a.k_cache) + o;
-        vdst = static_cast<O*>(a.v_cache) + o;
+        cache_at = page * a.page_stride + off * a.token_stride;
     } else if (slot >= 0 && lane == 0) {
         atomicOr(&g_rope_error, 1u);
     }
-    __syncwarp();
+    if (SHARE == kWarps) __syncthreads();
+    else __syncwarp();
 
-    // this lane's 8 pairs, kept in registers: from shared memory in every pass, 64 bytes apart, they
-    // were the bound (85% of the L1 rate, three quarters of it bank conflicts)
+    // This lane's 8 pairs, kept in registers: from shared memory in every pass, 64 bytes apart, they
+    // were the bound (85% of the L1 rate, three quarters of it bank conflicts).
     float2 cs[4], sn[4];  // of neighbouring pairs
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         cs[i] = sn[i] = make_float2(0.f, 0.f);
         if (turned) {
-            const float2 c = s_turn[warp][8 * j + 2 * i], d = s_turn[warp][8 * j + 2 * i + 1];
+            const float2 c = s_turn[8 * j + 2 * i], d = s_turn[8 * j + 2 * i + 1];
             cs[i] = make_float2(c.x, d.x);
             sn[i] = make_float2(c.y, d.y);
         }
     }
-    float2 wa[4], wb[4];  // and its weights, of the queries' or the keys' norm
-    const float* held = nullptr;
+    float2 wa[4], wb[4];  // and its weights, where the section has a norm
+    bool normed = false, turn = false, kept = false;
+    int r = row_base + sub, end = 0;
+    O* dst = nullptr;
+    int64_t dst_step = 0;
+    const uint4* entry = s_raw[warp][0][sub];
+    int out_at = 0;
 
-    for (int pass = 0; pass < a.passes; ++pass, r += 4) {
-        Raw8<X> na = {}, nb = {};  // the next four rows
-        if (pass + 1 < a.passes) load(r + 4, na, nb);
+    for (int pass = 0; pass < a.passes; ++pass, r += kStep) {
+        cp_async_wait<kDepth - 1>();
+        __syncwarp();
         float2 fa[4], fb[4];
-        ra.get(fa);
-        rb.get(fb);
-        ra = na, rb = nb;
-        const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv;
-        const float* w = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
+        take8<X>(entry + out_at, ca, fa);
+        take8<X>(entry + out_at, cb, fb);
+        out_at = out_at + 4 * kPieces < kDepth * 4 * kPieces ? out_at + 4 * kPieces : 0;
+        if (r >= end && r < rows) {
+            const float* w = nullptr;
+            if (r < a.Hq) {
+                dst = static_cast<O*>(a.q_out) + t * a.qo_token_stride + r * a.qo_head_stride;
+                dst_step = kStep * a.qo_head_stride;
+                end = a.Hq, w = a.q_weight, turn = turned, kept = true;
+            } else {
+                const bool key = r < a.Hq + a.Hkv;
+                const int h = r - (key ? a.Hq : a.Hq + a.Hkv);
+                dst = static_cast<O*>(key ? a.k_cache : a.v_cache) + cache_at + h * a.head_stride;
+                dst_step = kStep * a.head_stride;
+                end = key ? a.Hq + a.Hkv : rows, w = key ? a.k_weight : nullptr, turn = key && turned, kept = cache_at >= 0;
+            }
+            normed = w != nullptr;
+            if (normed) {
+                load8(w + ca, wa);
+                load8(w + cb, wb);
+            }
+        }
         float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sq = ffma2(fa[i], fa[i], ffma2(fb[i], fb[i], sq));
         float sum = sq.x + sq.y;
 #pragma unroll
         for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        O* dst = nullptr;
-        if (is_q) dst = qo + r * a.qo_head_stride;
-        else if (is_k) dst = kdst != nullptr ? kdst + (r - a.Hq) * a.head_stride : nullptr;
-        else if (r < rows) dst = vdst != nullptr ? vdst + (r - a.Hq - a.Hkv) * a.head_stride : nullptr;
-        if (dst == nullptr) continue;
-        if (w != nullptr) {
-            if (w != held) {
-                held = w;
-                Raw8<float> t8;
-                t8.load(w + ca);
-                t8.get(wa);
-                t8.load(w + cb);
-                t8.get(wb);
-            }
+        load();  // into the entry that the warp has just read
+        if (normed) {
             const float inv = rsqrtf(sum * (1.0f / kTile) + a.eps);
             const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
@@ -195,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) rope_qkv_kernel(RopeArgs a) {
                 fb[i] = fmul2(fb[i], fmul2(inv2, wb[i]));
             }
         }
-        if (turned && (is_q || is_k)) {
+        if (turn) {
             if (INTERLEAVED) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -208,33 +249,39 @@ __global__ void __launch_bounds__(kThreads) rope_qkv_kernel(RopeArgs a) {
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 x = fa[i], y = fb[i];
-                    fa[i] = ffma2(x, cs[i], fmul2(y, make_float2(-sn[i].x, -sn[i].y)));
+                    const float2 x = fa[i], y = fb[i], z = fmul2(y, sn[i]);
+                    fa[i] = ffma2(x, cs[i], make_float2(-z.x, -z.y));
                     fb[i] = ffma2(y, cs[i], fmul2(x, sn[i]));
                 }
             }
         }
-        store8(dst + ca, fa);
-        store8(dst + cb, fb);
+        if (kept && r < rows) {
+            store8(dst + ca, fa);
+            store8(dst + cb, fb);
+        }
+        dst += dst_step;
     }
 }
 
+template <typename X, typename O, int SHARE>
+cudaError_t launch(RopeArgs a, int slices, int dev, cudaStream_t stream) {
+    const int rounds = (a.Hq + 2 * a.Hkv + 4 * SHARE - 1) / (4 * SHARE);
+    slices = slices < 1 ? 1 : slices < rounds ? slices : rounds;
+    a.passes = (rounds + slices - 1) / slices;
+    const dim3 grid((unsigned)(((int64_t)a.n_tokens * SHARE + kWarps - 1) / kWarps), (unsigned)((rounds + a.passes - 1) / a.passes));
+    const auto kern = a.interleaved ? rope_qkv_kernel<X, O, SHARE, true> : rope_qkv_kernel<X, O, SHARE, false>;
+    const cudaError_t e = set_smem_limit_once(kern, 0, true, dev);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, grid, dim3(kThreads), 0, stream, a);
+}
+
 template <typename X, typename O>
-cudaError_t launch(RopeArgs a, cudaStream_t stream) {
+cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
     int dev = 0, sms = 0;
     const cudaError_t e = current_device(&dev, &sms);
     if (e != cudaSuccess) return e;
-    // a warp takes the whole token once there are tokens enough for 28 warps on every SM, so that the
-    // angles are made once; with fewer, a token is spread over more warps
-    const int quads = (a.Hq + 2 * a.Hkv + 3) / 4;
-    const int64_t passes = (int64_t)a.n_tokens * quads / (28 * (int64_t)sms);
-    a.passes = (int)(passes < 1 ? 1 : passes < quads ? passes : quads);
-    a.slices = (quads + a.passes - 1) / a.passes;
-    a.passes = (quads + a.slices - 1) / a.slices;
-    const int64_t warps = (int64_t)a.n_tokens * a.slices;
-    const dim3 grid((unsigned)((warps + kWarps - 1) / kWarps));
-    return a.interleaved ? launch_pdl(rope_qkv_kernel<X, O, true>, grid, dim3(kThreads), 0, stream, a)
-                         : launch_pdl(rope_qkv_kernel<X, O, false>, grid, dim3(kThreads), 0, stream, a);
+    if (a.n_tokens < 8 * sms) return launch<X, O, kWarps>(a, 4 * sms / a.n_tokens, dev, stream);
+    return launch<X, O, 1>(a, 40 * sms / a.n_tokens, dev, stream);
 }
 
 }  // namespace

@@ -7,10 +7,11 @@
 // waits for another's allotment, and the result does not depend on the schedule.
 //
 // What bounds it: latency.  A step moves a few words per token and per new page (at most some MB for a
-// long prefill) and is a chain of three dependent round trips (lengths, the page or stack entry, the
-// store) around one block-wide scan.  One launch, one cluster: every CTA scans all sequences itself,
-// which is cheaper than handing prefixes over, and the one cluster barrier only keeps the lengths,
-// counts and stack size, which may be updated in place, unwritten until every CTA has read them.
+// long prefill) and is a chain of dependent round trips (lengths, stack entry, page table, store) around
+// one block-wide scan and one barrier.  One launch, one cluster: every CTA scans all sequences itself,
+// which is cheaper than handing prefixes over; the one cluster barrier stands between everything that
+// reads the lengths, counts and stack size and their update, which may be in place, and between the
+// page table's new entries and the rows that look them up.
 #include <cooperative_groups.h>
 
 #include "kvarn_common.cuh"
@@ -170,80 +171,33 @@ __global__ void __launch_bounds__(kMaxThreads) step_tables_kernel(StepTablesArgs
     const int n_ctas = gridDim.x;
     const int first = blockIdx.x * threads + tid, step = n_ctas * threads;
     const int n_warps = step >> 5, warp_id = first >> 5;
-    // A warp takes 32 * kPerThread rows in a row: their sequences lie between those of the first and the
-    // last, found by the whole warp, and the lookups of a thread's rows overlap.
-    constexpr int kRun = 32 * kPerThread;
-    for (int run = warp_id * kRun; run < a.n_rows; run += n_warps * kRun) {
-        if (run >= total) {
-#pragma unroll
-            for (int i = 0; i < kPerThread; ++i) {
-                const int t = run + 32 * i + lane;
-                if (t < a.n_rows) a.positions[t] = a.slot_map[t] = -1;
-            }
-            continue;
-        }
-        const int b_lo = warp_last_at_most(pre_add, a.B, run, lane);
-        const int b_hi = warp_last_at_most(pre_add, a.B, min(run + kRun, total) - 1, lane) + 1;
-        int b[kPerThread], pos[kPerThread], count[kPerThread], page[kPerThread];
-        unsigned entry[kPerThread];  // of the page stack
-        bool old[kPerThread];        // or a page that the sequence holds already
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int t = min(run + 32 * i + lane, total - 1);
-            b[i] = last_at_most(pre_add, b_lo, b_hi, t);
-            pos[i] = a.seq_lens[b[i]] + (t - pre_add[b[i]]);
-            count[i] = a.page_counts[b[i]];
-        }
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int pi = page_of(a, pos[i]);
-            old[i] = pi < count[i];
-            entry[i] = old[i] ? 0u : top - 1u - (unsigned)(pre_fresh[b[i]] + pi - count[i]);
-            page[i] = -1;
-            if (old[i] || entry[i] < held)
-                page[i] = *(old[i] ? a.page_table + (size_t)b[i] * a.max_pages + pi : a.free_pages + entry[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-            const int t = run + 32 * i + lane;
-            if (!old[i] && entry[i] >= held) page[i] = stack(entry[i]);  // a page given back in this step
-            const int slot = (int)((unsigned)page[i] * (unsigned)a.page_size +
-                                   (unsigned)(pos[i] - page_of(a, pos[i]) * a.page_size));
-            if (t < a.n_rows) {
-                a.positions[t] = t < total ? pos[i] : -1;
-                a.slot_map[t] = t < total ? slot : -1;
-            }
-        }
-    }
-    for (int run = warp_id * 32; run < fresh; run += n_warps * 32) {
-        const int b_lo = warp_last_at_most(pre_fresh, a.B, run, lane);
-        const int k = run + lane;
-        if (k >= fresh) continue;
-        const int b = last_at_most(pre_fresh, b_lo, a.B, k);
+
+    // ---- pages: taken, and given back for good ----
+    for (int k = first; k < fresh; k += step) {
+        const int b = last_at_most(pre_fresh, 0, a.B, k);
         const int i = a.page_counts[b] + (k - pre_fresh[b]);
         const int page = stack(top - 1u - (unsigned)k);
         a.page_table[(size_t)b * a.max_pages + i] = page;
         for (int h = 0; h < a.Hkv; ++h)
             a.block_table[((size_t)b * a.Hkv + h) * a.max_pages + i] = page * a.Hkv + h;
     }
-    // the pages given back that stay on the stack
     const int kept = ok && left > F ? (int)(left - F) : 0;
     for (int r = first; r < kept; r += step) a.free_pages[F + r] = stack(held + (unsigned)r);
-    for (int b = first; b <= a.B; b += step)
-        a.cu_tokens[b] = !ok ? 0 : b < a.B ? pre_add[b] : total;
+    for (int b = first; b <= a.B; b += step) a.cu_tokens[b] = !ok ? 0 : b < a.B ? pre_add[b] : total;
 
-    // everything that may alias an input, once every CTA has read it
+    // From here on the lengths and counts may be overwritten in place: the old lengths move to shared memory.
+    __syncthreads();
+    int* old_len = pre_given;
+    for (int b = tid; b < a.B; b += threads) old_len[b] = a.seq_lens[b];
     if (n_ctas > 1) cg::this_cluster().sync();
     else __syncthreads();
+
     for (int b = first; b < a.B; b += step) {
-        const Seq s = load_seq(a, b);
-        int kv = s.len, pages = s.count;
+        const int len = old_len[b], n_new = a.n_new[b], count = a.page_counts[b];
+        int kv = len, pages = count;
         if (ok) {
-            if (s.n_new < 0) kv = pages = 0;
-            else {
-                kv = s.len + s.n_new;
-                pages = max(pages, kv > 0 ? page_of(a, kv - 1) + 1 : 0);
-            }
+            kv = n_new < 0 ? 0 : len + n_new;
+            pages = n_new < 0 ? 0 : max(count, kv > 0 ? page_of(a, kv - 1) + 1 : 0);
         }
         a.kv_lens[b] = kv;
         a.page_counts_out[b] = pages;
@@ -252,6 +206,42 @@ __global__ void __launch_bounds__(kMaxThreads) step_tables_kernel(StepTablesArgs
         *a.free_count_out = ok ? (int)left : F;
         *a.status = (int)status;
         if (!ok) atomicOr(&g_tables_error, 1u);
+    }
+
+    // ---- rows ----
+    // A warp takes 32 * kPerThread rows in a row: their sequences lie between those of the first and the
+    // last, found by the whole warp, and the lookups of a thread's rows overlap.  Every page is in the
+    // table by now, written by any CTA of the cluster, hence the loads from L2.
+    constexpr int kRun = 32 * kPerThread;
+    for (int run = warp_id * kRun; run < a.n_rows; run += n_warps * kRun) {
+        int pos[kPerThread], slot[kPerThread];
+        if (run < total) {
+            int b_lo = 0, b_hi = a.B;
+            if (a.B > 64) {  // a whole warp's search is two to three probes, a thread's log2(B)
+                b_lo = warp_last_at_most(pre_add, a.B, run, lane);
+                b_hi = warp_last_at_most(pre_add, a.B, min(run + kRun, total) - 1, lane) + 1;
+            }
+            int page[kPerThread];
+#pragma unroll
+            for (int i = 0; i < kPerThread; ++i) {
+                const int t = min(run + 32 * i + lane, total - 1);
+                const int b = last_at_most(pre_add, b_lo, b_hi, t);
+                pos[i] = old_len[b] + (t - pre_add[b]);
+                page[i] = __ldcg(a.page_table + (size_t)b * a.max_pages + page_of(a, pos[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < kPerThread; ++i)
+                slot[i] = (int)((unsigned)page[i] * (unsigned)a.page_size +
+                                (unsigned)(pos[i] - page_of(a, pos[i]) * a.page_size));
+        }
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            const int t = run + 32 * i + lane;
+            if (t < a.n_rows) {
+                a.positions[t] = t < total ? pos[i] : -1;
+                a.slot_map[t] = t < total ? slot[i] : -1;
+            }
+        }
     }
 }
 
