@@ -27,7 +27,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMaxThreads = 1024;
-constexpr int kCluster = 8;
+constexpr int kCluster = 16;                 // 8 took 13.4 us where 16 take 10.8 (1000 mixed requests, 72k rows)
 constexpr int kPerThread = 4;                // rows in flight per thread
 constexpr unsigned kMost = 0x7fffffffu;
 
@@ -262,6 +262,14 @@ cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const size_t smem = (size_t)3 * a.B * sizeof(int);
     e = set_smem_limit_once(step_tables_kernel, 3 * kMaxTableSeqs * (int)sizeof(int), false, dev);
+    if (e == cudaSuccess) {  // 16 CTAs in a cluster are past the portable size
+        static std::atomic<unsigned long long> allowed{0};
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) & bit)) {
+            e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess && dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
+        }
+    }
     if (e != cudaSuccess) return e;
     // one CTA, as small as the step is, until it would make more than two rounds
     const int most = a.n_rows > a.B ? a.n_rows : a.B;
