@@ -148,7 +148,9 @@ cudaError_t read_and_clear_rope_error(unsigned int* out);
 struct PagedAttnArgs {
     int B, Hq, Hkv, page_size, max_pages, max_len, window, out_dtype;
     int64_t n_pages;
-    int group, rows, row_blocks, units;  // set by the launcher: query heads per kv head, per unit; units per sequence
+    // set by the launcher: query heads per kv head and (at most) per unit, units per kv head and per
+    // sequence, log2 of a page size that is a power of two (else -1)
+    int group, rows, row_blocks, units, page_shift;
     float scale, softcap, inv_softcap;
     const void* q;
     int64_t q_token_stride, q_head_stride;

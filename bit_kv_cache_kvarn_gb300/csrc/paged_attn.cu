@@ -50,12 +50,14 @@ constexpr int kRows = 16;                              // query heads per unit, 
 constexpr int kHalfBytes = kGroup * kTile * 2;         // K or V of a group
 constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kMaxCtas = 160;                          // CTAs of a grid, at most
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 8;
+constexpr int kAhead = 4;                              // parts that a warp of the join loads at once
 
 // Workspace: partial slots, each o[rows][128] then m[rows] and l[rows] (fp32; a slot is a multiple of 16
-// bytes, joins read four channels at a time): one per warp (the unit that began before its piece and ends
-// inside it), then two per CTA (slot 0: the unit that began before the CTA's pieces, slot 1: the one
-// that begins in them and goes on after them); then one Join per CTA.
+// bytes, joins read four channels at a time): two per CTA (slot 0: the unit that began before the CTA's
+// pieces, slot 1: the one that begins in them and goes on after them), then one per warp (the unit that
+// began before its piece and ends inside it; kept in shared memory where a slot has at most 8 rows);
+// then one Join per CTA.
 struct Join {
     int b, u;  // sequence and unit that slot 1 begins; b = -1: none
     int last;  // the last CTA that holds a part
@@ -160,39 +162,44 @@ __device__ __forceinline__ float score(const PagedAttnArgs& a, float dot, float 
     return fmaf(slope, dist, s) * kLog2e;
 }
 
-// Joins `parts` partials of one row: part(i) points at o[row][0], at_m(i) at m and l of that row.  Lane j
-// holds channels 4j..4j+3.  The sum runs over the parts first, first + step, ...; m over all of them.
-struct RowSum {
-    float m, l;  // m: the reference subtracted (0 where every part's maximum is -inf)
+// A partial of one row as a lane holds it: channels 4 lane .. 4 lane + 3.
+struct RowPart {
+    float m, l;
     float4 o;
 };
-template <typename Slot>
-__device__ __forceinline__ RowSum join_row(Slot slot, int rows, int r, int parts, int first, int step, int lane) {
-    float mx = -CUDART_INF_F;
-    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, slot(i)[rows * kTile + r]);
-    mx = warp_max(mx);
-    RowSum s = {mx == -CUDART_INF_F ? 0.f : mx, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-    for (int i = first; i < parts; i += step) {
-        const float* p = slot(i);
-        const float4 v = *reinterpret_cast<const float4*>(p + r * kTile + 4 * lane);
-        const float w = exp2f(p[rows * kTile + r] - s.m);
-        s.l = fmaf(w, p[rows * kTile + rows + r], s.l);
-        s.o.x = fmaf(w, v.x, s.o.x);
-        s.o.y = fmaf(w, v.y, s.o.y);
-        s.o.z = fmaf(w, v.z, s.o.z);
-        s.o.w = fmaf(w, v.w, s.o.w);
-    }
-    return s;
+__device__ __forceinline__ RowPart load_part(const float* slot, int rows, int r, int lane) {
+    RowPart p;
+    p.o = *reinterpret_cast<const float4*>(slot + r * kTile + 4 * lane);
+    p.m = slot[rows * kTile + r];
+    p.l = slot[rows * kTile + rows + r];
+    return p;
+}
+// s joined with p; m = -inf: nothing yet (o and l are 0), or only scores of -inf
+__device__ __forceinline__ void join_part(RowPart& s, const RowPart& p) {
+    const float m = fmaxf(s.m, p.m);
+    const float ref = m == -CUDART_INF_F ? 0.f : m;
+    const float a = exp2f(s.m - ref), b = exp2f(p.m - ref);
+    s.m = m;
+    s.l = fmaf(b, p.l, a * s.l);
+    s.o.x = fmaf(b, p.o.x, a * s.o.x);
+    s.o.y = fmaf(b, p.o.y, a * s.o.y);
+    s.o.z = fmaf(b, p.o.z, a * s.o.z);
+    s.o.w = fmaf(b, p.o.w, a * s.o.w);
 }
 __device__ __forceinline__ float lse_of(float m, float l) {  // l = 0: no key, or only scores of -inf
     return l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
 }
-__device__ __forceinline__ void store_row(const PagedAttnArgs& a, int64_t row, const RowSum& s, int lane) {
+__device__ __forceinline__ void store_row(const PagedAttnArgs& a, int64_t row, const RowPart& s, int lane) {
     const float inv = s.l != 0.f ? 1.f / s.l : 0.f;
     store2(a, row * kTile + 4 * lane, s.o.x * inv, s.o.y * inv);
     store2(a, row * kTile + 4 * lane + 2, s.o.z * inv, s.o.w * inv);
     if (a.lse != nullptr && lane == 0) a.lse[row] = lse_of(s.m, s.l);
+}
+
+// x / y, both at least 0: 64-bit division takes five times as long as the 32-bit one, which nearly
+// always suffices
+__device__ __forceinline__ long long divide(long long x, long long y) {
+    return (x | y) >> 32 ? x / y : (long long)((unsigned)x / (unsigned)y);
 }
 
 // Query heads of a unit: the first one and how many (the last block of a kv head's may be short).
@@ -212,22 +219,22 @@ struct Workspace {
     float* base;
     size_t stride;
     int ctas;
-    __device__ __forceinline__ float* warp_slot(int worker) const { return base + worker * stride; }
-    __device__ __forceinline__ float* cta_slot(int cta, int which) const {
-        return base + ((size_t)ctas * kWarps + 2 * cta + which) * stride;
-    }
-    __device__ __forceinline__ Join* joins() const { return reinterpret_cast<Join*>(cta_slot(ctas, 0)); }
+    __device__ __forceinline__ float* cta_slot(int cta, int which) const { return base + (2 * (size_t)cta + which) * stride; }
+    __device__ __forceinline__ float* warp_slot(int worker) const { return base + (2 * (size_t)ctas + worker) * stride; }
+    __device__ __forceinline__ Join* joins() const { return reinterpret_cast<Join*>(warp_slot(ctas * kWarps)); }
 };
 
 // What a warp leaves for the join at its CTA's end.
 struct Left {
     int b, u;
-    bool open;    // the warp's last unit is in its shared slot:
-    bool starts;  //   it begins in this warp's piece
-    bool ends;    //   it ends with this warp's piece
-    bool head;    // its first unit began before its piece, ended inside it, and is in its workspace slot
+    unsigned flags;
+    int pad;
     long long end;  // stream position of the last group of the open unit (where it starts here)
 };
+constexpr unsigned kOpen = 1;    // the warp's last unit is in its ring:
+constexpr unsigned kStarts = 2;  //   it begins in this warp's piece
+constexpr unsigned kEnds = 4;    //   it ends with this warp's piece
+constexpr unsigned kHead = 8;    // its first unit began before its piece, ended inside it, and is in its head slot
 
 __device__ __forceinline__ void store1(const PagedAttnArgs& a, int64_t at, float x) {
     if (a.out_dtype == KVARN_DTYPE_FP32) static_cast<float*>(a.out)[at] = x;
@@ -241,71 +248,92 @@ template <typename T, int PIECES, int NT, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ long long s_scan[kWarps];
-    __shared__ long long s_pre[kThreads];
     __shared__ Left s_left[kWarps];
+    long long* s_pre = reinterpret_cast<long long*>(dsm);  // before anything is fetched
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- this warp's piece of the stream ----
     const int worker = blockIdx.x * kWarps + warp, workers = gridDim.x * kWarps;
-    long long total = -1;
-    if (a.B > kThreads) {  // else the one chunk below gives it
-        long long sum = 0;
-        for (int b = tid; b < a.B; b += kThreads) sum += load_span(a, b).groups();
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        if (lane == 0) s_scan[warp] = sum;
-        __syncthreads();
-        total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) total += s_scan[w];
-        total *= a.units;
-        __syncthreads();
-    }
     Cursor at = {};
-    long long piece = 1, begin = 0, seq_begin = 0, carry = 0;
+    long long piece = 1, begin = 0, seq_begin = 0;
     int len = 0;
-    for (int base = 0; base < a.B; base += kThreads) {
-        const int b = base + tid;
-        long long inc = b < a.B ? (long long)load_span(a, b).groups() * a.units : 0;
+    if (a.B <= 32) {  // every warp by itself
+        const Span s = lane < a.B ? load_span(a, lane) : Span{0, 0};
+        long long inc = (long long)s.groups() * a.units;
 #pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, inc, s);
-            if (lane >= s) inc += o;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
         }
-        if (base > 0) __syncthreads();  // s_scan and s_pre are reused
-        if (lane == 31) s_scan[warp] = inc;
-        __syncthreads();
-        const long long chunk_begin = carry;
+        const long long total = __shfl_sync(0xffffffffu, inc, 31);
+        piece = max(divide(total + workers - 1, workers), 1LL);
+        begin = min(total, piece * worker);
+        len = (int)(min(total, begin + piece) - begin);
+        const int b = min(__popc(__ballot_sync(0xffffffffu, inc <= begin)), 31);
+        at.b = b;
+        at.s.lo = __shfl_sync(0xffffffffu, s.lo, b);
+        at.s.len = __shfl_sync(0xffffffffu, s.len, b);
+        at.n = at.s.groups();
+        seq_begin = __shfl_sync(0xffffffffu, inc, b) - (long long)at.n * a.units;
+    } else {
+        long long total = -1, carry = 0;
+        if (a.B > kThreads) {  // else the one chunk below gives it
+            long long sum = 0;
+            for (int b = tid; b < a.B; b += kThreads) sum += load_span(a, b).groups();
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) inc += s_scan[w];
-            carry += s_scan[w];
-        }
-        s_pre[tid] = chunk_begin + inc;  // end of sequence b in the stream
-        __syncthreads();
-        if (base == 0) {
-            if (total < 0) total = carry;
-            piece = max((total + workers - 1) / workers, 1LL);
-            begin = min(total, piece * worker);
-            len = (int)(min(total, begin + piece) - begin);
-        }
-        if (begin >= chunk_begin && begin < carry) {
-            int skip = 0;  // sequences of this chunk that end at or before the piece's begin
+            for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+            if (lane == 0) s_scan[warp] = sum;
+            __syncthreads();
+            total = 0;
 #pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i)
-                skip += __popc(__ballot_sync(0xffffffffu, s_pre[32 * i + lane] <= begin));
-            at.b = base + skip;
-            at.s = load_span(a, at.b);
-            at.n = at.s.groups();
-            seq_begin = s_pre[skip] - (long long)at.n * a.units;
+            for (int w = 0; w < kWarps; ++w) total += s_scan[w];
+            total *= a.units;
+            __syncthreads();
         }
+        for (int base = 0; base < a.B; base += kThreads) {
+            const int b = base + tid;
+            long long inc = b < a.B ? (long long)load_span(a, b).groups() * a.units : 0;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, inc, s);
+                if (lane >= s) inc += o;
+            }
+            if (base > 0) __syncthreads();  // s_scan and s_pre are reused
+            if (lane == 31) s_scan[warp] = inc;
+            __syncthreads();
+            const long long chunk_begin = carry;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) inc += s_scan[w];
+                carry += s_scan[w];
+            }
+            s_pre[tid] = chunk_begin + inc;  // end of sequence b in the stream
+            __syncthreads();
+            if (base == 0) {
+                if (total < 0) total = carry;
+                piece = max(divide(total + workers - 1, workers), 1LL);
+                begin = min(total, piece * worker);
+                len = (int)(min(total, begin + piece) - begin);
+            }
+            if (begin >= chunk_begin && begin < carry) {
+                int skip = 0;  // sequences of this chunk that end at or before the piece's begin
+#pragma unroll
+                for (int i = 0; i < kThreads / 32; ++i)
+                    skip += __popc(__ballot_sync(0xffffffffu, s_pre[32 * i + lane] <= begin));
+                at.b = base + skip;
+                at.s = load_span(a, at.b);
+                at.n = at.s.groups();
+                seq_begin = s_pre[skip] - (long long)at.n * a.units;
+            }
+        }
+        __syncthreads();  // s_pre lies in the rings
     }
     const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.rows), (int)gridDim.x};
     if (len > 0) {
         const long long in_seq = begin - seq_begin;
-        at.u = (int)(in_seq / at.n);
+        at.u = (int)divide(in_seq, at.n);
         at.g = (int)(in_seq - (long long)at.u * at.n);
     }
 
@@ -319,18 +347,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
     uint32_t c_dst[4];  // row r of a copy: 256 r + 16 (chunk ^ (r mod 8)), r = 2 i + c_row
 #pragma unroll
     for (int i = 0; i < 4; ++i) c_dst[i] = ring + (2 * i + c_row) * (kTile * 2) + ((c_chunk ^ (2 * i + c_row)) << 4);
-    Cursor in = at;  // next group to fetch, and its page
-    auto page_of = [&](const Cursor& c) { return a.page_table[(int64_t)c.b * a.max_pages + c.token() / a.page_size]; };
-    int page = len > 0 ? page_of(in) : 0;
+    Cursor in = at;  // next group to fetch: its token, its page's place in the table, and its page
+    auto entry_of = [&](int b, int t) {
+        return (int64_t)b * a.max_pages + (a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size);
+    };
+    int in_t = in.token();
+    int64_t entry = entry_of(in.b, in_t);
+    int page = len > 0 ? a.page_table[entry] : 0;
     int fetched = 0;
     uint32_t in_stage = 0;
     auto fetch = [&]() {
         if (fetched < len) {
-            const int t0 = in.token();
+            const int t0 = in_t;
             const bool bad = page < 0 || page >= a.n_pages;
             if (bad && lane == 0) atomicOr(&g_paged_attn_error, 1u);
             const int64_t o = (int64_t)(bad ? 0 : page) * a.page_stride + (int64_t)(in.u / a.row_blocks) * a.head_stride +
-                              (int64_t)(t0 % a.page_size) * a.token_stride;
+                              (int64_t)(a.page_shift >= 0 ? t0 & (a.page_size - 1) : t0 % a.page_size) * a.token_stride;
             const T* ks = kbase + o;
             const T* vs = vbase + o;
             if (!bad && t0 >= in.s.lo && t0 + kGroup <= in.s.len) {
@@ -357,7 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
             in_stage = in_stage + kStageBytes < kStages * kStageBytes ? in_stage + kStageBytes : 0;
             if (++fetched < len) {
                 in.next(a);
-                page = page_of(in);
+                in_t = in.token();
+                const int64_t e = entry_of(in.b, in_t);
+                if (e != entry) page = a.page_table[e];  // mostly the same page
+                entry = e;
             }
         }
         cp_async_commit();
@@ -380,6 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
     const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row that this lane addresses
     const int k_row = ((mi & 1) << 3) + mr, k_sel = mi >> 1;
     const int v_row = ((mi >> 1) << 3) + mr, v_sel = mi & 1;
+    // where warp w leaves its first unit: a few rows fit beside the rings
+    auto head_slot = [&](int w) -> float* {
+        return NT == 1 ? reinterpret_cast<float*>(dsm + kWarps * kStages * kStageBytes) + w * ws.stride
+                       : ws.warp_slot(blockIdx.x * kWarps + w);
+    };
     int done = 0;
     uint32_t stage = 0;
     Left left = {};
@@ -506,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
         // the last unit of the piece, if not whole, waits in shared memory (this warp's ring is read out) for
         // the join at the CTA's end; one that ended before goes to the workspace
         if (!whole && last) cp_async_wait<0>();
-        float* slot = last ? reinterpret_cast<float*>(own) : warp == 0 ? ws.cta_slot(blockIdx.x, 0) : ws.warp_slot(worker);
+        float* slot = last ? reinterpret_cast<float*>(own) : warp == 0 ? ws.cta_slot(blockIdx.x, 0) : head_slot(warp);
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
 #pragma unroll
@@ -538,75 +578,104 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
             }
         }
         if (!whole && last) {
-            left.b = b, left.u = u, left.open = true, left.starts = starts, left.ends = ends;
+            left.b = b, left.u = u;
+            left.flags |= kOpen | (starts ? kStarts : 0u) | (ends ? kEnds : 0u);
             left.end = begin + done - steps + n - 1;
         } else if (!whole) {
-            left.head = true;
+            left.flags |= kHead;
         }
     }
 
     // ---- join of the units that cross warps of this CTA: chains of warps, a row at a time ----
     if (lane == 0) s_left[warp] = left;
-    __syncthreads();
     const int cta = blockIdx.x;
     if (tid == 0) ws.joins()[cta].b = -1;
+    __syncthreads();
+    const unsigned flags = lane < kWarps ? s_left[lane].flags : 0u;
+    const unsigned open = __ballot_sync(0xffffffffu, flags & kOpen), begins = __ballot_sync(0xffffffffu, flags & kStarts);
+    const unsigned closes = __ballot_sync(0xffffffffu, flags & kEnds), heads = __ballot_sync(0xffffffffu, flags & kHead);
+    const unsigned goes_on = open & ~begins;  // warps whose open unit is that of the warp before
     int task = 0;
-    for (int w0 = 0; w0 < kWarps; ++w0) {
-        if (!s_left[w0].open || (w0 > 0 && !s_left[w0].starts)) continue;
-        // members: the shared slots of w0 .. w1, and the workspace slot of w1 + 1 where the unit ends in it
+    for (unsigned firsts = open & (begins | 1u); firsts != 0; firsts &= firsts - 1) {
+        // members: the rings of w0 .. w1, and the head slot of w1 + 1 where the unit ends in it
+        const int w0 = __ffs(firsts) - 1;
         int w1 = w0;
-        while (!s_left[w1].ends && w1 + 1 < kWarps && s_left[w1 + 1].open && !s_left[w1 + 1].starts && !s_left[w1 + 1].head) ++w1;
-        const bool tail = !s_left[w1].ends && w1 + 1 < kWarps && s_left[w1 + 1].head;
-        const bool starts = s_left[w0].starts, ends = s_left[w1].ends || tail;
-        const Heads hd = heads_of(a, s_left[w0].u);
-        const int64_t row = (int64_t)s_left[w0].b * a.Hq + hd.first;
-        const int parts = w1 - w0 + 1 + (tail ? 1 : 0);
-        const float* beyond = ws.warp_slot(cta * kWarps + w1 + 1);
-        auto part = [&](int i) -> const float* {
-            return w0 + i <= w1 ? reinterpret_cast<const float*>(dsm + (w0 + i) * kStages * kStageBytes) : beyond;
-        };
+        while (!(closes >> w1 & 1u) && (goes_on >> (w1 + 1) & 1u)) ++w1;
+        const bool tail = !(closes >> w1 & 1u) && (heads >> (w1 + 1) & 1u);
+        const bool starts = begins >> w0 & 1u, ends = (closes >> w1 & 1u) || tail;
+        const int b = s_left[w0].b, u = s_left[w0].u;
+        const Heads hd = heads_of(a, u);
         for (int r = 0; r < hd.rows; ++r, ++task) {
             if (task % kWarps != warp) continue;
-            const RowSum s = join_row(part, a.rows, r, parts, 0, 1, lane);
+            RowPart s = load_part(reinterpret_cast<const float*>(dsm + w0 * kStages * kStageBytes), a.rows, r, lane);
+            if (tail) join_part(s, load_part(head_slot(w1 + 1), a.rows, r, lane));
+#pragma unroll 4
+            for (int w = w0 + 1; w <= w1; ++w)
+                join_part(s, load_part(reinterpret_cast<const float*>(dsm + w * kStages * kStageBytes), a.rows, r, lane));
             if (starts && ends) {
-                store_row(a, row + r, s, lane);
+                store_row(a, (int64_t)b * a.Hq + hd.first + r, s, lane);
             } else {
                 float* slot = ws.cta_slot(cta, starts ? 1 : 0);
                 *reinterpret_cast<float4*>(slot + r * kTile + 4 * lane) = s.o;
                 if (lane == 0) {
-                    slot[a.rows * kTile + r] = s.l != 0.f ? s.m : -CUDART_INF_F;
+                    slot[a.rows * kTile + r] = s.m;
                     slot[a.rows * kTile + a.rows + r] = s.l;
                 }
             }
         }
-        if (starts && !ends && tid == 0)
-            ws.joins()[cta] = Join{s_left[w0].b, s_left[w0].u, (int)(s_left[w0].end / (piece * kWarps)), 0};
+        if (starts && !ends && tid == 0) ws.joins()[cta] = Join{b, u, (int)divide(s_left[w0].end, piece * kWarps), 0};
     }
 }
 
-// One CTA per CTA of the split whose last unit goes on in others: kJoinWarps warps share the unit's rows.
+// One CTA per CTA of the split whose last unit goes on in others.  A warp takes a row, or its share of a
+// row's parts where there are fewer rows than warps.  The first parts are loaded before it is known
+// whether they are needed: one round trip instead of two.
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(PagedAttnArgs a) {
-    __shared__ RowSum s_sum[kJoinWarps][32];
+    __shared__ RowPart s_part[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.rows), (int)gridDim.x};
     const int c0 = blockIdx.x;
+    const int share = a.rows < kJoinWarps ? kJoinWarps / a.rows : 1, sub = warp % share;
+    auto load = [&](int i, int r) {  // part 0 is slot 1 of c0, part i slot 0 of c0 + i
+        return load_part(ws.cta_slot(min(c0 + i, ws.ctas - 1), i == 0 ? 1 : 0), a.rows, r, lane);
+    };
     const Join jn = ws.joins()[c0];
+    RowPart ahead[kAhead];
+    int r = warp / share;
+    if (r < a.rows) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) ahead[k] = load(sub + k * share, r);
+    }
     if (jn.b < 0) return;
     const Heads hd = heads_of(a, jn.u);
-    const int share = kJoinWarps / hd.rows;  // warps of a row, rows <= kRows <= kJoinWarps
-    const int r = warp / share, sub = warp % share;
-    auto part = [&](int i) -> const float* { return ws.cta_slot(c0 + i, i == 0 ? 1 : 0); };
-    if (r < hd.rows) s_sum[warp][lane] = join_row(part, a.rows, r, jn.last - c0 + 1, sub, share, lane);
-    __syncthreads();
-    if (r >= hd.rows || sub != 0) return;
-    RowSum s = s_sum[warp][lane];
-    for (int i = 1; i < share; ++i) {  // the same m in all of them
-        const RowSum t = s_sum[warp + i][lane];
-        s.l += t.l;
-        s.o.x += t.o.x, s.o.y += t.o.y, s.o.z += t.o.z, s.o.w += t.o.w;
+    const int parts = jn.last - c0 + 1;
+    for (; r < a.rows; r += kJoinWarps / share) {  // more than once only where share is 1
+        RowPart s = {-CUDART_INF_F, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int i = sub; i < parts; i += kAhead * share) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i + k * share < parts) join_part(s, ahead[k]);
+            const bool more = i + kAhead * share < parts;
+            if (more || (share == 1 && r + kJoinWarps < a.rows)) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    ahead[k] = more ? load(i + (kAhead + k) * share, r) : load(k, r + kJoinWarps);
+            }
+        }
+        if (share == 1) {
+            if (r < hd.rows) store_row(a, (int64_t)jn.b * a.Hq + hd.first + r, s, lane);
+        } else {
+            s_part[warp][lane] = s;
+        }
     }
+    if (share == 1) return;
+    __syncthreads();
+    r = warp / share;
+    if (sub != 0 || r >= hd.rows) return;
+    RowPart s = s_part[warp][lane];
+    for (int i = 1; i < share; ++i) join_part(s, s_part[warp + i][lane]);
     store_row(a, (int64_t)jn.b * a.Hq + hd.first + r, s, lane);
 }
 
@@ -651,9 +720,11 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stre
     a.row_blocks = (a.group + kRows - 1) / kRows;
     a.units = a.Hkv * a.row_blocks;
     a.inv_softcap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+    a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     const int64_t cap = a.window > 0 && a.window < a.max_len ? (int64_t)a.window + kGroup : a.max_len;
     const int ctas = grid_ctas((int64_t)a.B * a.units * ((cap + kGroup - 1) / kGroup), sms);
-    const size_t smem = (size_t)kWarps * kStages * kStageBytes;
+    const size_t heads = a.rows <= 8 ? kWarps * slot_floats(a.rows) * sizeof(float) : 0;
+    const size_t smem = (size_t)kWarps * kStages * kStageBytes + heads;
     const Kernel kern = dtype == KVARN_DTYPE_FP16             ? pick<__half, 2>(a)
                         : a.out_dtype == KVARN_DTYPE_FP32 ? pick<__nv_bfloat16, 3>(a)
                                                           : pick<__nv_bfloat16, 2>(a);
