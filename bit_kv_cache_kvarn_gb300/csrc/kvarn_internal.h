@@ -149,8 +149,9 @@ struct PagedAttnArgs {
     int B, Hq, Hkv, page_size, max_pages, max_len, window, out_dtype;
     int64_t n_pages;
     // set by the launcher: query heads per kv head and (at most) per unit, units per kv head and per
-    // sequence, log2 of a page size that is a power of two (else -1)
-    int group, rows, row_blocks, units, page_shift;
+    // sequence, log2 of a page size that is a power of two (else -1), whether first units of warps wait
+    // in shared memory for their join
+    int group, rows, row_blocks, units, page_shift, heads_near;
     float scale, softcap, inv_softcap;
     const void* q;
     int64_t q_token_stride, q_head_stride;

@@ -31,6 +31,8 @@
 // group's P V is added to the running output by an fp32 addition, rounded to nearest.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "kvarn_common.cuh"
 #include "kvarn_internal.h"
 
@@ -42,16 +44,22 @@ __device__ unsigned int g_paged_attn_error = 0;
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;
 constexpr int kGroup = 16;                             // tokens per step
 constexpr int kRows = 16;                              // query heads per unit, at most
 constexpr int kHalfBytes = kGroup * kTile * 2;         // K or V of a group
 constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kMaxCtas = 160;                          // CTAs of a grid, at most
-constexpr int kJoinWarps = 8;
-constexpr int kAhead = 4;                              // parts that a warp of the join loads at once
+constexpr int kMaxWarps = 12;                          // warps of a CTA, at most
+constexpr int kSmemLimit = 227 * 1024 - 2048;          // dynamic shared memory of a CTA, beside the static
+
+// Warps of a CTA and groups in a warp's ring, by the eights of query heads in a unit.
+template <int NT>
+struct Shape {
+    static constexpr int kWarps = NT == 1 ? 12 : 8, kStages = NT == 1 ? 2 : 3;
+    static constexpr int kThreads = 32 * kWarps, kRing = kStages * kStageBytes;  // bytes of a warp
+};
+constexpr int kJoinWarps = 16;
+constexpr int kAhead = 2;                              // parts that a warp of the join loads at once
 
 // Workspace: partial slots, each o[rows][128] then m[rows] and l[rows] (fp32; a slot is a multiple of 16
 // bytes, joins read four channels at a time): two per CTA (slot 0: the unit that began before the CTA's
@@ -112,14 +120,17 @@ __device__ __forceinline__ uint32_t take2(float& x, float& y, __half) {
     y -= f.y;
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store2(const PagedAttnArgs& a, int64_t at, float x, float y) {
-    if (a.out_dtype == KVARN_DTYPE_FP32) {
-        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(x, y);
-    } else if (a.out_dtype == KVARN_DTYPE_BF16) {
-        *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + at) = __floats2bfloat162_rn(x, y);
-    } else {
-        *reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + at) = __floats2half2_rn(x, y);
-    }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void store1(__half* p, float x) { *p = __float2half_rn(x); }
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+__device__ __forceinline__ void store4(__half* p, float4 v) {
+    const __half2 x = __floats2half2_rn(v.x, v.y), y = __floats2half2_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
 // Visible keys [lo, len) of a sequence and its groups of 16 tokens: [lo / 16, ceil(len / 16)).
@@ -189,10 +200,10 @@ __device__ __forceinline__ void join_part(RowPart& s, const RowPart& p) {
 __device__ __forceinline__ float lse_of(float m, float l) {  // l = 0: no key, or only scores of -inf
     return l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
 }
+template <typename O>
 __device__ __forceinline__ void store_row(const PagedAttnArgs& a, int64_t row, const RowPart& s, int lane) {
     const float inv = s.l != 0.f ? 1.f / s.l : 0.f;
-    store2(a, row * kTile + 4 * lane, s.o.x * inv, s.o.y * inv);
-    store2(a, row * kTile + 4 * lane + 2, s.o.z * inv, s.o.w * inv);
+    store4(static_cast<O*>(a.out) + row * kTile + 4 * lane, make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv));
     if (a.lse != nullptr && lane == 0) a.lse[row] = lse_of(s.m, s.l);
 }
 
@@ -218,10 +229,10 @@ __device__ __forceinline__ Heads heads_of(const PagedAttnArgs& a, int u) {
 struct Workspace {
     float* base;
     size_t stride;
-    int ctas;
+    int ctas, warps;  // of the split's grid and of its CTAs
     __device__ __forceinline__ float* cta_slot(int cta, int which) const { return base + (2 * (size_t)cta + which) * stride; }
     __device__ __forceinline__ float* warp_slot(int worker) const { return base + (2 * (size_t)ctas + worker) * stride; }
-    __device__ __forceinline__ Join* joins() const { return reinterpret_cast<Join*>(warp_slot(ctas * kWarps)); }
+    __device__ __forceinline__ Join* joins() const { return reinterpret_cast<Join*>(warp_slot(ctas * warps)); }
 };
 
 // What a warp leaves for the join at its CTA's end.
@@ -236,16 +247,14 @@ constexpr unsigned kStarts = 2;  //   it begins in this warp's piece
 constexpr unsigned kEnds = 4;    //   it ends with this warp's piece
 constexpr unsigned kHead = 8;    // its first unit began before its piece, ended inside it, and is in its head slot
 
-__device__ __forceinline__ void store1(const PagedAttnArgs& a, int64_t at, float x) {
-    if (a.out_dtype == KVARN_DTYPE_FP32) static_cast<float*>(a.out)[at] = x;
-    else if (a.out_dtype == KVARN_DTYPE_BF16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(x);
-    else static_cast<__half*>(a.out)[at] = __float2half_rn(x);
-}
-
-// T: type of q and the cache; PIECES: 16-bit pieces of a probability; NT: eights of query heads in a
-// unit; CAP: scores are capped.
-template <typename T, int PIECES, int NT, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
+// T: type of q and the cache; O: type of the output; NT: eights of query heads in a unit; CAP: scores are
+// capped.  Instructions are fetched from L2 past the loop's, which costs microseconds while the cache
+// streams through it: what runs once per unit or call is kept short, not unrolled.
+template <typename T, typename O, int NT, bool CAP>
+__global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
+    constexpr int kWarps = Shape<NT>::kWarps, kThreads = Shape<NT>::kThreads, kRing = Shape<NT>::kRing;
+    constexpr int kStages = Shape<NT>::kStages;
+    constexpr int PIECES = sizeof(O) == 4 && std::is_same<T, __nv_bfloat16>::value ? 3 : 2;  // of a probability
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ long long s_scan[kWarps];
     __shared__ Left s_left[kWarps];
@@ -254,11 +263,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- this warp's piece of the stream ----
-    const int worker = blockIdx.x * kWarps + warp, workers = gridDim.x * kWarps;
+    // ---- this warp's piece of the stream: equal pieces for the CTAs, cut into equal ones for the warps ----
+    const int worker = blockIdx.x * kWarps + warp;
     Cursor at = {};
-    long long piece = 1, begin = 0, seq_begin = 0;
+    long long piece = 1, begin = 0, seq_begin = 0;  // piece: groups of a CTA
     int len = 0;
+    auto cut = [&](long long total) {
+        piece = max(divide(total + gridDim.x - 1, gridDim.x), 1LL);
+        const long long own = divide(piece + kWarps - 1, kWarps), first = min(total, piece * blockIdx.x);
+        const long long past = min(total, first + piece);
+        begin = min(past, first + own * warp);
+        len = (int)(min(past, begin + own) - begin);
+    };
     if (a.B <= 32) {  // every warp by itself
         const Span s = lane < a.B ? load_span(a, lane) : Span{0, 0};
         long long inc = (long long)s.groups() * a.units;
@@ -268,9 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
             if (lane >= d) inc += o;
         }
         const long long total = __shfl_sync(0xffffffffu, inc, 31);
-        piece = max(divide(total + workers - 1, workers), 1LL);
-        begin = min(total, piece * worker);
-        len = (int)(min(total, begin + piece) - begin);
+        cut(total);
         const int b = min(__popc(__ballot_sync(0xffffffffu, inc <= begin)), 31);
         at.b = b;
         at.s.lo = __shfl_sync(0xffffffffu, s.lo, b);
@@ -313,9 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
             __syncthreads();
             if (base == 0) {
                 if (total < 0) total = carry;
-                piece = max(divide(total + workers - 1, workers), 1LL);
-                begin = min(total, piece * worker);
-                len = (int)(min(total, begin + piece) - begin);
+                cut(total);
             }
             if (begin >= chunk_begin && begin < carry) {
                 int skip = 0;  // sequences of this chunk that end at or before the piece's begin
@@ -330,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
         }
         __syncthreads();  // s_pre lies in the rings
     }
-    const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.rows), (int)gridDim.x};
+    const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.rows), (int)gridDim.x, kWarps};
     if (len > 0) {
         const long long in_seq = begin - seq_begin;
         at.u = (int)divide(in_seq, at.n);
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
     }
 
     // ---- fetching ----
-    uint8_t* own = dsm + warp * kStages * kStageBytes;
+    uint8_t* own = dsm + warp * kRing;
     const uint32_t ring = smem_addr(own);
     const int c_row = lane >> 4, c_chunk = lane & 15;  // a copy instruction covers two rows
     const int64_t c_off = c_row * a.token_stride + 8 * c_chunk;
@@ -358,14 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
     uint32_t in_stage = 0;
     auto fetch = [&]() {
         if (fetched < len) {
-            const int t0 = in_t;
             const bool bad = page < 0 || page >= a.n_pages;
             if (bad && lane == 0) atomicOr(&g_paged_attn_error, 1u);
             const int64_t o = (int64_t)(bad ? 0 : page) * a.page_stride + (int64_t)(in.u / a.row_blocks) * a.head_stride +
-                              (int64_t)(a.page_shift >= 0 ? t0 & (a.page_size - 1) : t0 % a.page_size) * a.token_stride;
+                              (int64_t)(a.page_shift >= 0 ? in_t & (a.page_size - 1) : in_t % a.page_size) * a.token_stride;
             const T* ks = kbase + o;
             const T* vs = vbase + o;
-            if (!bad && t0 >= in.s.lo && t0 + kGroup <= in.s.len) {
+            if (!bad && in_t >= in.s.lo && in_t + kGroup <= in.s.len) {
 #pragma unroll
                 for (int i = 0; i < kGroup / 2; ++i) {
                     const uint32_t d = c_dst[i & 3] + in_stage + (i >> 2) * 8 * kTile * 2;
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
             } else {  // rows that are not visible are not read but zero
 #pragma unroll 1
                 for (int i = 0; i < kGroup / 2; ++i) {
-                    const int r = 2 * i + c_row, t = t0 + r;
+                    const int r = 2 * i + c_row, t = in_t + r;
                     const bool read = !bad && t >= in.s.lo && t < in.s.len;
                     const uint32_t d = ring + in_stage + r * (kTile * 2) + ((c_chunk ^ (r & 7)) << 4);
                     cp_async16(d, read ? ks : kbase, read);
@@ -386,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
                     vs += 2 * a.token_stride;
                 }
             }
-            in_stage = in_stage + kStageBytes < kStages * kStageBytes ? in_stage + kStageBytes : 0;
+            in_stage = in_stage + kStageBytes < kRing ? in_stage + kStageBytes : 0;
             if (++fetched < len) {
                 in.next(a);
                 in_t = in.token();
@@ -397,13 +408,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
         }
         cp_async_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) fetch();
 
     // sequences with nothing visible: zeros, log-sum-exp -inf
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (load_span(a, b).groups() > 0) continue;
-        for (int i = tid; i < a.Hq * kTile / 2; i += kThreads) store2(a, (int64_t)b * a.Hq * kTile + 2 * i, 0.f, 0.f);
+        for (int i = tid; i < a.Hq * kTile / 4; i += kThreads)
+            store4(static_cast<O*>(a.out) + (int64_t)b * a.Hq * kTile + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
         if (a.lse != nullptr)
             for (int h = tid; h < a.Hq; h += kThreads) a.lse[(int64_t)b * a.Hq + h] = -CUDART_INF_F;
     }
@@ -415,9 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
     const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row that this lane addresses
     const int k_row = ((mi & 1) << 3) + mr, k_sel = mi >> 1;
     const int v_row = ((mi >> 1) << 3) + mr, v_sel = mi & 1;
-    // where warp w leaves its first unit: a few rows fit beside the rings
+    // where warp w leaves its first unit: beside the rings where that fits
     auto head_slot = [&](int w) -> float* {
-        return NT == 1 ? reinterpret_cast<float*>(dsm + kWarps * kStages * kStageBytes) + w * ws.stride
+        return a.heads_near ? reinterpret_cast<float*>(dsm + kWarps * kRing) + w * ws.stride
                        : ws.warp_slot(blockIdx.x * kWarps + w);
     };
     int done = 0;
@@ -463,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
             __syncwarp();
             fetch();  // into the stage consumed in the step before
             const uint32_t kb = ring + stage, vb = kb + kHalfBytes;
-            stage = stage + kStageBytes < kStages * kStageBytes ? stage + kStageBytes : 0;
+            stage = stage + kStageBytes < kRing ? stage + kStageBytes : 0;
             float s[NT][2][4] = {};  // [eight][chain]
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
@@ -558,10 +570,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
                 if (whole) {
                     const int64_t row = (int64_t)b * a.Hq + hd.first + r;
                     const float inv = l[e][i] != 0.f ? 1.f / l[e][i] : 0.f;
+                    O* out = static_cast<O*>(a.out) + row * kTile + row0;
 #pragma unroll
                     for (int cc = 0; cc < 8; ++cc) {
-                        store1(a, row * kTile + 16 * cc + row0, o[e][cc][i] * inv);
-                        store1(a, row * kTile + 16 * cc + row0 + 8, o[e][cc][i + 2] * inv);
+                        store1(out + 16 * cc, o[e][cc][i] * inv);
+                        store1(out + 16 * cc + 8, o[e][cc][i + 2] * inv);
                     }
                     if (a.lse != nullptr && row0 == 0) a.lse[row] = lse_of(m[e][i], l[e][i]);
                 } else {
@@ -607,13 +620,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
         const Heads hd = heads_of(a, u);
         for (int r = 0; r < hd.rows; ++r, ++task) {
             if (task % kWarps != warp) continue;
-            RowPart s = load_part(reinterpret_cast<const float*>(dsm + w0 * kStages * kStageBytes), a.rows, r, lane);
+            RowPart s = load_part(reinterpret_cast<const float*>(dsm + w0 * kRing), a.rows, r, lane);
             if (tail) join_part(s, load_part(head_slot(w1 + 1), a.rows, r, lane));
-#pragma unroll 4
+#pragma unroll 1
             for (int w = w0 + 1; w <= w1; ++w)
-                join_part(s, load_part(reinterpret_cast<const float*>(dsm + w * kStages * kStageBytes), a.rows, r, lane));
+                join_part(s, load_part(reinterpret_cast<const float*>(dsm + w * kRing), a.rows, r, lane));
             if (starts && ends) {
-                store_row(a, (int64_t)b * a.Hq + hd.first + r, s, lane);
+                store_row<O>(a, (int64_t)b * a.Hq + hd.first + r, s, lane);
             } else {
                 float* slot = ws.cta_slot(cta, starts ? 1 : 0);
                 *reinterpret_cast<float4*>(slot + r * kTile + 4 * lane) = s.o;
@@ -623,19 +636,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_split_kernel(PagedAttnArgs 
                 }
             }
         }
-        if (starts && !ends && tid == 0) ws.joins()[cta] = Join{b, u, (int)divide(s_left[w0].end, piece * kWarps), 0};
+        if (starts && !ends && tid == 0) ws.joins()[cta] = Join{b, u, (int)divide(s_left[w0].end, piece), 0};
     }
 }
 
 // One CTA per CTA of the split whose last unit goes on in others.  A warp takes a row, or its share of a
 // row's parts where there are fewer rows than warps.  The first parts are loaded before it is known
 // whether they are needed: one round trip instead of two.
+template <typename O>
 __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(PagedAttnArgs a) {
     __shared__ RowPart s_part[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.rows), (int)gridDim.x};
+    const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.rows), (int)gridDim.x, a.rows <= 8 ? Shape<1>::kWarps : Shape<2>::kWarps};
     const int c0 = blockIdx.x;
     const int share = a.rows < kJoinWarps ? kJoinWarps / a.rows : 1, sub = warp % share;
     auto load = [&](int i, int r) {  // part 0 is slot 1 of c0, part i slot 0 of c0 + i
@@ -665,7 +679,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(PagedAttnAr
             }
         }
         if (share == 1) {
-            if (r < hd.rows) store_row(a, (int64_t)jn.b * a.Hq + hd.first + r, s, lane);
+            if (r < hd.rows) store_row<O>(a, (int64_t)jn.b * a.Hq + hd.first + r, s, lane);
         } else {
             s_part[warp][lane] = s;
         }
@@ -676,18 +690,26 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(PagedAttnAr
     if (sub != 0 || r >= hd.rows) return;
     RowPart s = s_part[warp][lane];
     for (int i = 1; i < share; ++i) join_part(s, s_part[warp + i][lane]);
-    store_row(a, (int64_t)jn.b * a.Hq + hd.first + r, s, lane);
+    store_row<O>(a, (int64_t)jn.b * a.Hq + hd.first + r, s, lane);
 }
 
-using Kernel = void (*)(PagedAttnArgs);
-template <typename T, int PIECES>
-Kernel pick(const PagedAttnArgs& a) {
-    if (a.rows <= 8) return a.softcap > 0.f ? paged_split_kernel<T, PIECES, 1, true> : paged_split_kernel<T, PIECES, 1, false>;
-    return a.softcap > 0.f ? paged_split_kernel<T, PIECES, 2, true> : paged_split_kernel<T, PIECES, 2, false>;
+struct Kernels {
+    void (*split)(PagedAttnArgs);
+    void (*join)(PagedAttnArgs);
+    int warps, ring;
+};
+template <typename T, typename O, int NT>
+Kernels pick(const PagedAttnArgs& a) {
+    return {a.softcap > 0.f ? paged_split_kernel<T, O, NT, true> : paged_split_kernel<T, O, NT, false>, paged_join_kernel<O>,
+            Shape<NT>::kWarps, Shape<NT>::kRing};
+}
+template <typename T, typename O>
+Kernels pick(const PagedAttnArgs& a) {
+    return a.rows <= 8 ? pick<T, O, 1>(a) : pick<T, O, 2>(a);
 }
 
-int grid_ctas(int64_t max_groups, int sms) {
-    const int64_t fill = (max_groups + kWarps - 1) / kWarps;
+int grid_ctas(int64_t max_groups, int warps, int sms) {
+    const int64_t fill = (max_groups + warps - 1) / warps;
     const int most = sms < kMaxCtas ? sms : kMaxCtas;
     return (int)(fill < 1 ? 1 : fill < most ? fill : most);
 }
@@ -697,7 +719,7 @@ int grid_ctas(int64_t max_groups, int sms) {
 size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv) {
     (void)B;
     const int group = Hq / Hkv, rows = group < kRows ? group : kRows;
-    const size_t slots = (size_t)kMaxCtas * (kWarps + 2);
+    const size_t slots = (size_t)kMaxCtas * (kMaxWarps + 2);
     const size_t bytes = slots * slot_floats(rows) * sizeof(float) + kMaxCtas * sizeof(Join);
     return (bytes + 255) & ~(size_t)255;
 }
@@ -721,18 +743,20 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stre
     a.units = a.Hkv * a.row_blocks;
     a.inv_softcap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
+    const bool wide = a.out_dtype == KVARN_DTYPE_FP32;
+    const Kernels k = dtype == KVARN_DTYPE_FP16 ? (wide ? pick<__half, float>(a) : pick<__half, __half>(a))
+                                                : (wide ? pick<__nv_bfloat16, float>(a) : pick<__nv_bfloat16, __nv_bfloat16>(a));
     const int64_t cap = a.window > 0 && a.window < a.max_len ? (int64_t)a.window + kGroup : a.max_len;
-    const int ctas = grid_ctas((int64_t)a.B * a.units * ((cap + kGroup - 1) / kGroup), sms);
-    const size_t heads = a.rows <= 8 ? kWarps * slot_floats(a.rows) * sizeof(float) : 0;
-    const size_t smem = (size_t)kWarps * kStages * kStageBytes + heads;
-    const Kernel kern = dtype == KVARN_DTYPE_FP16             ? pick<__half, 2>(a)
-                        : a.out_dtype == KVARN_DTYPE_FP32 ? pick<__nv_bfloat16, 3>(a)
-                                                          : pick<__nv_bfloat16, 2>(a);
-    e = set_smem_limit_once(kern, (int)smem, false, dev);
+    const int ctas = grid_ctas((int64_t)a.B * a.units * ((cap + kGroup - 1) / kGroup), k.warps, sms);
+    size_t smem = (size_t)k.warps * k.ring;
+    const size_t heads = k.warps * slot_floats(a.rows) * sizeof(float);
+    a.heads_near = smem + heads <= kSmemLimit;
+    if (a.heads_near) smem += heads;
+    e = set_smem_limit_once(k.split, (int)smem, false, dev);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, a);
+    e = launch_pdl(k.split, dim3(ctas), dim3(32 * k.warps), smem, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_join_kernel, dim3(ctas), dim3(32 * kJoinWarps), 0, stream, a);
+    return launch_pdl(k.join, dim3(ctas), dim3(32 * kJoinWarps), 0, stream, a);
 }
 
 }  // namespace kvarn
