@@ -14,6 +14,10 @@ tensors.  The projections, norm and RoPE are plain PyTorch (fp32, TF32 off); eve
 codec -- the encode of each finished block and the attention over the packed cache -- runs in
 libkvarn's kernels: a block's 128 queries are 128 one-query "sequences" sharing the block table of
 the previous blocks, with lengths 128 j + t + 1 and the current block as their bf16 tail.
+
+The unquantised run is plain PyTorch, or (paged=True) libkvarn's 16-bit serving step: the block's pages
+and slots come from kvarn_step_tables, the rotation and the write of keys and values from
+kvarn_rope_qkv, and the attention from kvarn_paged_attention over pages of 128 tokens.
 """
 from __future__ import annotations
 
@@ -68,9 +72,45 @@ def _exact_attention(q, k_all, v_all, n_prev, scale):
     return torch.bmm(torch.softmax(s, dim=-1), vv).permute(1, 0, 2)  # [T, Hq, 128]
 
 
-def run(kv, cfg, weights, x, hq: int, hkv: int, quantised: bool = True, capture=None, kv_token_scale=None):
+class _PagedCache:
+    """The 16-bit cache of one growing sequence in libkvarn's pages: one page per block, layer by layer."""
+
+    def __init__(self, kv, layers, n_blocks, hq, hkv, dev):
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.kv, self.hq, self.hkv = kv, hq, hkv
+        self.pages = [tuple(torch.empty(n_blocks, hkv, BLOCK, HEAD, dtype=torch.bfloat16, device=dev) for _ in range(2))
+                      for _ in range(layers)]
+        self.freqs = kv.kvarn_rope_frequencies(HEAD, ROPE_BASE)[0].to(dev)
+        self.length, self.count = torch.zeros(1, **i32), torch.zeros(1, **i32)
+        self.table = torch.full((1, n_blocks), -1, **i32)
+        self.free, self.n_free = torch.arange(n_blocks, **i32), torch.full((1,), n_blocks, **i32)
+        self.new, self.cu, self.status = torch.full((1,), BLOCK, **i32), torch.zeros(2, **i32), torch.zeros(1, **i32)
+        self.positions, self.slots = torch.empty(BLOCK, **i32), torch.empty(BLOCK, **i32)
+        self.q = torch.empty(BLOCK, hq, HEAD, dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty(BLOCK, hq, HEAD, device=dev)
+        self.ws = torch.empty(kv.kvarn_paged_attention_workspace_size(BLOCK, hq, hkv), dtype=torch.uint8, device=dev)
+
+    def next_block(self):
+        self.kv.kvarn_step_tables(self.length, self.new, self.count, self.table, self.free, self.n_free, BLOCK,
+                                  self.length, self.count, self.n_free, self.cu, self.positions, self.slots, self.status)
+        # every token of the block is a query of its own, over the same pages
+        self.tables, self.lens = self.table.expand(BLOCK, -1).contiguous(), self.positions + 1
+
+    def attend(self, layer, q, k, v, scale):
+        """q [128, hq, 128], k, v [128, hkv, 128] fp32 before the rotation -> attention [128, hq, 128]."""
+        kp, vp = self.pages[layer]
+        self.kv.kvarn_rope_qkv(q, k, v, self.positions, self.freqs, self.q, kp, vp, slot_map=self.slots)
+        self.kv.kvarn_paged_attention(self.q, kp, vp, self.tables, self.lens, self.out, scale, self.ws)
+        return self.out.clone()
+
+
+def run(kv, cfg, weights, x, hq: int, hkv: int, quantised: bool = True, capture=None, kv_token_scale=None,
+        paged: bool = False):
     """Free-running pseudo-decode over all blocks of x.  Returns (attn, seconds) with attn[j][l]
     the fp32 attention output [128, hq, 128] of block j, layer l.
+
+    paged: the unquantised run (quantised=False) through libkvarn's 16-bit paged cache instead of
+    PyTorch; capture then stores dict(q, k_pages, v_pages, table, attn), the pages as written so far.
 
     kv_token_scale: optional [tokens] multipliers of each position's K and V projections (the
     outlier variant, synthetic.pseudo_decode_token_scales).
@@ -79,6 +119,8 @@ def run(kv, cfg, weights, x, hq: int, hkv: int, quantised: bool = True, capture=
     output at that point are stored as its value -- dict(q, k_blk, v_blk, attn, pools,
     n_prev_blocks), pools = the packed tiles of the previous blocks (tile id = block * hkv + kv
     head) -- for a teacher-forced check."""
+    if paged and quantised:
+        raise ValueError("paged is a form of the unquantised run")
     dev = x.device
     n_blocks = x.shape[0] // BLOCK
     layers = len(weights)
@@ -101,9 +143,10 @@ def run(kv, cfg, weights, x, hq: int, hkv: int, quantised: bool = True, capture=
                           torch.empty(n_tiles, HEAD * 16 * vb, dtype=torch.uint8, device=dev),
                           torch.empty(n_tiles, 512, dtype=torch.uint8, device=dev),
                           torch.empty(n_tiles, dtype=torch.float32, device=dev)))
-        else:
+        elif not paged:
             exact.append((torch.empty(n_blocks * BLOCK, hkv, HEAD, device=dev),
                           torch.empty(n_blocks * BLOCK, hkv, HEAD, device=dev)))
+    pages = _PagedCache(kv, layers, n_blocks, hq, hkv, dev) if paged and n_blocks else None
     max_tiles = max(n_blocks, 1)
     table = (torch.arange(max_tiles, device=dev, dtype=torch.int32)[None, :] * hkv
              + torch.arange(hkv, device=dev, dtype=torch.int32)[:, None])  # [hkv, max_tiles]
@@ -119,14 +162,25 @@ def run(kv, cfg, weights, x, hq: int, hkv: int, quantised: bool = True, capture=
         h = x[j * BLOCK:(j + 1) * BLOCK].float()
         pos = torch.arange(j * BLOCK, (j + 1) * BLOCK, device=dev)
         per_layer = []
+        if paged:
+            pages.next_block()
         for l, w in enumerate(weights):
             n = _rmsnorm(h)
-            q = _rope((n @ w["wq"].float().T).reshape(BLOCK, hq, HEAD), pos).to(torch.bfloat16)
+            q_proj = (n @ w["wq"].float().T).reshape(BLOCK, hq, HEAD)
             k_proj = n @ w["wk"].float().T
             v_proj = n @ w["wv"].float().T
             if tok_scale is not None:
                 ts = tok_scale[j * BLOCK:(j + 1) * BLOCK, None]
                 k_proj, v_proj = k_proj * ts, v_proj * ts
+            if paged:
+                a = pages.attend(l, q_proj, k_proj.reshape(BLOCK, hkv, HEAD), v_proj.reshape(BLOCK, hkv, HEAD), scale)
+                if capture is not None and (j, l) in capture:
+                    capture[(j, l)] = dict(q=pages.q.clone(), k_pages=pages.pages[l][0].clone(),
+                                           v_pages=pages.pages[l][1].clone(), table=pages.table.clone(), attn=a.clone())
+                per_layer.append(a)
+                h = h + a.reshape(BLOCK, hq * HEAD) @ w["wo"].float().T
+                continue
+            q = _rope(q_proj, pos).to(torch.bfloat16)
             k = _rope(k_proj.reshape(BLOCK, hkv, HEAD), pos).to(torch.bfloat16)
             v = v_proj.reshape(BLOCK, hkv, HEAD).to(torch.bfloat16)
             if quantised:
@@ -193,6 +247,7 @@ def main():
     ap.add_argument("--blocks", type=int, default=64)
     ap.add_argument("--seed", type=int, default=4)
     ap.add_argument("--kv-outliers", action="store_true")
+    ap.add_argument("--paged", action="store_true", help="also the unquantised run through the 16-bit paged cache")
     args = ap.parse_args()
     kv.load()
     w = make_weights(args.seed, args.layers, args.hidden, args.hq, args.hkv, kv_outliers=args.kv_outliers)
@@ -200,6 +255,10 @@ def main():
     ts = synthetic.pseudo_decode_token_scales(args.seed, args.blocks * BLOCK) if args.kv_outliers else None
     ref, t_ref = run(kv, None, w, x, args.hq, args.hkv, quantised=False, kv_token_scale=ts)
     res = {"config": vars(args), "reference_s": round(t_ref, 3)}
+    if args.paged:
+        a, t = run(kv, None, w, x, args.hq, args.hkv, quantised=False, kv_token_scale=ts, paged=True)
+        res["bf16_paged"] = {"seconds": round(t, 3), "mae": mae_curves(a, ref),
+                             "relative_mae": mae_curves(a, ref, relative=True)}
     for name, c in presets(kv):
         a, t = run(kv, c, w, x, args.hq, args.hkv, quantised=True, kv_token_scale=ts)
         res[name] = {"seconds": round(t, 3), "mae": mae_curves(a, ref),

@@ -640,3 +640,30 @@ def test_serving_steps_over_paged_and_packed_caches(kv):
                 assert np.all(np.abs(np64(out[b, h]) - want) <= tol)
                 assert rel_l2(np64(pout[b, h]), ref_packed[b, h]) <= 1e-3
     assert int(n_free) + int(counts.sum()) == n_pages
+
+
+def test_pseudo_decode_over_the_paged_cache(kv):
+    """The unquantised pseudo-decode through the serving step's kernels, block by block and layer by layer:
+    its attention from the queries and pages it had, and against the plain PyTorch run."""
+    from bit_kv_cache_kvarn_gb300 import pseudo_decode as pd
+
+    hq, hkv, layers, blocks = 4, 2, 2, 4
+    w = pd.make_weights(41, layers, 256, hq, hkv)
+    x = pd.make_input(41, blocks * 128, 256)
+    cap = {(j, l): None for j in range(blocks) for l in range(layers)}
+    attn, _ = pd.run(kv, None, w, x, hq, hkv, quantised=False, paged=True, capture=cap)
+    plain, _ = pd.run(kv, None, w, x, hq, hkv, quantised=False)
+    scale = 1 / math.sqrt(128)
+    for (j, l), c in cap.items():
+        lens = i32([128 * j + t + 1 for t in range(128)])
+        case = dict(q=c["q"], kc=c["k_pages"], vc=c["v_pages"], table=c["table"].expand(128, -1), lens=lens, starts=None, window=0)
+        _, lse, mass, reach = o.paged_attention(np64(c["q"]), np64(c["k_pages"]), np64(c["v_pages"]), case["table"].cpu().numpy(),
+                                                lens.tolist(), scale)
+        attn_check(case, attn[j][l], torch.tensor(lse), scale=scale)
+        if l == 0:
+            # the runs' queries, keys and values are the same fp32 numbers up to their last bits, so each
+            # bf16 value differs by a step (2^-7) at most; a score then by 2 * 2^-7 reach
+            tol = np.expm1(4 * reach * 2.0 ** -7)[..., None] * mass + 2.0 ** -7 * mass
+            assert np.all(np.abs(np64(attn[j][0]) - np64(plain[j][0])) <= tol)
+    with pytest.raises(ValueError, match="paged"):
+        pd.run(kv, None, w, x, hq, hkv, quantised=True, paged=True)
