@@ -47,6 +47,22 @@ cudaError_t set_smem_limit_once(const void* kernel, int bytes, bool max_carveout
     return e;
 }
 
+cudaError_t allow_large_cluster_once(const void* kernel, int dev) {
+    struct Entry {
+        const void* kernel;
+        int dev;
+    };
+    static std::mutex mutex;
+    static Entry done[256];
+    static int n_done = 0;
+    std::lock_guard<std::mutex> lock(mutex);
+    for (int i = 0; i < n_done; ++i)
+        if (done[i].kernel == kernel && done[i].dev == dev) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && n_done < 256) done[n_done++] = Entry{kernel, dev};
+    return e;
+}
+
 }  // namespace kvarn
 
 namespace {

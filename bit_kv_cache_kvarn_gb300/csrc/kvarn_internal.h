@@ -98,6 +98,34 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, c
     return cudaLaunchKernelEx(&lc, kern, args...);
 }
 
+// The same with clusters of `cluster` CTAs; past 8 the kernel needs allow_large_cluster_once.
+template <typename... P, typename... A>
+cudaError_t launch_pdl_cluster(void (*kern)(P...), dim3 grid, int cluster, dim3 block, size_t smem, cudaStream_t stream,
+                               const A&... args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    return cudaLaunchKernelEx(&lc, kern, args...);
+}
+
+// Allow the kernel clusters past the portable 8 CTAs, unless an earlier call did so on this device.
+cudaError_t allow_large_cluster_once(const void* kernel, int dev);
+template <typename Kern>
+cudaError_t allow_large_cluster_once(Kern kern, int dev) {
+    return allow_large_cluster_once(reinterpret_cast<const void*>(kern), dev);
+}
+
 // A step's tables: see kvarn_step_tables for the arrays.
 constexpr int kMaxTableSeqs = 16384;  // three prefix sums per sequence in shared memory
 struct StepTablesArgs {

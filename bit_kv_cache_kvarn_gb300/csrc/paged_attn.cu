@@ -29,6 +29,7 @@
 // by up to 2^-18, 2.3e-6 of an output whose other errors are 4e-7, so an fp32 output takes three
 // pieces (2^-26) and a bf16 output, which rounds by 2^-9 itself, two.  fp16: two pieces (2^-22).  Each
 // group's P V is added to the running output by an fp32 addition, rounded to nearest.
+#include <cooperative_groups.h>
 #include <math_constants.h>
 
 #include <type_traits>
@@ -43,6 +44,8 @@ namespace kvarn {
 __device__ unsigned int g_paged_attn_error = 0;
 
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kGroup = 16;                             // tokens per step
 constexpr int kRows = 16;                              // query heads per unit, at most
@@ -250,7 +253,10 @@ constexpr unsigned kHead = 8;    // its first unit began before its piece, ended
 // T: type of q and the cache; O: type of the output; NT: eights of query heads in a unit; CAP: scores are
 // capped.  Instructions are fetched from L2 past the loop's, which costs microseconds while the cache
 // streams through it: what runs once per unit or call is kept short, not unrolled.
-template <typename T, typename O, int NT, bool CAP>
+//
+// CLUSTER: a thread-block cluster takes one unit, its CTAs equal parts of it, and the parts are joined
+// through the cluster's shared memory: no second launch.
+template <typename T, typename O, int NT, bool CAP, bool CLUSTER>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
     constexpr int kWarps = Shape<NT>::kWarps, kThreads = Shape<NT>::kThreads, kRing = Shape<NT>::kRing;
     constexpr int kStages = Shape<NT>::kStages;
@@ -275,7 +281,16 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
         begin = min(past, first + own * warp);
         len = (int)(min(past, begin + own) - begin);
     };
-    if (a.B <= 32) {  // every warp by itself
+    const int n_parts = CLUSTER ? (int)cg::this_cluster().num_blocks() : 1, part = CLUSTER ? blockIdx.x % n_parts : 0;
+    if (CLUSTER) {
+        const int unit = blockIdx.x / n_parts;
+        at.b = unit / a.units, at.u = unit - at.b * a.units;
+        at.s = load_span(a, at.b), at.n = at.s.groups();
+        piece = (at.n + n_parts - 1) / n_parts;
+        const int own = ((int)piece + kWarps - 1) / kWarps, past = min(at.n, (int)piece * (part + 1));
+        at.g = min(past, (int)piece * part + own * warp);
+        len = min(past, at.g + own) - at.g;
+    } else if (a.B <= 32) {  // every warp by itself
         const Span s = lane < a.B ? load_span(a, lane) : Span{0, 0};
         long long inc = (long long)s.groups() * a.units;
 #pragma unroll
@@ -342,8 +357,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
         }
         __syncthreads();  // s_pre lies in the rings
     }
+    const int at_n = at.n;  // groups of the cluster's unit
     const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.rows), (int)gridDim.x, kWarps};
-    if (len > 0) {
+    if (!CLUSTER && len > 0) {
         const long long in_seq = begin - seq_begin;
         at.u = (int)divide(in_seq, at.n);
         at.g = (int)(in_seq - (long long)at.u * at.n);
@@ -554,7 +570,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
 
         // ---- end of the unit, or of this warp's part of it ----
         const bool starts = g_begin == 0, ends = g_begin + steps == n;
-        const bool whole = starts && ends, last = done == len;
+        const bool whole = !CLUSTER && starts && ends, last = done == len;
         // the last unit of the piece, if not whole, waits in shared memory (this warp's ring is read out) for
         // the join at the CTA's end; one that ended before goes to the workspace
         if (!whole && last) cp_async_wait<0>();
@@ -602,7 +618,14 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
     // ---- join of the units that cross warps of this CTA: chains of warps, a row at a time ----
     if (lane == 0) s_left[warp] = left;
     const int cta = blockIdx.x;
-    if (tid == 0) ws.joins()[cta].b = -1;
+    if (!CLUSTER && tid == 0) ws.joins()[cta].b = -1;
+    float* near = reinterpret_cast<float*>(dsm);  // warp 0's ring: where a cluster's CTA leaves its part
+    if (CLUSTER && len == 0 && warp == 0) {       // no groups of the unit are this CTA's
+        for (int r = 0; r < a.rows; ++r) {
+            store4(near + r * kTile + 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f));
+            if (lane == 0) near[a.rows * kTile + r] = -CUDART_INF_F, near[a.rows * kTile + a.rows + r] = 0.f;
+        }
+    }
     __syncthreads();
     const unsigned flags = lane < kWarps ? s_left[lane].flags : 0u;
     const unsigned open = __ballot_sync(0xffffffffu, flags & kOpen), begins = __ballot_sync(0xffffffffu, flags & kStarts);
@@ -625,10 +648,12 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
 #pragma unroll 1
             for (int w = w0 + 1; w <= w1; ++w)
                 join_part(s, load_part(reinterpret_cast<const float*>(dsm + w * kRing), a.rows, r, lane));
-            if (starts && ends) {
+            if (!CLUSTER && starts && ends) {
                 store_row<O>(a, (int64_t)b * a.Hq + hd.first + r, s, lane);
             } else {
-                float* slot = ws.cta_slot(cta, starts ? 1 : 0);
+                // (in a cluster over row r of warp 0's part, which only this warp reads)
+                float* slot = CLUSTER ? near : ws.cta_slot(cta, starts ? 1 : 0);
+                __syncwarp();
                 *reinterpret_cast<float4*>(slot + r * kTile + 4 * lane) = s.o;
                 if (lane == 0) {
                     slot[a.rows * kTile + r] = s.m;
@@ -636,7 +661,20 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
                 }
             }
         }
-        if (starts && !ends && tid == 0) ws.joins()[cta] = Join{b, u, (int)divide(s_left[w0].end, piece), 0};
+        if (!CLUSTER && starts && !ends && tid == 0) ws.joins()[cta] = Join{b, u, (int)divide(s_left[w0].end, piece), 0};
+    }
+    if constexpr (CLUSTER) {
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();  // every CTA's part is in its shared memory
+        const int unit = cta / n_parts, b = unit / a.units;
+        const Heads hd = heads_of(a, unit - b * a.units);
+        for (int r = part + n_parts * warp; at_n > 0 && r < hd.rows; r += n_parts * kWarps) {  // the CTAs first
+            RowPart s = load_part(cluster.map_shared_rank(near, 0), a.rows, r, lane);
+#pragma unroll 4
+            for (int i = 1; i < n_parts; ++i) join_part(s, load_part(cluster.map_shared_rank(near, i), a.rows, r, lane));
+            store_row<O>(a, (int64_t)b * a.Hq + hd.first + r, s, lane);
+        }
+        cluster.sync();  // no CTA leaves while its part is read
     }
 }
 
@@ -699,13 +737,64 @@ struct Kernels {
     int warps, ring;
 };
 template <typename T, typename O, int NT>
-Kernels pick(const PagedAttnArgs& a) {
-    return {a.softcap > 0.f ? paged_split_kernel<T, O, NT, true> : paged_split_kernel<T, O, NT, false>, paged_join_kernel<O>,
-            Shape<NT>::kWarps, Shape<NT>::kRing};
+Kernels pick(const PagedAttnArgs& a, bool cluster) {
+    const bool cap = a.softcap > 0.f;
+    return {cluster ? (cap ? paged_split_kernel<T, O, NT, true, true> : paged_split_kernel<T, O, NT, false, true>)
+                    : (cap ? paged_split_kernel<T, O, NT, true, false> : paged_split_kernel<T, O, NT, false, false>),
+            paged_join_kernel<O>, Shape<NT>::kWarps, Shape<NT>::kRing};
 }
 template <typename T, typename O>
-Kernels pick(const PagedAttnArgs& a) {
-    return a.rows <= 8 ? pick<T, O, 1>(a) : pick<T, O, 2>(a);
+Kernels pick(const PagedAttnArgs& a, bool cluster) {
+    return a.rows <= 8 ? pick<T, O, 1>(a, cluster) : pick<T, O, 2>(a, cluster);
+}
+
+// How many clusters of n = 1, 2, 4, 8, 16 of the split's CTAs (one to an SM) run at once; queried once per
+// device, since it depends on how a chip's SMs are grouped (152, 76, 36, 15, 7 on the one measured).
+cudaError_t cluster_room(int log2n, int dev, int sms, int* room) {
+    static std::atomic<int> known[kMaxCachedDevices][5] = {};
+    const bool cached = dev >= 0 && dev < kMaxCachedDevices;
+    *room = log2n == 0 ? sms : cached ? known[dev][log2n].load(std::memory_order_relaxed) : 0;
+    if (*room > 0) return cudaSuccess;
+    const auto kern = paged_split_kernel<__nv_bfloat16, float, 1, false, true>;
+    const int smem = Shape<1>::kWarps * Shape<1>::kRing;
+    cudaError_t e = set_smem_limit_once(kern, smem, false, dev);
+    if (e == cudaSuccess) e = allow_large_cluster_once(kern, dev);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1 << log2n;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(1 << log2n);
+    lc.blockDim = dim3(Shape<1>::kThreads);
+    lc.dynamicSmemBytes = smem;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(room, kern, &lc);
+    if (e == cudaSuccess && cached) known[dev][log2n].store(*room, std::memory_order_relaxed);
+    return e;
+}
+
+// CTAs of a cluster that takes one unit, 0: the stream is split instead.  A cluster needs no second launch
+// (10.8 -> 6.6 us at B 1, 8 kv heads, 512 tokens; 14.3 -> 10.0 at B 16), but a long unit has only its own
+// SMs: taken while no warp gets more than four groups, when even one long sequence among empty ones costs
+// no more than the split stream (about 10 us).
+cudaError_t cluster_ctas(const PagedAttnArgs& a, int64_t unit_groups, int warps, int dev, int sms, int* ctas) {
+    const int64_t units = (int64_t)a.B * a.units;
+    *ctas = 0;
+    for (int log2n = 4; log2n >= 0; --log2n) {
+        const int64_t n = 1ll << log2n;
+        if (units * n > sms || (log2n > 0 && n / 2 * warps >= unit_groups)) continue;  // a group for every warp
+        if (unit_groups > 4 * n * warps) return cudaSuccess;  // nor with a smaller one
+        int room = 0;
+        const cudaError_t e = cluster_room(log2n, dev, sms, &room);
+        if (e != cudaSuccess) return e;
+        if (units > room) continue;
+        *ctas = (int)n;
+        return cudaSuccess;
+    }
+    return cudaSuccess;
 }
 
 int grid_ctas(int64_t max_groups, int warps, int sms) {
@@ -744,17 +833,29 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stre
     a.inv_softcap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     const bool wide = a.out_dtype == KVARN_DTYPE_FP32;
-    const Kernels k = dtype == KVARN_DTYPE_FP16 ? (wide ? pick<__half, float>(a) : pick<__half, __half>(a))
-                                                : (wide ? pick<__nv_bfloat16, float>(a) : pick<__nv_bfloat16, __nv_bfloat16>(a));
-    const int64_t cap = a.window > 0 && a.window < a.max_len ? (int64_t)a.window + kGroup : a.max_len;
-    const int ctas = grid_ctas((int64_t)a.B * a.units * ((cap + kGroup - 1) / kGroup), k.warps, sms);
-    size_t smem = (size_t)k.warps * k.ring;
-    const size_t heads = k.warps * slot_floats(a.rows) * sizeof(float);
+    const int64_t most = a.window > 0 && a.window < a.max_len ? (int64_t)a.window + kGroup : a.max_len;
+    const int64_t unit_groups = (most + kGroup - 1) / kGroup;
+    const int warps = a.rows <= 8 ? Shape<1>::kWarps : Shape<2>::kWarps;
+    int parts = 0;
+    e = cluster_ctas(a, unit_groups, warps, dev, sms, &parts);
+    if (e != cudaSuccess) return e;
+    const Kernels k = dtype == KVARN_DTYPE_FP16
+                          ? (wide ? pick<__half, float>(a, parts > 0) : pick<__half, __half>(a, parts > 0))
+                          : (wide ? pick<__nv_bfloat16, float>(a, parts > 0) : pick<__nv_bfloat16, __nv_bfloat16>(a, parts > 0));
+    size_t smem = (size_t)warps * k.ring;
+    if (parts > 0) {
+        e = set_smem_limit_once(k.split, (int)smem, false, dev);
+        if (e == cudaSuccess && parts > 8) e = allow_large_cluster_once(k.split, dev);
+        if (e != cudaSuccess) return e;
+        return launch_pdl_cluster(k.split, dim3(a.B * a.units * parts), parts, dim3(32 * warps), smem, stream, a);
+    }
+    const int ctas = grid_ctas((int64_t)a.B * a.units * unit_groups, warps, sms);
+    const size_t heads = warps * slot_floats(a.rows) * sizeof(float);
     a.heads_near = smem + heads <= kSmemLimit;
     if (a.heads_near) smem += heads;
     e = set_smem_limit_once(k.split, (int)smem, false, dev);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k.split, dim3(ctas), dim3(32 * k.warps), smem, stream, a);
+    e = launch_pdl(k.split, dim3(ctas), dim3(32 * warps), smem, stream, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(k.join, dim3(ctas), dim3(32 * kJoinWarps), 0, stream, a);
 }

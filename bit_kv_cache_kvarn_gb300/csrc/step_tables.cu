@@ -262,14 +262,7 @@ cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const size_t smem = (size_t)3 * a.B * sizeof(int);
     e = set_smem_limit_once(step_tables_kernel, 3 * kMaxTableSeqs * (int)sizeof(int), false, dev);
-    if (e == cudaSuccess) {  // 16 CTAs in a cluster are past the portable size
-        static std::atomic<unsigned long long> allowed{0};
-        const unsigned long long bit = 1ull << (dev & 63);
-        if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) & bit)) {
-            e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e == cudaSuccess && dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
-        }
-    }
+    if (e == cudaSuccess) e = allow_large_cluster_once(step_tables_kernel, dev);
     if (e != cudaSuccess) return e;
     // one CTA, as small as the step is, until it would make more than two rounds
     const int most = a.n_rows > a.B ? a.n_rows : a.B;
@@ -277,21 +270,7 @@ cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
     const int threads = most > kMaxThreads / 2 ? kMaxThreads : most > 128 ? kMaxThreads / 2 : 128;
     StepTablesArgs args = a;
     args.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(ctas);
-    lc.blockDim = dim3(threads);
-    lc.dynamicSmemBytes = smem;
-    lc.stream = stream;
-    lc.attrs = attr;
-    lc.numAttrs = 2;
-    return cudaLaunchKernelEx(&lc, step_tables_kernel, args);
+    return launch_pdl_cluster(step_tables_kernel, dim3(ctas), ctas, dim3(threads), smem, stream, args);
 }
 
 }  // namespace kvarn

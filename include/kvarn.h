@@ -424,7 +424,8 @@ size_t kvarn_paged_attention_workspace_size(int B, int Hq, int Hkv);
  * Sequences without a visible key (and rows whose scores are all -inf) get zeros and lse -inf.
  * Hq a positive multiple of Hkv, Hq <= 65535, B <= 65535, 1 <= max_pages, max_pages * page_size <=
  * 2^31 - 64.  B = 0 is a no-op.  The query heads of a kv head are taken 16 at a time; each block
- * reads the kv head's tokens once.  Launches: one split and one join kernel. */
+ * reads the kv head's tokens once.  One launch for few and short sequences (by B, Hkv and max_pages *
+ * page_size or window), else a split and a join kernel. */
 kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, const void* q,
                                    int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
                                    const void* v_cache, int64_t n_pages, int page_size,

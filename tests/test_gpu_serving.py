@@ -335,10 +335,12 @@ def test_rope_python_refusals(kv):
 
 
 # ---- paged attention ---------------------------------------------------------------------------------------
-def attn_case(seed, lens, hq, hkv, P=16, dt=BF, layout="hnd", starts=None, window=0, garbage=float("nan"), spread=1.0, spare=3):
-    """Every slot outside the visible tokens holds `garbage`, every unused page table entry an id far outside."""
+def attn_case(seed, lens, hq, hkv, P=16, dt=BF, layout="hnd", starts=None, window=0, garbage=float("nan"), spread=1.0, spare=3,
+              wide=False):
+    """Every slot outside the visible tokens holds `garbage`, every unused page table entry an id far outside.
+    wide: a page table for 100 000 tokens, so that the split over the stream serves short sequences too."""
     g = torch.Generator(device="cuda").manual_seed(seed)
-    B, width = len(lens), max(1, -(-max(lens) // P)) + 1
+    B, width = len(lens), max(1, -(-max(lens) // P), -(-100000 // P) if wide else 0) + 1
     used = [-(-n // P) for n in lens]
     n_pages = sum(used) + spare
     perm = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)
@@ -401,14 +403,16 @@ LENS = [0, 1, 15, 16, 17, 127, 128, 129, 500, 0, 1000, 33]
 
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (8, 1), (8, 2), (5, 1), (32, 2), (17, 1), (48, 2), (71, 1)])
 @pytest.mark.parametrize("P,layout,dt", [(16, "hnd", BF), (48, "nhd", HF), (128, "both", BF)])
-def test_attention_matches_the_oracle(kv, hq, hkv, P, layout, dt):
-    c = attn_case(31, LENS, hq, hkv, P=P, dt=dt, layout=layout)
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_matches_the_oracle(kv, hq, hkv, P, layout, dt, wide):
+    c = attn_case(31, LENS, hq, hkv, P=P, dt=dt, layout=layout, wide=wide)
     attn_check(c, *attn_call(kv, c))
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("lens", [[0], [1], [16], [17], [0, 0, 0], [4000], [3, 5000, 1], [2000] * 3, [1] * 300, list(range(0, 700))])
-def test_attention_lengths(kv, lens):
-    c = attn_case(32, lens, 4, 2, P=32)
+def test_attention_lengths(kv, lens, wide):
+    c = attn_case(32, lens, 4, 2, P=32, wide=wide)
     attn_check(c, *attn_call(kv, c))
 
 
@@ -420,7 +424,7 @@ def test_attention_modifiers(kv, kw, out_dtype):
     lens = LENS + [2500]
     starts = [0, 1, 15, 3, 16, 126, 200, 17, 499, 5, -4, 32, 1111] if kw.get("starts") else None
     dt = HF if out_dtype == HF else BF
-    c = attn_case(33, lens, 12, 3, P=32, dt=dt, starts=starts, window=kw.get("window", 0))
+    c = attn_case(33, lens, 12, 3, P=32, dt=dt, starts=starts, window=kw.get("window", 0), wide=out_dtype == BF)
     slopes = 2.0 ** (-8 * torch.arange(1, 13, device="cuda") / 12) if kw.get("slopes") else None
     m = dict(scale=kw.get("scale", 1 / math.sqrt(128)), softcap=kw.get("softcap", 0.0), slopes=slopes)
     attn_check(c, *attn_call(kv, c, out_dtype=out_dtype, **m), **m)
