@@ -664,6 +664,7 @@ kvarn_status kvarn_rope_qkv(kvarn_dtype x_dtype, kvarn_dtype out_dtype, int n_to
         KV_TRY(check_ptr(v, 16, "v"));
         KV_TRY(check_strides("k, v", kv_token_stride, kv_head_stride, x_step));
         KV_TRY(check_cache(k_cache, v_cache, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
+        if (k_cache == v_cache) return fail(KVARN_ERR_INVALID_ARG, "k_cache and v_cache are the same array");
         if (k_weight) KV_TRY(check_ptr(k_weight, 16, "k_weight"));
         if (slot_map) KV_TRY(check_ptr(slot_map, 4, "slot_map"));
         else if (n_tokens > n_pages * page_size)

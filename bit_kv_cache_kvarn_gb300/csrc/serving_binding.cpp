@@ -87,6 +87,11 @@ float as_float(PyObject* o) {
     if (v == -1.0 && PyErr_Occurred()) throw PythonError();
     return (float)v;
 }
+int as_bool(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonError();
+    return v;
+}
 kvarn_stream_t as_stream(PyObject* o, int dev) {
     if (o == Py_None) return (kvarn_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
     void* p = PyLong_AsVoidPtr(o);
@@ -211,7 +216,7 @@ kvarn_status rope_qkv(PyObject* const* x) {
         as_dtype(xt, "q, k, v"), as_dtype(ot, "q_out and the cache"), narrow(T, "T"), narrow(hq, "Hq"), narrow(hkv, "Hkv"), rq.p,
         rq.token, rq.head, rk.p, rv.p, rk.token, rk.head, c.ints(x[3], {T}, "positions"),
         freq ? c.array<double>(*freq, at::kDouble, {pairs}, "inv_freq") : nullptr, narrow(2 * pairs, "rot_dim"),
-        PyObject_IsTrue(x[13]) > 0 ? 1 : 0, as_float(x[12]), c.floats_or_null(x[9], {KVARN_HEAD_DIM}, "q_weight"),
+        as_bool(x[13]), as_float(x[12]), c.floats_or_null(x[9], {KVARN_HEAD_DIM}, "q_weight"),
         c.floats_or_null(x[10], {KVARN_HEAD_DIM}, "k_weight"), as_float(x[11]), ro.p, ro.token, ro.head, kv.k, kv.v, kv.n_pages,
         kv.page_size, kv.page_stride, kv.head_stride, kv.token_stride, c.ints_or_null(x[8], {T}, "slot_map"),
         as_stream(x[14], c.dev));

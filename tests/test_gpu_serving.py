@@ -16,6 +16,9 @@ Tolerances, from the arithmetic:
                        output's rounding, and lse by the score's error plus 2^-22 of itself.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -187,6 +190,20 @@ def test_tables_replay(kv):
     assert np.array_equal(got["slot_map"].cpu().numpy(), r["slot_map"])
 
 
+def test_tables_of_a_long_chunk_replay(kv):
+    # a cluster of CTAs under capture, not in place: the same step again and again
+    s = table_state(10, 300, 16, 500, 90, hkv=2)
+    keep = {}
+
+    def call(step):
+        keep["g"] = _capture(step)
+        keep["g"].replay()
+        torch.cuda.synchronize()
+
+    assert s["rows"] > 2048
+    same_tables(run_tables(kv, s, call=call), s)
+
+
 # ---- norm, rotation, cache write -------------------------------------------------------------------------
 def rope_case(seed, T, hq, hkv, xt=BF, ct=BF, P=16, rot=128, interleaved=False, norm="qk", layout="hnd", fused=False,
               positions=None, spare=2):
@@ -269,6 +286,13 @@ def rope_check(c, freqs, before_q, before_k, before_v, q=None, k=None):
 def test_rope_matches_the_oracle(kv, T, kw):
     c = rope_case(11 + T, T, **kw)
     c["scale"] = 1.25
+    before = [c[k].clone() for k in ("qo", "kc", "vc")]
+    rope_check(c, rope_call(kv, c), *before)
+
+
+def test_rope_long_chunk_matches_the_oracle(kv):
+    # more tokens than run at once: warps go on from token to token
+    c = rope_case(19, 11003, 2, 1, rot=16, P=64, norm="qk", fused=True)
     before = [c[k].clone() for k in ("qo", "kc", "vc")]
     rope_check(c, rope_call(kv, c), *before)
 
@@ -538,6 +562,61 @@ def test_attention_on_side_streams_with_their_own_workspaces(kv):
     for c, (out, lse) in got:
         i = [x is c for x in cs].index(True)
         assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_attention_without_log_sums(kv):
+    for wide in (False, True):
+        c = attn_case(48, [0, 700, 31], 8, 2, P=32, wide=wide)
+        want, _ = attn_call(kv, c)
+        out = torch.full_like(want, float("nan"))
+        ws = torch.empty(kv.kvarn_paged_attention_workspace_size(3, 8, 2), dtype=torch.uint8, device="cuda")
+        kv.kvarn_paged_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], out, 1 / math.sqrt(128), ws)
+        assert torch.equal(out, want)
+
+
+def test_first_calls_of_a_process_may_be_captured(kv):
+    """In a process of its own, so that nothing is loaded or looked up before the capture."""
+    code = """
+import torch, bit_kv_cache_kvarn_gb300 as kv
+kv.load()
+i32 = dict(dtype=torch.int32, device="cuda")
+B, T, P = 2, 40, 16
+lens, new, cnt, nf = torch.zeros(B, **i32), torch.tensor([15, 25], **i32), torch.zeros(B, **i32), torch.tensor([9], **i32)
+out = [torch.empty(B, **i32), torch.empty(B, **i32), torch.empty(1, **i32), torch.empty(B + 1, **i32), torch.empty(T, **i32),
+       torch.empty(T, **i32), torch.empty(1, **i32)]
+table, free = torch.full((B, 4), -1, **i32), torch.arange(9, **i32)
+qkv = torch.randn(T, 6, 128, device="cuda").to(torch.bfloat16)
+f = kv.kvarn_rope_frequencies()[0].cuda()
+qo = torch.empty(T, 4, 128, dtype=torch.bfloat16, device="cuda")
+kc, vc = (torch.zeros(9, 1, P, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+wide = torch.zeros(B, 5000, **i32)
+ws = torch.empty(kv.kvarn_paged_attention_workspace_size(B, 4, 1), dtype=torch.uint8, device="cuda")
+res = [torch.empty(B, 4, 128, device="cuda") for _ in range(2)]
+
+def step():
+    kv.kvarn_step_tables(lens, new, cnt, table, free, nf, P, *out, )
+    kv.kvarn_rope_qkv(qkv[:, :4], qkv[:, 4:5], qkv[:, 5:], out[4], f, qo, kc, vc, slot_map=out[5])
+    kv.kvarn_paged_attention(qo[14:16], kc, vc, table, out[0], res[0], 0.1, ws)
+    wide[:, :4] = table
+    kv.kvarn_paged_attention(qo[14:16], kc, vc, wide, out[0], res[1], 0.1, ws)
+
+torch.cuda.synchronize()
+s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+with torch.cuda.stream(s):
+    with torch.cuda.graph(g, stream=s):
+        step()
+g.replay()
+torch.cuda.synchronize()
+a, b = res[0].clone(), res[1].clone()
+assert torch.isfinite(a).all() and a.abs().max() > 0 and torch.allclose(a, b, rtol=1e-4, atol=1e-5)
+step()
+torch.cuda.synchronize()
+assert torch.equal(a, res[0]) and torch.equal(b, res[1]) and kv.kvarn_device_error() == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_attention_python_refusals(kv):

@@ -35,7 +35,7 @@ def test_step_tables_refusals(lib):
 
 
 def _rope(lib, xt=0, ot=0, T=4, hq=4, hkv=2, q=FAKE, qs=(512, 128), k=FAKE, v=FAKE, kvs=(256, 128), pos=FAKE, freq=FAKE,
-          rot=128, inter=0, scale=1.0, qw=None, kw=None, eps=1e-6, qo=FAKE + 4096, qos=(512, 128), kc=FAKE, vc=FAKE,
+          rot=128, inter=0, scale=1.0, qw=None, kw=None, eps=1e-6, qo=FAKE + 4096, qos=(512, 128), kc=FAKE, vc=FAKE + 65536,
           pages=4, page=16, cs=(4096, 2048, 128), slots=FAKE):
     return lib.kvarn_rope_qkv(xt, ot, T, hq, hkv, q, *qs, k, v, *kvs, pos, freq, rot, inter, scale, qw, kw, eps, qo,
                               *qos, kc, vc, pages, page, *cs, slots, None)
@@ -47,7 +47,7 @@ def test_rope_refusals(lib):
                 dict(rot=-16), dict(inter=2), dict(scale=math.inf), dict(scale=math.nan), dict(eps=-1.0), dict(eps=math.nan),
                 dict(pos=None), dict(freq=None), dict(freq=FAKE + 4), dict(q=None), dict(q=FAKE + 8), dict(qo=None),
                 dict(qs=(-512, 128)), dict(qs=(512, 132)), dict(qos=(512, 132)), dict(qos=(128, 128)), dict(qos=(0, 128)),
-                dict(k=None), dict(v=FAKE + 2), dict(kvs=(4, 128)), dict(kc=None), dict(vc=FAKE + 8), dict(pages=0),
+                dict(k=None), dict(v=FAKE + 2), dict(kvs=(4, 128)), dict(kc=None), dict(vc=FAKE + 8), dict(vc=FAKE), dict(pages=0),
                 dict(page=0), dict(pages=1 << 28), dict(cs=(4096, 2048, 64)), dict(cs=(2048, 2048, 128)),
                 dict(cs=(0, 2048, 128)), dict(cs=(-4096, 2048, 128)), dict(cs=(4100, 2048, 128)),
                 dict(cs=(1 << 41, 2048, 128)), dict(qw=FAKE + 4), dict(kw=FAKE + 8), dict(slots=FAKE + 2),
