@@ -10,11 +10,12 @@
 // What bounds it: every visible key and value is read once (512 bytes per kv head and token) for 512
 // operations per query head: HBM.  So the work is arranged around keeping bytes in flight:
 //   - the visible tokens of all (sequence, kv head, block of 16 query heads) units, in groups of 16,
-//     form one stream that is cut into equal contiguous pieces, one per warp of a persistent grid
-//     (one CTA per SM), so the load is even whatever the lengths;
-//   - a warp is on its own: it fetches its next groups into its own 3-stage ring in shared memory
-//     (16-byte asynchronous copies, 8 KB per group, 128 to 192 KB in flight per SM) across the ends of
-//     units, and never waits for another warp until its piece is done;
+//     form one stream that is cut into equal contiguous pieces, one per warp of a persistent grid (one
+//     CTA of 12 warps per SM, 8 for 9 to 16 query heads), so the load is even whatever the lengths;
+//   - a warp is on its own: it fetches its next group into its own ring in shared memory (16-byte
+//     asynchronous copies, 8 KB per group, 96 to 192 KB in flight per SM) across the ends of units, and
+//     never waits for another warp until its piece is done.  12 warps with two groups each took 88 us
+//     where 8 with three took 98 (256 sequences of 1 to 900 tokens), 305 and 318 (16 x 32k);
 //   - both products are taken transposed, m16n8k16: scores^T = K Q^T with the group's 16 tokens as rows
 //     (K as it lies, ldmatrix) and 8 query heads as columns, out^T = V^T P^T with 16 channels as rows
 //     (V through the transposing ldmatrix) and the probabilities turned in registers (movmatrix).  With
@@ -26,9 +27,13 @@
 //     a second launch of one CTA per boundary.
 // Rounding: the products take the cache's type exactly; scores, maximum, sums and outputs are fp32.
 // A probability enters the second product in 16-bit pieces that add up to it.  bf16: two pieces are off
-// by up to 2^-18, 2.3e-6 of an output whose other errors are 4e-7, so an fp32 output takes three
-// pieces (2^-26) and a bf16 output, which rounds by 2^-9 itself, two.  fp16: two pieces (2^-22).  Each
-// group's P V is added to the running output by an fp32 addition, rounded to nearest.
+// by up to 2^-16, on average 2.3e-6 of an output whose other errors are 4e-7, so an fp32 output takes
+// three pieces (2^-24) and a bf16 output, which rounds by 2^-8 itself, two.  fp16: two pieces (2^-22) of
+// 2^15 p, since p itself would lose its digits below 2^-14 (the factor is taken off the maximum that
+// the sums refer to).  Each group's P V is added to the running output by an fp32 addition, to nearest.
+//
+// Measured (among others, us): 16 x 32k tokens, 32 over 8 heads 312 (6.87 TB/s), 256 x 1-900 tokens, 64 over 8,
+// fp16, capped 93 (5.2 TB/s), one sequence of 4k 10.4.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -260,6 +265,7 @@ template <typename T, typename O, int NT, bool CAP, bool CLUSTER>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
     constexpr int kWarps = Shape<NT>::kWarps, kThreads = Shape<NT>::kThreads, kRing = Shape<NT>::kRing;
     constexpr int kStages = Shape<NT>::kStages;
+    constexpr float kLift = std::is_same<T, __half>::value ? 15.f : 0.f;  // log2 of the probabilities' factor
     constexpr int PIECES = sizeof(O) == 4 && std::is_same<T, __nv_bfloat16>::value ? 3 : 2;  // of a probability
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ long long s_scan[kWarps];
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
 #pragma unroll
             for (int e = 0; e < NT; ++e) {
                 // a row whose scores are all -inf so far has no maximum to subtract
-                const float ref[2] = {m[e][0] == -CUDART_INF_F ? 0.f : m[e][0], m[e][1] == -CUDART_INF_F ? 0.f : m[e][1]};
+                const float ref[2] = {m[e][0] == -CUDART_INF_F ? 0.f : m[e][0] - kLift, m[e][1] == -CUDART_INF_F ? 0.f : m[e][1] - kLift};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float p0 = exp2f(s[e][0][2 * h] - ref[0]), p1 = exp2f(s[e][0][2 * h + 1] - ref[1]);
@@ -592,7 +598,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
                         store1(out + 16 * cc, o[e][cc][i] * inv);
                         store1(out + 16 * cc + 8, o[e][cc][i + 2] * inv);
                     }
-                    if (a.lse != nullptr && row0 == 0) a.lse[row] = lse_of(m[e][i], l[e][i]);
+                    if (a.lse != nullptr && row0 == 0) a.lse[row] = lse_of(m[e][i] - kLift, l[e][i]);
                 } else {
 #pragma unroll
                     for (int cc = 0; cc < 8; ++cc) {
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
                         slot[r * kTile + 16 * cc + row0 + 8] = o[e][cc][i + 2];
                     }
                     if (row0 == 0) {
-                        slot[a.rows * kTile + r] = m[e][i];
+                        slot[a.rows * kTile + r] = m[e][i] - kLift;
                         slot[a.rows * kTile + a.rows + r] = l[e][i];
                     }
                 }
