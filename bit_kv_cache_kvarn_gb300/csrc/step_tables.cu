@@ -27,8 +27,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMaxThreads = 1024;
-constexpr int kCluster = 16;                 // 8 took 13.4 us where 16 take 10.8 (1000 mixed requests, 72k rows)
-constexpr int kPerThread = 4;                // rows in flight per thread
+constexpr int kCluster = 16;
+constexpr int kPerThread = 8;                // rows in flight per thread
 constexpr unsigned kMost = 0x7fffffffu;
 
 // Sums over sequences: new tokens and pages taken (both saturating, beyond every allowed total), pages
@@ -123,10 +123,15 @@ __global__ void __launch_bounds__(kMaxThreads) step_tables_kernel(StepTablesArgs
     // prefix sums, one sequence per thread at a time
     Sums carry = {0, 0, 0};
     unsigned bad = 0;
+    int my_len = 0;  // of the sequence that the thread took last
     for (int base = 0; base < a.B; base += threads) {
         const int b = base + tid;
         Sums own = {0, 0, 0};
-        if (b < a.B) own = seq_sums(a, load_seq(a, b), bad);
+        if (b < a.B) {
+            const Seq s = load_seq(a, b);
+            my_len = s.len;
+            own = seq_sums(a, s, bad);
+        }
         const Sums inc = warp_inclusive(own, lane);
         if (lane == 31) s_warp[warp] = inc;
         __syncthreads();
@@ -172,23 +177,31 @@ __global__ void __launch_bounds__(kMaxThreads) step_tables_kernel(StepTablesArgs
     const int first = blockIdx.x * threads + tid, step = n_ctas * threads;
     const int n_warps = step >> 5, warp_id = first >> 5;
 
-    // ---- pages: taken, and given back for good ----
-    for (int k = first; k < fresh; k += step) {
-        const int b = last_at_most(pre_fresh, 0, a.B, k);
-        const int i = a.page_counts[b] + (k - pre_fresh[b]);
-        const int page = stack(top - 1u - (unsigned)k);
+    // ---- pages: taken, and given back for good; one lookup each, all in one round where they fit ----
+    const int kept = ok && left > F ? (int)(left - F) : 0;
+    for (unsigned k = first; k < (unsigned)fresh + (unsigned)kept; k += step) {
+        if (k >= (unsigned)fresh) {
+            const unsigned j = held + (k - (unsigned)fresh);
+            a.free_pages[j] = stack(j);
+            continue;
+        }
+        const int b = last_at_most(pre_fresh, 0, a.B, (int)k);
+        const int i = a.page_counts[b] + ((int)k - pre_fresh[b]);
+        const int page = stack(top - 1u - k);
         a.page_table[(size_t)b * a.max_pages + i] = page;
         for (int h = 0; h < a.Hkv; ++h)
             a.block_table[((size_t)b * a.Hkv + h) * a.max_pages + i] = page * a.Hkv + h;
     }
-    const int kept = ok && left > F ? (int)(left - F) : 0;
-    for (int r = first; r < kept; r += step) a.free_pages[F + r] = stack(held + (unsigned)r);
     for (int b = first; b <= a.B; b += step) a.cu_tokens[b] = !ok ? 0 : b < a.B ? pre_add[b] : total;
 
     // From here on the lengths and counts may be overwritten in place: the old lengths move to shared memory.
     __syncthreads();
     int* old_len = pre_given;
-    for (int b = tid; b < a.B; b += threads) old_len[b] = a.seq_lens[b];
+    if (a.B <= threads) {
+        if (tid < a.B) old_len[tid] = my_len;
+    } else {
+        for (int b = tid; b < a.B; b += threads) old_len[b] = a.seq_lens[b];
+    }
     if (n_ctas > 1) cg::this_cluster().sync();
     else __syncthreads();
 
@@ -209,38 +222,39 @@ __global__ void __launch_bounds__(kMaxThreads) step_tables_kernel(StepTablesArgs
     }
 
     // ---- rows ----
-    // A warp takes 32 * kPerThread rows in a row: their sequences lie between those of the first and the
-    // last, found by the whole warp, and the lookups of a thread's rows overlap.  Every page is in the
-    // table by now, written by any CTA of the cluster, hence the loads from L2.
-    constexpr int kRun = 32 * kPerThread;
-    for (int run = warp_id * kRun; run < a.n_rows; run += n_warps * kRun) {
-        int pos[kPerThread], slot[kPerThread];
+    // The rows are cut evenly over the warps, at multiples of 32, and a warp takes 32 * kPerThread at a time:
+    // their sequences lie between those of the first and the last, found by the whole warp, and the lookups of
+    // a thread's rows overlap.  Every page is in the table by now, written by any CTA of the cluster, hence the
+    // loads from L2.
+    const int per_warp = ((a.n_rows + n_warps - 1) / n_warps + 31) & ~31;
+    const int row_begin = (int)min((long long)warp_id * per_warp, (long long)a.n_rows);
+    const int row_end = min(row_begin + per_warp, a.n_rows);
+    for (int run = row_begin; run < row_end; run += 32 * kPerThread) {
+        const int last = min(min(run + 32 * kPerThread, row_end), total);  // rows run .. last - 1 hold tokens
+        int pos[kPerThread], page[kPerThread];
         if (run < total) {
             int b_lo = 0, b_hi = a.B;
             if (a.B > 64) {  // a whole warp's search is two to three probes, a thread's log2(B)
                 b_lo = warp_last_at_most(pre_add, a.B, run, lane);
-                b_hi = warp_last_at_most(pre_add, a.B, min(run + kRun, total) - 1, lane) + 1;
+                b_hi = warp_last_at_most(pre_add, a.B, last - 1, lane) + 1;
             }
-            int page[kPerThread];
 #pragma unroll
             for (int i = 0; i < kPerThread; ++i) {
-                const int t = min(run + 32 * i + lane, total - 1);
+                if (run + 32 * i >= last) break;
+                const int t = min(run + 32 * i + lane, last - 1);
                 const int b = last_at_most(pre_add, b_lo, b_hi, t);
                 pos[i] = old_len[b] + (t - pre_add[b]);
                 page[i] = __ldcg(a.page_table + (size_t)b * a.max_pages + page_of(a, pos[i]));
             }
-#pragma unroll
-            for (int i = 0; i < kPerThread; ++i)
-                slot[i] = (int)((unsigned)page[i] * (unsigned)a.page_size +
-                                (unsigned)(pos[i] - page_of(a, pos[i]) * a.page_size));
         }
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) {
             const int t = run + 32 * i + lane;
-            if (t < a.n_rows) {
-                a.positions[t] = t < total ? pos[i] : -1;
-                a.slot_map[t] = t < total ? slot[i] : -1;
-            }
+            if (t >= row_end) break;
+            int slot = -1;
+            if (t < last) slot = (int)((unsigned)page[i] * (unsigned)a.page_size + (unsigned)(pos[i] - page_of(a, pos[i]) * a.page_size));
+            a.positions[t] = t < last ? pos[i] : -1;
+            a.slot_map[t] = slot;
         }
     }
 }
@@ -264,10 +278,13 @@ cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
     e = set_smem_limit_once(step_tables_kernel, 3 * kMaxTableSeqs * (int)sizeof(int), false, dev);
     if (e == cudaSuccess) e = allow_large_cluster_once(step_tables_kernel, dev);
     if (e != cudaSuccess) return e;
-    // one CTA, as small as the step is, until it would make more than two rounds
+    // One CTA, as small as the step is, until it would take more than two rounds, then the cluster, with more
+    // threads once there is a round of four rows for each (us): 64 sequences and rows 2.8, 256 4.3, 1259 rows
+    // 3.8 (4.1 in one CTA), 3262 4.8 (5.4 with 1024 threads), 4901 5.5 (6.3), 70778 8.8 (10.6 with 512; 12.0 in a
+    // cluster of 8).
     const int most = a.n_rows > a.B ? a.n_rows : a.B;
-    const int ctas = most > 2 * kMaxThreads ? kCluster : 1;
-    const int threads = most > kMaxThreads / 2 ? kMaxThreads : most > 128 ? kMaxThreads / 2 : 128;
+    const int ctas = most > kMaxThreads ? kCluster : 1;
+    const int threads = most <= 128 ? 128 : most > 4 * kCluster * kMaxThreads / 2 ? kMaxThreads : kMaxThreads / 2;
     StepTablesArgs args = a;
     args.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     return launch_pdl_cluster(step_tables_kernel, dim3(ctas), ctas, dim3(threads), smem, stream, args);
