@@ -181,6 +181,7 @@ struct PagedAttnArgs {
     // in shared memory for their join
     int group, rows, row_blocks, units, page_shift, heads_near;
     float scale, softcap, inv_softcap;
+    float lift;  // set by the launcher: log2 of the factor that a row's sum carries
     const void* q;
     int64_t q_token_stride, q_head_stride;
     const void* k_cache;

@@ -29,8 +29,7 @@
 // A probability enters the second product in 16-bit pieces that add up to it.  bf16: two pieces are off
 // by up to 2^-16, on average 2.3e-6 of an output whose other errors are 4e-7, so an fp32 output takes
 // three pieces (2^-24) and a bf16 output, which rounds by 2^-8 itself, two.  fp16: two pieces (2^-22) of
-// 2^15 p, since p itself would lose its digits below 2^-14 (the factor is taken off the maximum that
-// the sums refer to).  Each group's P V is added to the running output by an fp32 addition, to nearest.
+// 2^15 p, since p itself would lose its digits below 2^-14 (sums and outputs carry the factor alike).  Each group's P V is added to the running output by an fp32 addition, to nearest.
 //
 // Measured (among others, us): 16 x 32k tokens, 32 over 8 heads 312 (6.87 TB/s), 256 x 1-900 tokens, 64 over 8,
 // fp16, capped 93 (5.2 TB/s), one sequence of 4k 10.4.
@@ -66,14 +65,15 @@ struct Shape {
     static constexpr int kWarps = NT == 1 ? 12 : 8, kStages = NT == 1 ? 2 : 3;
     static constexpr int kThreads = 32 * kWarps, kRing = kStages * kStageBytes;  // bytes of a warp
 };
+constexpr float kHalfLift = 15.f;                      // fp16 probabilities are multiplied by 2^15
 constexpr int kJoinWarps = 16;
 constexpr int kAhead = 2;                              // parts that a warp of the join loads at once
 
 // Workspace: partial slots, each o[rows][128] then m[rows] and l[rows] (fp32; a slot is a multiple of 16
 // bytes, joins read four channels at a time): two per CTA (slot 0: the unit that began before the CTA's
 // pieces, slot 1: the one that begins in them and goes on after them), then one per warp (the unit that
-// began before its piece and ends inside it; kept in shared memory where a slot has at most 8 rows);
-// then one Join per CTA.
+// began before its piece and ends inside it; in shared memory where that fits beside the rings); then one
+// Join per CTA.
 struct Join {
     int b, u;  // sequence and unit that slot 1 begins; b = -1: none
     int last;  // the last CTA that holds a part
@@ -205,14 +205,15 @@ __device__ __forceinline__ void join_part(RowPart& s, const RowPart& p) {
     s.o.z = fmaf(b, p.o.z, a * s.o.z);
     s.o.w = fmaf(b, p.o.w, a * s.o.w);
 }
-__device__ __forceinline__ float lse_of(float m, float l) {  // l = 0: no key, or only scores of -inf
-    return l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+// Natural log of the row's sum; l carries the factor 2^lift.  l = 0: no key, or only scores of -inf.
+__device__ __forceinline__ float lse_of(const PagedAttnArgs& a, float m, float l) {
+    return l != 0.f ? (m + (log2f(l) - a.lift)) * 0.69314718055994531f : -CUDART_INF_F;
 }
 template <typename O>
 __device__ __forceinline__ void store_row(const PagedAttnArgs& a, int64_t row, const RowPart& s, int lane) {
     const float inv = s.l != 0.f ? 1.f / s.l : 0.f;
     store4(static_cast<O*>(a.out) + row * kTile + 4 * lane, make_float4(s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv));
-    if (a.lse != nullptr && lane == 0) a.lse[row] = lse_of(s.m, s.l);
+    if (a.lse != nullptr && lane == 0) a.lse[row] = lse_of(a, s.m, s.l);
 }
 
 // x / y, both at least 0: 64-bit division takes five times as long as the 32-bit one, which nearly
@@ -256,16 +257,14 @@ constexpr unsigned kEnds = 4;    //   it ends with this warp's piece
 constexpr unsigned kHead = 8;    // its first unit began before its piece, ended inside it, and is in its head slot
 
 // T: type of q and the cache; O: type of the output; NT: eights of query heads in a unit; CAP: scores are
-// capped.  Instructions are fetched from L2 past the loop's, which costs microseconds while the cache
-// streams through it: what runs once per unit or call is kept short, not unrolled.
-//
+// capped.
 // CLUSTER: a thread-block cluster takes one unit, its CTAs equal parts of it, and the parts are joined
 // through the cluster's shared memory: no second launch.
 template <typename T, typename O, int NT, bool CAP, bool CLUSTER>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
     constexpr int kWarps = Shape<NT>::kWarps, kThreads = Shape<NT>::kThreads, kRing = Shape<NT>::kRing;
     constexpr int kStages = Shape<NT>::kStages;
-    constexpr float kLift = std::is_same<T, __half>::value ? 15.f : 0.f;  // log2 of the probabilities' factor
+    constexpr float kLift = std::is_same<T, __half>::value ? kHalfLift : 0.f;  // log2 of the probabilities' factor
     constexpr int PIECES = sizeof(O) == 4 && std::is_same<T, __nv_bfloat16>::value ? 3 : 2;  // of a probability
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ long long s_scan[kWarps];
@@ -276,7 +275,6 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- this warp's piece of the stream: equal pieces for the CTAs, cut into equal ones for the warps ----
-    const int worker = blockIdx.x * kWarps + warp;
     Cursor at = {};
     long long piece = 1, begin = 0, seq_begin = 0;  // piece: groups of a CTA
     int len = 0;
@@ -598,7 +596,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
                         store1(out + 16 * cc, o[e][cc][i] * inv);
                         store1(out + 16 * cc + 8, o[e][cc][i + 2] * inv);
                     }
-                    if (a.lse != nullptr && row0 == 0) a.lse[row] = lse_of(m[e][i] - kLift, l[e][i]);
+                    if (a.lse != nullptr && row0 == 0) a.lse[row] = lse_of(a, m[e][i], l[e][i]);
                 } else {
 #pragma unroll
                     for (int cc = 0; cc < 8; ++cc) {
@@ -606,7 +604,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
                         slot[r * kTile + 16 * cc + row0 + 8] = o[e][cc][i + 2];
                     }
                     if (row0 == 0) {
-                        slot[a.rows * kTile + r] = m[e][i] - kLift;
+                        slot[a.rows * kTile + r] = m[e][i];
                         slot[a.rows * kTile + a.rows + r] = l[e][i];
                     }
                 }
@@ -760,7 +758,7 @@ cudaError_t cluster_room(int log2n, int dev, int sms, int* room) {
     static std::atomic<int> known[kMaxCachedDevices][5] = {};
     const bool cached = dev >= 0 && dev < kMaxCachedDevices;
     *room = log2n == 0 ? sms : cached ? known[dev][log2n].load(std::memory_order_relaxed) : 0;
-    if (*room > 0) return cudaSuccess;
+    if (*room != 0) return cudaSuccess;
     const auto kern = paged_split_kernel<__nv_bfloat16, float, 1, false, true>;
     const int smem = Shape<1>::kWarps * Shape<1>::kRing;
     cudaError_t e = set_smem_limit_once(kern, smem, false, dev);
@@ -777,9 +775,12 @@ cudaError_t cluster_room(int log2n, int dev, int sms, int* room) {
     lc.dynamicSmemBytes = smem;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(room, kern, &lc);
-    if (e == cudaSuccess && cached) known[dev][log2n].store(*room, std::memory_order_relaxed);
-    return e;
+    if (cudaOccupancyMaxActiveClusters(room, kern, &lc) != cudaSuccess) {
+        cudaGetLastError();  // no such cluster on this device
+        *room = 0;
+    }
+    if (cached) known[dev][log2n].store(*room > 0 ? *room : -1, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 // CTAs of a cluster that takes one unit, 0: the stream is split instead.  A cluster needs no second launch
@@ -836,6 +837,7 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stre
     a.rows = a.group < kRows ? a.group : kRows;
     a.row_blocks = (a.group + kRows - 1) / kRows;
     a.units = a.Hkv * a.row_blocks;
+    a.lift = dtype == KVARN_DTYPE_FP16 ? kHalfLift : 0.f;
     a.inv_softcap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     const bool wide = a.out_dtype == KVARN_DTYPE_FP32;
