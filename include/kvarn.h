@@ -325,8 +325,8 @@ typedef enum {
  *                 kv_lens, page_counts_out and free_count_out repeat the inputs, cu_tokens is 0,
  *                 positions and slot_map are -1, and value 16 of kvarn_device_error is set.
  * All arrays are int32 on the device.  0 <= B <= 16384, page_size 1..65536, 1 <= max_pages,
- * B * max_pages <= 2^30 (times Hkv: <= 2^40), 0 <= n_rows, free_capacity <= 2^30.  B = 0 is a no-op.
- * One launch. */
+ * B * max_pages <= 2^30, 0 <= Hkv <= 1024, 0 <= n_rows, free_capacity <= 2^30.  B = 0 is a no-op (no
+ * output is written).  One launch. */
 kvarn_status kvarn_step_tables(int B, int max_pages, int page_size, const int32_t* seq_lens,
                                const int32_t* n_new, const int32_t* page_counts, int32_t* page_table,
                                int32_t* free_pages, const int32_t* free_count, int free_capacity,
@@ -378,7 +378,8 @@ kvarn_status kvarn_rope_frequencies(const kvarn_rope_config* cfg, double* freqs,
  *                 up to 128 (0: no rotation, inv_freq may be NULL).
  *   q_weight, k_weight : [128] float32, device, 16-byte aligned, or NULL for no norm.
  *   q_out       : [n_tokens][Hq][128] with its strides; may be q itself (same type and strides).
- *   k_cache, v_cache and their sizes and strides: the paged cache; rows go to slot slot_map[t].
+ *   k_cache, v_cache and their sizes and strides: the paged cache (two arrays); rows go to slot
+ *                 slot_map[t].
  *   slot_map    : [n_tokens] int32 or NULL (slot t).  -1: the row's key and value are not written; one
  *                 past the cache is not written either and sets value 32 of kvarn_device_error.  Slots
  *                 are distinct.
