@@ -308,7 +308,8 @@ typedef enum {
  * says that it is finished: its pages go back and its length becomes 0.  Sequences stand in order:
  *   pages given back are pushed on the stack free_pages in (sequence, page) order, then the pages that
  *   the new tokens need beyond page_counts[b] are popped in (sequence, page) order; a sequence that
- *   holds more pages than it needs (a rejected draft) keeps them.
+ *   holds more pages than it needs (a rejected draft) keeps them.  A page is held by one sequence: pages
+ *   that several rows name would be given back several times.
  * Inputs: seq_lens, n_new, page_counts : [B]; page_table : [B][max_pages]; free_pages :
  * [free_capacity], its first *free_count entries valid.  Page ids are not checked; a slot
  * (page * page_size + offset) has to fit 31 bits.
