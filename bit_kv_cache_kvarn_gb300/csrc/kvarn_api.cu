@@ -679,7 +679,7 @@ kvarn_status kvarn_rope_qkv(kvarn_dtype x_dtype, kvarn_dtype out_dtype, int n_to
     a.interleaved = interleaved;
     a.page_size = Hkv > 0 ? page_size : 1;
     a.n_slots = Hkv > 0 ? (int)(n_pages * page_size) : 0;
-    a.slices = a.passes = 0;
+    a.passes = 0;
     a.rope_scale = rope_scale;
     a.eps = eps;
     a.q = q;

@@ -152,7 +152,7 @@ cudaError_t read_and_clear_tables_error(unsigned int* out);
 // Norm, rotation and cache write: see kvarn_rope_qkv.  Strides in elements.
 struct RopeArgs {
     int n_tokens, Hq, Hkv, rot_dim, interleaved, page_size, n_slots;
-    int slices, passes;  // set by the launcher: items of a token, times four rows of a warp in an item
+    int passes;  // set by the launcher: times four rows that a warp takes of a token
     float rope_scale, eps;
     const void* q;
     const void* k;

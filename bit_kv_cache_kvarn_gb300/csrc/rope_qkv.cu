@@ -86,8 +86,8 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f) {
     return (long long)bits < 0 ? 0ull - r : r;
 }
 
-// X: type of q, k, v; O: type of q_out and the cache; SHARE: warps that share a token and its angles.  An
-// item is a.passes times 4 SHARE of a token's Hq + 2 Hkv rows, a token a.slices items.
+// X: type of q, k, v; O: type of q_out and the cache; SHARE: warps that share a token and its angles.  A
+// warp takes a.passes times four of a token's Hq + 2 Hkv rows.
 template <typename X, typename O, int SHARE, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 4) rope_qkv_kernel(RopeArgs a) {
     constexpr int kDepth = sizeof(X) == 4 ? 3 : 4;     // passes in flight per warp
@@ -99,10 +99,10 @@ __global__ void __launch_bounds__(kThreads, 4) rope_qkv_kernel(RopeArgs a) {
     float2* s_turn = s_turns[warp / SHARE];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // items: (token, slice), this warp's (or CTA's) every `stride`th
-    const unsigned n_items = (unsigned)a.n_tokens * (unsigned)a.slices, stride = gridDim.x * (kWarps / SHARE);
-    unsigned item = blockIdx.x * (kWarps / SHARE) + warp / SHARE;
-    if (item >= n_items) return;  // SHARE > 1: the whole CTA
+    // this warp's (or CTA's) tokens: every `stride`th; grid.y: the slices of a token
+    const unsigned n_tokens = (unsigned)a.n_tokens, stride = gridDim.x * (kWarps / SHARE);
+    unsigned t = blockIdx.x * (kWarps / SHARE) + warp / SHARE;
+    if (t >= n_tokens) return;  // SHARE > 1: the whole CTA
     const int rows = a.Hq + 2 * a.Hkv, pairs = a.rot_dim >> 1;
     const int sub = lane >> 3, j = lane & 7;
     const bool turned = j < (a.rot_dim >> 4);
@@ -117,18 +117,14 @@ __global__ void __launch_bounds__(kThreads, 4) rope_qkv_kernel(RopeArgs a) {
     // each row they were half of the kernel's instructions.
     constexpr uint32_t kEntry = sizeof(s_raw[0][0]);
     const uint32_t ring = smem_addr(s_raw[warp][0][sub]);
-    auto token_of = [&](unsigned i) { return (int)(a.slices == 1 ? i : i / (unsigned)a.slices); };
-    auto row_of = [&](unsigned i) {  // first row of this lane in item i
-        const int slice = a.slices == 1 ? 0 : (int)(i % (unsigned)a.slices);
-        return 4 * (slice * a.passes * SHARE + warp % SHARE) + sub;
-    };
-    unsigned in_item = item;
-    int in_pass = 0, in_t = token_of(item), in_row = row_of(item), in_end = 0;
+    const int first_row = SHARE == 1 ? sub : 4 * ((int)blockIdx.y * a.passes * SHARE + warp % SHARE) + sub;
+    unsigned in_t = t;
+    int in_pass = 0, in_row = first_row, in_end = 0;
     const uint4* src = nullptr;
     int64_t src_step = 0;
     uint32_t in_at = 0;
     auto load = [&]() {
-        if (in_item < n_items) {
+        if (in_t < n_tokens) {
             if (in_row >= in_end && in_row < rows) {  // the first row, or one of another section
                 const X* p;
                 int64_t head = a.kv_head_stride;
@@ -151,9 +147,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_qkv_kernel(RopeArgs a) {
             }
             src += src_step;
             in_row += kStep;
-            if (++in_pass == a.passes) {  // on to the next item: the ring does not run dry between tokens
-                in_item += stride;
-                in_pass = 0, in_t = token_of(in_item), in_row = row_of(in_item), in_end = 0;
+            if (++in_pass == a.passes) {  // on to the next token: the ring does not run dry between them
+                in_t += stride;
+                in_pass = 0, in_row = first_row, in_end = 0;
             }
         }
         in_at = in_at + kEntry < kDepth * kEntry ? in_at + kEntry : 0;
@@ -163,8 +159,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_qkv_kernel(RopeArgs a) {
     for (int i = 0; i < kDepth; ++i) load();  // on their way while the angles are made
     const uint4* entry = s_raw[warp][0][sub];
     int out_at = 0;
-    int t = token_of(item);
-    int pos = a.positions[t], slot = a.Hkv == 0 ? -1 : a.slot_map != nullptr ? a.slot_map[t] : t;
+    int pos = a.positions[t], slot = a.Hkv == 0 ? -1 : a.slot_map != nullptr ? a.slot_map[t] : (int)t;
 
     constexpr int kPairs = kHalf / (32 * SHARE) > 0 ? kHalf / (32 * SHARE) : 1;  // of a lane, to make angles for
     unsigned long long freq[kPairs];
@@ -176,12 +171,11 @@ __global__ void __launch_bounds__(kThreads, 4) rope_qkv_kernel(RopeArgs a) {
 
     for (;;) {
         // the next token's position and slot come while this one is turned
-        const unsigned next = item + stride;
-        int next_t = 0, next_pos = 0, next_slot = 0;
-        if (next < n_items) {
-            next_t = token_of(next);
-            next_pos = a.positions[next_t];
-            next_slot = a.Hkv == 0 ? -1 : a.slot_map != nullptr ? a.slot_map[next_t] : next_t;
+        const unsigned next = t + stride;
+        int next_pos = 0, next_slot = 0;
+        if (next < n_tokens) {
+            next_pos = a.positions[next];
+            next_slot = a.Hkv == 0 ? -1 : a.slot_map != nullptr ? a.slot_map[next] : (int)next;
         }
         const bool padding = pos < 0;  // nothing of the row is written
 #pragma unroll
@@ -218,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_qkv_kernel(RopeArgs a) {
         }
         float2 wa[4], wb[4];  // and its weights, where the section has a norm
         bool normed = false, turn = false, kept = false;
-        int r = row_of(item), end = 0;
+        int r = first_row, end = 0;
         O* dst = nullptr;
         int64_t dst_step = 0;
 
@@ -289,8 +283,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_qkv_kernel(RopeArgs a) {
             }
             dst += dst_step;
         }
-        if (next >= n_items) break;
-        item = next, t = next_t, pos = next_pos, slot = next_slot;
+        if (next >= n_tokens) break;
+        t = next, pos = next_pos, slot = next_slot;
     }
 }
 
@@ -299,19 +293,19 @@ cudaError_t launch(RopeArgs a, int slices, int dev, int sms, cudaStream_t stream
     const int rounds = (a.Hq + 2 * a.Hkv + 4 * SHARE - 1) / (4 * SHARE);
     slices = slices < 1 ? 1 : slices < rounds ? slices : rounds;
     a.passes = (rounds + slices - 1) / slices;
-    a.slices = (rounds + a.passes - 1) / a.passes;
-    int64_t ctas = ((int64_t)a.n_tokens * a.slices * SHARE + kWarps - 1) / kWarps;
+    int64_t ctas = ((int64_t)a.n_tokens * SHARE + kWarps - 1) / kWarps;
     // past 16 CTAs for an SM (four run at once) warps go on from token to token, eight CTAs for an SM
     if (SHARE == 1 && ctas > 16 * (int64_t)sms) ctas = 8 * (int64_t)sms;
     const auto kern = a.interleaved ? rope_qkv_kernel<X, O, SHARE, true> : rope_qkv_kernel<X, O, SHARE, false>;
     const cudaError_t e = set_smem_limit_once(kern, 0, true, dev);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), 0, stream, a);
+    return launch_pdl(kern, dim3((unsigned)ctas, (unsigned)((rounds + a.passes - 1) / a.passes)), dim3(kThreads), 0, stream, a);
 }
 
-// Measured, 32 + 2 x 8 heads bf16 (us): a warp per token against four sharing it: 300 tokens 4.2 / 4.2, 600
-// 8.3 / 4.6, 1000 10.0 / 7.9, 1500 11.1 / 12.5, 2000 12.0 / 16.6, 5003 27.0 / 27.0, 16384 66 / 97.  Four that
-// share are sliced further while that leaves at most four CTAs for an SM; 3 tokens 2.4.
+// Measured, 32 + 2 x 8 heads bf16 (us): a warp per token against four sharing it: 3 tokens 6.4 / 2.3, 300 6.7 /
+// 3.8, 600 8.4 / 4.5, 1000 10.1 / 7.4, 1215 7.7 / 7.9, 1500 10.6 / 10.3, 2000 10.8 / 13.1, 5003 25.7 / 32.4,
+// 16384 66 / 96.  Four that share are sliced further while that leaves at most four CTAs for an SM.  The slices
+// are the grid's second dimension: as one index, divided in the kernel, 3 tokens took 2.8 and 256 4.1 (now 3.8).
 template <typename X, typename O>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
     int dev = 0, sms = 0;
