@@ -1,0 +1,58 @@
+"""The serving step's calls at the ends of their ranges, on the GPU."""
+import pytest
+import torch
+
+from tests.test_gpu_serving import BF, _no_device_error, attn_call, attn_case, attn_check, i32  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _ms(f, reps=3):
+    f()
+    times = []
+    for _ in range(reps):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        torch.cuda.synchronize()
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times)
+
+
+def _sparse_batch(B, live, seed=61, starts=False):
+    """B sequences of which `live` ({index: length}) hold tokens; the others are empty slots of a batch of fixed size."""
+    lens = [live.get(b, 0) for b in range(B)]
+    c = attn_case(seed, [n for n in lens if n], 4, 2, P=16)
+    idx = torch.tensor(sorted(live), device="cuda")
+    q = torch.randn(B, 4, 128, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").to(BF)
+    q[idx] = c["q"]
+    table = torch.full((B, c["table"].shape[1]), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    table[idx] = c["table"]
+    first = None
+    if starts:  # empty because everything lies before the first visible key
+        first = torch.where(i32(lens) > 0, 0, 50).to(torch.int32)
+        lens = [n or 50 for n in lens]
+    return dict(c, q=q, table=table, lens=i32(lens), starts=first)
+
+
+@pytest.mark.parametrize("starts", [False, True])
+@pytest.mark.parametrize("B,live", [(40, {0: 33}), (40, {39: 100}), (300, {0: 500, 299: 3}), (2048, {5: 40, 36: 17, 37: 1, 69: 200, 1500: 700}),
+                                    (2048, {i: 1 + i % 50 for i in range(0, 2048, 33)}), (600, {i: 20 for i in range(31, 600, 32)})])
+def test_attention_of_mostly_empty_batches(kv, B, live, starts):
+    c = _sparse_batch(B, live, starts=starts)
+    attn_check(c, *attn_call(kv, c))
+
+
+def test_attention_passes_over_empty_sequences_quickly(kv):
+    # One by one, with a dependent load for each, they cost some 95 ns apiece; 32 at a time, and even with a load
+    # from memory (600 ns) for each 32, less than 20.
+    B = 30000
+    ws = torch.empty(kv.kvarn_paged_attention_workspace_size(B, 4, 2), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(B, 4, 128, device="cuda"), torch.empty(B, 4, device="cuda")
+    t = {}
+    for name, live in (("together", {B - 2: 64, B - 1: 64}), ("before", {0: 64, 1: 64}), ("around", {0: 64, B - 1: 64})):
+        c = _sparse_batch(B, live)
+        t[name] = _ms(lambda: attn_call(kv, c, ws=ws, out=out, lse=lse))
+    assert t["before"] - t["together"] <= 2e-5 * B and t["around"] - t["together"] <= 2e-5 * B, t
