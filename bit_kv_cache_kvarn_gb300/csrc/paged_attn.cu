@@ -554,10 +554,14 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
 #pragma unroll
             for (int e = 0; e < NT; ++e) {
                 // a row whose scores are all -inf so far has no maximum to subtract
-                const float ref[2] = {m[e][0] == -CUDART_INF_F ? 0.f : m[e][0] - kLift, m[e][1] == -CUDART_INF_F ? 0.f : m[e][1] - kLift};
+                const float ref[2] = {m[e][0] == -CUDART_INF_F ? 0.f : m[e][0], m[e][1] == -CUDART_INF_F ? 0.f : m[e][1]};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float p0 = exp2f(s[e][0][2 * h] - ref[0]), p1 = exp2f(s[e][0][2 * h + 1] - ref[1]);
+                    // The lift is added to the difference: a maximum past 2^24 less 15 may be rounded to the maximum
+                    // less 16, and 2^16 is no fp16 number any more.
+                    float x0 = s[e][0][2 * h] - ref[0], x1 = s[e][0][2 * h + 1] - ref[1];
+                    if constexpr (kLift != 0.f) x0 += kLift, x1 += kLift;
+                    float p0 = exp2f(x0), p1 = exp2f(x1);
                     l[e][0] += p0;
                     l[e][1] += p1;
 #pragma unroll

@@ -2,9 +2,37 @@
 import pytest
 import torch
 
-from tests.test_gpu_serving import BF, _no_device_error, attn_call, attn_case, attn_check, i32  # noqa: F401
+from tests.test_gpu_serving import BF, F32, HF, _no_device_error, attn_call, attn_case, attn_check, i32  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dt", [HF, BF])
+@pytest.mark.parametrize("out_dtype", [F32, "16"])
+def test_attention_of_huge_scores(kv, dt, wide, sign, out_dtype):
+    # Scores beyond 2^24 (in the log2 domain, where neighbouring fp32 numbers are 2 and more apart).  Keys differ by
+    # at least 4096 * 4 in the score, so one key takes all: the output is its value and lse its score, which is
+    # off by the roundings of the products with scale and log2 e, the sum with the lift and the product with
+    # ln 2: four half steps, 2^-22, of itself.
+    lens, hq = [40, 200], 16
+    c = attn_case(60, lens, hq, 2, P=16, dt=dt, wide=wide)
+    c["q"].zero_()
+    step = 4.0 if dt == HF else 32.0  # neighbours of 4096 in fp16 and bf16
+    c["q"][:, :, 0] = (4096 + step * torch.arange(hq, device="cuda")).to(dt)
+    best = []
+    for b, n in enumerate(lens):
+        for t in range(n):
+            c["kc"][int(c["table"][b, t // 16]), :, t % 16, 0] = sign * (4096 + step * ((37 * t) % n))
+        best.append(max(range(n), key=lambda t: sign * ((37 * t) % n)))
+    out, lse = attn_call(kv, c, scale=1.0, out_dtype=dt if out_dtype == "16" else F32)
+    for b in range(len(lens)):
+        page, off = int(c["table"][b, best[b] // 16]), best[b] % 16
+        for h in range(hq):
+            assert torch.equal(out[b, h], c["vc"][page, h // 8, off].to(out.dtype))
+            want = float(c["q"][b, h, 0]) * float(c["kc"][page, h // 8, off, 0])
+            assert abs(float(lse[b, h]) - want) <= 2.0 ** -22 * abs(want)
 
 
 def _ms(f, reps=3):
