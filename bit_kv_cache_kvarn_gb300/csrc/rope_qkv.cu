@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_qkv_kernel(RopeArgs a) {
         if (slot >= 0 && slot < a.n_slots) {
             const int page = slot / a.page_size, off = slot - page * a.page_size;
             cache_at = page * a.page_stride + off * a.token_stride;
-        } else if (slot >= 0 && !padding && lane == 0) {
+        } else if (slot != -1 && !padding && lane == 0) {
             atomicOr(&g_rope_error, 1u);
         }
         if (SHARE == kWarps) __syncthreads();

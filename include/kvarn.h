@@ -381,9 +381,9 @@ kvarn_status kvarn_rope_frequencies(const kvarn_rope_config* cfg, double* freqs,
  *   q_out       : [n_tokens][Hq][128] with its strides; may be q itself (same type and strides).
  *   k_cache, v_cache and their sizes and strides: the paged cache (two arrays); rows go to slot
  *                 slot_map[t].
- *   slot_map    : [n_tokens] int32 or NULL (slot t).  -1: the row's key and value are not written; one
- *                 past the cache is not written either and sets value 32 of kvarn_device_error.  Slots
- *                 are distinct.
+ *   slot_map    : [n_tokens] int32 or NULL (slot t).  -1: the row's key and value are not written; any
+ *                 other slot outside the cache (below -1 too: a slot that did not fit 31 bits) is not
+ *                 written either and sets value 32 of kvarn_device_error.  Slots are distinct.
  * With page_size = n_new, NULL slot_map and n_tokens = B * n_new the cache layout is
  * kvarn_append_tokens' [B][Hkv][n_new][128].  Hq = 0 (no queries) or Hkv = 0 (no keys and values)
  * leaves the pointers of that side unused.  Outputs do not overlap inputs otherwise.

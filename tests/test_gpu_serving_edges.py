@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from tests.test_gpu_serving import BF, F32, HF, _no_device_error, attn_call, attn_case, attn_check, i32  # noqa: F401
+from tests.test_gpu_serving import BF, F32, HF, _no_device_error, attn_call, attn_case, attn_check, i32, rope_call, rope_case, rope_check  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +84,20 @@ def test_attention_passes_over_empty_sequences_quickly(kv):
         c = _sparse_batch(B, live)
         t[name] = _ms(lambda: attn_call(kv, c, ws=ws, out=out, lse=lse))
     assert t["before"] - t["together"] <= 2e-5 * B and t["around"] - t["together"] <= 2e-5 * B, t
+
+
+@pytest.mark.parametrize("T", [6, 1300])
+def test_rope_slots_below_minus_one_are_reported(kv, T):
+    c = rope_case(62, T, 4, 2)
+    c["slots"][1] = -1
+    before = [c[k].clone() for k in ("qo", "kc", "vc")]
+    rope_check(c, rope_call(kv, c), *before)
+    assert kv.kvarn_device_error() == 0
+    c = rope_case(63, T, 4, 2)
+    c["slots"][1], c["slots"][4] = -2, -(2 ** 31)
+    before = [c[k].clone() for k in ("qo", "kc", "vc")]
+    rope_check(c, rope_call(kv, c), *before)
+    assert kv.kvarn_device_error() == 32
+    c["positions"][1] = c["positions"][4] = -1  # a padding row's slot is not looked at
+    rope_call(kv, c)
+    assert kv.kvarn_device_error() == 0
