@@ -1,4 +1,5 @@
 // libkvarn C-ABI: argument validation and kernel launches.  See include/kvarn.h for the contract.
+#include <float.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -733,7 +734,9 @@ kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, co
     if (out_dtype != KVARN_DTYPE_FP32 && out_dtype != dtype)
         return fail(KVARN_ERR_INVALID_ARG, "out_dtype = %d; expected fp32 or dtype (%d)", (int)out_dtype, (int)dtype);
     if (!isfinite(softmax_scale)) return fail(KVARN_ERR_INVALID_ARG, "softmax_scale is not finite");
-    if (!(softcap >= 0.f) || !isfinite(softcap)) return fail(KVARN_ERR_INVALID_ARG, "softcap = %g; need a finite cap >= 0", softcap);
+    // the reciprocal of a cap below the normal numbers may be infinite
+    if (softcap != 0.f && (!(softcap >= FLT_MIN) || !isfinite(softcap)))
+        return fail(KVARN_ERR_INVALID_ARG, "softcap = %g; need 0 or a finite cap of at least 2^-126", softcap);
     if (window < 0) return fail(KVARN_ERR_INVALID_ARG, "window = %d < 0", window);
     if (page_size < 16 || page_size % 16 != 0)
         return fail(KVARN_ERR_INVALID_ARG, "page_size = %d; need a positive multiple of 16", page_size);

@@ -12,6 +12,7 @@
 
 #include <climits>
 #include <initializer_list>
+#include <limits>
 #include <stdexcept>
 #include <string>
 
@@ -86,6 +87,11 @@ float as_float(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw PythonError();
     return (float)v;
+}
+// the same, but only 0 itself becomes 0
+float as_float_or_zero(PyObject* o) {
+    const float v = as_float(o);
+    return v == 0.f && PyFloat_AsDouble(o) != 0.0 ? std::numeric_limits<float>::denorm_min() : v;
 }
 int as_bool(PyObject* o) {
     const int v = PyObject_IsTrue(o);
@@ -241,7 +247,7 @@ kvarn_status paged_attention(PyObject* const* x) {
         as_dtype(dt, "q"), narrow(B, "B"), narrow(hq, "Hq"), narrow(kv.heads, "Hkv"), rq.p, rq.token, rq.head, kv.k, kv.v,
         kv.n_pages, kv.page_size, kv.page_stride, kv.head_stride, kv.token_stride, c.ints(x[3], {B, width}, "page_table"),
         narrow(width, "max_pages"), c.ints(x[4], {B}, "kv_lens"), c.ints_or_null(x[11], {B}, "kv_starts"),
-        as_int(x[10], "window"), as_float(x[6]), as_float(x[8]), c.floats_or_null(x[9], {hq}, "slopes"), ws.data_ptr(),
+        as_int(x[10], "window"), as_float(x[6]), as_float_or_zero(x[8]), c.floats_or_null(x[9], {hq}, "slopes"), ws.data_ptr(),
         (size_t)ws.nbytes(), as_dtype(out.scalar_type(), "out"),
         c.array<void>(out, out.scalar_type(), {B, hq, KVARN_HEAD_DIM}, "out"), c.floats_or_null(x[12], {B, hq}, "lse"),
         as_stream(x[13], c.dev));

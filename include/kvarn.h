@@ -418,7 +418,7 @@ size_t kvarn_paged_attention_workspace_size(int B, int Hq, int Hkv);
  *   kv_lens     : [B] int32 (kvarn_step_tables' kv_lens); kv_starts : [B] int32 or NULL: first visible
  *                 token (left padding, or another document before it); negative counts as 0.
  *   window      : 0, or the number of last tokens that are visible, the query's own among them.
- *   softcap     : 0 (none) or positive; slopes : [Hq] float32 or NULL.
+ *   softcap     : 0 (none) or at least 2^-126; slopes : [Hq] float32 or NULL.
  *   out         : [B][Hq][128] of out_dtype (KVARN_DTYPE_FP32 or dtype).
  *   lse         : [B][Hq] float32 or NULL: natural log of sum_j exp(s_j).
  *   workspace   : >= kvarn_paged_attention_workspace_size(B, Hq, Hkv) bytes, 16-byte aligned; needs no

@@ -101,3 +101,13 @@ def test_rope_slots_below_minus_one_are_reported(kv, T):
     c["positions"][1] = c["positions"][4] = -1  # a padding row's slot is not looked at
     rope_call(kv, c)
     assert kv.kvarn_device_error() == 0
+
+
+def test_attention_refuses_caps_below_the_normal_range(kv):
+    # 1e-50 is no fp32 number but 0, which would mean no cap
+    c = attn_case(64, [20], 4, 2)
+    for cap in (1e-39, 1e-50, 5e-324):
+        with pytest.raises(kv.KvarnError, match="softcap"):
+            attn_call(kv, c, softcap=cap)
+    for cap in (2.0 ** -126, 1e-30):  # all scores are capped to about 0: the mean of the values
+        attn_check(c, *attn_call(kv, c, softcap=cap), softcap=cap)

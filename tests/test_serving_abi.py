@@ -95,6 +95,12 @@ def test_paged_attention_refusals(lib):
     assert b"workspace" in lib.kvarn_last_error()
 
 
+def test_paged_attention_refuses_caps_without_a_reciprocal(lib):
+    for cap in (2.0 ** -149, 1e-40, 2.0 ** -126 - 2.0 ** -149, -(2.0 ** -149)):
+        assert _attn(lib, cap=cap) == INV, cap
+        assert b"softcap" in lib.kvarn_last_error()
+
+
 def test_paged_attention_workspace_size(lib):
     import bit_kv_cache_kvarn_gb300 as kv
 
