@@ -71,7 +71,6 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, SOURCES))
-        binding_obj = binding.result()
     log = "".join(err for _, err in results)
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         f.write(log)
@@ -84,7 +83,7 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    link_binding(binding_obj)
+    link_binding(binding.result())  # last: a C caller needs neither the binding nor torch's headers
     return LIB
 
 
