@@ -85,6 +85,7 @@ class _PagedCache:
         self.table = torch.full((1, n_blocks), -1, **i32)
         self.free, self.n_free = torch.arange(n_blocks, **i32), torch.full((1,), n_blocks, **i32)
         self.new, self.cu, self.status = torch.full((1,), BLOCK, **i32), torch.zeros(2, **i32), torch.zeros(1, **i32)
+        self.refused = torch.zeros(1, **i32)
         self.positions, self.slots = torch.empty(BLOCK, **i32), torch.empty(BLOCK, **i32)
         self.q = torch.empty(BLOCK, hq, HEAD, dtype=torch.bfloat16, device=dev)
         self.out = torch.empty(BLOCK, hq, HEAD, device=dev)
@@ -93,8 +94,14 @@ class _PagedCache:
     def next_block(self):
         self.kv.kvarn_step_tables(self.length, self.new, self.count, self.table, self.free, self.n_free, BLOCK,
                                   self.length, self.count, self.n_free, self.cu, self.positions, self.slots, self.status)
+        self.refused |= self.status  # kept on the device: blocks do not wait for the host
         # every token of the block is a query of its own, over the same pages
         self.tables, self.lens = self.table.expand(BLOCK, -1).contiguous(), self.positions + 1
+
+    def check(self):
+        """Raise if a block's step was refused: its rows were padding and its attention zeros."""
+        if status := int(self.refused):
+            raise RuntimeError(f"kvarn_step_tables refused a block of the pseudo-decode (status {status})")
 
     def attend(self, layer, q, k, v, scale):
         """q [128, hq, 128], k, v [128, hkv, 128] fp32 before the rotation -> attention [128, hq, 128]."""
@@ -211,6 +218,8 @@ def run(kv, cfg, weights, x, hq: int, hkv: int, quantised: bool = True, capture=
     torch.cuda.synchronize()
     seconds = time.perf_counter() - t0
     torch.backends.cuda.matmul.allow_tf32 = old_tf32
+    if pages is not None:
+        pages.check()
     return attn, seconds
 
 

@@ -111,3 +111,21 @@ def test_attention_refuses_caps_below_the_normal_range(kv):
             attn_call(kv, c, softcap=cap)
     for cap in (2.0 ** -126, 1e-30):  # all scores are capped to about 0: the mean of the values
         attn_check(c, *attn_call(kv, c, softcap=cap), softcap=cap)
+
+
+def test_pseudo_decode_raises_when_a_step_is_refused(kv, monkeypatch):
+    from bit_kv_cache_kvarn_gb300 import pseudo_decode as pd
+
+    made = pd._PagedCache.__init__
+
+    def short(self, *args):
+        made(self, *args)
+        self.n_free.fill_(2)  # pages for two of the four blocks
+
+    monkeypatch.setattr(pd._PagedCache, "__init__", short)
+    w, x = pd.make_weights(41, 1, 256, 4, 2), pd.make_input(41, 4 * 128, 256)
+    try:
+        with pytest.raises(RuntimeError, match="status 1"):
+            pd.run(kv, None, w, x, 4, 2, quantised=False, paged=True)
+    finally:
+        kv.kvarn_device_error()
