@@ -358,7 +358,8 @@ def kvarn_step_tables(seq_lens, n_new, page_counts, page_table, free_pages, free
 
 def kvarn_rope_frequencies(rot_dim: int = TILE, base: float = 10000.0, scaling: int = KVARN_ROPE_PLAIN,
                            factor: float = 1.0, original_len: float = 0.0, low: float = 1.0, high: float = 4.0):
-    """(frequencies [rot_dim / 2], a float64 CPU tensor; rope_scale) for kvarn_rope_qkv."""
+    """(frequencies [rot_dim / 2], a float64 CPU tensor; rope_scale) for kvarn_rope_qkv, which takes both
+    (the frequencies on its device)."""
     cfg = kvarn_rope_config(rot_dim, scaling, base, factor, original_len, low, high)
     freqs, scale = (ctypes.c_double * (TILE // 2))(), _f32()
     _check(load().kvarn_rope_frequencies(ctypes.byref(cfg), freqs, ctypes.byref(scale)))
