@@ -373,8 +373,9 @@ def kvarn_rope_qkv(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slot_m
     q [T, Hq, 128], k, v [T, Hkv, 128]: views with contiguous channels, of q_out's type or fp32;
     positions [T] int32 (negative: padding row); inv_freq [R / 2] float64 or None (no rotation); q_out
     [T, Hq, 128] bf16 or fp16 (may be q); k_cache, v_cache [n_pages, Hkv, page_size, 128] views of one
-    layout; slot_map [T] int32 or None (slot t); weights [128] float32 or None.  q and q_out, or k, v
-    and the caches, may be None together."""
+    layout; slot_map [T] int32 or None (slot t; -1: not written, any other slot outside the cache is
+    reported by kvarn_device_error); weights [128] float32 or None; rope_scale: kvarn_rope_frequencies'.
+    q and q_out, or k, v and the caches, may be None together."""
     _call(_native().rope_qkv(q, k, v, positions, inv_freq, q_out, k_cache, v_cache, slot_map, q_weight, k_weight, eps,
                              rope_scale, interleaved, _raw(stream)))
 
@@ -389,10 +390,10 @@ def kvarn_paged_attention(q, k_cache, v_cache, page_table, kv_lens, out, softmax
 
     q [B, Hq, 128] (contiguous channels), k_cache, v_cache [n_pages, Hkv, page_size, 128] views of one
     layout and q's type, page_table [B, max_pages] int32, kv_lens [B] int32; out [B, Hq, 128] float32 or
-    q's type; workspace: kvarn_paged_attention_workspace_size bytes.  softcap > 0 caps the scores by
-    tanh, slopes [Hq] float32 adds slope * (key position - query position), window > 0 leaves the last
-    `window` tokens, kv_starts [B] int32 hides the tokens before it; lse [B, Hq] float32 receives the
-    log-sum-exp.  A sequence without visible keys gets zeros and -inf."""
+    q's type; workspace: kvarn_paged_attention_workspace_size bytes.  softcap (0: none, else at least
+    2^-126) caps the scores by tanh, slopes [Hq] float32 adds slope * (key position - query position),
+    window > 0 leaves the last `window` tokens, kv_starts [B] int32 hides the tokens before it; lse
+    [B, Hq] float32 receives the log-sum-exp.  A sequence without visible keys gets zeros and -inf."""
     _call(_native().paged_attention(q, k_cache, v_cache, page_table, kv_lens, out, softmax_scale, workspace, softcap,
                                     slopes, window, kv_starts, lse, _raw(stream)))
 

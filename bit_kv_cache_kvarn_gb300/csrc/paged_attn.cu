@@ -29,10 +29,11 @@
 // A probability enters the second product in 16-bit pieces that add up to it.  bf16: two pieces are off
 // by up to 2^-16, on average 2.3e-6 of an output whose other errors are 4e-7, so an fp32 output takes
 // three pieces (2^-24) and a bf16 output, which rounds by 2^-8 itself, two.  fp16: two pieces (2^-22) of
-// 2^15 p, since p itself would lose its digits below 2^-14 (sums and outputs carry the factor alike).  Each group's P V is added to the running output by an fp32 addition, to nearest.
+// 2^15 p, since p itself would lose its digits below 2^-14 (sums and outputs carry the factor alike).  Each
+// group's P V is added to the running output by an fp32 addition, to nearest.
 //
 // Measured (among others, us): 16 x 32k tokens, 32 over 8 heads 312 (6.87 TB/s), 256 x 1-900 tokens, 64 over 8,
-// fp16, capped 93 (5.2 TB/s), one sequence of 4k 10.4.
+// fp16, capped 93 to 99 by the lengths drawn (5.2 TB/s at 93; without the cap 1 less), one sequence of 4k 10.4.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -161,7 +162,7 @@ struct Cursor {
     Span s;
     // By the whole warp, and only where the stream goes on: the unused slots behind a batch's last sequence are
     // never walked through.  Empty sequences before the next one are passed over 32 at a time: one by one they cost
-    // 95 ns each (2048 slots, two of them in use at the start: 186 us, now 17).
+    // 95 ns each (2048 slots, two of them in use at the start: 186 us, now 16).
     __device__ __forceinline__ void next(const PagedAttnArgs& a, int lane) {
         if (++g < n) return;
         g = 0;

@@ -12,9 +12,10 @@
 // for a step of 256 tokens).  cos and sin of that fraction are then taken in fp32.
 //
 // What bounds it: every element is read and written once and nothing is read again, so HBM for
-// chunks of thousands of tokens and launch latency for a decode step.  Eight lanes hold a head, two
-// 16-byte pieces each, chosen so that both channels of every pair are in the same lane in either
-// layout: no element is exchanged between lanes, only the three shuffles of the sum of squares.
+// chunks of thousands of tokens and launch latency for a decode step.  Rows come into a ring in shared
+// memory that each warp fills and reads alone; from there eight lanes hold a row, two runs of eight
+// channels each, chosen so that both channels of every pair are in the same lane in either layout: past
+// the ring the lanes of a row exchange nothing but the three shuffles of the sum of squares.
 #include "kvarn_common.cuh"
 #include "kvarn_internal.h"
 
@@ -43,7 +44,7 @@ __device__ __forceinline__ uint32_t pack2(float2 v, __half) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Channels c .. c + 7 of a row in shared memory, in the pieces' order above.
+// Channels c .. c + 7 of a row in shared memory, whose 16-byte piece p lies at p ^ (p / 8 mod 4).
 template <typename X>
 __device__ __forceinline__ void take8(const uint4* row, int c, float2 (&f)[4]) {
     const int p = c * (int)sizeof(X) / 16;
@@ -302,10 +303,18 @@ cudaError_t launch(RopeArgs a, int slices, int dev, int sms, cudaStream_t stream
     return launch_pdl(kern, dim3((unsigned)ctas, (unsigned)((rounds + a.passes - 1) / a.passes)), dim3(kThreads), 0, stream, a);
 }
 
-// Measured, 32 + 2 x 8 heads bf16 (us): a warp per token against four sharing it: 3 tokens 6.4 / 2.3, 300 6.7 /
-// 3.8, 600 8.4 / 4.5, 1000 10.1 / 7.4, 1215 7.7 / 7.9, 1500 10.6 / 10.3, 2000 10.8 / 13.1, 5003 25.7 / 32.4,
-// 16384 66 / 96.  Four that share are sliced further while that leaves at most four CTAs for an SM.  The slices
-// are the grid's second dimension: as one index, divided in the kernel, 3 tokens took 2.8 and 256 4.1 (now 3.8).
+// Measured, bf16 with norm, device time (us), the same inputs each time (in L2) and, in brackets, inputs from
+// HBM; a warp per token / four sharing it:
+//   32 + 2 x 8 heads:  3 tokens 6.3 / 2.2 (the same), 256 6.5 / 3.7 (7.2 / 4.3), 600 8.8 / 4.4 (9.1 / 5.7),
+//     1000 10.0 / 7.4 (10.8 / 9.3), 1215 7.6 / 7.8 (8.7 / 9.9), 1500 10.5 / 10.2 (11.4 / 12.3), 2000 10.7 / 13.0
+//     (11.9 / 15.6), 5003 25.5 / 32.2 (25.8 / 32.3), 16384 66 / 96 (66 / 96)
+//   1 + 2 x 1:  600 3.3 / 2.8, 1000 3.5 / 4.7, 1215 3.0 / 5.1, 2000 3.6 / 8.5
+//   128 + 2 x 8:  1000 25 / 13, 1215 18 / 15, 1500 27 / 21, 2000 27.5 / 27.6, 5003 66 / 61, 16384 204 / 188
+// A warp per token is fastest where its CTAs, four tokens each, come out even on the SMs: 1215 tokens are two
+// on every SM, and take less time than 1000.  The rule is taken from the first row, with 48 rows a token; with 3 the
+// crossing lies before 1000 tokens, with 144 past 2000.  Four that share are sliced further while that leaves
+// at most four CTAs for an SM.  The slices are the grid's second dimension: as one index, divided in the kernel,
+// 3 tokens took 2.8 and 256 4.1.
 template <typename X, typename O>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
     int dev = 0, sms = 0;

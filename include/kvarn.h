@@ -423,7 +423,9 @@ size_t kvarn_paged_attention_workspace_size(int B, int Hq, int Hkv);
  *   lse         : [B][Hq] float32 or NULL: natural log of sum_j exp(s_j).
  *   workspace   : >= kvarn_paged_attention_workspace_size(B, Hq, Hkv) bytes, 16-byte aligned; needs no
  *                 clearing.  Calls that may overlap on the GPU need one each.
- * Sequences without a visible key (and rows whose scores are all -inf) get zeros and lse -inf.
+ * Sequences without a visible key (and rows whose scores are all -inf) get zeros and lse -inf.  An
+ * infinite element of a visible value makes its channel of the output infinite or NaN (a probability enters
+ * the product in pieces, of which one may be 0 or negative); the other channels are as without it.
  * Hq a positive multiple of Hkv, Hq <= 65535, B <= 65535, 1 <= max_pages, max_pages * page_size <=
  * 2^31 - 64.  B = 0 is a no-op.  The query heads of a kv head are taken 16 at a time; each block
  * reads the kv head's tokens once.  One launch for few and short sequences (by B, Hkv and max_pages *

@@ -129,3 +129,15 @@ def test_pseudo_decode_raises_when_a_step_is_refused(kv, monkeypatch):
             pd.run(kv, None, w, x, 4, 2, quantised=False, paged=True)
     finally:
         kv.kvarn_device_error()
+
+
+@pytest.mark.parametrize("dt", [HF, BF])
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_infinite_values_stay_in_their_channel(kv, dt, wide):
+    c = attn_case(65, [40, 100], 4, 2, dt=dt, wide=wide)
+    want, want_lse = attn_call(kv, c)
+    c["vc"][int(c["table"][1, 3]), 1, 5, 77] = float("inf")
+    out, lse = attn_call(kv, c)
+    assert not torch.isfinite(out[1, 2:, 77]).any()
+    out[1, 2:, 77] = want[1, 2:, 77]
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
