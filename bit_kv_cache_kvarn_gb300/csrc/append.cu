@@ -89,14 +89,7 @@ size_t append_workspace_bytes(int B, int Hkv) {
     return 2 * tiles * kTile * kTile * sizeof(__nv_bfloat16) + ((tiles * sizeof(int32_t) + 255) & ~(size_t)255);
 }
 
-cudaError_t read_and_clear_append_error(unsigned int* out) {
-    unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_append_error, sizeof(v));
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyToSymbol(g_append_error, &zero, sizeof(zero));
-    *out = v;
-    return e;
-}
+cudaError_t read_and_clear_append_error(unsigned int* out) { return read_and_clear_word(&g_append_error, out); }
 
 cudaError_t launch_append(const AppendArgs& a, int B, int k_bits, int v_bits, int iters, int rotate,
                           int normalize, void* k_codes, void* k_params, float* k_scale, void* v_codes,

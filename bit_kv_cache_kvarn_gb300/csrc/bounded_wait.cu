@@ -39,13 +39,6 @@ cudaError_t launch_bounded_wait_check(uint32_t limit_us, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-cudaError_t read_and_clear_selftest_error(unsigned int* out) {
-    unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_selftest_error, sizeof(v));
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyToSymbol(g_selftest_error, &zero, sizeof(zero));
-    *out = v;
-    return e;
-}
+cudaError_t read_and_clear_selftest_error(unsigned int* out) { return read_and_clear_word(&g_selftest_error, out); }
 
 }  // namespace kvarn

@@ -1260,14 +1260,7 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int max_tiles) {
     return p;
 }
 
-cudaError_t read_and_clear_decode_error(unsigned int* out) {
-    unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_decode_error, sizeof(v));
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyToSymbol(g_decode_error, &zero, sizeof(zero));
-    *out = v;
-    return e;
-}
+cudaError_t read_and_clear_decode_error(unsigned int* out) { return read_and_clear_word(&g_decode_error, out); }
 
 cudaError_t launch_decode(int k_bits, int v_bits, int group, const void* q, int B, int Hq, int Hkv,
                           const void* k_codes, const void* k_params, const float* k_scale,

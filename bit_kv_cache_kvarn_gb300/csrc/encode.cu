@@ -711,14 +711,7 @@ __global__ void __launch_bounds__(kThreads, 2) encode_kv_kernel(EncodeKV a) {
 
 size_t encode_smem_bytes() { return sizeof(EncodeSmem); }
 
-cudaError_t read_and_clear_device_error(unsigned int* out) {
-    unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_encode_error, sizeof(v));
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyToSymbol(g_encode_error, &zero, sizeof(zero));
-    *out = v;
-    return e;
-}
+cudaError_t read_and_clear_device_error(unsigned int* out) { return read_and_clear_word(&g_encode_error, out); }
 
 cudaError_t launch_encode(int bits, int kind, const void* x, int64_t n_tiles, void* codes,
                           void* params, float* tile_scale, int iters, int rotate, int normalize,

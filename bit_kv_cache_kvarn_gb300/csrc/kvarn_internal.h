@@ -26,6 +26,17 @@ cudaError_t set_smem_limit_once(Kern kern, int bytes, bool max_carveout, int dev
     return set_smem_limit_once(reinterpret_cast<const void*>(kern), bytes, max_carveout, dev);
 }
 
+// Read a kernel family's device error word (symbol: its address on the host) and clear it where it was set: a copy
+// from the device synchronises and takes 8.5 us, the clearing one 4, and the words are nearly always 0.
+inline cudaError_t read_and_clear_word(const void* symbol, unsigned int* out) {
+    unsigned int v = 0;
+    const unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, symbol, sizeof(v));
+    if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(symbol, &zero, sizeof(zero));
+    if (e == cudaSuccess) *out = v;
+    return e;
+}
+
 size_t encode_smem_bytes();
 cudaError_t read_and_clear_device_error(unsigned int* out);
 cudaError_t read_and_clear_decode_error(unsigned int* out);

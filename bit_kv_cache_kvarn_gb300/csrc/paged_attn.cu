@@ -836,14 +836,7 @@ size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv) {
     return (bytes + 255) & ~(size_t)255;
 }
 
-cudaError_t read_and_clear_paged_attn_error(unsigned int* out) {
-    unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_paged_attn_error, sizeof(v));
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyToSymbol(g_paged_attn_error, &zero, sizeof(zero));
-    *out = v;
-    return e;
-}
+cudaError_t read_and_clear_paged_attn_error(unsigned int* out) { return read_and_clear_word(&g_paged_attn_error, out); }
 
 cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stream) {
     int dev = 0, sms = 0;

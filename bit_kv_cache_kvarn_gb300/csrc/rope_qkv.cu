@@ -326,14 +326,7 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t read_and_clear_rope_error(unsigned int* out) {
-    unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_rope_error, sizeof(v));
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyToSymbol(g_rope_error, &zero, sizeof(zero));
-    *out = v;
-    return e;
-}
+cudaError_t read_and_clear_rope_error(unsigned int* out) { return read_and_clear_word(&g_rope_error, out); }
 
 cudaError_t launch_rope_qkv(const RopeArgs& a, int x_dtype, int out_dtype, cudaStream_t stream) {
     if (out_dtype == KVARN_DTYPE_BF16)

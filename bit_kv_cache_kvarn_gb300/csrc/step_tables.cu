@@ -261,14 +261,7 @@ __global__ void __launch_bounds__(kMaxThreads) step_tables_kernel(StepTablesArgs
 
 }  // namespace
 
-cudaError_t read_and_clear_tables_error(unsigned int* out) {
-    unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_tables_error, sizeof(v));
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyToSymbol(g_tables_error, &zero, sizeof(zero));
-    *out = v;
-    return e;
-}
+cudaError_t read_and_clear_tables_error(unsigned int* out) { return read_and_clear_word(&g_tables_error, out); }
 
 cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t stream) {
     int dev = 0, sms = 0;

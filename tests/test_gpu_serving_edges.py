@@ -1,4 +1,8 @@
 """The serving step's calls at the ends of their ranges, on the GPU."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -141,3 +145,37 @@ def test_attention_infinite_values_stay_in_their_channel(kv, dt, wide):
     assert not torch.isfinite(out[1, 2:, 77]).any()
     out[1, 2:, 77] = want[1, 2:, 77]
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_device_error_is_cleared_by_reading(kv):
+    for slot, bits in ((-2, 32), (-1, 0)):
+        c = rope_case(66, 4, 2, 1)
+        c["slots"][1] = slot
+        rope_call(kv, c)
+        assert kv.kvarn_device_error() == bits and kv.kvarn_device_error() == 0
+
+
+def test_device_error_is_no_slower_for_callers_without_a_serving_step(kv):
+    """In a process of its own that makes no serving call.  Four words are read and nothing is written: with
+    the synchronisation no more than five copies of a number to the host, and one for the call itself."""
+    code = """
+import time, torch, bit_kv_cache_kvarn_gb300 as kv
+kv.load()
+x = torch.zeros(1, device="cuda")
+
+def us(f):
+    best = 1e9
+    for _ in range(9):
+        t = time.perf_counter()
+        for _ in range(100):
+            f()
+        best = min(best, (time.perf_counter() - t) / 100 * 1e6)
+    return best
+
+item, error = us(x.item), us(kv.kvarn_device_error)
+assert error <= 6 * item, (error, item)
+print("quick")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "quick" in r.stdout, r.stderr[-2000:]
