@@ -105,6 +105,10 @@ _SIGNATURES = {
     "kvarn_paged_attention_workspace_size": (_sz, [_i32, _i32, _i32]),
     "kvarn_paged_attention": (_i32, [_i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _i64,
                                      _vp, _i32, _vp, _vp, _i32, _f32, _f32, _vp, _vp, _sz, _i32, _vp, _vp, _vp]),
+    "kvarn_prompt_attention_workspace_size": (_sz, [_i64, _i32, _i32]),
+    "kvarn_prompt_attention": (_i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _i64, _i64,
+                                      _i64, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _f32, _f32, _vp, _vp, _sz, _vp, _vp,
+                                      _vp]),
     "kvarn_status_string": (ctypes.c_char_p, [_i32]),
     "kvarn_last_error": (ctypes.c_char_p, []),
 }
@@ -396,6 +400,27 @@ def kvarn_paged_attention(q, k_cache, v_cache, page_table, kv_lens, out, softmax
     [B, Hq] float32 receives the log-sum-exp.  A sequence without visible keys gets zeros and -inf."""
     _call(_native().paged_attention(q, k_cache, v_cache, page_table, kv_lens, out, softmax_scale, workspace, softcap,
                                     slopes, window, kv_starts, lse, _raw(stream)))
+
+
+def kvarn_prompt_attention_workspace_size(T: int, Hq: int, Hkv: int) -> int:
+    return int(load().kvarn_prompt_attention_workspace_size(T, Hq, Hkv))
+
+
+def kvarn_prompt_attention(q, k_cache, v_cache, page_table, cu_tokens, kv_lens, out, softmax_scale: float, workspace,
+                           causal: bool = True, softcap: float = 0.0, slopes=None, window: int = 0, kv_starts=None,
+                           lse=None, stream=None):
+    """Attention of the new tokens of packed sequences over a paged 16-bit cache that holds them already.
+
+    q [T, Hq, 128] (contiguous channels): rows cu_tokens[b] .. cu_tokens[b + 1] - 1 are sequence b's last
+    tokens, the last one at position kv_lens[b] - 1 (kvarn_step_tables' cu_tokens [B + 1] and kv_lens [B],
+    int32); k_cache, v_cache [n_pages, Hkv, page_size, 128] views of one layout and q's type, page_table
+    [B, max_pages] int32; out [T, Hq, 128] of q's type; workspace: kvarn_prompt_attention_workspace_size
+    bytes.  causal False: every row sees its whole sequence.  softcap, slopes [Hq] float32 (slope * (key
+    position - row position)), window and kv_starts [B] int32 as for kvarn_paged_attention; lse [T, Hq]
+    float32 receives the log-sum-exp.  A row without visible keys gets zeros and -inf; rows outside the
+    sequences are left as they were."""
+    _call(_native().prompt_attention(q, k_cache, v_cache, page_table, cu_tokens, kv_lens, out, softmax_scale, workspace,
+                                     causal, softcap, slopes, window, kv_starts, lse, _raw(stream)))
 
 
 def kvarn_device_error() -> int:

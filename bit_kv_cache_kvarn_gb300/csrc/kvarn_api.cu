@@ -321,9 +321,10 @@ kvarn_status kvarn_decode_attention_sink(const kvarn_config* cfg, const void* q_
                        k_tail_bf16, v_tail_bf16, softmax_scale, workspace, workspace_bytes, out, stream);
 }
 
-// Whether a serving-step call of this process was enqueued or captured: without one its three error words are 0
+// Whether a serving-step call of this process was enqueued or captured: without one its error words are 0
 // and not read (54 us -> 91 with them and a clearing copy for every word; now 37, with them 64).
 static std::atomic<bool> g_serving_used = {false};
+static std::atomic<bool> g_prompt_used = {false};  // the same for the calls with many queries
 
 kvarn_status kvarn_device_error(uint32_t* code_out) {
     if (!code_out) return fail(KVARN_ERR_INVALID_ARG, "code_out is NULL");
@@ -350,7 +351,16 @@ kvarn_status kvarn_device_error(uint32_t* code_out) {
         e = kvarn::read_and_clear_paged_attn_error(&serving[2]);
         if (e != cudaSuccess) return cuda_fail(e, "device error word");
     }
-    *code_out = v | (w << 1) | (x << 2) | (y << 3) | (serving[0] << 4) | (serving[1] << 5) | (serving[2] << 6);
+    unsigned int prompt = 0;
+    if (g_prompt_used.load()) {
+        unsigned int page = 0;
+        e = kvarn::read_and_clear_prompt_page_error(&page);
+        if (e != cudaSuccess) return cuda_fail(e, "device error word");
+        e = kvarn::read_and_clear_prompt_error(&prompt);
+        if (e != cudaSuccess) return cuda_fail(e, "device error word");
+        serving[2] |= page;
+    }
+    *code_out = v | (w << 1) | (x << 2) | (y << 3) | (serving[0] << 4) | (serving[1] << 5) | (serving[2] << 6) | (prompt << 7);
     if (*code_out & KVARN_DEVICE_TIMEOUT_BITS)
         return fail(KVARN_ERR_TIMEOUT, "a bounded device wait gave up (device error bits 0x%x)", *code_out);
     return ok();
@@ -716,6 +726,13 @@ kvarn_status kvarn_rope_qkv(kvarn_dtype x_dtype, kvarn_dtype out_dtype, int n_to
     return ok();
 }
 
+static kvarn_status check_softcap(float softcap) {
+    // the reciprocal of a cap below the normal numbers may be infinite
+    if (softcap != 0.f && (!(softcap >= FLT_MIN) || !isfinite(softcap)))
+        return fail(KVARN_ERR_INVALID_ARG, "softcap = %g; need 0 or a finite cap of at least 2^-126", softcap);
+    return KVARN_OK;
+}
+
 static kvarn_status check_paged_shape(int B, int Hq, int Hkv) {
     if (B < 0 || B > 65535) return fail(KVARN_ERR_INVALID_ARG, "B = %d outside 0..65535", B);
     if (Hq <= 0 || Hkv <= 0 || Hq > 65535 || Hq % Hkv != 0)
@@ -742,9 +759,7 @@ kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, co
     if (out_dtype != KVARN_DTYPE_FP32 && out_dtype != dtype)
         return fail(KVARN_ERR_INVALID_ARG, "out_dtype = %d; expected fp32 or dtype (%d)", (int)out_dtype, (int)dtype);
     if (!isfinite(softmax_scale)) return fail(KVARN_ERR_INVALID_ARG, "softmax_scale is not finite");
-    // the reciprocal of a cap below the normal numbers may be infinite
-    if (softcap != 0.f && (!(softcap >= FLT_MIN) || !isfinite(softcap)))
-        return fail(KVARN_ERR_INVALID_ARG, "softcap = %g; need 0 or a finite cap of at least 2^-126", softcap);
+    KV_TRY(check_softcap(softcap));
     if (window < 0) return fail(KVARN_ERR_INVALID_ARG, "window = %d < 0", window);
     if (page_size < 16 || page_size % 16 != 0)
         return fail(KVARN_ERR_INVALID_ARG, "page_size = %d; need a positive multiple of 16", page_size);
@@ -794,6 +809,103 @@ kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, co
     g_serving_used.store(true);
     cudaError_t e = kvarn::launch_paged_attention(a, (int)dtype, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+    return ok();
+}
+
+static kvarn_status check_prompt_shape(int64_t T, int Hq, int Hkv) {
+    if (T < 0 || T > 0x7fffffffLL) return fail(KVARN_ERR_INVALID_ARG, "T = %lld outside 0..2^31 - 1", (long long)T);
+    if (Hq <= 0 || Hkv <= 0 || Hq > 65535 || Hq % Hkv != 0)
+        return fail(KVARN_ERR_INVALID_ARG, "Hq = %d, Hkv = %d: need Hq a positive multiple of Hkv, up to 65535", Hq, Hkv);
+    if (T * (Hq / Hkv) > 0x7fffffffLL - 1023)
+        return fail(KVARN_ERR_INVALID_ARG, "T = %lld: need T * Hq / Hkv <= 2^31 - 1024", (long long)T);
+    return KVARN_OK;
+}
+
+// What kvarn_prompt_attention and kvarn_prefix_attention ask of the cache: the strides of a tiled copy.
+static kvarn_status check_tiled_cache(const void* k, const void* v, int64_t n_pages, int Hkv, int page_size, int64_t page_stride,
+                                      int64_t head_stride, int64_t token_stride) {
+    if (page_size < 16 || page_size % 16 != 0)
+        return fail(KVARN_ERR_INVALID_ARG, "page_size = %d; need a positive multiple of 16", page_size);
+    KV_TRY(check_cache(k, v, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
+    const int64_t most = 1LL << 38;
+    if (token_stride > most || (Hkv > 1 && head_stride > most) || (n_pages > 1 && page_stride > most))
+        return fail(KVARN_ERR_UNSUPPORTED, "cache strides %lld, %lld, %lld: allowed up to 2^38", (long long)page_stride,
+                    (long long)head_stride, (long long)token_stride);
+    return KVARN_OK;
+}
+
+size_t kvarn_prompt_attention_workspace_size(int64_t T, int Hq, int Hkv) {
+    if (check_prompt_shape(T, Hq, Hkv) != KVARN_OK) return 0;
+    return kvarn::prompt_attention_workspace_bytes(T, Hq, Hkv);
+}
+
+kvarn_status kvarn_prompt_attention(kvarn_dtype dtype, int B, int T, int Hq, int Hkv, const void* q, int64_t q_token_stride,
+                                    int64_t q_head_stride, const void* k_cache, const void* v_cache, int64_t n_pages,
+                                    int page_size, int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                    const int32_t* page_table, int max_pages, const int32_t* cu_tokens,
+                                    const int32_t* kv_lens, const int32_t* kv_starts, int causal, int window,
+                                    float softmax_scale, float softcap, const float* slopes, void* workspace,
+                                    size_t workspace_bytes, void* out, float* lse, kvarn_stream_t stream) {
+    KV_TRY(check_prompt_shape(T, Hq, Hkv));
+    if (B < 0 || B > kvarn::kMaxPromptSeqs)
+        return fail(KVARN_ERR_INVALID_ARG, "B = %d outside 0..%d", B, kvarn::kMaxPromptSeqs);
+    if (!is_16bit(dtype)) return fail(KVARN_ERR_INVALID_ARG, "dtype = %d; expected bf16 or fp16", (int)dtype);
+    if (!isfinite(softmax_scale)) return fail(KVARN_ERR_INVALID_ARG, "softmax_scale is not finite");
+    KV_TRY(check_softcap(softcap));
+    if (causal != 0 && causal != 1) return fail(KVARN_ERR_INVALID_ARG, "causal = %d; expected 0 or 1", causal);
+    if (window < 0) return fail(KVARN_ERR_INVALID_ARG, "window = %d < 0", window);
+    if (!causal && window > 0) return fail(KVARN_ERR_INVALID_ARG, "window = %d: a window goes with causal = 1", window);
+    if (!causal && slopes) return fail(KVARN_ERR_INVALID_ARG, "slopes go with causal = 1");
+    if (max_pages < 1 || (int64_t)max_pages * page_size > 0x7fffffffLL - 255)
+        return fail(KVARN_ERR_INVALID_ARG, "max_pages = %d: need at least 1 and max_pages * page_size <= 2^31 - 256", max_pages);
+    if (B == 0 || T == 0) return ok();
+    KV_TRY(check_ptr(q, 16, "q"));
+    KV_TRY(check_strides("q", q_token_stride, q_head_stride, 8));
+    KV_TRY(check_tiled_cache(k_cache, v_cache, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
+    KV_TRY(check_ptr(page_table, 4, "page_table"));
+    KV_TRY(check_ptr(cu_tokens, 4, "cu_tokens"));
+    KV_TRY(check_ptr(kv_lens, 4, "kv_lens"));
+    if (kv_starts) KV_TRY(check_ptr(kv_starts, 4, "kv_starts"));
+    if (slopes) KV_TRY(check_ptr(slopes, 4, "slopes"));
+    KV_TRY(check_ptr(out, 16, "out"));
+    if (lse) KV_TRY(check_ptr(lse, 4, "lse"));
+    KV_TRY(check_ptr(workspace, 16, "workspace"));
+    const size_t need = kvarn::prompt_attention_workspace_bytes(T, Hq, Hkv);
+    if (workspace_bytes < need)
+        return fail(KVARN_ERR_WORKSPACE, "workspace_bytes = %zu < required %zu", workspace_bytes, need);
+    kvarn::PromptArgs a = {};
+    a.B = B;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.max_len = max_pages * page_size;
+    a.window = window;
+    a.causal = causal;
+    a.out_dtype = (int)dtype;
+    a.n_pages = n_pages;
+    a.scale = softmax_scale;
+    a.softcap = softcap;
+    a.q = q;
+    a.q_token_stride = q_token_stride;
+    a.q_head_stride = q_head_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.page_stride = page_stride;
+    a.head_stride = head_stride;
+    a.token_stride = token_stride;
+    a.page_table = page_table;
+    a.cu = cu_tokens;
+    a.kv_lens = kv_lens;
+    a.kv_starts = kv_starts;
+    a.slopes = slopes;
+    a.workspace = workspace;
+    a.out = out;
+    a.lse = lse;
+    g_prompt_used.store(true);
+    cudaError_t e = kvarn::launch_prompt_attention(a, (int)dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
     return ok();
 }
 

@@ -210,6 +210,35 @@ size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv);
 cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stream);
 cudaError_t read_and_clear_paged_attn_error(unsigned int* out);
 
+// Attention of the new tokens of packed sequences over a paged 16-bit cache: see kvarn_prompt_attention.  Strides
+// in elements.
+constexpr int kMaxPromptSeqs = 16384;  // tiles of each sequence in shared memory
+struct PromptArgs {
+    int B, T, Hq, Hkv, page_size, max_pages, max_len, window, causal, out_dtype;
+    int64_t n_pages;
+    // set by the launcher: query heads per kv head, tokens of a copy, rows of a partial slot, whether 32-byte
+    // stores are aligned
+    int group, box, slot_rows, wide_out;
+    float scale, softcap, inv_softcap;
+    const void* q;
+    int64_t q_token_stride, q_head_stride;
+    const void* k_cache;
+    const void* v_cache;
+    int64_t page_stride, head_stride, token_stride;
+    const int32_t* page_table;
+    const int32_t* cu;
+    const int32_t* kv_lens;
+    const int32_t* kv_starts;
+    const float* slopes;
+    void* workspace;
+    void* out;
+    float* lse;
+};
+size_t prompt_attention_workspace_bytes(int64_t T, int Hq, int Hkv);
+cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream);
+cudaError_t read_and_clear_prompt_error(unsigned int* out);
+cudaError_t read_and_clear_prompt_page_error(unsigned int* out);
+
 // Self-check: one kernel whose bounded mbarrier wait runs out after limit_us (see bounded_wait.cu).
 cudaError_t launch_bounded_wait_check(uint32_t limit_us, cudaStream_t stream);
 cudaError_t read_and_clear_selftest_error(unsigned int* out);

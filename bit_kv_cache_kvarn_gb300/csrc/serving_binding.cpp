@@ -1,7 +1,7 @@
 // Python entry of the serving-step calls: checks of the tensors and the C calls, in compiled code.
 //
 // A decode step's kernels run for 3 to 10 microseconds; checking and passing their 15 to 30 arguments in
-// Python and ctypes took 21 microseconds a call on the Grace cores, so these three calls come through the
+// Python and ctypes took 21 microseconds a call on the Grace cores, so these calls come through the
 // CPython interface.  Each function takes its arguments by position and returns the kvarn_status; a
 // wrong tensor raises ValueError naming it.
 #define PY_SSIZE_T_CLEAN
@@ -253,6 +253,30 @@ kvarn_status paged_attention(PyObject* const* x) {
         as_stream(x[13], c.dev));
 }
 
+kvarn_status prompt_attention(PyObject* const* x) {
+    const Checker c = {(int)c10::cuda::current_device()};
+    const at::Tensor& q = *tensor(x[0], "q");
+    if (q.dim() != 3) bad("q must be [T, Hq, 128]");
+    const int64_t T = q.size(0), hq = q.size(1);
+    const at::ScalarType dt = q.scalar_type();
+    const Rows rq = rows(c, q, dt, T, hq, "q");
+    const Cache kv = cache(c, *tensor(x[1], "k_cache"), *tensor(x[2], "v_cache"), dt);
+    const at::Tensor& table = *tensor(x[3], "page_table");
+    if (table.dim() != 2) bad("page_table must be [B, max_pages]");
+    const int64_t B = table.size(0), width = table.size(1);
+    const at::Tensor& ws = *tensor(x[8], "workspace");
+    c.device(ws, "workspace");
+    if (!ws.is_contiguous()) bad("workspace must be contiguous");
+    return kvarn_prompt_attention(
+        as_dtype(dt, "q"), narrow(B, "B"), narrow(T, "T"), narrow(hq, "Hq"), narrow(kv.heads, "Hkv"), rq.p, rq.token, rq.head,
+        kv.k, kv.v, kv.n_pages, kv.page_size, kv.page_stride, kv.head_stride, kv.token_stride,
+        c.ints(x[3], {B, width}, "page_table"), narrow(width, "max_pages"), c.ints(x[4], {B + 1}, "cu_tokens"),
+        c.ints(x[5], {B}, "kv_lens"), c.ints_or_null(x[13], {B}, "kv_starts"), as_bool(x[9]), as_int(x[12], "window"),
+        as_float(x[7]), as_float_or_zero(x[10]), c.floats_or_null(x[11], {hq}, "slopes"), ws.data_ptr(), (size_t)ws.nbytes(),
+        c.array<void>(*tensor(x[6], "out"), dt, {T, hq, KVARN_HEAD_DIM}, "out"), c.floats_or_null(x[14], {T, hq}, "lse"),
+        as_stream(x[15], c.dev));
+}
+
 // No C++ exception leaves through the interpreter.
 template <kvarn_status (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -277,7 +301,8 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<step_tables, 16>("step_tables"), method<rope_qkv, 15>("rope_qkv"),
-                         method<paged_attention, 14>("paged_attention"), {nullptr, nullptr, 0, nullptr}};
+                         method<paged_attention, 14>("paged_attention"),
+                         method<prompt_attention, 16>("prompt_attention"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

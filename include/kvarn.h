@@ -440,13 +440,55 @@ kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, co
                                    size_t workspace_bytes, kvarn_dtype out_dtype, void* out, float* lse,
                                    kvarn_stream_t stream);
 
+/* Bytes of device workspace kvarn_prompt_attention needs for T rows of queries and these heads, whatever the
+ * lengths (never smaller for a larger T); 0 for an invalid shape. */
+size_t kvarn_prompt_attention_workspace_size(int64_t T, int Hq, int Hkv);
+
+/* Attention of the new tokens of packed sequences over a paged 16-bit cache, grouped-query heads: prompts,
+ * chunks of prompts behind what the cache holds already, drafts, and single tokens, mixed in one call.  Rows
+ * cu_tokens[b] .. cu_tokens[b + 1] - 1 of q are sequence b's last n tokens, at the positions L - n .. L - 1,
+ * L = kv_lens[b] (kvarn_step_tables' cu_tokens and kv_lens; their keys and values are in the cache).  The row at
+ * position p sees the keys j in [max(kv_starts[b], p + 1 - window, 0), p] when causal, else [kv_starts[b], L), and
+ *   s_j = softmax_scale q.k_j;  s_j = softcap tanh(s_j / softcap) if softcap > 0;
+ *   s_j += slopes[h] (j - p) if slopes are given;  out = sum_j softmax(s)_j v_j.
+ *   dtype       : type of q, the cache and out, KVARN_DTYPE_BF16 or _FP16.
+ *   q           : [T][Hq][128], element (t, h, c) at t * q_token_stride + h * q_head_stride + c; strides
+ *                 non-negative multiples of 8.  T is the rows that q and out have; cu_tokens is clamped to it.
+ *   cache       : as described above; page_size a multiple of 16, strides up to 2^38.  Slots outside the
+ *                 tokens that some row sees may hold anything, NaN and infinities included.
+ *   page_table  : [B][max_pages] int32; entry i of row b is the page of tokens [i P, (i + 1) P).  Only entries
+ *                 of visible tokens are read; one outside 0..n_pages - 1 is not followed: its keys and values
+ *                 count as zeros and value 64 of kvarn_device_error is set.
+ *   cu_tokens   : [B + 1] int32, non-decreasing; kv_lens : [B] int32, clamped to 0..max_pages * page_size;
+ *                 kv_starts : [B] int32 or NULL: first visible token; negative counts as 0.
+ *   causal      : 1, or 0: every row sees all tokens of its sequence (then without window and slopes).
+ *   window      : 0, or the number of last tokens that a row sees, its own among them.
+ *   softcap     : 0 (none) or at least 2^-126; slopes : [Hq] float32 or NULL.
+ *   out         : [T][Hq][128]; lse : [T][Hq] float32 or NULL: natural log of sum_j exp(s_j).  Rows outside
+ *                 the sequences are left as they were.
+ *   workspace   : >= kvarn_prompt_attention_workspace_size(T, Hq, Hkv) bytes, 16-byte aligned; needs no
+ *                 clearing.  Calls that may overlap on the GPU need one each.
+ * Rows without a visible key (and rows whose scores are all -inf) get zeros and lse -inf.  Probabilities are
+ * rounded to dtype for the product with the values (scores, maxima, sums and outputs are fp32 until the output's
+ * own rounding); lse is not affected.  0 <= B <= 16384, Hq a positive multiple of Hkv, Hq <= 65535, T * Hq / Hkv
+ * <= 2^31 - 1024, 1 <= max_pages, max_pages * page_size <= 2^31 - 256.  B = 0 and T = 0 are no-ops.  A split and
+ * a join kernel. */
+kvarn_status kvarn_prompt_attention(kvarn_dtype dtype, int B, int T, int Hq, int Hkv, const void* q,
+                                    int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+                                    const void* v_cache, int64_t n_pages, int page_size, int64_t page_stride,
+                                    int64_t head_stride, int64_t token_stride, const int32_t* page_table,
+                                    int max_pages, const int32_t* cu_tokens, const int32_t* kv_lens,
+                                    const int32_t* kv_starts, int causal, int window, float softmax_scale,
+                                    float softcap, const float* slopes, void* workspace, size_t workspace_bytes,
+                                    void* out, float* lse, kvarn_stream_t stream);
+
 /* Reads and clears the device-side error words of the current device, after synchronising it.
  * Bit 1 (value 1): an encoder TMA bulk copy did not complete within its bounded wait (the affected
  * tiles are left unwritten).  Bit 2 (value 2): a decode wait gave up.  Bit 3 (value 4): an append
  * found no block-table slot for a completed block.  Bit 4 (value 8): the wait of
  * kvarn_check_bounded_wait gave up.  Bits 5, 6 and 7 (values 16, 32, 64): a step's tables could not be
- * built, a slot lay outside its cache, a page table entry lay outside its cache.  *code_out = 0 means no
- * such event.
+ * built, a slot lay outside its cache, a page table entry lay outside its cache.  Bit 8 (value 128): a wait
+ * of kvarn_prompt_attention gave up.  *code_out = 0 means no such event.
  * Kernels cannot return a status to the call that enqueued them (that call has returned long
  * before they run), so a device wait that gives up sets its bit, ends its kernel normally -- the
  * CUDA context stays usable -- and is reported here: the call returns KVARN_ERR_TIMEOUT when any
@@ -454,7 +496,7 @@ kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, co
  * *code_out with KVARN_OK); *code_out is filled in both cases.  The bits stay set until read: until
  * then every bounded wait of the kernel family that set one gives up at once.
  * (A library diagnostic; the pages have no counterpart.) */
-#define KVARN_DEVICE_TIMEOUT_BITS 0xBu
+#define KVARN_DEVICE_TIMEOUT_BITS 0x8Bu
 kvarn_status kvarn_device_error(uint32_t* code_out);
 
 /* Self-check of the bounded device waits (a library diagnostic; the pages have no counterpart).

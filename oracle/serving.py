@@ -168,3 +168,62 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, scale, softcap=0.0
             mass[b, h] = p @ np.abs(v) / p.sum()
             lse[b, h] = m + math.log(p.sum())
     return out, lse, mass, reach
+
+
+def prompt_attention(q, k_cache, v_cache, page_table, cu_tokens, kv_lens, scale, causal=True, softcap=0.0, slopes=None,
+                     window=0, kv_starts=None):
+    """q [T, Hq, 128], caches [pages, Hkv, P, 128] (fp64) -> out, lse (NaN in rows outside the sequences) and, per
+    row, the bound's terms: mass = sum_j p_j |v_j|, reach = |scale| * max_j sum_c |q_c k_jc| and the number of
+    visible keys."""
+    T, hq, D = q.shape
+    n_pages, hkv, P, _ = k_cache.shape
+    group = hq // hkv
+    out, lse = np.full((T, hq, D), np.nan), np.full((T, hq), np.nan)
+    mass, reach, count = np.zeros((T, hq, D)), np.zeros((T, hq)), np.zeros((T, hq))
+    for b in range(len(kv_lens)):
+        t0, t1 = int(cu_tokens[b]), int(cu_tokens[b + 1])
+        n, L = t1 - t0, min(max(int(kv_lens[b]), 0), page_table.shape[1] * P)
+        if n == 0:
+            continue
+        out[t0:t1], lse[t0:t1] = 0.0, -np.inf
+        start = max(int(kv_starts[b]), 0) if kv_starts is not None else 0
+        pos = L - n + np.arange(n)
+        lo = np.full(n, start)
+        if window:
+            lo = np.maximum(lo, pos + 1 - window)
+        hi = np.minimum(pos + 1, L) if causal else np.full(n, L)
+        some = hi > lo
+        if not some.any():
+            continue
+        first, last = int(lo[some].min()), int(hi[some].max())
+        j = np.arange(first, last)
+        seen = (j >= lo[:, None]) & (j < hi[:, None])
+        pages = page_table[b, j // P]
+        known = (pages >= 0) & (pages < n_pages)
+        pages = np.where(known, pages, 0)
+        for h in range(hq):
+            k = np.where(known[:, None], k_cache[pages, h // group, j % P], 0.0)
+            v = np.where(known[:, None], v_cache[pages, h // group, j % P], 0.0)
+            x = q[t0:t1, h]
+            with np.errstate(invalid="ignore"):
+                s = scale * (x @ k.T)
+                reach[t0:t1, h] = np.where(seen, abs(scale) * (np.abs(x) @ np.abs(k).T), 0.0).max(1)
+                if softcap > 0:
+                    s = softcap * np.tanh(s / softcap)
+                if slopes is not None:
+                    s = s + slopes[h] * (j - pos[:, None])
+                s = np.where(seen, s, -np.inf)
+                m = s.max(1)
+                p = np.where(seen, np.exp(s - np.where(np.isneginf(m), 0.0, m)[:, None]), 0.0)
+            z = p.sum(1)
+            row = z > 0
+            w = np.where(row, z, 1.0)[:, None]
+            # a value that a row does not see has no part in it, whatever it holds
+            clean = np.where(np.isfinite(v), v, 0.0)
+            out[t0:t1, h] = np.where(row[:, None], p @ clean / w, 0.0)
+            odd = (~np.isfinite(v)).astype(float)
+            out[t0:t1, h] = np.where(seen.astype(float) @ odd > 0, np.nan, out[t0:t1, h])
+            mass[t0:t1, h] = p @ np.abs(clean) / w
+            lse[t0:t1, h] = np.where(row, np.where(np.isneginf(m), 0.0, m) + np.log(w[:, 0]), -np.inf)
+            count[t0:t1, h] = seen.sum(1)
+    return out, lse, mass, reach, count
