@@ -109,6 +109,14 @@ _SIGNATURES = {
     "kvarn_prompt_attention": (_i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _i64, _i64,
                                       _i64, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _f32, _f32, _vp, _vp, _sz, _vp, _vp,
                                       _vp]),
+    "kvarn_prefix_attention_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "kvarn_prefix_attention": (_i32, [_i32, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _i64, _i64,
+                                      _i64, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _f32, _f32, _vp, _sz, _vp, _vp, _vp]),
+    "kvarn_quantize_kv": (_i32, [_i32, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _vp,
+                                 _vp, _vp]),
+    "kvarn_paged_attention_q8": (_i32, [_i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i32, _i64,
+                                        _i64, _i64, _vp, _i32, _vp, _vp, _i32, _f32, _f32, _vp, _vp, _sz, _i32, _vp, _vp,
+                                        _vp]),
     "kvarn_status_string": (ctypes.c_char_p, [_i32]),
     "kvarn_last_error": (ctypes.c_char_p, []),
 }
@@ -421,6 +429,44 @@ def kvarn_prompt_attention(q, k_cache, v_cache, page_table, cu_tokens, kv_lens, 
     sequences are left as they were."""
     _call(_native().prompt_attention(q, k_cache, v_cache, page_table, cu_tokens, kv_lens, out, softmax_scale, workspace,
                                      causal, softcap, slopes, window, kv_starts, lse, _raw(stream)))
+
+
+def kvarn_prefix_attention_workspace_size(B: int, Hq: int, Hkv: int) -> int:
+    return int(load().kvarn_prefix_attention_workspace_size(B, Hq, Hkv))
+
+
+def kvarn_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, cu_seqs, page_table, kv_lens, out,
+                           softmax_scale: float, workspace, softcap: float = 0.0, lse=None, stream=None):
+    """Attention of one query per sequence over a prefix that groups of sequences share, read once for all of
+    them, and over each sequence's own tokens, in one paged 16-bit cache.
+
+    q [B, Hq, 128], k_cache, v_cache [n_pages, Hkv, page_size, 128]; sequences cu_seqs[g] .. cu_seqs[g + 1] - 1
+    (cu_seqs [n_groups + 1] int32) share the prefix_lens[g] tokens in the pages of row g of prefix_table
+    [n_groups, max_prefix_pages] int32; kv_lens [B] int32 own tokens, the query's among them, in the pages of
+    page_table [B, max_pages] int32; out [B, Hq, 128] of q's type; workspace:
+    kvarn_prefix_attention_workspace_size bytes; lse [B, Hq] float32 receives the log-sum-exp."""
+    _call(_native().prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, cu_seqs, page_table, kv_lens, out,
+                                     softmax_scale, workspace, softcap, lse, _raw(stream)))
+
+
+def kvarn_quantize_kv(k, v, k_cache, v_cache, k_exp, v_exp, slot_map=None, stream=None):
+    """Keys and values of new tokens into a paged 8-bit cache: x = code * 2^exponent, an E4M3 code for each
+    element and an exponent for each token and head.
+
+    k, v [T, Hkv, 128] bf16, fp16 or float32 views with contiguous channels and the same strides; k_cache, v_cache
+    [n_pages, Hkv, page_size, 128] float8_e4m3fn views of one layout; k_exp, v_exp [n_pages, Hkv, page_size] int8;
+    slot_map [T] int32 or None (slot t; -1: not written, any other slot outside the cache is reported by
+    kvarn_device_error)."""
+    _call(_native().quantize_kv(k, v, k_cache, v_cache, k_exp, v_exp, slot_map, _raw(stream)))
+
+
+def kvarn_paged_attention_q8(q, k_cache, v_cache, k_exp, v_exp, page_table, kv_lens, out, softmax_scale: float, workspace,
+                             softcap: float = 0.0, slopes=None, window: int = 0, kv_starts=None, lse=None, stream=None):
+    """kvarn_paged_attention over a paged 8-bit cache (kvarn_quantize_kv's): k_cache, v_cache float8_e4m3fn with the
+    exponents k_exp, v_exp [n_pages, Hkv, page_size] int8; q bf16 or fp16; the rest as there, with the same
+    workspace."""
+    _call(_native().paged_attention_q8(q, k_cache, v_cache, k_exp, v_exp, page_table, kv_lens, out, softmax_scale, workspace,
+                                       softcap, slopes, window, kv_starts, lse, _raw(stream)))
 
 
 def kvarn_device_error() -> int:

@@ -14,7 +14,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvarn.so")
 BINDING = os.path.join(PKG, "_serving.so")
 SOURCES = ["kvarn_api.cu", "encode.cu", "dequant.cu", "decode_attn.cu", "append.cu", "bounded_wait.cu",
-           "step_tables.cu", "rope_qkv.cu", "paged_attn.cu", "prompt_attn.cu"]
+           "step_tables.cu", "rope_qkv.cu", "paged_attn.cu", "paged_attn_q8.cu",
+           "prompt_attn.cu", "quantize_kv.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]

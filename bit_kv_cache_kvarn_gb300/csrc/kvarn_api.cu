@@ -324,7 +324,8 @@ kvarn_status kvarn_decode_attention_sink(const kvarn_config* cfg, const void* q_
 // Whether a serving-step call of this process was enqueued or captured: without one its error words are 0
 // and not read (54 us -> 91 with them and a clearing copy for every word; now 37, with them 64).
 static std::atomic<bool> g_serving_used = {false};
-static std::atomic<bool> g_prompt_used = {false};  // the same for the calls with many queries
+static std::atomic<bool> g_prompt_used = {false};  // the same for the calls with many queries,
+static std::atomic<bool> g_q8_used = {false};      // and for those with 8-bit caches
 
 kvarn_status kvarn_device_error(uint32_t* code_out) {
     if (!code_out) return fail(KVARN_ERR_INVALID_ARG, "code_out is NULL");
@@ -358,6 +359,15 @@ kvarn_status kvarn_device_error(uint32_t* code_out) {
         if (e != cudaSuccess) return cuda_fail(e, "device error word");
         e = kvarn::read_and_clear_prompt_error(&prompt);
         if (e != cudaSuccess) return cuda_fail(e, "device error word");
+        serving[2] |= page;
+    }
+    if (g_q8_used.load()) {
+        unsigned int slot = 0, page = 0;
+        e = kvarn::read_and_clear_quantize_error(&slot);
+        if (e != cudaSuccess) return cuda_fail(e, "device error word");
+        e = kvarn::read_and_clear_paged_q8_error(&page);
+        if (e != cudaSuccess) return cuda_fail(e, "device error word");
+        serving[1] |= slot;
         serving[2] |= page;
     }
     *code_out = v | (w << 1) | (x << 2) | (y << 3) | (serving[0] << 4) | (serving[1] << 5) | (serving[2] << 6) | (prompt << 7);
@@ -600,7 +610,7 @@ kvarn_status check_strides(const char* name, int64_t token, int64_t head, int mu
 }
 
 kvarn_status check_cache(const void* k, const void* v, int64_t n_pages, int Hkv, int page_size, int64_t page_stride,
-                         int64_t head_stride, int64_t token_stride) {
+                         int64_t head_stride, int64_t token_stride, int multiple = 8) {
     if (page_size < 1 || n_pages < 1 || n_pages > 0x7fffffffLL / page_size)
         return fail(KVARN_ERR_INVALID_ARG, "n_pages = %lld, page_size = %d: need positive sizes and n_pages * page_size <= 2^31 - 1",
                     (long long)n_pages, page_size);
@@ -611,9 +621,9 @@ kvarn_status check_cache(const void* k, const void* v, int64_t n_pages, int Hkv,
         int64_t stride, size;
     } ax[3] = {{page_stride, n_pages}, {head_stride, Hkv}, {token_stride, page_size}};
     for (int i = 0; i < 3; ++i)  // the stride of a single entry is never used
-        if (ax[i].size > 1 && (ax[i].stride <= 0 || ax[i].stride % 8 != 0 || ax[i].stride > (1LL << 40)))
-            return fail(KVARN_ERR_INVALID_ARG, "cache strides %lld, %lld, %lld: need positive multiples of 8 up to 2^40",
-                        (long long)page_stride, (long long)head_stride, (long long)token_stride);
+        if (ax[i].size > 1 && (ax[i].stride <= 0 || ax[i].stride % multiple != 0 || ax[i].stride > (1LL << 40)))
+            return fail(KVARN_ERR_INVALID_ARG, "cache strides %lld, %lld, %lld: need positive multiples of %d up to 2^40",
+                        (long long)page_stride, (long long)head_stride, (long long)token_stride, multiple);
     for (int i = 0; i < 2; ++i)
         for (int j = 0; j < 2 - i; ++j)
             if (ax[j].stride > ax[j + 1].stride || (ax[j].stride == ax[j + 1].stride && ax[j].size > ax[j + 1].size)) {
@@ -745,15 +755,14 @@ size_t kvarn_paged_attention_workspace_size(int B, int Hq, int Hkv) {
     return kvarn::paged_attention_workspace_bytes(B, Hq, Hkv);
 }
 
-kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, const void* q,
-                                   int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
-                                   const void* v_cache, int64_t n_pages, int page_size,
-                                   int64_t page_stride, int64_t head_stride, int64_t token_stride,
-                                   const int32_t* page_table, int max_pages, const int32_t* kv_lens,
-                                   const int32_t* kv_starts, int window, float softmax_scale,
-                                   float softcap, const float* slopes, void* workspace,
-                                   size_t workspace_bytes, kvarn_dtype out_dtype, void* out, float* lse,
-                                   kvarn_stream_t stream) {
+static kvarn_status paged_impl(bool q8, const int8_t* k_exp, const int8_t* v_exp, kvarn_dtype dtype, int B, int Hq,
+                               int Hkv, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                               const void* k_cache, const void* v_cache, int64_t n_pages, int page_size,
+                               int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                               const int32_t* page_table, int max_pages, const int32_t* kv_lens,
+                               const int32_t* kv_starts, int window, float softmax_scale, float softcap,
+                               const float* slopes, void* workspace, size_t workspace_bytes, kvarn_dtype out_dtype,
+                               void* out, float* lse, kvarn_stream_t stream) {
     KV_TRY(check_paged_shape(B, Hq, Hkv));
     if (!is_16bit(dtype)) return fail(KVARN_ERR_INVALID_ARG, "dtype = %d; expected bf16 or fp16", (int)dtype);
     if (out_dtype != KVARN_DTYPE_FP32 && out_dtype != dtype)
@@ -768,7 +777,11 @@ kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, co
     if (B == 0) return ok();
     KV_TRY(check_ptr(q, 16, "q"));
     KV_TRY(check_strides("q", q_token_stride, q_head_stride, 8));
-    KV_TRY(check_cache(k_cache, v_cache, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
+    KV_TRY(check_cache(k_cache, v_cache, n_pages, Hkv, page_size, page_stride, head_stride, token_stride, q8 ? 16 : 8));
+    if (q8) {
+        KV_TRY(check_ptr(k_exp, 16, "k_exp"));
+        KV_TRY(check_ptr(v_exp, 16, "v_exp"));
+    }
     KV_TRY(check_ptr(page_table, 4, "page_table"));
     KV_TRY(check_ptr(kv_lens, 4, "kv_lens"));
     if (kv_starts) KV_TRY(check_ptr(kv_starts, 4, "kv_starts"));
@@ -799,6 +812,8 @@ kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, co
     a.page_stride = page_stride;
     a.head_stride = head_stride;
     a.token_stride = token_stride;
+    a.k_exp = k_exp;
+    a.v_exp = v_exp;
     a.page_table = page_table;
     a.kv_lens = kv_lens;
     a.kv_starts = kv_starts;
@@ -807,8 +822,84 @@ kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, co
     a.out = out;
     a.lse = lse;
     g_serving_used.store(true);
-    cudaError_t e = kvarn::launch_paged_attention(a, (int)dtype, (cudaStream_t)stream);
+    if (q8) g_q8_used.store(true);
+    cudaError_t e = q8 ? kvarn::launch_paged_attention_q8(a, (int)dtype, (cudaStream_t)stream)
+                       : kvarn::launch_paged_attention(a, (int)dtype, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+    return ok();
+}
+
+kvarn_status kvarn_paged_attention(kvarn_dtype dtype, int B, int Hq, int Hkv, const void* q, int64_t q_token_stride,
+                                   int64_t q_head_stride, const void* k_cache, const void* v_cache, int64_t n_pages,
+                                   int page_size, int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                   const int32_t* page_table, int max_pages, const int32_t* kv_lens,
+                                   const int32_t* kv_starts, int window, float softmax_scale, float softcap,
+                                   const float* slopes, void* workspace, size_t workspace_bytes, kvarn_dtype out_dtype,
+                                   void* out, float* lse, kvarn_stream_t stream) {
+    return paged_impl(false, nullptr, nullptr, dtype, B, Hq, Hkv, q, q_token_stride, q_head_stride, k_cache, v_cache,
+                      n_pages, page_size, page_stride, head_stride, token_stride, page_table, max_pages, kv_lens,
+                      kv_starts, window, softmax_scale, softcap, slopes, workspace, workspace_bytes, out_dtype, out,
+                      lse, stream);
+}
+
+kvarn_status kvarn_paged_attention_q8(kvarn_dtype dtype, int B, int Hq, int Hkv, const void* q, int64_t q_token_stride,
+                                      int64_t q_head_stride, const void* k_cache, const void* v_cache,
+                                      const int8_t* k_exp, const int8_t* v_exp, int64_t n_pages, int page_size,
+                                      int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                      const int32_t* page_table, int max_pages, const int32_t* kv_lens,
+                                      const int32_t* kv_starts, int window, float softmax_scale, float softcap,
+                                      const float* slopes, void* workspace, size_t workspace_bytes,
+                                      kvarn_dtype out_dtype, void* out, float* lse, kvarn_stream_t stream) {
+    return paged_impl(true, k_exp, v_exp, dtype, B, Hq, Hkv, q, q_token_stride, q_head_stride, k_cache, v_cache,
+                      n_pages, page_size, page_stride, head_stride, token_stride, page_table, max_pages, kv_lens,
+                      kv_starts, window, softmax_scale, softcap, slopes, workspace, workspace_bytes, out_dtype, out,
+                      lse, stream);
+}
+
+kvarn_status kvarn_quantize_kv(kvarn_dtype x_dtype, int n_tokens, int Hkv, const void* k, const void* v,
+                               int64_t kv_token_stride, int64_t kv_head_stride, void* k_cache, void* v_cache,
+                               int64_t n_pages, int page_size, int64_t page_stride, int64_t head_stride,
+                               int64_t token_stride, int8_t* k_exp, int8_t* v_exp, const int32_t* slot_map,
+                               kvarn_stream_t stream) {
+    if (!is_16bit(x_dtype) && x_dtype != KVARN_DTYPE_FP32)
+        return fail(KVARN_ERR_INVALID_ARG, "x_dtype = %d; expected bf16, fp16 or fp32", (int)x_dtype);
+    if (n_tokens < 0) return fail(KVARN_ERR_INVALID_ARG, "n_tokens = %d < 0", n_tokens);
+    if (Hkv < 1 || Hkv > 65535) return fail(KVARN_ERR_INVALID_ARG, "Hkv = %d outside 1..65535", Hkv);
+    if (n_tokens == 0) return ok();
+    KV_TRY(check_ptr(k, 16, "k"));
+    KV_TRY(check_ptr(v, 16, "v"));
+    KV_TRY(check_strides("k, v", kv_token_stride, kv_head_stride, x_dtype == KVARN_DTYPE_FP32 ? 4 : 8));
+    KV_TRY(check_cache(k_cache, v_cache, n_pages, Hkv, page_size, page_stride, head_stride, token_stride, 16));
+    if (k_cache == v_cache) return fail(KVARN_ERR_INVALID_ARG, "k_cache and v_cache are the same array");
+    KV_TRY(check_ptr(k_exp, 1, "k_exp"));
+    KV_TRY(check_ptr(v_exp, 1, "v_exp"));
+    if (k_exp == v_exp) return fail(KVARN_ERR_INVALID_ARG, "k_exp and v_exp are the same array");
+    if (slot_map) KV_TRY(check_ptr(slot_map, 4, "slot_map"));
+    else if (n_tokens > n_pages * page_size)
+        return fail(KVARN_ERR_INVALID_ARG, "n_tokens = %d rows without a slot_map; the cache has %lld slots", n_tokens,
+                    (long long)(n_pages * page_size));
+    if ((int64_t)n_tokens * Hkv > (1LL << 34))
+        return fail(KVARN_ERR_INVALID_ARG, "n_tokens = %d, Hkv = %d: need n_tokens * Hkv <= 2^34", n_tokens, Hkv);
+    kvarn::QuantizeArgs a = {};
+    a.n_tokens = n_tokens;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.n_slots = (int)(n_pages * page_size);
+    a.k = k;
+    a.v = v;
+    a.kv_token_stride = kv_token_stride;
+    a.kv_head_stride = kv_head_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.page_stride = page_stride;
+    a.head_stride = head_stride;
+    a.token_stride = token_stride;
+    a.k_exp = k_exp;
+    a.v_exp = v_exp;
+    a.slot_map = slot_map;
+    g_q8_used.store(true);
+    cudaError_t e = kvarn::launch_quantize_kv(a, (int)x_dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "quantize launch");
     return ok();
 }
 
@@ -823,7 +914,7 @@ static kvarn_status check_prompt_shape(int64_t T, int Hq, int Hkv) {
 
 // What kvarn_prompt_attention and kvarn_prefix_attention ask of the cache: the strides of a tiled copy.
 static kvarn_status check_tiled_cache(const void* k, const void* v, int64_t n_pages, int Hkv, int page_size, int64_t page_stride,
-                                      int64_t head_stride, int64_t token_stride) {
+                                      int64_t head_stride, int64_t token_stride, int multiple = 8) {
     if (page_size < 16 || page_size % 16 != 0)
         return fail(KVARN_ERR_INVALID_ARG, "page_size = %d; need a positive multiple of 16", page_size);
     KV_TRY(check_cache(k, v, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
@@ -906,6 +997,137 @@ kvarn_status kvarn_prompt_attention(kvarn_dtype dtype, int B, int T, int Hq, int
     g_prompt_used.store(true);
     cudaError_t e = kvarn::launch_prompt_attention(a, (int)dtype, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+    return ok();
+}
+
+namespace {
+
+// Parts of kvarn_prefix_attention's workspace, one after the other.
+struct PrefixWorkspace {
+    size_t prompt, paged, out, lse, total;  // bytes of each (out and lse twice)
+    PrefixWorkspace(int B, int Hq, int Hkv) {
+        auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+        prompt = kvarn::prompt_attention_workspace_bytes(B, Hq, Hkv);
+        paged = kvarn::paged_attention_workspace_bytes(B, Hq, Hkv);
+        out = up((size_t)B * Hq * KVARN_HEAD_DIM * sizeof(float));
+        lse = up((size_t)B * Hq * sizeof(float));
+        total = prompt + paged + 2 * (out + lse);
+    }
+};
+
+}  // namespace
+
+size_t kvarn_prefix_attention_workspace_size(int B, int Hq, int Hkv) {
+    if (B > kvarn::kMaxPromptSeqs || check_paged_shape(B, Hq, Hkv) != KVARN_OK || check_prompt_shape(B, Hq, Hkv) != KVARN_OK) return 0;
+    return PrefixWorkspace(B, Hq, Hkv).total;
+}
+
+kvarn_status kvarn_prefix_attention(kvarn_dtype dtype, int B, int n_groups, int Hq, int Hkv, const void* q,
+                                    int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+                                    const void* v_cache, int64_t n_pages, int page_size, int64_t page_stride,
+                                    int64_t head_stride, int64_t token_stride, const int32_t* prefix_table,
+                                    int max_prefix_pages, const int32_t* prefix_lens, const int32_t* cu_seqs,
+                                    const int32_t* page_table, int max_pages, const int32_t* kv_lens,
+                                    float softmax_scale, float softcap, void* workspace, size_t workspace_bytes,
+                                    void* out, float* lse, kvarn_stream_t stream) {
+    KV_TRY(check_paged_shape(B, Hq, Hkv));
+    KV_TRY(check_prompt_shape(B, Hq, Hkv));
+    if (B > kvarn::kMaxPromptSeqs) return fail(KVARN_ERR_INVALID_ARG, "B = %d outside 0..%d", B, kvarn::kMaxPromptSeqs);
+    if (n_groups < 0 || n_groups > kvarn::kMaxPromptSeqs)
+        return fail(KVARN_ERR_INVALID_ARG, "n_groups = %d outside 0..%d", n_groups, kvarn::kMaxPromptSeqs);
+    if (!is_16bit(dtype)) return fail(KVARN_ERR_INVALID_ARG, "dtype = %d; expected bf16 or fp16", (int)dtype);
+    if (!isfinite(softmax_scale)) return fail(KVARN_ERR_INVALID_ARG, "softmax_scale is not finite");
+    KV_TRY(check_softcap(softcap));
+    const struct {
+        int pages;
+        const char* name;
+    } widths[] = {{max_prefix_pages, "max_prefix_pages"}, {max_pages, "max_pages"}};
+    for (const auto& w : widths)
+        if (w.pages < 1 || (int64_t)w.pages * page_size > 0x7fffffffLL - 255)
+            return fail(KVARN_ERR_INVALID_ARG, "%s = %d: need at least 1 and %s * page_size <= 2^31 - 256", w.name, w.pages, w.name);
+    if (B == 0) return ok();
+    KV_TRY(check_ptr(q, 16, "q"));
+    KV_TRY(check_strides("q", q_token_stride, q_head_stride, 8));
+    KV_TRY(check_tiled_cache(k_cache, v_cache, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
+    KV_TRY(check_ptr(prefix_table, 4, "prefix_table"));
+    KV_TRY(check_ptr(prefix_lens, 4, "prefix_lens"));
+    KV_TRY(check_ptr(cu_seqs, 4, "cu_seqs"));
+    KV_TRY(check_ptr(page_table, 4, "page_table"));
+    KV_TRY(check_ptr(kv_lens, 4, "kv_lens"));
+    KV_TRY(check_ptr(out, 16, "out"));
+    if (lse) KV_TRY(check_ptr(lse, 4, "lse"));
+    KV_TRY(check_ptr(workspace, 16, "workspace"));
+    const PrefixWorkspace need(B, Hq, Hkv);
+    if (workspace_bytes < need.total)
+        return fail(KVARN_ERR_WORKSPACE, "workspace_bytes = %zu < required %zu", workspace_bytes, need.total);
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    kvarn::PromptArgs p = {};
+    p.B = n_groups;
+    p.T = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.page_size = page_size;
+    p.max_pages = max_prefix_pages;
+    p.max_len = max_prefix_pages * page_size;
+    p.out_dtype = KVARN_DTYPE_FP32;
+    p.n_pages = n_pages;
+    p.scale = softmax_scale;
+    p.softcap = softcap;
+    p.q = q;
+    p.q_token_stride = q_token_stride;
+    p.q_head_stride = q_head_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.page_stride = page_stride;
+    p.head_stride = head_stride;
+    p.token_stride = token_stride;
+    p.page_table = prefix_table;
+    p.cu = cu_seqs;
+    p.kv_lens = prefix_lens;
+    kvarn::PagedAttnArgs a = {};
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.max_len = max_pages * page_size;
+    a.out_dtype = KVARN_DTYPE_FP32;
+    a.n_pages = n_pages;
+    a.scale = softmax_scale;
+    a.softcap = softcap;
+    a.q = q;
+    a.q_token_stride = q_token_stride;
+    a.q_head_stride = q_head_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.page_stride = page_stride;
+    a.head_stride = head_stride;
+    a.token_stride = token_stride;
+    a.page_table = page_table;
+    a.kv_lens = kv_lens;
+    kvarn::PrefixMergeArgs m = {};
+    m.B = B;
+    m.Hq = Hq;
+    m.n_groups = n_groups;
+    m.cu = cu_seqs;
+    m.out = out;
+    m.lse = lse;
+    p.workspace = at;
+    a.workspace = at += need.prompt;
+    m.prefix_out = reinterpret_cast<float*>(at += need.paged);
+    m.prefix_lse = reinterpret_cast<float*>(at += need.out);
+    m.own_out = reinterpret_cast<float*>(at += need.lse);
+    m.own_lse = reinterpret_cast<float*>(at += need.out);
+    p.out = const_cast<float*>(m.prefix_out);
+    p.lse = const_cast<float*>(m.prefix_lse);
+    a.out = const_cast<float*>(m.own_out);
+    a.lse = const_cast<float*>(m.own_lse);
+    g_serving_used.store(true);
+    g_prompt_used.store(true);
+    cudaError_t e = n_groups > 0 ? kvarn::launch_prompt_attention(p, (int)dtype, (cudaStream_t)stream) : cudaSuccess;
+    if (e == cudaSuccess) e = kvarn::launch_paged_attention(a, (int)dtype, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = kvarn::launch_prefix_merge(m, (int)dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
     return ok();
 }
 

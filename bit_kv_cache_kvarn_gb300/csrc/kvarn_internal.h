@@ -198,6 +198,8 @@ struct PagedAttnArgs {
     const void* k_cache;
     const void* v_cache;
     int64_t page_stride, head_stride, token_stride;
+    const int8_t* k_exp;  // [n_pages][Hkv][page_size] exponents of an 8-bit cache (strides in bytes), else null
+    const int8_t* v_exp;
     const int32_t* page_table;
     const int32_t* kv_lens;
     const int32_t* kv_starts;
@@ -209,6 +211,26 @@ struct PagedAttnArgs {
 size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv);
 cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stream);
 cudaError_t read_and_clear_paged_attn_error(unsigned int* out);
+cudaError_t launch_paged_attention_q8(PagedAttnArgs a, int dtype, cudaStream_t stream);
+cudaError_t read_and_clear_paged_q8_error(unsigned int* out);
+
+// Keys and values into a paged 8-bit cache: see kvarn_quantize_kv.  Input strides in elements, cache strides in bytes.
+struct QuantizeArgs {
+    int n_tokens, Hkv, page_size, n_slots;
+    int64_t n_rows;  // set by the launcher: keys and values, a row of 128 channels each
+    int page_shift;  // set by the launcher: log2 of a page size that is a power of two, else -1
+    const void* k;
+    const void* v;
+    int64_t kv_token_stride, kv_head_stride;
+    void* k_cache;
+    void* v_cache;
+    int64_t page_stride, head_stride, token_stride;
+    int8_t* k_exp;
+    int8_t* v_exp;
+    const int32_t* slot_map;
+};
+cudaError_t launch_quantize_kv(QuantizeArgs a, int x_dtype, cudaStream_t stream);
+cudaError_t read_and_clear_quantize_error(unsigned int* out);
 
 // Attention of the new tokens of packed sequences over a paged 16-bit cache: see kvarn_prompt_attention.  Strides
 // in elements.
@@ -236,6 +258,19 @@ struct PromptArgs {
 };
 size_t prompt_attention_workspace_bytes(int64_t T, int Hq, int Hkv);
 cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream);
+
+// The two parts of kvarn_prefix_attention's rows: [B][Hq][128] and [B][Hq] each.
+struct PrefixMergeArgs {
+    int B, Hq, n_groups;
+    const int32_t* cu;
+    const float* prefix_out;
+    const float* prefix_lse;
+    const float* own_out;
+    const float* own_lse;
+    void* out;
+    float* lse;
+};
+cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, int dtype, cudaStream_t stream);
 cudaError_t read_and_clear_prompt_error(unsigned int* out);
 cudaError_t read_and_clear_prompt_page_error(unsigned int* out);
 

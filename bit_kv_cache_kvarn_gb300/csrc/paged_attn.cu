@@ -1,5 +1,5 @@
-// Attention of one new token per sequence over a paged 16-bit cache, split over the cache's length and
-// joined.
+// Attention of one new token per sequence over a paged 16-bit cache, or one of 8-bit values with an exponent for each
+// token and head, split over the cache's length and joined.
 //
 // Mathematics, per sequence and query head, over the visible keys j in [lo, L):
 //   s_j = scale q.k_j;  s_j = cap tanh(s_j / cap)  (cap > 0);  s_j += slope (j - (L - 1));
@@ -44,27 +44,33 @@
 
 namespace kvarn {
 
+namespace {
+
+#ifndef KVARN_PAGED_Q8
+#define KVARN_PAGED_Q8 0
+#endif
+constexpr bool kQ8 = KVARN_PAGED_Q8;  // which caches this unit is compiled for
+
 // Set when a page table entry lies outside the cache (its keys and values count as zeros).  Read by
 // kvarn_device_error.
 __device__ unsigned int g_paged_attn_error = 0;
-
-namespace {
 
 namespace cg = cooperative_groups;
 
 constexpr int kGroup = 16;                             // tokens per step
 constexpr int kRows = 16;                              // query heads per unit, at most
-constexpr int kHalfBytes = kGroup * kTile * 2;         // K or V of a group
-constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kMaxCtas = 160;                          // CTAs of a grid, at most
 constexpr int kMaxWarps = 12;                          // warps of a CTA, at most
 constexpr int kSmemLimit = 227 * 1024 - 2048;          // dynamic shared memory of a CTA, beside the static
 
 // Warps of a CTA and groups in a warp's ring, by the eights of query heads in a unit.
-template <int NT>
+template <int NT, bool Q8 = false>
 struct Shape {
-    static constexpr int kWarps = NT == 1 ? 12 : 8, kStages = NT == 1 ? 2 : 3;
-    static constexpr int kThreads = 32 * kWarps, kRing = kStages * kStageBytes;  // bytes of a warp
+    static constexpr int kWarps = NT == 1 ? 12 : 8, kStages = Q8 ? (NT == 1 ? 4 : 6) : NT == 1 ? 2 : 3;
+    static constexpr int kRowBytes = Q8 ? kTile : 2 * kTile;                  // a token's keys or values
+    static constexpr int kHalf = kGroup * kRowBytes;                          // keys or values of a group
+    static constexpr int kStage = 2 * kHalf + (Q8 ? 2 * kGroup : 0);          // with the 8-bit ones' exponents
+    static constexpr int kThreads = 32 * kWarps, kRing = kStages * kStage;    // bytes of a warp
 };
 constexpr float kHalfLift = 15.f;                      // fp16 probabilities are multiplied by 2^15
 constexpr int kJoinWarps = 16;
@@ -184,10 +190,10 @@ struct Cursor {
     __device__ __forceinline__ int token() const { return (s.first() + g) * kGroup; }
 };
 
-template <bool CAP>
+template <bool CAP, bool SCALED>
 __device__ __forceinline__ float score(const PagedAttnArgs& a, float dot, float slope, float dist) {
     // in the log2 domain
-    float s = dot * a.scale;
+    float s = SCALED ? dot : dot * a.scale;
     if (CAP) s = a.softcap * tanhf(s * a.inv_softcap);
     return fmaf(slope, dist, s) * kLog2e;
 }
@@ -267,16 +273,33 @@ constexpr unsigned kStarts = 2;  //   it begins in this warp's piece
 constexpr unsigned kEnds = 4;    //   it ends with this warp's piece
 constexpr unsigned kHead = 8;    // its first unit began before its piece, ended inside it, and is in its head slot
 
+// E4M3 pairs (the low or the high half of x) to fp16 pairs, exactly
+__device__ __forceinline__ uint32_t half2_of_low(uint32_t x) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
+    return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+__device__ __forceinline__ uint32_t half2_of_high(uint32_t x) { return half2_of_low(x >> 16); }
+// 2^e for e of -127..127
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float(e > -127 ? (e + 127) << 23 : 1 << 22); }
+
 // T: type of q and the cache; O: type of the output; NT: eights of query heads in a unit; CAP: scores are
 // capped.
+// Q8: the cache holds E4M3 values c and an exponent e for each token and head, x = c 2^e.  The products take c as
+// fp16, exactly, and queries as fp16 with a power of two of their own (so that a bf16 query keeps its digits over
+// 2^-39 of its largest element); keys' exponents scale the scores.  Values' exponents go into the probabilities:
+// with their own maximum m' = max(s + e), 2^(s + e - m') is at most 1 for fp16, while l keeps 2^(s - m), and the
+// factor 2^(m' - m) joins them at the end of a unit.
 // CLUSTER: a thread-block cluster takes one unit, its CTAs equal parts of it, and the parts are joined
 // through the cluster's shared memory: no second launch.
-template <typename T, typename O, int NT, bool CAP, bool CLUSTER>
-__global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
-    constexpr int kWarps = Shape<NT>::kWarps, kThreads = Shape<NT>::kThreads, kRing = Shape<NT>::kRing;
-    constexpr int kStages = Shape<NT>::kStages;
-    constexpr float kLift = std::is_same<T, __half>::value ? kHalfLift : 0.f;  // log2 of the probabilities' factor
-    constexpr int PIECES = sizeof(O) == 4 && std::is_same<T, __nv_bfloat16>::value ? 3 : 2;  // of a probability
+template <typename T, typename O, int NT, bool CAP, bool CLUSTER, bool Q8>
+__global__ void __launch_bounds__(Shape<NT, Q8>::kThreads, 1) paged_split_kernel(PagedAttnArgs a) {
+    constexpr int kWarps = Shape<NT, Q8>::kWarps, kThreads = Shape<NT, Q8>::kThreads, kRing = Shape<NT, Q8>::kRing;
+    constexpr int kStages = Shape<NT, Q8>::kStages, kStageBytes = Shape<NT, Q8>::kStage, kHalfBytes = Shape<NT, Q8>::kHalf;
+    constexpr int kRowBytes = Shape<NT, Q8>::kRowBytes;
+    using P = typename std::conditional<Q8, __half, T>::type;  // of the products
+    using C = typename std::conditional<Q8, uint8_t, T>::type;  // of the cache
+    constexpr float kLift = std::is_same<P, __half>::value ? kHalfLift : 0.f;  // log2 of the probabilities' factor
+    constexpr int PIECES = sizeof(O) == 4 && std::is_same<P, __nv_bfloat16>::value ? 3 : 2;  // of a probability
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ long long s_scan[kWarps];
     __shared__ Left s_left[kWarps];
@@ -383,13 +406,15 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
     // ---- fetching ----
     uint8_t* own = dsm + warp * kRing;
     const uint32_t ring = smem_addr(own);
-    const int c_row = lane >> 4, c_chunk = lane & 15;  // a copy instruction covers two rows
-    const int64_t c_off = c_row * a.token_stride + 8 * c_chunk;
-    const T* kbase = static_cast<const T*>(a.k_cache) + c_off;
-    const T* vbase = static_cast<const T*>(a.v_cache) + c_off;
-    uint32_t c_dst[4];  // row r of a copy: 256 r + 16 (chunk ^ (r mod 8)), r = 2 i + c_row
+    constexpr int kCopyRows = Q8 ? 4 : 2, kCopies = kGroup / kCopyRows;  // a copy instruction covers that many rows
+    const int c_row = Q8 ? lane >> 3 : lane >> 4, c_chunk = Q8 ? lane & 7 : lane & 15;
+    const int64_t c_off = c_row * a.token_stride + 16 / (int)sizeof(C) * c_chunk;
+    const C* kbase = static_cast<const C*>(a.k_cache) + c_off;
+    const C* vbase = static_cast<const C*>(a.v_cache) + c_off;
+    uint32_t c_dst[8 / kCopyRows];  // row r of a copy: kRowBytes r + 16 (chunk ^ (r mod 8)), r = kCopyRows i + c_row
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c_dst[i] = ring + (2 * i + c_row) * (kTile * 2) + ((c_chunk ^ (2 * i + c_row)) << 4);
+    for (int i = 0; i < 8 / kCopyRows; ++i)
+        c_dst[i] = ring + (kCopyRows * i + c_row) * kRowBytes + ((c_chunk ^ (kCopyRows * i + c_row)) << 4);
     Cursor in = at;  // next group to fetch: its token, its page's place in the table, and its page
     auto entry_of = [&](int b, int t) {
         return (int64_t)b * a.max_pages + (a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size);
@@ -403,30 +428,36 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
         if (fetched < len) {
             const bool bad = page < 0 || page >= a.n_pages;
             if (bad && lane == 0) atomicOr(&g_paged_attn_error, 1u);
+            const int in_page = a.page_shift >= 0 ? in_t & (a.page_size - 1) : in_t % a.page_size;
             const int64_t o = (int64_t)(bad ? 0 : page) * a.page_stride + (int64_t)(in.u / a.row_blocks) * a.head_stride +
-                              (int64_t)(a.page_shift >= 0 ? in_t & (a.page_size - 1) : in_t % a.page_size) * a.token_stride;
-            const T* ks = kbase + o;
-            const T* vs = vbase + o;
+                              (int64_t)in_page * a.token_stride;
+            const C* ks = kbase + o;
+            const C* vs = vbase + o;
             if (!bad && in_t >= in.s.lo && in_t + kGroup <= in.s.len) {
 #pragma unroll
-                for (int i = 0; i < kGroup / 2; ++i) {
-                    const uint32_t d = c_dst[i & 3] + in_stage + (i >> 2) * 8 * kTile * 2;
+                for (int i = 0; i < kCopies; ++i) {
+                    const uint32_t d = c_dst[i % (8 / kCopyRows)] + in_stage + (i / (8 / kCopyRows)) * 8 * kRowBytes;
                     cp_async16(d, ks, true);
                     cp_async16(d + kHalfBytes, vs, true);
-                    ks += 2 * a.token_stride;
-                    vs += 2 * a.token_stride;
+                    ks += kCopyRows * a.token_stride;
+                    vs += kCopyRows * a.token_stride;
                 }
             } else {  // rows that are not visible are not read but zero
 #pragma unroll 1
-                for (int i = 0; i < kGroup / 2; ++i) {
-                    const int r = 2 * i + c_row, t = in_t + r;
+                for (int i = 0; i < kCopies; ++i) {
+                    const int r = kCopyRows * i + c_row, t = in_t + r;
                     const bool read = !bad && t >= in.s.lo && t < in.s.len;
-                    const uint32_t d = ring + in_stage + r * (kTile * 2) + ((c_chunk ^ (r & 7)) << 4);
+                    const uint32_t d = ring + in_stage + r * kRowBytes + ((c_chunk ^ (r & 7)) << 4);
                     cp_async16(d, read ? ks : kbase, read);
                     cp_async16(d + kHalfBytes, read ? vs : vbase, read);
-                    ks += 2 * a.token_stride;
-                    vs += 2 * a.token_stride;
+                    ks += kCopyRows * a.token_stride;
+                    vs += kCopyRows * a.token_stride;
                 }
+            }
+            if constexpr (Q8) {  // the group's 16 exponents of keys, and of values
+                const int8_t* es = (lane == 0 ? a.k_exp : a.v_exp) +
+                                   ((int64_t)(bad ? 0 : page) * a.Hkv + in.u / a.row_blocks) * a.page_size + in_page;
+                if (lane < 2) cp_async16(ring + in_stage + 2 * kHalfBytes + lane * kGroup, es, !bad);
             }
             in_stage = in_stage + kStageBytes < kRing ? in_stage + kStageBytes : 0;
             if (++fetched < len) {
@@ -474,30 +505,57 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
         const int rows = hd.rows;
         // the unit's queries as the products' right operand, zeros past the last head
         uint32_t qf[NT][8][2];
-        float slope[NT][2];
+        float slope[NT][2], q_scale[NT][2];  // (q_scale: Q8, the factor of a head's scores)
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
             const int r = 8 * e + row0;
             const T* q = static_cast<const T*>(a.q) + (int64_t)b * a.q_token_stride +
-                         (int64_t)(hd.first + (r < rows ? r : 0)) * a.q_head_stride + col0;
+                         (int64_t)(hd.first + (r < rows ? r : 0)) * a.q_head_stride + (Q8 ? 2 * col0 : col0);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    qf[e][kk][i] = r < rows ? *reinterpret_cast<const uint32_t*>(q + 16 * kk + 8 * i) : 0u;
+                    qf[e][kk][i] = r < rows ? *reinterpret_cast<const uint32_t*>(q + 16 * kk + (Q8 ? 2 : 8) * i) : 0u;
+            if constexpr (Q8) {
+                float own_scale = 1.f;
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                    uint32_t top = 0;  // the largest magnitude's bits
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) top = max(top, max(qf[e][kk][i] & 0x7fffu, (qf[e][kk][i] >> 16) & 0x7fffu));
+#pragma unroll
+                    for (int d = 1; d < 4; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    // by 2^-lift the largest lies in [2^14, 2^15)
+                    const int lift = min(max((int)(top >> 7) - 127 - 14, -126), 126);
+                    const float down = power_of_two(-lift);
+                    own_scale = power_of_two(lift);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t x = qf[e][kk][i];
+                            const __half2 h = __floats2half2_rn(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
+                            qf[e][kk][i] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) q_scale[e][i] = a.scale * __shfl_sync(0xffffffffu, own_scale, 4 * (col0 + i));
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 slope[e][i] = a.slopes != nullptr && 8 * e + col0 + i < rows ? a.slopes[hd.first + 8 * e + col0 + i] : 0.f;
         }
         float o[NT][8][4];
         float m[NT][2], l[NT][2];
+        float mo[NT][2];  // the maximum that the output carries: m, or Q8's m'
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[e][i][c] = 0.f;
-            m[e][0] = m[e][1] = -CUDART_INF_F;
+            m[e][0] = m[e][1] = mo[e][0] = mo[e][1] = -CUDART_INF_F;
             l[e][0] = l[e][1] = 0.f;
         }
 
@@ -508,23 +566,50 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
             const uint32_t kb = ring + stage, vb = kb + kHalfBytes;
             stage = stage + kStageBytes < kRing ? stage + kStageBytes : 0;
             float s[NT][2][4] = {};  // [eight][chain]
+            int v_exp[2] = {0, 0};    // Q8: exponents of this lane's two tokens' values
+            if constexpr (Q8) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-                uint32_t f[4];
-                ldm4(f, kb + k_row * (kTile * 2) + (((2 * kk + k_sel) ^ mr) << 4));
+                for (int c2 = 0; c2 < 4; ++c2) {  // 32 channels: a lane has four neighbouring ones of each 16
+                    uint32_t f[4];
+                    ldm4(f, kb + k_row * kRowBytes + (((2 * c2 + k_sel) ^ mr) << 4));
 #pragma unroll
-                for (int e = 0; e < NT; ++e) mma(s[e][kk & 1], f, qf[e][kk][0], qf[e][kk][1], T());
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w[4] = {half2_of_low(f[2 * i]), half2_of_low(f[2 * i + 1]), half2_of_high(f[2 * i]),
+                                               half2_of_high(f[2 * i + 1])};
+#pragma unroll
+                        for (int e = 0; e < NT; ++e) mma(s[e][i], w, qf[e][2 * c2 + i][0], qf[e][2 * c2 + i][1], P());
+                    }
+                }
+                const int8_t* es = reinterpret_cast<const int8_t*>(own + (kb - ring) + 2 * kHalfBytes);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float k_scale = power_of_two(es[row0 + 8 * i]);
+                    v_exp[i] = es[kGroup + row0 + 8 * i];
+#pragma unroll
+                    for (int e = 0; e < NT; ++e)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            s[e][0][2 * i + c] = (s[e][0][2 * i + c] + s[e][1][2 * i + c]) * (k_scale * q_scale[e][c]), s[e][1][2 * i + c] = 0.f;
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    uint32_t f[4];
+                    ldm4(f, kb + k_row * kRowBytes + (((2 * kk + k_sel) ^ mr) << 4));
+#pragma unroll
+                    for (int e = 0; e < NT; ++e) mma(s[e][kk & 1], f, qf[e][kk][0], qf[e][kk][1], P());
+                }
             }
             const int t0 = (span.first() + g_begin + st) * kGroup + row0;
             const bool seen[2] = {t0 >= span.lo && t0 < span.len, t0 + 8 >= span.lo && t0 + 8 < span.len};
             const float dist = (float)(t0 - (span.len - 1));
-            float mx[NT][2];
+            float mx[NT][2], mv[NT][2];
             bool grew = false;
 #pragma unroll
             for (int e = 0; e < NT; ++e) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float x = score<CAP>(a, s[e][0][c] + s[e][1][c], slope[e][c & 1], dist + 8 * (c >> 1));
+                    const float x = score<CAP, Q8>(a, s[e][0][c] + s[e][1][c], slope[e][c & 1], dist + 8 * (c >> 1));
                     s[e][0][c] = seen[c >> 1] ? x : -CUDART_INF_F;
                 }
 #pragma unroll
@@ -533,6 +618,12 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx[e][i] = fmaxf(mx[e][i], __shfl_xor_sync(0xffffffffu, mx[e][i], d));
                     grew |= mx[e][i] > m[e][i];
+                    if constexpr (Q8) {
+                        mv[e][i] = fmaxf(fmaxf(s[e][0][i] + v_exp[0], s[e][0][i + 2] + v_exp[1]), mo[e][i]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mv[e][i] = fmaxf(mv[e][i], __shfl_xor_sync(0xffffffffu, mv[e][i], d));
+                        grew |= mv[e][i] > mo[e][i];
+                    }
                 }
             }
             if (__any_sync(0xffffffffu, grew)) {
@@ -544,6 +635,10 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
                         al[i] = mx[e][i] > m[e][i] ? exp2f(m[e][i] - mx[e][i]) : 1.f;
                         m[e][i] = mx[e][i];
                         l[e][i] *= al[i];
+                        if constexpr (Q8) {
+                            al[i] = mv[e][i] > mo[e][i] ? exp2f(mo[e][i] - mv[e][i]) : 1.f;
+                            mo[e][i] = mv[e][i];
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -556,30 +651,58 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
             for (int e = 0; e < NT; ++e) {
                 // a row whose scores are all -inf so far has no maximum to subtract
                 const float ref[2] = {m[e][0] == -CUDART_INF_F ? 0.f : m[e][0], m[e][1] == -CUDART_INF_F ? 0.f : m[e][1]};
+                const float ref_o[2] = {mo[e][0] == -CUDART_INF_F ? 0.f : mo[e][0], mo[e][1] == -CUDART_INF_F ? 0.f : mo[e][1]};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     // The lift is added to the difference: a maximum past 2^24 less 15 may be rounded to the maximum
                     // less 16, and 2^16 is no fp16 number any more.
                     float x0 = s[e][0][2 * h] - ref[0], x1 = s[e][0][2 * h + 1] - ref[1];
+                    if constexpr (Q8) {
+                        l[e][0] += exp2f(x0);
+                        l[e][1] += exp2f(x1);
+                        x0 = s[e][0][2 * h] + v_exp[h] - ref_o[0];
+                        x1 = s[e][0][2 * h + 1] + v_exp[h] - ref_o[1];
+                    }
                     if constexpr (kLift != 0.f) x0 += kLift, x1 += kLift;
                     float p0 = exp2f(x0), p1 = exp2f(x1);
-                    l[e][0] += p0;
-                    l[e][1] += p1;
+                    if constexpr (!Q8) {
+                        l[e][0] += p0;
+                        l[e][1] += p1;
+                    }
 #pragma unroll
-                    for (int i = 0; i < PIECES; ++i) p[e][i][h] = turn8(take2(p0, p1, T()));
+                    for (int i = 0; i < PIECES; ++i) p[e][i][h] = turn8(take2(p0, p1, P()));
                 }
             }
-#pragma unroll
-            for (int cc = 0; cc < 8; ++cc) {
-                uint32_t f[4];
-                ldm4t(f, vb + v_row * (kTile * 2) + (((2 * cc + v_sel) ^ mr) << 4));
+            auto add = [&](int cc, const uint32_t(&f)[4]) {
 #pragma unroll
                 for (int e = 0; e < NT; ++e) {
                     float d[4] = {};
 #pragma unroll
-                    for (int i = PIECES - 1; i >= 0; --i) mma(d, f, p[e][i][0], p[e][i][1], T());  // the small pieces first
+                    for (int i = PIECES - 1; i >= 0; --i) mma(d, f, p[e][i][0], p[e][i][1], P());  // the small pieces first
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[e][cc][c] += d[c];
+                }
+            };
+            if constexpr (Q8) {
+#pragma unroll
+                for (int c2 = 0; c2 < 4; ++c2) {
+                    // turned as pairs of channels: a lane has channels 2 j and 2 j + 1 of two tokens, j = lane / 4, and
+                    // takes the even channels as the product's rows 0..7 and the odd ones as 8..15
+                    uint32_t g[4];
+                    ldm4t(g, vb + k_row * kRowBytes + (((2 * c2 + k_sel) ^ mr) << 4));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t x = __byte_perm(g[2 * i], 0, 0x3120), y = __byte_perm(g[2 * i + 1], 0, 0x3120);
+                        const uint32_t f[4] = {half2_of_low(x), half2_of_high(x), half2_of_low(y), half2_of_high(y)};
+                        add(2 * c2 + i, f);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int cc = 0; cc < 8; ++cc) {
+                    uint32_t f[4];
+                    ldm4t(f, vb + v_row * kRowBytes + (((2 * cc + v_sel) ^ mr) << 4));
+                    add(cc, f);
                 }
             }
             __syncwarp();  // the stage is read before a later step fetches into it
@@ -594,10 +717,16 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
         // the join at the CTA's end; one that ended before goes to the workspace
         if (!whole && last) cp_async_wait<0>();
         float* slot = last ? reinterpret_cast<float*>(own) : warp == 0 ? ws.cta_slot(blockIdx.x, 0) : head_slot(warp);
+        const int ch0 = Q8 ? 2 * row0 : row0, ch1 = Q8 ? 1 : 8;  // channels of a lane in each 16: the first, and how far the second
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                if constexpr (Q8) {  // from the output's maximum and lift to the sum's
+                    const float f = mo[e][i] == -CUDART_INF_F ? 0.f : exp2f(mo[e][i] - m[e][i] - kLift);
+#pragma unroll
+                    for (int cc = 0; cc < 8; ++cc) o[e][cc][i] *= f, o[e][cc][i + 2] *= f;
+                }
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[e][i] += __shfl_xor_sync(0xffffffffu, l[e][i], d);
                 const int r = 8 * e + col0 + i;
@@ -605,18 +734,18 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1) paged_split_kernel(Pag
                 if (whole) {
                     const int64_t row = (int64_t)b * a.Hq + hd.first + r;
                     const float inv = l[e][i] != 0.f ? 1.f / l[e][i] : 0.f;
-                    O* out = static_cast<O*>(a.out) + row * kTile + row0;
+                    O* out = static_cast<O*>(a.out) + row * kTile + ch0;
 #pragma unroll
                     for (int cc = 0; cc < 8; ++cc) {
                         store1(out + 16 * cc, o[e][cc][i] * inv);
-                        store1(out + 16 * cc + 8, o[e][cc][i + 2] * inv);
+                        store1(out + 16 * cc + ch1, o[e][cc][i + 2] * inv);
                     }
                     if (a.lse != nullptr && row0 == 0) a.lse[row] = lse_of(a, m[e][i], l[e][i]);
                 } else {
 #pragma unroll
                     for (int cc = 0; cc < 8; ++cc) {
-                        slot[r * kTile + 16 * cc + row0] = o[e][cc][i];
-                        slot[r * kTile + 16 * cc + row0 + 8] = o[e][cc][i + 2];
+                        slot[r * kTile + 16 * cc + ch0] = o[e][cc][i];
+                        slot[r * kTile + 16 * cc + ch0 + ch1] = o[e][cc][i + 2];
                     }
                     if (row0 == 0) {
                         slot[a.rows * kTile + r] = m[e][i];
@@ -756,16 +885,16 @@ struct Kernels {
     void (*join)(PagedAttnArgs);
     int ring;  // bytes of a warp's
 };
-template <typename T, typename O, int NT>
+template <typename T, typename O, int NT, bool Q8>
 Kernels pick(const PagedAttnArgs& a, bool cluster) {
     const bool cap = a.softcap > 0.f;
-    return {cluster ? (cap ? paged_split_kernel<T, O, NT, true, true> : paged_split_kernel<T, O, NT, false, true>)
-                    : (cap ? paged_split_kernel<T, O, NT, true, false> : paged_split_kernel<T, O, NT, false, false>),
-            paged_join_kernel<O>, Shape<NT>::kRing};
+    return {cluster ? (cap ? paged_split_kernel<T, O, NT, true, true, Q8> : paged_split_kernel<T, O, NT, false, true, Q8>)
+                    : (cap ? paged_split_kernel<T, O, NT, true, false, Q8> : paged_split_kernel<T, O, NT, false, false, Q8>),
+            paged_join_kernel<O>, Shape<NT, Q8>::kRing};
 }
 template <typename T, typename O>
 Kernels pick(const PagedAttnArgs& a, bool cluster) {
-    return a.rows <= 8 ? pick<T, O, 1>(a, cluster) : pick<T, O, 2>(a, cluster);
+    return a.rows <= 8 ? pick<T, O, 1, kQ8>(a, cluster) : pick<T, O, 2, kQ8>(a, cluster);
 }
 
 // How many clusters of n = 1, 2, 4, 8, 16 of the split's CTAs (one to an SM) run at once; queried once per
@@ -775,8 +904,8 @@ cudaError_t cluster_room(int log2n, int dev, int sms, int* room) {
     const bool cached = dev >= 0 && dev < kMaxCachedDevices;
     *room = log2n == 0 ? sms : cached ? known[dev][log2n].load(std::memory_order_relaxed) : 0;
     if (*room != 0) return cudaSuccess;
-    const auto kern = paged_split_kernel<__nv_bfloat16, float, 1, false, true>;
-    const int smem = Shape<1>::kWarps * Shape<1>::kRing;
+    const auto kern = paged_split_kernel<__nv_bfloat16, float, 1, false, true, kQ8>;
+    const int smem = Shape<1, kQ8>::kWarps * Shape<1, kQ8>::kRing;
     cudaError_t e = set_smem_limit_once(kern, smem, false, dev);
     if (e == cudaSuccess) e = allow_large_cluster_once(kern, dev);
     if (e != cudaSuccess) return e;
@@ -828,6 +957,7 @@ int grid_ctas(int64_t max_groups, int warps, int sms) {
 
 }  // namespace
 
+#if !KVARN_PAGED_Q8
 size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv) {
     (void)B;
     const int group = Hq / Hkv, rows = group < kRows ? group : kRows;
@@ -839,6 +969,11 @@ size_t paged_attention_workspace_bytes(int B, int Hq, int Hkv) {
 cudaError_t read_and_clear_paged_attn_error(unsigned int* out) { return read_and_clear_word(&g_paged_attn_error, out); }
 
 cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stream) {
+#else
+cudaError_t read_and_clear_paged_q8_error(unsigned int* out) { return read_and_clear_word(&g_paged_attn_error, out); }
+
+cudaError_t launch_paged_attention_q8(PagedAttnArgs a, int dtype, cudaStream_t stream) {
+#endif
     int dev = 0, sms = 0;
     cudaError_t e = current_device(&dev, &sms);
     if (e != cudaSuccess) return e;
@@ -846,7 +981,7 @@ cudaError_t launch_paged_attention(PagedAttnArgs a, int dtype, cudaStream_t stre
     a.rows = a.group < kRows ? a.group : kRows;
     a.row_blocks = (a.group + kRows - 1) / kRows;
     a.units = a.Hkv * a.row_blocks;
-    a.lift = dtype == KVARN_DTYPE_FP16 ? kHalfLift : 0.f;
+    a.lift = dtype == KVARN_DTYPE_FP16 && !kQ8 ? kHalfLift : 0.f;
     a.inv_softcap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     const bool wide = a.out_dtype == KVARN_DTYPE_FP32;

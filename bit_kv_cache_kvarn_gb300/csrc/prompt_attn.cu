@@ -802,6 +802,27 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a)
     }
 }
 
+// Two parts of every row, each with its log-sum-exp, into one: the prefix's where the row has one.
+template <typename T>
+__global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixMergeArgs a) {
+    const int lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= (int64_t)a.B * a.Hq) return;
+    const int b = (int)(row / a.Hq);
+    const bool some = b >= a.cu[0] && b < a.cu[a.n_groups];  // rows outside the groups have no prefix
+    const float x = some ? a.prefix_lse[row] : -CUDART_INF_F, y = a.own_lse[row], top = fmaxf(x, y);
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    const float wx = exp2f((x - ref) * kLog2e), wy = exp2f((y - ref) * kLog2e), sum = wx + wy;
+    const float4 p = some ? *reinterpret_cast<const float4*>(a.prefix_out + row * kTile + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 o = *reinterpret_cast<const float4*>(a.own_out + row * kTile + 4 * lane);
+    const float inv = sum != 0.f ? 1.f / sum : 0.f, fx = wx * inv, fy = wy * inv;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * kTile + 4 * lane) =
+        make_uint2(pack2(fmaf(fx, p.x, fy * o.x), fmaf(fx, p.y, fy * o.y), T()), pack2(fmaf(fx, p.z, fy * o.z), fmaf(fx, p.w, fy * o.w), T()));
+    if (a.lse != nullptr && lane == 0) a.lse[row] = sum != 0.f ? top + log2f(sum) * 0.69314718055994531f : -CUDART_INF_F;
+}
+
 struct Kernels {
     void (*split)(CUtensorMap, CUtensorMap, PromptArgs);
     void (*join)(PromptArgs);
@@ -886,6 +907,12 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     e = launch_pdl(k.split, dim3(ctas), dim3(kThreads), kSmem, stream, k_map, v_map, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(k.join, dim3(ctas, (a.slot_rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, stream, a);
+}
+
+cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, int dtype, cudaStream_t stream) {
+    const int64_t ctas = ((int64_t)a.B * a.Hq + 7) / 8;
+    return launch_pdl(dtype == KVARN_DTYPE_FP16 ? prefix_merge_kernel<__half> : prefix_merge_kernel<__nv_bfloat16>,
+                      dim3((unsigned)ctas), dim3(256), 0, stream, a);
 }
 
 }  // namespace kvarn

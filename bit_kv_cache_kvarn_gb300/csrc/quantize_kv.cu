@@ -1,0 +1,113 @@
+// Keys and values of new tokens into a paged 8-bit cache: E4M3 values times a power of two for each token and head.
+//
+// Mathematics, per token and head, over the row's 128 channels: e = ceil(log2(max |x| / 448)) (448: E4M3's largest),
+// at least -127, and code = round(x / 2^e) to E4M3, to nearest, ties to even.  x / 2^e is exact, so a code is off by
+// that one rounding, and the same inputs give the same codes everywhere.
+//
+// What bounds it: 256 bytes read and 129 written per row (16-bit inputs): HBM.  Half a warp takes a row, 16 bytes a
+// lane, and has kAhead rows in flight.
+#include <type_traits>
+
+#include "kvarn_common.cuh"
+#include "kvarn_internal.h"
+
+namespace kvarn {
+
+// Set when a slot lies outside the cache.  Read by kvarn_device_error.
+__device__ unsigned int g_quantize_error = 0;
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kAhead = 4;  // rows that half a warp loads at once
+
+// eight neighbouring channels
+__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16* p) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+__device__ __forceinline__ void load8(float (&x)[8], const __half* p) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void load8(float (&x)[8], const float* p) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+    }
+}
+
+// Rows in the order (token, keys or values, head).
+template <typename T>
+__global__ void __launch_bounds__(32 * kWarps) quantize_kv_kernel(QuantizeArgs a) {
+    const int lane = threadIdx.x & 31, part = lane & 15;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (2 * kAhead) + (lane >> 4);
+    float x[kAhead][8];
+    int slot[kAhead], kind[kAhead], head[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int64_t row = first + 2 * i;
+        slot[i] = -1;
+        if (row < a.n_rows) {
+            const unsigned token = (unsigned)(row / (unsigned)(2 * a.Hkv)), r = (unsigned)(row - (int64_t)token * (2 * a.Hkv));
+            kind[i] = r >= (unsigned)a.Hkv;
+            head[i] = (int)r - (kind[i] ? a.Hkv : 0);
+            slot[i] = a.slot_map != nullptr ? __ldg(a.slot_map + token) : (int)token;
+            load8(x[i], static_cast<const T*>(kind[i] ? a.v : a.k) + (int64_t)token * a.kv_token_stride + (int64_t)head[i] * a.kv_head_stride + 8 * part);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(x[i][c]));
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if (slot[i] < 0 || slot[i] >= a.n_slots) {
+            if (slot[i] != -1 && part == 0) atomicOr(&g_quantize_error, 1u);
+            continue;
+        }
+        // top = 1.f 2^E, 448 = 1.75 2^8
+        const uint32_t bits = __float_as_uint(top);
+        const int e = max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -127);
+        const float scale = __uint_as_float((uint32_t)(127 - e) << 23);
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[i][4 * h] * scale, x[i][4 * h + 1] * scale), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[i][4 * h + 2] * scale, x[i][4 * h + 3] * scale), __NV_SATFINITE, __NV_E4M3);
+            w[h] = lo | hi << 16;
+        }
+        const int page = a.page_shift >= 0 ? slot[i] >> a.page_shift : slot[i] / a.page_size, in_page = slot[i] - page * a.page_size;
+        uint8_t* dst = static_cast<uint8_t*>(kind[i] ? a.v_cache : a.k_cache) + (int64_t)page * a.page_stride +
+                       (int64_t)head[i] * a.head_stride + (int64_t)in_page * a.token_stride;
+        *reinterpret_cast<uint2*>(dst + 8 * part) = make_uint2(w[0], w[1]);
+        if (part == 0) (kind[i] ? a.v_exp : a.k_exp)[((int64_t)page * a.Hkv + head[i]) * a.page_size + in_page] = (int8_t)e;
+    }
+}
+
+}  // namespace
+
+cudaError_t read_and_clear_quantize_error(unsigned int* out) { return read_and_clear_word(&g_quantize_error, out); }
+
+cudaError_t launch_quantize_kv(QuantizeArgs a, int x_dtype, cudaStream_t stream) {
+    a.n_rows = (int64_t)a.n_tokens * 2 * a.Hkv;
+    a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
+    const int64_t ctas = (a.n_rows + kWarps * 2 * kAhead - 1) / (kWarps * 2 * kAhead);
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const auto kern = x_dtype == KVARN_DTYPE_FP32 ? quantize_kv_kernel<float>
+                      : x_dtype == KVARN_DTYPE_FP16 ? quantize_kv_kernel<__half> : quantize_kv_kernel<__nv_bfloat16>;
+    return launch_pdl(kern, dim3((unsigned)ctas), dim3(32 * kWarps), 0, stream, a);
+}
+
+}  // namespace kvarn

@@ -158,6 +158,11 @@ Cache cache(const Checker& c, const at::Tensor& k, const at::Tensor& v, at::Scal
     return r;
 }
 
+// the exponents beside an 8-bit cache
+int8_t* exponents(const Checker& c, PyObject* o, const Cache& kv, const char* name) {
+    return c.array<int8_t>(*tensor(o, name), at::kChar, {kv.n_pages, kv.heads, kv.page_size}, name);
+}
+
 kvarn_status step_tables(PyObject* const* x) {
     const Checker c = {(int)c10::cuda::current_device()};
     const at::Tensor& table = *tensor(x[3], "page_table");
@@ -253,6 +258,73 @@ kvarn_status paged_attention(PyObject* const* x) {
         as_stream(x[13], c.dev));
 }
 
+kvarn_status prefix_attention(PyObject* const* x) {
+    const Checker c = {(int)c10::cuda::current_device()};
+    const at::Tensor& q = *tensor(x[0], "q");
+    if (q.dim() != 3) bad("q must be [B, Hq, 128]");
+    const int64_t B = q.size(0), hq = q.size(1);
+    const at::ScalarType dt = q.scalar_type();
+    const Rows rq = rows(c, q, dt, B, hq, "q");
+    const Cache kv = cache(c, *tensor(x[1], "k_cache"), *tensor(x[2], "v_cache"), dt);
+    const at::Tensor& prefix = *tensor(x[3], "prefix_table");
+    const at::Tensor& table = *tensor(x[6], "page_table");
+    if (prefix.dim() != 2) bad("prefix_table must be [n_groups, max_prefix_pages]");
+    if (table.dim() != 2) bad("page_table must be [B, max_pages]");
+    const int64_t groups = prefix.size(0), prefix_width = prefix.size(1), width = table.size(1);
+    const at::Tensor& ws = *tensor(x[10], "workspace");
+    c.device(ws, "workspace");
+    if (!ws.is_contiguous()) bad("workspace must be contiguous");
+    return kvarn_prefix_attention(
+        as_dtype(dt, "q"), narrow(B, "B"), narrow(groups, "n_groups"), narrow(hq, "Hq"), narrow(kv.heads, "Hkv"), rq.p, rq.token,
+        rq.head, kv.k, kv.v, kv.n_pages, kv.page_size, kv.page_stride, kv.head_stride, kv.token_stride,
+        c.ints(x[3], {groups, prefix_width}, "prefix_table"), narrow(prefix_width, "max_prefix_pages"),
+        c.ints(x[4], {groups}, "prefix_lens"), c.ints(x[5], {groups + 1}, "cu_seqs"), c.ints(x[6], {B, width}, "page_table"),
+        narrow(width, "max_pages"), c.ints(x[7], {B}, "kv_lens"), as_float(x[9]), as_float_or_zero(x[11]), ws.data_ptr(),
+        (size_t)ws.nbytes(), c.array<void>(*tensor(x[8], "out"), dt, {B, hq, KVARN_HEAD_DIM}, "out"),
+        c.floats_or_null(x[12], {B, hq}, "lse"), as_stream(x[13], c.dev));
+}
+
+kvarn_status quantize_kv(PyObject* const* x) {
+    const Checker c = {(int)c10::cuda::current_device()};
+    const at::Tensor& k = *tensor(x[0], "k");
+    if (k.dim() != 3) bad("k must be [T, Hkv, 128]");
+    const int64_t T = k.size(0), hkv = k.size(1);
+    const at::ScalarType dt = k.scalar_type();
+    const Rows rk = rows(c, k, dt, T, hkv, "k"), rv = rows(c, *tensor(x[1], "v"), dt, T, hkv, "v");
+    if (rk.token != rv.token || rk.head != rv.head) bad("k and v must have the same strides");
+    const Cache kv = cache(c, *tensor(x[2], "k_cache"), *tensor(x[3], "v_cache"), at::kFloat8_e4m3fn);
+    if (kv.heads != hkv) bad("the cache has " + std::to_string(kv.heads) + " heads, k has " + std::to_string(hkv));
+    return kvarn_quantize_kv(as_dtype(dt, "k, v"), narrow(T, "T"), narrow(hkv, "Hkv"), rk.p, rv.p, rk.token, rk.head, kv.k, kv.v,
+                             kv.n_pages, kv.page_size, kv.page_stride, kv.head_stride, kv.token_stride,
+                             exponents(c, x[4], kv, "k_exp"), exponents(c, x[5], kv, "v_exp"),
+                             c.ints_or_null(x[6], {T}, "slot_map"), as_stream(x[7], c.dev));
+}
+
+kvarn_status paged_attention_q8(PyObject* const* x) {
+    const Checker c = {(int)c10::cuda::current_device()};
+    const at::Tensor& q = *tensor(x[0], "q");
+    if (q.dim() != 3) bad("q must be [B, Hq, 128]");
+    const int64_t B = q.size(0), hq = q.size(1);
+    const at::ScalarType dt = q.scalar_type();
+    const Rows rq = rows(c, q, dt, B, hq, "q");
+    const Cache kv = cache(c, *tensor(x[1], "k_cache"), *tensor(x[2], "v_cache"), at::kFloat8_e4m3fn);
+    const at::Tensor& table = *tensor(x[5], "page_table");
+    if (table.dim() != 2) bad("page_table must be [B, max_pages]");
+    const int64_t width = table.size(1);
+    const at::Tensor& out = *tensor(x[7], "out");
+    const at::Tensor& ws = *tensor(x[9], "workspace");
+    c.device(ws, "workspace");
+    if (!ws.is_contiguous()) bad("workspace must be contiguous");
+    return kvarn_paged_attention_q8(
+        as_dtype(dt, "q"), narrow(B, "B"), narrow(hq, "Hq"), narrow(kv.heads, "Hkv"), rq.p, rq.token, rq.head, kv.k, kv.v,
+        exponents(c, x[3], kv, "k_exp"), exponents(c, x[4], kv, "v_exp"), kv.n_pages, kv.page_size, kv.page_stride,
+        kv.head_stride, kv.token_stride, c.ints(x[5], {B, width}, "page_table"), narrow(width, "max_pages"),
+        c.ints(x[6], {B}, "kv_lens"), c.ints_or_null(x[13], {B}, "kv_starts"), as_int(x[12], "window"), as_float(x[8]),
+        as_float_or_zero(x[10]), c.floats_or_null(x[11], {hq}, "slopes"), ws.data_ptr(), (size_t)ws.nbytes(),
+        as_dtype(out.scalar_type(), "out"), c.array<void>(out, out.scalar_type(), {B, hq, KVARN_HEAD_DIM}, "out"),
+        c.floats_or_null(x[14], {B, hq}, "lse"), as_stream(x[15], c.dev));
+}
+
 kvarn_status prompt_attention(PyObject* const* x) {
     const Checker c = {(int)c10::cuda::current_device()};
     const at::Tensor& q = *tensor(x[0], "q");
@@ -302,7 +374,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<step_tables, 16>("step_tables"), method<rope_qkv, 15>("rope_qkv"),
                          method<paged_attention, 14>("paged_attention"),
-                         method<prompt_attention, 16>("prompt_attention"), {nullptr, nullptr, 0, nullptr}};
+                         method<prompt_attention, 16>("prompt_attention"), method<prefix_attention, 14>("prefix_attention"),
+                         method<quantize_kv, 8>("quantize_kv"), method<paged_attention_q8, 16>("paged_attention_q8"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

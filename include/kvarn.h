@@ -482,6 +482,71 @@ kvarn_status kvarn_prompt_attention(kvarn_dtype dtype, int B, int T, int Hq, int
                                     float softcap, const float* slopes, void* workspace, size_t workspace_bytes,
                                     void* out, float* lse, kvarn_stream_t stream);
 
+/* Bytes of device workspace kvarn_prefix_attention needs for these heads and up to B sequences; 0 for an invalid
+ * shape. */
+size_t kvarn_prefix_attention_workspace_size(int B, int Hq, int Hkv);
+
+/* Attention of one query per sequence over a prefix that several sequences share and over the sequence's own
+ * tokens, both in one paged 16-bit cache: a system prompt, several answers to one question, a beam's common part.
+ * Sequences cu_seqs[g] .. cu_seqs[g + 1] - 1 share the prefix g of prefix_lens[g] tokens in the pages of row g of
+ * prefix_table, which is read once for all of them (and once for each 256 query heads of a kv head); sequence b's
+ * own kv_lens[b] tokens, the query's among them, lie in the pages of row b of page_table.  The result is
+ * kvarn_paged_attention's over the prefix's tokens followed by the sequence's own.
+ *   cu_seqs     : [n_groups + 1] int32, non-decreasing, clamped to 0..B; sequences outside the groups have no
+ *                 prefix.  prefix_lens : [n_groups] int32, kv_lens : [B] int32, clamped to what their tables
+ *                 hold; 0 is allowed in both.
+ *   prefix_table: [n_groups][max_prefix_pages], page_table : [B][max_pages] int32, as for kvarn_prompt_attention.
+ *   dtype, q, cache, softcap, out, lse : as for kvarn_prompt_attention, with T = B.
+ *   workspace   : >= kvarn_prefix_attention_workspace_size(B, Hq, Hkv) bytes, 16-byte aligned; needs no clearing.
+ *                 Calls that may overlap on the GPU need one each.
+ * Sequences without a visible key get zeros and lse -inf.  0 <= B, n_groups <= 16384; B = 0 is a no-op. */
+kvarn_status kvarn_prefix_attention(kvarn_dtype dtype, int B, int n_groups, int Hq, int Hkv, const void* q,
+                                    int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+                                    const void* v_cache, int64_t n_pages, int page_size, int64_t page_stride,
+                                    int64_t head_stride, int64_t token_stride, const int32_t* prefix_table,
+                                    int max_prefix_pages, const int32_t* prefix_lens, const int32_t* cu_seqs,
+                                    const int32_t* page_table, int max_pages, const int32_t* kv_lens,
+                                    float softmax_scale, float softcap, void* workspace, size_t workspace_bytes,
+                                    void* out, float* lse, kvarn_stream_t stream);
+
+/* ---- a paged 8-bit cache -------------------------------------------------------------------------
+ *
+ * Between the 16-bit pages and the packed tiles: each token's 128 channels of a head are E4M3 values c and one
+ * exponent e, x = c 2^e: 129 bytes instead of 256, written token by token, without a block to be completed.
+ * e = ceil(log2(max |x| / 448)), at least -127 (-127 for a row of zeros); x / 2^e is exact, so c is x rounded once
+ * (to nearest, ties to even): off by at most 2^-4 of x, or 2^-10 of 2^e for the smallest.  An infinity takes
+ * 448 * 2^120 (and the row's e is 120); NaN stays NaN and does not count for e.
+ * The values lie in two arrays like those of a paged 16-bit cache, of one byte per element: strides in bytes,
+ * positive multiples of 16 under which no two elements coincide, pointers 16-byte aligned.  The exponents of keys
+ * and of values are [n_pages][Hkv][page_size] int8 each. */
+
+/* Quantise the keys and values of new tokens into a paged 8-bit cache.
+ *   k, v        : [n_tokens][Hkv][128] of x_dtype (any kvarn_dtype), element (t, h, c) at t * kv_token_stride +
+ *                 h * kv_head_stride + c; strides non-negative multiples of 16 bytes, pointers 16-byte aligned.
+ *                 (kvarn_rope_qkv's output for slots 0 .. n_tokens - 1, say.)
+ *   slot_map    : [n_tokens] int32 or NULL (slot t): slot s is token s mod page_size of page s / page_size.  -1:
+ *                 not written; any other slot outside the cache is not written either and sets value 32 of
+ *                 kvarn_device_error.  Slots are distinct.
+ * n_tokens = 0 is a no-op.  1 <= Hkv <= 65535, page_size >= 1, n_pages * page_size <= 2^31 - 1, n_tokens * Hkv <=
+ * 2^34.  One launch. */
+kvarn_status kvarn_quantize_kv(kvarn_dtype x_dtype, int n_tokens, int Hkv, const void* k, const void* v,
+                               int64_t kv_token_stride, int64_t kv_head_stride, void* k_cache, void* v_cache,
+                               int64_t n_pages, int page_size, int64_t page_stride, int64_t head_stride,
+                               int64_t token_stride, int8_t* k_exp, int8_t* v_exp, const int32_t* slot_map,
+                               kvarn_stream_t stream);
+
+/* kvarn_paged_attention over a paged 8-bit cache: the same arguments and results, with k_exp and v_exp (16-byte
+ * aligned) beside the cache, whose strides are in bytes; dtype is the type of q.  Of the exponents the 16 of a group
+ * of tokens are read together, those of tokens that are not visible without effect. */
+kvarn_status kvarn_paged_attention_q8(kvarn_dtype dtype, int B, int Hq, int Hkv, const void* q, int64_t q_token_stride,
+                                      int64_t q_head_stride, const void* k_cache, const void* v_cache,
+                                      const int8_t* k_exp, const int8_t* v_exp, int64_t n_pages, int page_size,
+                                      int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                      const int32_t* page_table, int max_pages, const int32_t* kv_lens,
+                                      const int32_t* kv_starts, int window, float softmax_scale, float softcap,
+                                      const float* slopes, void* workspace, size_t workspace_bytes,
+                                      kvarn_dtype out_dtype, void* out, float* lse, kvarn_stream_t stream);
+
 /* Reads and clears the device-side error words of the current device, after synchronising it.
  * Bit 1 (value 1): an encoder TMA bulk copy did not complete within its bounded wait (the affected
  * tiles are left unwritten).  Bit 2 (value 2): a decode wait gave up.  Bit 3 (value 4): an append

@@ -227,3 +227,63 @@ def prompt_attention(q, k_cache, v_cache, page_table, cu_tokens, kv_lens, scale,
             lse[t0:t1, h] = np.where(row, np.where(np.isneginf(m), 0.0, m) + np.log(w[:, 0]), -np.inf)
             count[t0:t1, h] = seen.sum(1)
     return out, lse, mass, reach, count
+
+
+def prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, cu_seqs, page_table, kv_lens, scale, softcap=0.0):
+    """One query per sequence over its group's prefix and its own tokens -> out, lse, mass, reach, count as
+    prompt_attention's."""
+    B, hq, D = q.shape
+    hkv, P = k_cache.shape[1:3]
+    n_pages = k_cache.shape[0]
+    out, lse = np.zeros((B, hq, D)), np.full((B, hq), -np.inf)
+    mass, reach, count = np.zeros((B, hq, D)), np.zeros((B, hq)), np.zeros((B, hq))
+
+    def tokens(cache, row, n):
+        j = np.arange(min(max(int(n), 0), len(row) * P))
+        pages = row[j // P]
+        known = (pages >= 0) & (pages < n_pages)
+        return np.where(known[:, None, None], cache[np.where(known, pages, 0), :, j % P], 0.0)
+
+    for b in range(B):
+        k, v = ([tokens(c, page_table[b], kv_lens[b])] for c in (k_cache, v_cache))
+        for g in range(len(prefix_lens)):
+            if cu_seqs[g] <= b < cu_seqs[g + 1]:
+                k.insert(0, tokens(k_cache, prefix_table[g], prefix_lens[g]))
+                v.insert(0, tokens(v_cache, prefix_table[g], prefix_lens[g]))
+        k, v = np.concatenate(k), np.concatenate(v)
+        if not len(k):
+            continue
+        for h in range(hq):
+            kh, vh = k[:, h * hkv // hq], v[:, h * hkv // hq]
+            s = scale * (kh @ q[b, h])
+            reach[b, h] = abs(scale) * (np.abs(kh) @ np.abs(q[b, h])).max()
+            if softcap > 0:
+                s = softcap * np.tanh(s / softcap)
+            p = np.exp(s - s.max())
+            out[b, h], mass[b, h] = p @ vh / p.sum(), p @ np.abs(vh) / p.sum()
+            lse[b, h], count[b, h] = s.max() + math.log(p.sum()), len(p)
+    return out, lse, mass, reach, count
+
+
+def e4m3_grid():
+    """The non-negative E4M3 values in order (codes 0 .. 126)."""
+    c = np.arange(127)
+    e, m = c >> 3, c & 7
+    return np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+
+
+def quantize_row(x):
+    """x [..., 128] (fp64) -> E4M3 values (fp64, signed) and exponents: the nearest grid value of x / 2^e, ties to the
+    even code, infinities to the largest."""
+    top = np.where(np.isnan(x), 0.0, np.abs(x)).max(-1)
+    e = np.full(top.shape, -127)
+    for i in range(-127, 121):
+        e = np.where(top > 448.0 * 2.0 ** (i - 1), i, e)
+    y = np.abs(x) / 2.0 ** e[..., None].astype(float)
+    grid = e4m3_grid()
+    hi = np.minimum(np.searchsorted(grid, y), 126)
+    lo = np.maximum(hi - 1, 0)
+    with np.errstate(invalid="ignore"):
+        up = (grid[hi] - y < y - grid[lo]) | ((grid[hi] - y == y - grid[lo]) & (hi % 2 == 0)) | (hi == 0)
+    value = np.where(up | (y > 448.0), grid[hi], grid[lo])
+    return np.where(np.isnan(x), np.nan, np.copysign(value, x)), e
