@@ -239,8 +239,8 @@ struct PromptArgs {
     int B, T, Hq, Hkv, page_size, max_pages, max_len, window, causal, out_dtype;
     int64_t n_pages;
     // set by the launcher: query heads per kv head, tokens of a copy, rows of a partial slot, whether 32-byte
-    // stores are aligned
-    int group, box, slot_rows, wide_out;
+    // stores are aligned, log2 of a page size that is a power of two (else -1)
+    int group, box, slot_rows, wide_out, page_shift;
     float scale, softcap, inv_softcap;
     const void* q;
     int64_t q_token_stride, q_head_stride;

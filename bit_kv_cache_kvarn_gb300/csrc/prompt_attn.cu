@@ -26,7 +26,8 @@ namespace {
 constexpr int kHalf = 128;                       // rows of a tile: a (token, query head) pair each
 constexpr int kUnit = 2 * kHalf;                 // rows that share a pass over the keys
 constexpr int kThreads = 384;                    // two warpgroups of softmax, one of the four warps below
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kRowWarp = 10, kEdgeWarp = 11;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kRowWarp = 10;  // and the last one, which plans
+constexpr int kPieces = 4, kReaders = 11;        // the planning warp's ring, and the warps that read it
 constexpr int kStages = 5;
 constexpr int kStageBytes = kTile * kTile * 2;   // keys or values of a tile
 constexpr int kSpan = kStageBytes / 2;           // 64 channels of it
@@ -37,6 +38,7 @@ constexpr int kMinPart = 2;                      // tiles of a unit that a CTA t
 constexpr int kColS = 0, kColO = 256, kCols = 512;  // tensor memory: scores of the halves, then their outputs
 constexpr float kGrow = 8.f;                     // how far (in powers of two) scores may pass the maximum in use
 constexpr float kHalfLift = 7.f;                 // fp16 probabilities are multiplied by 2^7
+constexpr int kSerialUnits = 16;                 // of a sequence, whose tiles one lane counts
 constexpr int kJoinRows = 32, kJoinThreads = 256;
 
 struct Join {
@@ -93,27 +95,25 @@ __device__ __forceinline__ int cost_of(const PromptArgs& a, const Seq& s, int u)
     return max(k.past() - k.first(), 1);
 }
 
-// A CTA's share of one unit: the tiles [t0, t1), and of them those of each half.
+// A CTA's share of one unit, as the planning warp hands it to the others: the tiles [t0, t1), and of them those of
+// each half.
 struct Piece {
-    Seq s;
-    int h, u;
-    unsigned f0;
-    int rows;        // of the unit
-    int t0, t1;
+    int t0, t1;          // t1 < t0: nothing more comes
     int a0[2], a1[2];
-    Keys keys;       // of the unit
-    bool starts, ends;
-    long long past;  // end of the unit in the stream
-    __device__ __forceinline__ bool active(int half, int t) const { return t >= a0[half] && t < a1[half]; }
-    __device__ __forceinline__ bool active(int t) const { return active(0, t) || active(1, t); }
+    int lo, hi;          // keys that some row of the unit sees
+    int b, h, u;
+    int q0, shift, len, start, f0;  // the sequence's first row of q, the position of its first row, ...
+    int rows;            // of the unit
+    int starts, ends;
+    int last;            // where the unit begins here and goes on: the last CTA that has a part
     __device__ __forceinline__ int half_rows(int half) const { return min(max(rows - half * kHalf, 0), kHalf); }
 };
 
-// A place in the stream of tiles, ordered by (sequence, kv head, unit, tile); run by whole warps.
+// A place in the stream of tiles, ordered by (sequence, kv head, unit, tile); run by a whole warp.
 struct Walk {
     Seq s;
     int h, u, o, units;
-    long long at, end;
+    long long at, end, piece;
     __device__ __forceinline__ bool next(const PromptArgs& a, Piece& p, int lane) {
         if (at >= end) return false;
         while (u >= units) {
@@ -136,22 +136,30 @@ struct Walk {
             s = load_seq(a, b);
             units = units_of(a, s);
         }
-        p.s = s, p.h = h, p.u = u;
-        p.f0 = (unsigned)u * kUnit;
-        const unsigned past = min(p.f0 + kUnit, (unsigned)s.n * (unsigned)a.group);
-        p.rows = (int)(past - p.f0);
-        p.keys = keys_of(a, s, p.f0, past);
-        const int first = p.keys.first(), cost = max(p.keys.past() - first, 1);
+        p.b = s.b, p.h = h, p.u = u;
+        p.q0 = s.q0, p.shift = s.len - s.n, p.len = s.len, p.start = s.start;
+        const unsigned f0 = (unsigned)u * kUnit, past = min(f0 + kUnit, (unsigned)s.n * (unsigned)a.group);
+        p.f0 = (int)f0;
+        p.rows = (int)(past - f0);
+        const Keys keys = keys_of(a, s, f0, past);
+        p.lo = keys.lo, p.hi = keys.hi;
+        const int first = keys.first(), cost = max(keys.past() - first, 1);
         const int o1 = (int)min((long long)cost, o + (end - at));
         p.t0 = first + o, p.t1 = first + o1;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const Keys k = keys_of(a, s, min(p.f0 + half * kHalf, past), min(p.f0 + (half + 1) * kHalf, past));
+            const Keys k = keys_of(a, s, min(f0 + half * kHalf, past), min(f0 + (half + 1) * kHalf, past));
             p.a0[half] = max(k.first(), p.t0);
             p.a1[half] = min(k.past(), p.t1);
         }
         p.starts = o == 0, p.ends = o1 == cost;
-        p.past = at - o + cost;
+        p.last = 0;
+        if (p.starts && !p.ends) {
+            // the CTA that takes the unit's last tile; its boundary may have moved to the unit's end
+            const long long unit_end = at - o + cost;
+            p.last = (int)((unit_end - 1) / piece);
+            if (unit_end - piece * p.last < kMinPart) --p.last;
+        }
         at += o1 - o;
         o = 0;
         ++u;
@@ -197,119 +205,100 @@ __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int
 struct Barriers {
     uint64_t full[kStages], raw[kStages], empty[kStages];
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t gave_up;
 };
 
-// T: type of q and the cache; O: type of the output; GEN: scores are capped or biased, or the scale has a sign or
-// size for which the maximum cannot be taken before it.
-template <typename T, typename O, bool GEN>
-__global__ void __launch_bounds__(kThreads, 1)
-    prompt_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, PromptArgs a) {
-    constexpr bool kIsHalf = std::is_same<T, __half>::value;
-    constexpr float kLift = kIsHalf ? kHalfLift : 0.f;
-    constexpr uint32_t kIdescS = kIsHalf ? tc::idesc_f16_f32(128, 128) : tc::idesc_as_bf16(tc::idesc_f16_f32(128, 128));
-    constexpr uint32_t kIdescO = kIsHalf ? tc::idesc_f16_f32_bmn(128, 128) : tc::idesc_as_bf16(tc::idesc_f16_f32_bmn(128, 128));
-    extern __shared__ uint8_t dsm_raw[];
-    __shared__ Barriers bar;
-    __shared__ uint32_t s_tmem;
-    __shared__ long long s_scan[kThreads / 32];
-    __shared__ long long s_at[2];          // the boundaries of this CTA's share
-    __shared__ int s_seq[2], s_place[3];   // their sequences; kv head, unit and tile of the first one
-    __shared__ long long s_in[2];
-    uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t* rows_smem = dsm;
-    uint8_t* ring = dsm + 2 * kRowBytes;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == kMmaWarp) tc::alloc(&s_tmem, kCols);
-    if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.raw[i], 1), mbar_init(&bar.empty[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_free[i], 1), mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
-        }
-        mbar_init(&bar.gave_up, 1);
-        fence_mbar_init();
+// The ring of pieces as one of its readers goes through it.
+struct Reader {
+    uint32_t slot = 0, parity = 0;
+    // a whole warp waits for the next piece and copies what it needs by `take`; false: nothing more
+    template <typename F>
+    __device__ __forceinline__ bool next(const Piece* ring, Barriers& bar, unsigned int* err, int lane, F take) {
+        if (!mbar_wait(&bar.piece_full[slot], parity, err)) return false;
+        const Piece& p = ring[slot];
+        const bool some = p.t1 >= p.t0;
+        if (some) take(p);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.piece_empty[slot]);
+        if (++slot == kPieces) slot = 0, parity ^= 1;
+        return some;
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+};
 
-    // ---- this CTA's share: the tiles of all units form one stream, cut into equal pieces ----
-    long long* s_cost = reinterpret_cast<long long*>(ring);  // tiles of a sequence's units, of one kv head
-    for (int base = warp * 32; base < a.B; base += kThreads) {
-        const bool in = base + lane < a.B;
-        const Seq s = in ? load_seq(a, base + lane) : Seq{0, 0, 0, 0, 0};
-        const int n = units_of(a, s);
-        long long cost = 0;
-        if (n <= 4)
-            for (int u = 0; u < n; ++u) cost += cost_of(a, s, u);
-        for (unsigned many = __ballot_sync(0xffffffffu, n > 4); many != 0; many &= many - 1) {  // by the whole warp
-            const int k = __ffs(many) - 1;
-            Seq w;
-            w.b = 0, w.q0 = 0;
-            w.n = __shfl_sync(0xffffffffu, s.n, k);
-            w.len = __shfl_sync(0xffffffffu, s.len, k);
-            w.start = __shfl_sync(0xffffffffu, s.start, k);
-            const int nw = units_of(a, w);
-            long long sum = 0;
-            for (int u = lane; u < nw; u += 32) sum += cost_of(a, w, u);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            if (lane == k) cost = sum;
-        }
-        if (in) s_cost[base + lane] = cost;
-    }
-    __syncthreads();
-    const int seg = (a.B + kThreads - 1) / kThreads, seg0 = min(tid * seg, a.B), seg1 = min(seg0 + seg, a.B);
-    long long mine = 0;
-    for (int b = seg0; b < seg1; ++b) mine += s_cost[b] * a.Hkv;
-    long long inc = mine;
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += v;
+        const long long o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
     }
-    if (lane == 31) s_scan[warp] = inc;
-    __syncthreads();
-    long long total = 0;
+    return v;
+}
+// Tiles of a CTA's share, but for the shifts of its boundaries to those of units.
+__device__ __forceinline__ long long piece_of(long long total) {
+    return max(total + gridDim.x > 0xffffffffLL ? (total + gridDim.x - 1) / gridDim.x
+                                                : (long long)((unsigned)(total + gridDim.x - 1) / gridDim.x),
+               (long long)kMinPart);
+}
+// Tiles of one kv head's units of sequence base + lane; by a whole warp, a long sequence by all of its lanes.
+__device__ __forceinline__ long long seq_cost(const PromptArgs& a, int base, int lane) {
+    const bool in = base + lane < a.B;
+    const Seq s = in ? load_seq(a, base + lane) : Seq{0, 0, 0, 0, 0};
+    const int n = units_of(a, s);
+    long long cost = 0;
+    if (n <= kSerialUnits)
+        for (int u = 0; u < n; ++u) cost += cost_of(a, s, u);
+    for (unsigned many = __ballot_sync(0xffffffffu, n > kSerialUnits); many != 0; many &= many - 1) {
+        const int k = __ffs(many) - 1;
+        Seq w;
+        w.b = 0, w.q0 = 0;
+        w.n = __shfl_sync(0xffffffffu, s.n, k);
+        w.len = __shfl_sync(0xffffffffu, s.len, k);
+        w.start = __shfl_sync(0xffffffffu, s.start, k);
+        const int nw = units_of(a, w);
+        long long sum = 0;
+        for (int u = lane; u < nw; u += 32) sum += cost_of(a, w, u);
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) inc += s_scan[w];
-        total += s_scan[w];
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == k) cost = sum;
     }
-    const long long piece = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinPart);
-#pragma unroll
+    return cost;
+}
+// The walk over this CTA's share, by one warp.  Up to 32 sequences it finds everything by itself, else the CTA found
+// `total` and the sequences of the share's ends (s_seq, s_in, s_cost).
+__device__ __forceinline__ void plan(const PromptArgs& a, Walk& walk, long long total, const int* s_seq, const long long* s_in,
+                                  const long long* s_cost, int lane) {
+    long long mine = 0, inc = 0;
+    if (a.B <= 32) {
+        mine = seq_cost(a, 0, lane);
+        inc = warp_scan(mine * a.Hkv, lane);
+        total = __shfl_sync(0xffffffffu, inc, 31);
+    }
+    walk.piece = piece_of(total);
+    long long at[2];
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
-        const long long pos = min(piece * (blockIdx.x + which), total);
-        if (pos >= total) {
-            if (tid == 0) s_seq[which] = -1;
-        } else if (pos >= inc - mine && pos < inc) {
-            long long in_seq = pos - (inc - mine);
-            int b = seg0;
-            for (; in_seq >= s_cost[b] * a.Hkv; ++b) in_seq -= s_cost[b] * a.Hkv;
-            s_seq[which] = b;
-            s_in[which] = in_seq;
-        }
-    }
-    __syncthreads();
-    if (warp < 2) {
-        const int b = s_seq[warp];
-        long long pos = min(piece * (blockIdx.x + warp), total);
-        if (b >= 0) {
+        long long pos = min(walk.piece * (blockIdx.x + which), total);
+        if (pos < total) {
+            int b;
+            long long in_seq, per_head;
+            if (a.B <= 32) {
+                b = __popc(__ballot_sync(0xffffffffu, inc <= pos));
+                in_seq = pos - __shfl_sync(0xffffffffu, inc - mine * a.Hkv, b);
+                per_head = __shfl_sync(0xffffffffu, mine, b);
+            } else {
+                b = s_seq[which], in_seq = s_in[which], per_head = s_cost[b];
+            }
             const Seq s = load_seq(a, b);
             const int units = units_of(a, s);
-            const long long per_head = s_cost[b];
-            const int h = (int)(s_in[warp] / per_head);
-            const long long want = s_in[warp] - h * per_head;
+            const int h = (in_seq | per_head) >> 32 ? (int)(in_seq / per_head) : (int)((unsigned)in_seq / (unsigned)per_head);
+            const long long want = in_seq - h * per_head;
             long long before = 0;
             int u = 0, o = 0, cost = 0;
             for (int u0 = 0; u0 < units; u0 += 32) {
                 const int c = u0 + lane < units ? cost_of(a, s, u0 + lane) : 0;
-                long long sum = c;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const long long v = __shfl_up_sync(0xffffffffu, sum, d);
-                    if (lane >= d) sum += v;
-                }
+                const long long sum = warp_scan(c, lane);
                 const unsigned ends_later = __ballot_sync(0xffffffffu, before + sum > want);
                 if (ends_later != 0) {
                     const int k = __ffs(ends_later) - 1;
@@ -329,9 +318,81 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o = 0;
                 ++u;
             }
-            if (warp == 0 && lane == 0) s_place[0] = h, s_place[1] = u, s_place[2] = o;
+            if (which == 0) walk.s = s, walk.h = h, walk.u = u, walk.o = o, walk.units = units;
         }
-        if (lane == 0) s_at[warp] = pos;
+        at[which] = pos;
+    }
+    walk.at = at[0], walk.end = at[1];
+}
+
+// T: type of q and the cache; O: type of the output; GEN: scores are capped or biased, or the scale has a sign or
+// size for which the maximum cannot be taken before it.
+template <typename T, typename O, bool GEN>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, PromptArgs a) {
+    constexpr bool kIsHalf = std::is_same<T, __half>::value;
+    constexpr float kLift = kIsHalf ? kHalfLift : 0.f;
+    constexpr uint32_t kIdescS = kIsHalf ? tc::idesc_f16_f32(128, 128) : tc::idesc_as_bf16(tc::idesc_f16_f32(128, 128));
+    constexpr uint32_t kIdescO = kIsHalf ? tc::idesc_f16_f32_bmn(128, 128) : tc::idesc_as_bf16(tc::idesc_f16_f32_bmn(128, 128));
+    extern __shared__ uint8_t dsm_raw[];
+    __shared__ Barriers bar;
+    __shared__ Piece s_piece[kPieces];
+    __shared__ uint32_t s_tmem;
+    __shared__ long long s_scan[kThreads / 32];
+    __shared__ int s_seq[2];      // the sequences in which this CTA's share begins and ends, -1: behind the last tile,
+    __shared__ long long s_in[2];  // and the places in them
+    uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* rows_smem = dsm;
+    uint8_t* ring = dsm + 2 * kRowBytes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == kMmaWarp) tc::alloc(&s_tmem, kCols);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.raw[i], 1), mbar_init(&bar.empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_free[i], 1), mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
+        }
+        for (int i = 0; i < kPieces; ++i) mbar_init(&bar.piece_full[i], 1), mbar_init(&bar.piece_empty[i], kReaders);
+        mbar_init(&bar.gave_up, 1);
+        fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- this CTA's share: the tiles of all units form one stream, cut into equal pieces ----
+    long long total = 0;
+    long long* s_cost = reinterpret_cast<long long*>(ring);  // tiles of a sequence's units, of one kv head
+    if (a.B > 32) {  // else the planning warp finds it by itself
+        for (int base = warp * 32; base < a.B; base += kThreads) {
+            const long long cost = seq_cost(a, base, lane);
+            if (base + lane < a.B) s_cost[base + lane] = cost;
+        }
+        __syncthreads();
+        const int seg = (a.B + kThreads - 1) / kThreads, seg0 = min(tid * seg, a.B), seg1 = min(seg0 + seg, a.B);
+        long long mine = 0;
+        for (int b = seg0; b < seg1; ++b) mine += s_cost[b] * a.Hkv;
+        long long inc = warp_scan(mine, lane);
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) inc += s_scan[w];
+            total += s_scan[w];
+        }
+        const long long piece = piece_of(total);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const long long pos = min(piece * (blockIdx.x + which), total);
+            if (pos >= total) {
+                if (tid == 0) s_seq[which] = -1;
+            } else if (pos >= inc - mine && pos < inc) {
+                long long in_seq = pos - (inc - mine);
+                int b = seg0;
+                for (; in_seq >= s_cost[b] * a.Hkv; ++b) in_seq -= s_cost[b] * a.Hkv;
+                s_seq[which] = b;
+                s_in[which] = in_seq;
+            }
+        }
     }
     fence_proxy_async();  // s_cost lies where the copies go
     tc::fence_before();
@@ -339,14 +400,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after();
     const uint32_t tmem = s_tmem;
     const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.slot_rows), (int)gridDim.x};
-    Walk walk;
-    walk.at = s_at[0], walk.end = s_at[1];
-    walk.units = 0;
-    if (walk.at < walk.end) {
-        walk.s = load_seq(a, s_seq[0]);
-        walk.h = s_place[0], walk.u = s_place[1], walk.o = s_place[2];
-        walk.units = units_of(a, walk.s);
-    }
     if (tid == 0) ws.joins()[blockIdx.x].b = -1;
     unsigned int* const err = &g_prompt_error;
 
@@ -359,14 +412,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s_parity = 0, o_parity = 0;
         const float c = GEN ? 1.f : a.scale * kLog2e;
         bool fine = true;
-        Piece p;
-        while (fine && walk.next(a, p, lane)) {
-            const int rows = p.half_rows(half);
+        Reader reader;
+        struct {
+            int first, past, rows, b, h, u, q0, shift, len, start, f0, starts, ends, last;
+        } p;
+        while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& from) {
+            p.first = from.a0[half], p.past = from.a1[half], p.rows = from.half_rows(half);
+            p.b = from.b, p.h = from.h, p.u = from.u, p.q0 = from.q0, p.shift = from.shift, p.len = from.len;
+            p.start = from.start, p.f0 = from.f0, p.starts = from.starts, p.ends = from.ends, p.last = from.last;
+        })) {
+            const int rows = p.rows;
             const bool real = r < rows;
-            const unsigned f = p.f0 + half * kHalf + r;
+            const unsigned f = (unsigned)p.f0 + half * kHalf + r;
             const int token = (int)(f / (unsigned)a.group), head = p.h * a.group + (int)(f - (unsigned)token * a.group);
-            const int pos = p.s.len - p.s.n + token;
-            int lo = p.s.start, hi = p.s.len;
+            const int pos = p.shift + token;
+            int lo = p.start, hi = p.len;
             if (a.causal) {
                 hi = min(hi, pos + 1);
                 if (a.window > 0) lo = max(lo, pos + 1 - a.window);
@@ -374,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!real) hi = lo;
             const float slope = GEN && a.slopes != nullptr && real ? a.slopes[head] : 0.f;
             float m = -CUDART_INF_F, l = 0.f;
-            const int first = p.a0[half], past = p.a1[half];
+            const int first = p.first, past = p.past;
             for (int t = first; t < past; ++t) {
                 if (!mbar_wait(&bar.s_full[half], s_parity, err)) {
                     fine = false;
@@ -458,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after();
             }
             const bool whole = p.starts && p.ends;
-            const int64_t row = (int64_t)(p.s.q0 + token) * a.Hq + head;
+            const int64_t row = (int64_t)(p.q0 + token) * a.Hq + head;
             float* slot = ws.slot(blockIdx.x, p.starts ? 1 : 0);
             const int rr = half * kHalf + r;
             const float inv = l != 0.f ? 1.f / l : 0.f;
@@ -510,17 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     slot[a.slot_rows * kTile + a.slot_rows + rr] = l;
                 }
             }
-            if (tid == 0 && p.starts && !p.ends) {
-                // the CTA that takes the unit's last tile; its boundary may have moved to the unit's end
-                int last = (int)((p.past - 1) / piece);
-                if (p.past - piece * last < kMinPart) --last;
-                ws.joins()[blockIdx.x] = Join{p.s.b, p.h, p.u, last};
-            }
+            if (tid == 0 && p.starts && !p.ends) ws.joins()[blockIdx.x] = Join{p.b, p.h, p.u, p.last};
             tc::fence_before();
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        Piece p;
+        Reader reader;
         if (warp == kLoadWarp) {
             // ---- keys and values, a tile at a time, page by page ----
             uint32_t stage = 0, parity = 1;
@@ -528,18 +583,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int boxes = kTile / a.box;
             uint64_t* last[kStages] = {};  // barrier of each stage's last copy, and its parity
             uint32_t last_parity = 0, raw_parity = 0;
-            while (fine && walk.next(a, p, lane)) {
-                for (int t = p.t0; fine && t < p.t1; ++t) {
-                    if (!p.active(t)) continue;
+            int t0, t1, a0[2], a1[2], lo, hi, h;
+            const int32_t* table;
+            while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
+                t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi, h = p.h;
+                a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
+                table = a.page_table + (int64_t)p.b * a.max_pages;
+            })) {
+                for (int t = t0; fine && t < t1; ++t) {
+                    if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
                     // lane i: box i of the tile
                     const int tok = t * kTile + lane * a.box;
-                    const bool want = lane < boxes && tok < p.keys.hi && tok + a.box > p.keys.lo;
-                    const int entry = tok / a.page_size, in_page = tok - entry * a.page_size;
-                    const int page = want ? a.page_table[(int64_t)p.s.b * a.max_pages + entry] : 0;
+                    const bool want = lane < boxes && tok < hi && tok + a.box > lo;
+                    const int entry = a.page_shift >= 0 ? tok >> a.page_shift : tok / a.page_size, in_page = tok - entry * a.page_size;
+                    const int page = want ? table[entry] : 0;
                     const bool bad = want && (page < 0 || page >= a.n_pages);
                     const unsigned good = __ballot_sync(0xffffffffu, want && !bad), zero = __ballot_sync(0xffffffffu, bad);
                     const uint32_t bytes = (uint32_t)__popc(good) * (uint32_t)a.box * (kTile * 2);
-                    const bool edge = t * kTile < p.keys.lo || (t + 1) * kTile > p.keys.hi;
+                    const bool edge = t * kTile < lo || (t + 1) * kTile > hi;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         if (!mbar_wait(&bar.empty[stage], parity, err)) {
@@ -573,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (want && !bad) {
                             const CUtensorMap* map = kv == 0 ? &k_map : &v_map;
                             uint8_t* d = dst + lane * a.box * kTile;
-                            tma_load4(d, map, 0, in_page, p.h, page, b);
-                            tma_load4(d + kSpan, map, 64, in_page, p.h, page, b);
+                            tma_load4(d, map, 0, in_page, h, page, b);
+                            tma_load4(d + kSpan, map, 64, in_page, h, page, b);
                         }
                         __syncwarp();
                         if (++stage == kStages) stage = 0, parity ^= 1;
@@ -594,90 +655,96 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == kMmaWarp) {
             // ---- products: S of the halves' next tile between the two halves' P V of this one ----
             uint32_t stage = 0, parity = 0;  // of the ring
-            uint32_t q_parity[2] = {0, 0}, p_parity[2] = {0, 0};
-            const uint32_t ring_addr = smem_addr(ring), q_addr = smem_addr(rows_smem);
+            uint32_t q_parity = 0, p_parity = 0;  // a bit for each half
+            const uint32_t ring_addr = smem_addr(ring);
+            const uint64_t q_desc = tc::smem_desc_sw128(smem_addr(rows_smem), 16, 1024);
+            const uint64_t k_desc = tc::smem_desc_sw128(ring_addr, 16, 1024), v_desc = tc::smem_desc_sw128(ring_addr, kSpan, 1024);
             bool fine = true;
-            Piece cur, nxt;
-            int t = 0, tn = 0;
+            struct Place {
+                int t, t1, a0[2], a1[2];
+                __device__ __forceinline__ bool active(int half) const { return t >= a0[half] && t < a1[half]; }
+            };
+            Place cur, nxt;
             auto next_stage = [&]() {
                 if (++stage == kStages) stage = 0, parity ^= 1;
             };
-            // the next tile that some half takes: of piece q from tile i on, or of a later piece
-            auto seek = [&](Piece& q, int& i, bool have) {
-                for (;;) {
-                    if (have)
-                        for (; i < q.t1; ++i)
-                            if (q.active(i)) return true;
-                    if (!walk.next(a, q, lane)) return false;
-                    i = q.t0;
-                    have = true;
-                }
+            // the next tile that some half takes of this piece, from tile q.t on
+            auto in_piece = [&](Place& q) {
+                for (; q.t < q.t1; ++q.t)
+                    if (q.active(0) || q.active(1)) return true;
+                return false;
             };
-            auto scores = [&](const Piece& q, int i, int half, uint32_t kb) {
-                if (i == q.a0[half]) {
-                    if (!mbar_wait(&bar.q_full[half], q_parity[half], err)) return false;
-                    q_parity[half] ^= 1;
+            bool more = true;  // pieces
+            auto next_piece = [&](Place& q) {
+                more = reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
+                    q.t = p.t0, q.t1 = p.t1;
+                    q.a0[0] = p.a0[0], q.a0[1] = p.a0[1], q.a1[0] = p.a1[0], q.a1[1] = p.a1[1];
+                });
+                return more && in_piece(q);
+            };
+            auto scores = [&](const Place& q, int half, uint32_t k_stage) {
+                if (q.t == q.a0[half]) {
+                    if (!mbar_wait(&bar.q_full[half], q_parity >> half & 1, err)) return false;
+                    q_parity ^= 1u << half;
                     tc::fence_after();
                 }
                 if (lane == 0) {
+                    const uint64_t qd = q_desc + half * (kRowBytes >> 4), kd = k_desc + k_stage * (kStageBytes >> 4);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const uint32_t off = (k >> 2) * kSpan + (k & 3) * 32;
-                        tc::mma_f16_ss(tmem + kColS + half * kTile, tc::smem_desc_sw128(q_addr + half * kRowBytes + off, 16, 1024),
-                                       tc::smem_desc_sw128(kb + off, 16, 1024), kIdescS, k > 0);
+                        const uint32_t off = ((k >> 2) * kSpan + (k & 3) * 32) >> 4;
+                        tc::mma_f16_ss(tmem + kColS + half * kTile, qd + off, kd + off, kIdescS, k > 0);
                     }
                     tc::commit(&bar.s_full[half]);
-                    if (i + 1 == q.a1[half]) tc::commit(&bar.q_free[half]);
+                    if (q.t + 1 == q.a1[half]) tc::commit(&bar.q_free[half]);
                 }
                 __syncwarp();
                 return true;
             };
-            bool have = seek(cur, t, false);
-            if (have) {
-                fine = mbar_wait(&bar.full[stage], parity, err);
-                tc::fence_after();
-                for (int half = 0; fine && half < 2; ++half)
-                    if (cur.active(half, t)) fine = scores(cur, t, half, ring_addr + stage * kStageBytes);
-                if (fine && lane == 0) tc::commit(&bar.empty[stage]);
-                next_stage();
-            }
-            while (fine && have) {
+            bool have = false;  // a tile whose scores are under way
+            while (fine) {
+                if (!have) {
+                    while (more && !have) have = next_piece(cur);
+                    if (!have) break;
+                    fine = mbar_wait(&bar.full[stage], parity, err);
+                    tc::fence_after();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        if (fine && cur.active(half)) fine = scores(cur, half, stage);
+                    if (fine && lane == 0) tc::commit(&bar.empty[stage]);
+                    __syncwarp();
+                    next_stage();
+                    if (!fine) break;
+                }
                 const uint32_t v_stage = stage, v_parity = parity;
                 next_stage();
                 nxt = cur;
-                tn = t + 1;
-                have = seek(nxt, tn, true);
+                ++nxt.t;
+                // One piece further at most before this tile's P V: the warps that wait for that may hold up those behind
+                // (a ring's length of pieces without keys would).
+                have = in_piece(nxt) || (more && next_piece(nxt));
                 const uint32_t k_stage = stage, k_parity = parity;
                 if (have) next_stage();
-                bool v_in = false, k_in = false;
-                for (int half = 0; fine && half < 2; ++half) {
-                    if (cur.active(half, t)) {
-                        if (!v_in) fine = mbar_wait(&bar.full[v_stage], v_parity, err);
-                        v_in = true;
-                        if (!fine || !mbar_wait(&bar.p_full[half], p_parity[half], err)) {
-                            fine = false;
-                            break;
-                        }
-                        p_parity[half] ^= 1;
+                fine = mbar_wait(&bar.full[v_stage], v_parity, err);
+                if (fine && have) fine = mbar_wait(&bar.full[k_stage], k_parity, err);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (fine && cur.active(half)) {
+                        fine = mbar_wait(&bar.p_full[half], p_parity >> half & 1, err);
+                        p_parity ^= 1u << half;
                         tc::fence_after();
-                        if (lane == 0) {
-                            const uint32_t vb = ring_addr + v_stage * kStageBytes;
+                        if (fine && lane == 0) {
+                            const uint64_t vd = v_desc + v_stage * (kStageBytes >> 4);
+                            const uint32_t more = cur.t > cur.a0[half];
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                tc::mma_f16_ts(tmem + kColO + half * kTile, tmem + kColS + half * kTile + 8 * k,
-                                               tc::smem_desc_sw128(vb + k * 2048, kSpan, 1024), kIdescO, k > 0 || t > cur.a0[half]);
-                            if (t + 1 == cur.a1[half]) tc::commit(&bar.o_full[half]);
+                                tc::mma_f16_ts(tmem + kColO + half * kTile, tmem + kColS + half * kTile + 8 * k, vd + k * (2048 >> 4),
+                                               kIdescO, k > 0 ? 1u : more);
+                            if (cur.t + 1 == cur.a1[half]) tc::commit(&bar.o_full[half]);
                         }
                         __syncwarp();
                     }
-                    if (have && nxt.active(half, tn)) {
-                        if (!k_in) {
-                            fine = mbar_wait(&bar.full[k_stage], k_parity, err);
-                            tc::fence_after();
-                        }
-                        k_in = true;
-                        if (fine) fine = scores(nxt, tn, half, ring_addr + k_stage * kStageBytes);
-                    }
+                    if (fine && have && nxt.active(half)) fine = scores(nxt, half, k_stage);
                 }
                 if (fine && lane == 0) {
                     tc::commit(&bar.empty[v_stage]);
@@ -685,7 +752,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 cur = nxt;
-                t = tn;
             }
             if (!fine) {
                 if (lane == 0) tc::commit(&bar.gave_up);
@@ -694,27 +760,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kRowWarp) {
             // ---- queries: rows of 256 bytes, gathered, chunk i of a row at i ^ (row mod 8) ----
-            uint32_t free_parity[2] = {1, 1};
+            uint32_t free_parity = 3;  // a bit for each half
             bool fine = true;
-            while (fine && walk.next(a, p, lane)) {
+            // rows go along the heads of a token and on to the next token's (with one head: along the tokens)
+            const int wrap = a.group > 1 ? a.group : 0x7fffffff, chunk = lane & 15;
+            const int64_t step = a.group > 1 ? a.q_head_stride : a.q_token_stride;
+            const int64_t wrap_step = a.q_token_stride - (int64_t)a.group * a.q_head_stride;
+            const T* const base = static_cast<const T*>(a.q) + 8 * chunk;
+            int rows_of_unit, h, q0;
+            unsigned f0, some;
+            while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
+                some = (p.a0[0] < p.a1[0] ? 1u : 0u) | (p.a0[1] < p.a1[1] ? 2u : 0u);
+                f0 = (unsigned)p.f0, h = p.h, q0 = p.q0, rows_of_unit = p.rows;
+            })) {
+#pragma unroll 1
                 for (int half = 0; fine && half < 2; ++half) {
-                    if (p.a0[half] >= p.a1[half]) continue;
-                    if (!mbar_wait(&bar.q_free[half], free_parity[half], err)) {
+                    if (!(some >> half & 1)) continue;
+                    const unsigned f = f0 + half * kHalf + (lane >> 4), token = f / (unsigned)a.group;
+                    int g = a.group > 1 ? (int)(f - token * a.group) : 0;
+                    const T* src = base + (int64_t)(q0 + (int)token) * a.q_token_stride + ((int64_t)h * a.group + g) * a.q_head_stride;
+                    if (!mbar_wait(&bar.q_free[half], free_parity >> half & 1, err)) {
                         fine = false;
                         break;
                     }
-                    free_parity[half] ^= 1;
-                    const int rows = p.half_rows(half), chunk = lane & 15;
-                    const uint32_t dst = smem_addr(rows_smem + half * kRowBytes) + (chunk >> 3) * kSpan;
-#pragma unroll 4
-                    for (int i = 0; i < kHalf / 2; ++i) {
-                        const int r = 2 * i + (lane >> 4);
+                    free_parity ^= 1u << half;
+                    const int rows = rows_of_unit - half * kHalf - (lane >> 4);
+                    const uint32_t dst = smem_addr(rows_smem + half * kRowBytes) + (chunk >> 3) * kSpan + (lane >> 4) * kTile;
+                    const uint32_t key = (uint32_t)(chunk & 7) ^ (uint32_t)(lane >> 4);
+#pragma unroll 8
+                    for (int r = 0; r < kHalf; r += 2) {
                         const bool real = r < rows;
-                        const unsigned f = real ? p.f0 + half * kHalf + r : p.f0;
-                        const unsigned token = f / (unsigned)a.group, g = f - token * a.group;
-                        const T* src = static_cast<const T*>(a.q) + (int64_t)(p.s.q0 + token) * a.q_token_stride +
-                                       (int64_t)(p.h * a.group + g) * a.q_head_stride + 8 * chunk;
-                        cp_async16(dst + r * kTile + (((chunk & 7) ^ (r & 7)) << 4), src, real);
+                        cp_async16(dst + r * kTile + ((key ^ (r & 6)) << 4), real ? src : base, real);
+                        src += 2 * step;
+                        g += 2;
+                        if (g >= wrap) g -= wrap, src += wrap_step;
                     }
                     cp_async_commit();
                     cp_async_wait<0>();
@@ -723,32 +802,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&bar.q_full[half]);
                 }
             }
-            for (int half = 0; fine && half < 2; ++half) fine = mbar_wait(&bar.q_free[half], free_parity[half], err);
+            for (int half = 0; fine && half < 2; ++half) fine = mbar_wait(&bar.q_free[half], free_parity >> half & 1, err);
         } else {
-            // ---- values at the edges of what a unit sees: rows outside are zeros ----
-            uint32_t stage = 0, raw_parity = 0;  // a bit for each stage
-            bool fine = true;
-            while (fine && walk.next(a, p, lane)) {
-                for (int t = p.t0; fine && t < p.t1; ++t) {
-                    if (!p.active(t)) continue;
+            // ---- the plan, and values at the edges of what a unit sees: rows outside are zeros ----
+            Walk walk;
+            walk.at = walk.end = 0;
+            walk.units = 0;
+            plan(a, walk, total, s_seq, s_in, s_cost, lane);
+            fence_proxy_async();
+            uint32_t slot = 0, slot_parity = 1, stage = 0, raw_parity = 0;  // raw_parity: a bit for each stage
+            bool fine = true, more = true, have = false;
+            int t0 = 0, t1 = 0, a0[2], a1[2], lo = 0, hi = 0;
+            while (fine && (more || have)) {
+                // the next piece goes out before this one's edges are seen to
+                Piece p;
+                if (more) {
+                    more = walk.next(a, p, lane);
+                    if (!more) p.t0 = 1, p.t1 = 0;
+                    fine = mbar_wait(&bar.piece_empty[slot], slot_parity, err);
+                    if (!fine) break;
+                    if (lane == 0) {
+                        s_piece[slot] = p;
+                        mbar_arrive(&bar.piece_full[slot]);
+                    }
+                    __syncwarp();
+                    if (++slot == kPieces) slot = 0, slot_parity ^= 1;
+                }
+                for (int t = t0; have && fine && t < t1; ++t) {
+                    if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
                     if (++stage == kStages) stage = 0;  // the keys' stage
-                    if (t * kTile < p.keys.lo || (t + 1) * kTile > p.keys.hi) {
+                    if (t * kTile < lo || (t + 1) * kTile > hi) {
                         fine = mbar_wait(&bar.raw[stage], (raw_parity >> stage) & 1, err);
                         if (!fine) break;
                         raw_parity ^= 1u << stage;
                         uint8_t* v = ring + stage * kStageBytes;
-                        const int lo = p.keys.lo - t * kTile, hi = p.keys.hi - t * kTile;
-                        for (int i = lane; i < kTile * 16; i += 32) {
-                            const int r = i >> 4;
-                            if (r < lo || r >= hi)
-                                *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kSpan + r * kTile + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
+                        const int lo_in = max(lo - t * kTile, 0), hi_in = min(hi - t * kTile, kTile);
+                        for (int i = lane; i < lo_in * 16; i += 32)
+                            *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kSpan + (i >> 4) * kTile + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int i = hi_in * 16 + lane; i < kTile * 16; i += 32)
+                            *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kSpan + (i >> 4) * kTile + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                         fence_proxy_async();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar.full[stage]);
                     }
                     if (++stage == kStages) stage = 0;
                 }
+                have = more;
+                t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi;
+                a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
             }
         }
     }
@@ -888,6 +989,7 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     a.group = a.Hq / a.Hkv;
     a.slot_rows = slot_rows(a.T, a.Hq, a.Hkv);
     a.inv_softcap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+    a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     a.box = a.page_size % 128 == 0 ? 128 : a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
     a.wide_out = ((uintptr_t)a.out & 31) == 0 && ((uintptr_t)a.workspace & 31) == 0;
     const float c = a.scale * kLog2e;

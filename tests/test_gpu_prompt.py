@@ -161,3 +161,14 @@ def test_modifiers(kv, kw, dt):
     softcap, scale = kw.pop("softcap", 0.0), kw.pop("scale", SCALE)
     c = case(7, new, ctx, 8, 2, 48, dt, **kw)
     check(c, *call(kv, c, scale=scale, softcap=softcap, slopes=slopes), scale=scale, softcap=softcap, slopes=slopes)
+
+
+def test_many_rows_without_keys_between_others(kv):
+    # runs of units that see nothing, longer than any look-ahead, behind units that do
+    new = [40, 3, 70, 9, 1, 33, 64, 5] * 80
+    starts = [0 if i % 8 == 0 else 10000 for i in range(len(new))]
+    c = case(21, new, [30] * len(new), 8, 2, 16, starts=starts)
+    check(c, *call(kv, c))
+    # and inside one sequence, for each head
+    c = case(22, [2500, 60], [0, 10], 8, 8, 48, HF, starts=[2000, 0], window=200)
+    check(c, *call(kv, c))
