@@ -25,9 +25,12 @@ namespace {
 
 constexpr int kHalf = 128;                       // rows of a tile: a (token, query head) pair each
 constexpr int kUnit = 2 * kHalf;                 // rows that share a pass over the keys
-constexpr int kThreads = 384;                    // two warpgroups of softmax, one of the four warps below
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kRowWarp = 10;  // and the last one, which plans
-constexpr int kPieces = 4, kReaders = 11;        // the planning warp's ring, and the warps that read it
+constexpr int kThreads = 512;                    // two warpgroups of softmax, then a warp for each of:
+constexpr int kKeyWarp = 8, kValueWarp = 9;      //   copies of keys, and of values,
+constexpr int kMmaWarp = 10;                     //   products of a half (and 11),
+constexpr int kRowWarp = 12;                     //   queries of a half (and 13),
+constexpr int kPlanWarp = 14;                    //   the plan, and (15) values at the edges of what a unit sees
+constexpr int kPieces = 4, kReaders = 15;        // the planning warp's ring, and the warps that read it
 constexpr int kStages = 5;
 constexpr int kStageBytes = kTile * kTile * 2;   // keys or values of a tile
 constexpr int kSpan = kStageBytes / 2;           // 64 channels of it
@@ -212,7 +215,7 @@ struct Barriers {
 // The ring of pieces as one of its readers goes through it.
 struct Reader {
     uint32_t slot = 0, parity = 0;
-    // a whole warp waits for the next piece and copies what it needs by `take`; false: nothing more
+    // A whole warp waits for the next piece and copies what it needs by `take`; false: nothing more
     template <typename F>
     __device__ __forceinline__ bool next(const Piece* ring, Barriers& bar, unsigned int* err, int lane, F take) {
         if (!mbar_wait(&bar.piece_full[slot], parity, err)) return false;
@@ -265,10 +268,10 @@ __device__ __forceinline__ long long seq_cost(const PromptArgs& a, int base, int
     }
     return cost;
 }
-// The walk over this CTA's share, by one warp.  Up to 32 sequences it finds everything by itself, else the CTA found
-// `total` and the sequences of the share's ends (s_seq, s_in, s_cost).
-__device__ __forceinline__ void plan(const PromptArgs& a, Walk& walk, long long total, const int* s_seq, const long long* s_in,
-                                  const long long* s_cost, int lane) {
+// Begin (which = 0, with the walk from there) or end of this CTA's share, by one warp.  Up to 32 sequences it finds
+// everything by itself, else the CTA found `total` and the sequences of the share's ends (s_seq, s_in, s_cost).
+__device__ __forceinline__ long long plan(const PromptArgs& a, Walk& walk, int which, long long total, const int* s_seq,
+                                          const long long* s_in, const long long* s_cost, int lane) {
     long long mine = 0, inc = 0;
     if (a.B <= 32) {
         mine = seq_cost(a, 0, lane);
@@ -276,54 +279,54 @@ __device__ __forceinline__ void plan(const PromptArgs& a, Walk& walk, long long 
         total = __shfl_sync(0xffffffffu, inc, 31);
     }
     walk.piece = piece_of(total);
-    long long at[2];
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        long long pos = min(walk.piece * (blockIdx.x + which), total);
-        if (pos < total) {
-            int b;
-            long long in_seq, per_head;
-            if (a.B <= 32) {
-                b = __popc(__ballot_sync(0xffffffffu, inc <= pos));
-                in_seq = pos - __shfl_sync(0xffffffffu, inc - mine * a.Hkv, b);
-                per_head = __shfl_sync(0xffffffffu, mine, b);
-            } else {
-                b = s_seq[which], in_seq = s_in[which], per_head = s_cost[b];
-            }
-            const Seq s = load_seq(a, b);
-            const int units = units_of(a, s);
-            const int h = (in_seq | per_head) >> 32 ? (int)(in_seq / per_head) : (int)((unsigned)in_seq / (unsigned)per_head);
-            const long long want = in_seq - h * per_head;
-            long long before = 0;
-            int u = 0, o = 0, cost = 0;
-            for (int u0 = 0; u0 < units; u0 += 32) {
-                const int c = u0 + lane < units ? cost_of(a, s, u0 + lane) : 0;
-                const long long sum = warp_scan(c, lane);
-                const unsigned ends_later = __ballot_sync(0xffffffffu, before + sum > want);
-                if (ends_later != 0) {
-                    const int k = __ffs(ends_later) - 1;
-                    u = u0 + k;
-                    cost = __shfl_sync(0xffffffffu, c, k);
-                    o = (int)(want - (before + __shfl_sync(0xffffffffu, sum, k) - cost));
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, sum, 31);
-            }
-            // parts of a unit have kMinPart tiles at least: the boundary moves to the unit's begin or end
-            if (o < kMinPart) {
-                pos -= o;
-                o = 0;
-            } else if (cost - o < kMinPart) {
-                pos += cost - o;
-                o = 0;
-                ++u;
-            }
-            if (which == 0) walk.s = s, walk.h = h, walk.u = u, walk.o = o, walk.units = units;
-        }
-        at[which] = pos;
+    long long pos = min(walk.piece * (blockIdx.x + which), total);
+    walk.at = pos;
+    if (pos >= total) return pos;
+    int b;
+    long long in_seq, per_head;
+    if (a.B <= 32) {
+        b = __popc(__ballot_sync(0xffffffffu, inc <= pos));
+        in_seq = pos - __shfl_sync(0xffffffffu, inc - mine * a.Hkv, b);
+        per_head = __shfl_sync(0xffffffffu, mine, b);
+    } else {
+        b = s_seq[which], in_seq = s_in[which], per_head = s_cost[b];
     }
-    walk.at = at[0], walk.end = at[1];
+    const Seq s = load_seq(a, b);
+    const int units = units_of(a, s);
+    const int h = (in_seq | per_head) >> 32 ? (int)(in_seq / per_head) : (int)((unsigned)in_seq / (unsigned)per_head);
+    const long long want = in_seq - h * per_head;
+    long long before = 0;
+    int u = 0, o = 0, cost = 0;
+    for (int u0 = 0; u0 < units; u0 += 32) {
+        const int c = u0 + lane < units ? cost_of(a, s, u0 + lane) : 0;
+        const long long sum = warp_scan(c, lane);
+        const unsigned ends_later = __ballot_sync(0xffffffffu, before + sum > want);
+        if (ends_later != 0) {
+            const int k = __ffs(ends_later) - 1;
+            u = u0 + k;
+            cost = __shfl_sync(0xffffffffu, c, k);
+            o = (int)(want - (before + __shfl_sync(0xffffffffu, sum, k) - cost));
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    // parts of a unit have kMinPart tiles at least: the boundary moves to the unit's begin or end
+    if (o < kMinPart) {
+        pos -= o;
+        o = 0;
+    } else if (cost - o < kMinPart) {
+        pos += cost - o;
+        o = 0;
+        ++u;
+    }
+    walk.s = s, walk.h = h, walk.u = u, walk.o = o, walk.units = units;
+    walk.at = pos;
+    return pos;
 }
+// lane 0's value, which the compiler then knows to be the same in all lanes
+template <typename V>
+__device__ __forceinline__ V uniform(V v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ void pair_sync() { asm volatile("bar.sync 1, 64;" ::: "memory"); }  // of the planning and the edge warp
 
 // T: type of q and the cache; O: type of the output; GEN: scores are capped or biased, or the scale has a sign or
 // size for which the maximum cannot be taken before it.
@@ -339,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Piece s_piece[kPieces];
     __shared__ uint32_t s_tmem;
     __shared__ long long s_scan[kThreads / 32];
+    __shared__ long long s_end;   // of this CTA's share
     __shared__ int s_seq[2];      // the sequences in which this CTA's share begins and ends, -1: behind the last tile,
     __shared__ long long s_in[2];  // and the places in them
     uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
@@ -348,13 +352,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == kMmaWarp) tc::alloc(&s_tmem, kCols);
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.raw[i], 1), mbar_init(&bar.empty[i], 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.raw[i], 1), mbar_init(&bar.empty[i], 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_free[i], 1), mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) mbar_init(&bar.piece_full[i], 1), mbar_init(&bar.piece_empty[i], kReaders);
-        mbar_init(&bar.gave_up, 1);
+        mbar_init(&bar.gave_up, 2);
         fence_mbar_init();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned int* const err = &g_prompt_error;
 
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---- softmax: a thread has a row of its half ----
         const int half = warp >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -574,15 +578,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_before();
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         Reader reader;
-        if (warp == kLoadWarp) {
-            // ---- keys and values, a tile at a time, page by page ----
-            uint32_t stage = 0, parity = 1;
+        if (warp == kKeyWarp || warp == kValueWarp) {
+            // ---- keys or values, a tile at a time, page by page; the ring has them in turn ----
+            const bool values = warp == kValueWarp;
+            const CUtensorMap* map = values ? &v_map : &k_map;
+            uint32_t stage = values, parity = 1;
             bool fine = true;
             const int boxes = kTile / a.box;
-            uint64_t* last[kStages] = {};  // barrier of each stage's last copy, and its parity
-            uint32_t last_parity = 0, raw_parity = 0;
+            uint32_t used = 0, on_raw = 0, last_parity = 0, raw_parity = 0;  // a bit for each stage: its last copy, for the way out
             int t0, t1, a0[2], a1[2], lo, hi, h;
             const int32_t* table;
             while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
                 table = a.page_table + (int64_t)p.b * a.max_pages;
             })) {
-                for (int t = t0; fine && t < t1; ++t) {
+                for (int t = t0; t < t1; ++t) {
                     if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
                     // lane i: box i of the tile
                     const int tok = t * kTile + lane * a.box;
@@ -600,237 +605,204 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool bad = want && (page < 0 || page >= a.n_pages);
                     const unsigned good = __ballot_sync(0xffffffffu, want && !bad), zero = __ballot_sync(0xffffffffu, bad);
                     const uint32_t bytes = (uint32_t)__popc(good) * (uint32_t)a.box * (kTile * 2);
-                    const bool edge = t * kTile < lo || (t + 1) * kTile > hi;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        if (!mbar_wait(&bar.empty[stage], parity, err)) {
-                            fine = false;
-                            break;
+                    fine = mbar_wait(&bar.empty[stage], parity, err);
+                    if (!fine) break;
+                    uint8_t* dst = ring + stage * kStageBytes;
+                    if (zero != 0) {  // keys and values of pages outside the cache count as zeros
+                        if (lane == 0) atomicOr(&g_prompt_page_error, 1u);
+                        for (unsigned z = zero; z != 0; z &= z - 1) {
+                            const int r0 = (__ffs(z) - 1) * a.box;
+                            for (int i = lane; i < a.box * 16; i += 32)
+                                *reinterpret_cast<uint4*>(dst + (i & 1) * kSpan + r0 * kTile + (i >> 1) * 16) = make_uint4(0, 0, 0, 0);
                         }
-                        uint8_t* dst = ring + stage * kStageBytes;
-                        if (zero != 0) {  // keys and values of pages outside the cache count as zeros
-                            if (lane == 0) atomicOr(&g_prompt_page_error, 1u);
-                            for (unsigned z = zero; z != 0; z &= z - 1) {
-                                const int r0 = (__ffs(z) - 1) * a.box;
-                                for (int i = lane; i < a.box * 16; i += 32)
-                                    *reinterpret_cast<uint4*>(dst + (i & 1) * kSpan + r0 * kTile + (i >> 1) * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async();
-                            __syncwarp();
-                        }
-                        // values with rows that nobody may see go through the edge warp
-                        uint64_t* b = kv == 1 && edge ? &bar.raw[stage] : &bar.full[stage];
-                        if (lane == 0) {
-                            if (bytes > 0) mbar_expect_tx(b, bytes);
-                            else mbar_arrive(b);
-                        }
+                        fence_proxy_async();
                         __syncwarp();
-                        const uint32_t bit = 1u << stage, phase = b == &bar.raw[stage] ? raw_parity & bit : parity != 0 ? 0u : bit;
-#pragma unroll
-                        for (int i = 0; i < kStages; ++i)
-                            if (i == (int)stage) last[i] = b;
-                        last_parity = (last_parity & ~bit) | phase;
-                        if (b == &bar.raw[stage]) raw_parity ^= bit;
-                        if (want && !bad) {
-                            const CUtensorMap* map = kv == 0 ? &k_map : &v_map;
-                            uint8_t* d = dst + lane * a.box * kTile;
-                            tma_load4(d, map, 0, in_page, h, page, b);
-                            tma_load4(d + kSpan, map, 64, in_page, h, page, b);
-                        }
-                        __syncwarp();
-                        if (++stage == kStages) stage = 0, parity ^= 1;
                     }
+                    // values with rows that nobody may see go through the edge warp
+                    const bool edge = values && (t * kTile < lo || (t + 1) * kTile > hi);
+                    uint64_t* b = edge ? &bar.raw[stage] : &bar.full[stage];
+                    if (lane == 0) {
+                        if (bytes > 0) mbar_expect_tx(b, bytes);
+                        else mbar_arrive(b);
+                    }
+                    __syncwarp();
+                    if (want && !bad) {
+                        uint8_t* d = dst + lane * a.box * kTile;
+                        tma_load4(d, map, 0, in_page, h, page, b);
+                        tma_load4(d + kSpan, map, 64, in_page, h, page, b);
+                    }
+                    __syncwarp();
+                    const uint32_t bit = 1u << stage;
+                    used |= bit;
+                    on_raw = edge ? on_raw | bit : on_raw & ~bit;
+                    last_parity = (last_parity & ~bit) | (edge ? raw_parity & bit : parity != 0 ? 0u : bit);
+                    if (edge) raw_parity ^= bit;
+                    stage += 2;
+                    if (stage >= kStages) stage -= kStages, parity ^= 1;
                 }
             }
-            // no copy and no arrival is on its way when the CTA leaves
-            for (int i = 0; fine && i < kStages; ++i) {
+            // No copy and no arrival is on its way when the CTA leaves: the ring's stages behind the last tile, in their
+            // order, are every other one for the keys and the ones between for the values.
+            for (int i = values; fine && i < kStages; i += 2) {
                 fine = mbar_wait(&bar.empty[stage], parity, err);
-                if (++stage == kStages) stage = 0, parity ^= 1;
+                stage += 2;
+                if (stage >= kStages) stage -= kStages, parity ^= 1;
             }
-            if (!fine) {
-#pragma unroll
+            if (!fine)
                 for (int i = 0; i < kStages; ++i)
-                    if (last[i] != nullptr) mbar_drain(last[i], last_parity >> i & 1u);
-            }
-        } else if (warp == kMmaWarp) {
-            // ---- products: S of the halves' next tile between the two halves' P V of this one ----
-            uint32_t stage = 0, parity = 0;  // of the ring
-            uint32_t q_parity = 0, p_parity = 0;  // a bit for each half
-            const uint32_t ring_addr = smem_addr(ring);
-            const uint64_t q_desc = tc::smem_desc_sw128(smem_addr(rows_smem), 16, 1024);
+                    if (used >> i & 1) mbar_drain(on_raw >> i & 1 ? &bar.raw[i] : &bar.full[i], last_parity >> i & 1);
+        } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            // ---- products of a half: while this warp waits for its half's softmax the other half's run ----
+            // An MMA's operands are uniform registers.  With one thread in a branch of its own, and operands that the
+            // compiler does not know to be uniform, a warp issued an MMA every 115 to 130 cycles; with elect and
+            // operands from lane 0 every 67 (64 is the tensor core's own time).
+            const int half = uniform(warp) - kMmaWarp;
+            uint32_t stage = 0, parity = 0, q_parity = 0, p_parity = 0;
+            const uint32_t ring_addr = uniform(smem_addr(ring)), q_addr = uniform(smem_addr(rows_smem)) + half * kRowBytes;
+            const uint32_t t_s = uniform(tmem) + kColS + half * kTile, t_o = uniform(tmem) + kColO + half * kTile;
+            const uint64_t q_desc = tc::smem_desc_sw128(q_addr, 16, 1024);
             const uint64_t k_desc = tc::smem_desc_sw128(ring_addr, 16, 1024), v_desc = tc::smem_desc_sw128(ring_addr, kSpan, 1024);
             bool fine = true;
-            struct Place {
-                int t, t1, a0[2], a1[2];
-                __device__ __forceinline__ bool active(int half) const { return t >= a0[half] && t < a1[half]; }
-            };
-            Place cur, nxt;
-            auto next_stage = [&]() {
-                if (++stage == kStages) stage = 0, parity ^= 1;
-            };
-            // the next tile that some half takes of this piece, from tile q.t on
-            auto in_piece = [&](Place& q) {
-                for (; q.t < q.t1; ++q.t)
-                    if (q.active(0) || q.active(1)) return true;
-                return false;
-            };
-            bool more = true;  // pieces
-            auto next_piece = [&](Place& q) {
-                more = reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
-                    q.t = p.t0, q.t1 = p.t1;
-                    q.a0[0] = p.a0[0], q.a0[1] = p.a0[1], q.a1[0] = p.a1[0], q.a1[1] = p.a1[1];
-                });
-                return more && in_piece(q);
-            };
-            auto scores = [&](const Place& q, int half, uint32_t k_stage) {
-                if (q.t == q.a0[half]) {
-                    if (!mbar_wait(&bar.q_full[half], q_parity >> half & 1, err)) return false;
-                    q_parity ^= 1u << half;
-                    tc::fence_after();
-                }
-                if (lane == 0) {
-                    const uint64_t qd = q_desc + half * (kRowBytes >> 4), kd = k_desc + k_stage * (kStageBytes >> 4);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t off = ((k >> 2) * kSpan + (k & 3) * 32) >> 4;
-                        tc::mma_f16_ss(tmem + kColS + half * kTile, qd + off, kd + off, kIdescS, k > 0);
-                    }
-                    tc::commit(&bar.s_full[half]);
-                    if (q.t + 1 == q.a1[half]) tc::commit(&bar.q_free[half]);
-                }
-                __syncwarp();
-                return true;
-            };
-            bool have = false;  // a tile whose scores are under way
-            while (fine) {
-                if (!have) {
-                    while (more && !have) have = next_piece(cur);
-                    if (!have) break;
+            int t, t1, a0, a1, b0, b1;  // tiles of the piece, of this half and of the other
+            while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
+                t = p.t0, t1 = p.t1, a0 = p.a0[half], a1 = p.a1[half], b0 = p.a0[half ^ 1], b1 = p.a1[half ^ 1];
+            })) {
+                for (; t < t1; ++t) {
+                    const bool mine = t >= a0 && t < a1;
+                    if (!mine && !(t >= b0 && t < b1)) continue;
                     fine = mbar_wait(&bar.full[stage], parity, err);
-                    tc::fence_after();
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        if (fine && cur.active(half)) fine = scores(cur, half, stage);
-                    if (fine && lane == 0) tc::commit(&bar.empty[stage]);
-                    __syncwarp();
-                    next_stage();
-                    if (!fine) break;
-                }
-                const uint32_t v_stage = stage, v_parity = parity;
-                next_stage();
-                nxt = cur;
-                ++nxt.t;
-                // One piece further at most before this tile's P V: the warps that wait for that may hold up those behind
-                // (a ring's length of pieces without keys would).
-                have = in_piece(nxt) || (more && next_piece(nxt));
-                const uint32_t k_stage = stage, k_parity = parity;
-                if (have) next_stage();
-                fine = mbar_wait(&bar.full[v_stage], v_parity, err);
-                if (fine && have) fine = mbar_wait(&bar.full[k_stage], k_parity, err);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (fine && cur.active(half)) {
-                        fine = mbar_wait(&bar.p_full[half], p_parity >> half & 1, err);
-                        p_parity ^= 1u << half;
+                    if (fine && mine && t == a0) {
+                        fine = mbar_wait(&bar.q_full[half], q_parity, err);
+                        q_parity ^= 1;
+                    }
+                    if (!__all_sync(0xffffffffu, fine)) break;
+                    if (mine) {
                         tc::fence_after();
-                        if (fine && lane == 0) {
-                            const uint64_t vd = v_desc + v_stage * (kStageBytes >> 4);
-                            const uint32_t more = cur.t > cur.a0[half];
+                        const uint32_t st = uniform(stage), last = uniform(t + 1 == a1);
+                        const uint64_t kd = k_desc + st * (kStageBytes >> 4);
+                        if (tc::elect()) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                tc::mma_f16_ts(tmem + kColO + half * kTile, tmem + kColS + half * kTile + 8 * k, vd + k * (2048 >> 4),
-                                               kIdescO, k > 0 ? 1u : more);
-                            if (cur.t + 1 == cur.a1[half]) tc::commit(&bar.o_full[half]);
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t off = ((k >> 2) * kSpan + (k & 3) * 32) >> 4;
+                                tc::mma_f16_ss(t_s, q_desc + off, kd + off, kIdescS, k > 0);
+                            }
+                            tc::commit(&bar.s_full[half]);
+                            tc::commit(&bar.empty[st]);
+                            if (last) tc::commit(&bar.q_free[half]);
                         }
                         __syncwarp();
+                    } else if (lane == 0) {
+                        mbar_arrive(&bar.empty[stage]);
                     }
-                    if (fine && have && nxt.active(half)) fine = scores(nxt, half, k_stage);
+                    if (++stage == kStages) stage = 0, parity ^= 1;
+                    fine = mbar_wait(&bar.full[stage], parity, err);
+                    if (fine && mine) {
+                        fine = mbar_wait(&bar.p_full[half], p_parity, err);
+                        p_parity ^= 1;
+                    }
+                    if (!__all_sync(0xffffffffu, fine)) break;
+                    if (mine) {
+                        tc::fence_after();
+                        const uint32_t st = uniform(stage), more = uniform(t > a0), last = uniform(t + 1 == a1);
+                        const uint64_t vd = v_desc + st * (kStageBytes >> 4);
+                        if (tc::elect()) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) tc::mma_f16_ts(t_o, t_s + 8 * k, vd + k * (2048 >> 4), kIdescO, k > 0 ? 1u : more);
+                            tc::commit(&bar.empty[st]);
+                            if (last) tc::commit(&bar.o_full[half]);
+                        }
+                        __syncwarp();
+                    } else if (lane == 0) {
+                        mbar_arrive(&bar.empty[stage]);
+                    }
+                    if (++stage == kStages) stage = 0, parity ^= 1;
                 }
-                if (fine && lane == 0) {
-                    tc::commit(&bar.empty[v_stage]);
-                    if (have) tc::commit(&bar.empty[k_stage]);
-                }
-                __syncwarp();
-                cur = nxt;
             }
             if (!fine) {
-                if (lane == 0) tc::commit(&bar.gave_up);
+                if (tc::elect()) tc::commit(&bar.gave_up);
                 __syncwarp();
                 mbar_drain(&bar.gave_up, 0);
             }
-        } else if (warp == kRowWarp) {
-            // ---- queries: rows of 256 bytes, gathered, chunk i of a row at i ^ (row mod 8) ----
-            uint32_t free_parity = 3;  // a bit for each half
+        } else if (warp == kRowWarp || warp == kRowWarp + 1) {
+            // ---- queries of a half: rows of 256 bytes, gathered, chunk i of a row at i ^ (row mod 8) ----
+            const int half = warp - kRowWarp;
+            uint32_t free_parity = 1;
             bool fine = true;
             // rows go along the heads of a token and on to the next token's (with one head: along the tokens)
             const int wrap = a.group > 1 ? a.group : 0x7fffffff, chunk = lane & 15;
             const int64_t step = a.group > 1 ? a.q_head_stride : a.q_token_stride;
             const int64_t wrap_step = a.q_token_stride - (int64_t)a.group * a.q_head_stride;
             const T* const base = static_cast<const T*>(a.q) + 8 * chunk;
-            int rows_of_unit, h, q0;
-            unsigned f0, some;
+            const uint32_t dst = smem_addr(rows_smem + half * kRowBytes) + (chunk >> 3) * kSpan + (lane >> 4) * kTile;
+            const uint32_t key = (uint32_t)(chunk & 7) ^ (uint32_t)(lane >> 4);
+            int rows, h, q0;
+            unsigned f;
+            bool some;
             while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
-                some = (p.a0[0] < p.a1[0] ? 1u : 0u) | (p.a0[1] < p.a1[1] ? 2u : 0u);
-                f0 = (unsigned)p.f0, h = p.h, q0 = p.q0, rows_of_unit = p.rows;
+                some = p.a0[half] < p.a1[half];
+                f = (unsigned)p.f0 + half * kHalf + (lane >> 4), h = p.h, q0 = p.q0, rows = p.rows - half * kHalf - (lane >> 4);
             })) {
-#pragma unroll 1
-                for (int half = 0; fine && half < 2; ++half) {
-                    if (!(some >> half & 1)) continue;
-                    const unsigned f = f0 + half * kHalf + (lane >> 4), token = f / (unsigned)a.group;
-                    int g = a.group > 1 ? (int)(f - token * a.group) : 0;
-                    const T* src = base + (int64_t)(q0 + (int)token) * a.q_token_stride + ((int64_t)h * a.group + g) * a.q_head_stride;
-                    if (!mbar_wait(&bar.q_free[half], free_parity >> half & 1, err)) {
-                        fine = false;
-                        break;
-                    }
-                    free_parity ^= 1u << half;
-                    const int rows = rows_of_unit - half * kHalf - (lane >> 4);
-                    const uint32_t dst = smem_addr(rows_smem + half * kRowBytes) + (chunk >> 3) * kSpan + (lane >> 4) * kTile;
-                    const uint32_t key = (uint32_t)(chunk & 7) ^ (uint32_t)(lane >> 4);
+                if (!some) continue;
+                const unsigned token = f / (unsigned)a.group;
+                int g = a.group > 1 ? (int)(f - token * a.group) : 0;
+                const T* src = base + (int64_t)(q0 + (int)token) * a.q_token_stride + ((int64_t)h * a.group + g) * a.q_head_stride;
+                fine = mbar_wait(&bar.q_free[half], free_parity, err);
+                if (!fine) break;
+                free_parity ^= 1;
 #pragma unroll 8
-                    for (int r = 0; r < kHalf; r += 2) {
-                        const bool real = r < rows;
-                        cp_async16(dst + r * kTile + ((key ^ (r & 6)) << 4), real ? src : base, real);
-                        src += 2 * step;
-                        g += 2;
-                        if (g >= wrap) g -= wrap, src += wrap_step;
-                    }
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.q_full[half]);
+                for (int r = 0; r < kHalf; r += 2) {
+                    const bool real = r < rows;
+                    cp_async16(dst + r * kTile + ((key ^ (r & 6)) << 4), real ? src : base, real);
+                    src += 2 * step;
+                    g += 2;
+                    if (g >= wrap) g -= wrap, src += wrap_step;
                 }
+                cp_async_commit();
+                cp_async_wait<0>();
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.q_full[half]);
             }
-            for (int half = 0; fine && half < 2; ++half) fine = mbar_wait(&bar.q_free[half], free_parity >> half & 1, err);
-        } else {
-            // ---- the plan, and values at the edges of what a unit sees: rows outside are zeros ----
+            if (fine) mbar_wait(&bar.q_free[half], free_parity, err);
+        } else if (warp == kPlanWarp) {
+            // ---- the plan ----
             Walk walk;
-            walk.at = walk.end = 0;
+            walk.at = 0;
             walk.units = 0;
-            plan(a, walk, total, s_seq, s_in, s_cost, lane);
-            fence_proxy_async();
-            uint32_t slot = 0, slot_parity = 1, stage = 0, raw_parity = 0;  // raw_parity: a bit for each stage
-            bool fine = true, more = true, have = false;
-            int t0 = 0, t1 = 0, a0[2], a1[2], lo = 0, hi = 0;
-            while (fine && (more || have)) {
-                // the next piece goes out before this one's edges are seen to
+            plan(a, walk, 0, total, s_seq, s_in, s_cost, lane);
+            pair_sync();
+            walk.end = s_end;
+            uint32_t slot = 0, parity = 1;
+            for (bool more = true; more;) {
                 Piece p;
-                if (more) {
-                    more = walk.next(a, p, lane);
-                    if (!more) p.t0 = 1, p.t1 = 0;
-                    fine = mbar_wait(&bar.piece_empty[slot], slot_parity, err);
-                    if (!fine) break;
-                    if (lane == 0) {
-                        s_piece[slot] = p;
-                        mbar_arrive(&bar.piece_full[slot]);
-                    }
-                    __syncwarp();
-                    if (++slot == kPieces) slot = 0, slot_parity ^= 1;
+                more = walk.next(a, p, lane);
+                if (!more) p.t0 = 1, p.t1 = 0;
+                if (!mbar_wait(&bar.piece_empty[slot], parity, err)) break;
+                if (lane == 0) {
+                    s_piece[slot] = p;
+                    mbar_arrive(&bar.piece_full[slot]);
                 }
-                for (int t = t0; have && fine && t < t1; ++t) {
+                __syncwarp();
+                if (++slot == kPieces) slot = 0, parity ^= 1;
+            }
+        } else {
+            // ---- the end of the share, for the plan; then values at the edges of what a unit sees: rows outside are zeros ----
+            {
+                Walk walk;
+                const long long end = plan(a, walk, 1, total, s_seq, s_in, s_cost, lane);
+                if (lane == 0) s_end = end;
+                fence_proxy_async();  // s_cost lies where the copies go, which wait for the plan
+                pair_sync();
+            }
+            uint32_t stage = 1, raw_parity = 0;  // the values' stage; a bit for each
+            bool fine = true;
+            int t0, t1, a0[2], a1[2], lo, hi;
+            while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
+                t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi;
+                a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
+            })) {
+                for (int t = t0; t < t1; ++t) {
                     if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
-                    if (++stage == kStages) stage = 0;  // the keys' stage
                     if (t * kTile < lo || (t + 1) * kTile > hi) {
                         fine = mbar_wait(&bar.raw[stage], (raw_parity >> stage) & 1, err);
                         if (!fine) break;
@@ -845,11 +817,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar.full[stage]);
                     }
-                    if (++stage == kStages) stage = 0;
+                    stage += 2;
+                    if (stage >= kStages) stage -= kStages;
                 }
-                have = more;
-                t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi;
-                a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
             }
         }
     }
