@@ -175,6 +175,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack2(float x, float y, __nv_bfloat16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -207,7 +212,7 @@ __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int
 
 struct Barriers {
     uint64_t full[kStages], raw[kStages], empty[kStages];
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], turn[2];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t gave_up;
 };
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.raw[i], 1), mbar_init(&bar.empty[i], 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1), mbar_init(&bar.q_free[i], 1), mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
+            mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1), mbar_init(&bar.turn[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) mbar_init(&bar.piece_full[i], 1), mbar_init(&bar.piece_empty[i], kReaders);
         mbar_init(&bar.gave_up, 2);
@@ -468,8 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-                    for (int i = 0; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i >> 5][i & 31]));
-                    const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+                    for (int i = 0; i < 128; i += 2)
+                        mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(x[i >> 5][i & 31]), __uint_as_float(x[i >> 5][(i & 31) + 1]));
+                    const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], m);
                     if (__any_sync(0xffffffffu, (top - m) * c > kGrow)) {
                         const float scale = top > m ? exp2_fast((m - top) * c) : 1.f;
                         m = top;
@@ -657,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // compiler does not know to be uniform, a warp issued an MMA every 115 to 130 cycles; with elect and
             // operands from lane 0 every 67 (64 is the tensor core's own time).
             const int half = uniform(warp) - kMmaWarp;
-            uint32_t stage = 0, parity = 0, q_parity = 0, p_parity = 0;
+            uint32_t stage = 0, parity = 0, q_parity = 0, p_parity = 0, turn_parity = half == 0;  // half 0 goes first
             const uint32_t ring_addr = uniform(smem_addr(ring)), q_addr = uniform(smem_addr(rows_smem)) + half * kRowBytes;
             const uint32_t t_s = uniform(tmem) + kColS + half * kTile, t_o = uniform(tmem) + kColO + half * kTile;
             const uint64_t q_desc = tc::smem_desc_sw128(q_addr, 16, 1024);
@@ -667,56 +673,79 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
                 t = p.t0, t1 = p.t1, a0 = p.a0[half], a1 = p.a1[half], b0 = p.a0[half ^ 1], b1 = p.a1[half ^ 1];
             })) {
-                for (; t < t1; ++t) {
-                    const bool mine = t >= a0 && t < a1;
-                    if (!mine && !(t >= b0 && t < b1)) continue;
-                    fine = mbar_wait(&bar.full[stage], parity, err);
-                    if (fine && mine && t == a0) {
-                        fine = mbar_wait(&bar.q_full[half], q_parity, err);
-                        q_parity ^= 1;
+                auto pass = [&](uint32_t& st, uint32_t& par) {
+                    if (++st == kStages) st = 0, par ^= 1;
+                };
+                auto my_turn = [&]() {
+                    const bool got = mbar_wait(&bar.turn[half], turn_parity, err);
+                    turn_parity ^= 1;
+                    return got;
+                };
+                auto skip = [&]() {  // a tile that only the other half takes
+                    for (int i = 0; fine && i < 2; ++i) {
+                        fine = __all_sync(0xffffffffu, mbar_wait(&bar.full[stage], parity, err));
+                        if (lane == 0) mbar_arrive(&bar.empty[stage]);
+                        pass(stage, parity);
                     }
-                    if (!__all_sync(0xffffffffu, fine)) break;
-                    if (mine) {
-                        tc::fence_after();
-                        const uint32_t st = uniform(stage), last = uniform(t + 1 == a1);
-                        const uint64_t kd = k_desc + st * (kStageBytes >> 4);
-                        if (tc::elect()) {
+                    fine = __all_sync(0xffffffffu, fine && my_turn());
+                    if (lane == 0) mbar_arrive(&bar.turn[half ^ 1]);
+                };
+                auto scores = [&](uint32_t st) {  // by the elected lane
+                    const uint64_t kd = k_desc + st * (kStageBytes >> 4);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const uint32_t off = ((k >> 2) * kSpan + (k & 3) * 32) >> 4;
-                                tc::mma_f16_ss(t_s, q_desc + off, kd + off, kIdescS, k > 0);
-                            }
-                            tc::commit(&bar.s_full[half]);
-                            tc::commit(&bar.empty[st]);
-                            if (last) tc::commit(&bar.q_free[half]);
-                        }
-                        __syncwarp();
-                    } else if (lane == 0) {
-                        mbar_arrive(&bar.empty[stage]);
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t off = ((k >> 2) * kSpan + (k & 3) * 32) >> 4;
+                        tc::mma_f16_ss(t_s, q_desc + off, kd + off, kIdescS, k > 0);
                     }
-                    if (++stage == kStages) stage = 0, parity ^= 1;
-                    fine = mbar_wait(&bar.full[stage], parity, err);
-                    if (fine && mine) {
-                        fine = mbar_wait(&bar.p_full[half], p_parity, err);
-                        p_parity ^= 1;
-                    }
+                    tc::commit(&bar.s_full[half]);
+                };
+                if (a0 >= a1) a0 = a1 = t1;
+                for (; fine && t < a0; ++t)
+                    if (t >= b0 && t < b1) skip();
+                if (fine && t < a1) {
+                    fine = mbar_wait(&bar.full[stage], parity, err) && mbar_wait(&bar.q_full[half], q_parity, err);
+                    q_parity ^= 1;
                     if (!__all_sync(0xffffffffu, fine)) break;
-                    if (mine) {
-                        tc::fence_after();
-                        const uint32_t st = uniform(stage), more = uniform(t > a0), last = uniform(t + 1 == a1);
-                        const uint64_t vd = v_desc + st * (kStageBytes >> 4);
-                        if (tc::elect()) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) tc::mma_f16_ts(t_o, t_s + 8 * k, vd + k * (2048 >> 4), kIdescO, k > 0 ? 1u : more);
-                            tc::commit(&bar.empty[st]);
-                            if (last) tc::commit(&bar.o_full[half]);
-                        }
-                        __syncwarp();
-                    } else if (lane == 0) {
-                        mbar_arrive(&bar.empty[stage]);
+                    tc::fence_after();
+                    const uint32_t st = uniform(stage), last = uniform(a0 + 1 == a1);
+                    if (tc::elect()) {
+                        scores(st);
+                        tc::commit(&bar.empty[st]);
+                        if (last) tc::commit(&bar.q_free[half]);
                     }
-                    if (++stage == kStages) stage = 0, parity ^= 1;
+                    __syncwarp();
+                    pass(stage, parity);
                 }
+                for (; fine && t < a1; ++t) {
+                    // this tile's values, the next one's keys, this half's probabilities, and the other half's products done
+                    uint32_t k_stage = stage, k_parity = parity;
+                    pass(k_stage, k_parity);
+                    const uint32_t vs = uniform(stage), ks = uniform(k_stage), more = uniform(t > a0), left = uniform(a1 - t - 1);
+                    const uint64_t vd = v_desc + vs * (kStageBytes >> 4);
+                    fine = mbar_wait(&bar.full[stage], parity, err) && (left == 0 || mbar_wait(&bar.full[k_stage], k_parity, err)) &&
+                           mbar_wait(&bar.p_full[half], p_parity, err) && my_turn();
+                    p_parity ^= 1;
+                    if (!__all_sync(0xffffffffu, fine)) break;
+                    tc::fence_after();
+                    if (tc::elect()) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) tc::mma_f16_ts(t_o, t_s + 8 * k, vd + k * (2048 >> 4), kIdescO, k > 0 ? 1u : more);
+                        if (left > 0) {
+                            scores(ks);
+                            tc::commit(&bar.empty[ks]);
+                            if (left == 1) tc::commit(&bar.q_free[half]);
+                        } else {
+                            tc::commit(&bar.o_full[half]);
+                        }
+                        tc::commit(&bar.empty[vs]);
+                        mbar_arrive(&bar.turn[half ^ 1]);
+                    }
+                    __syncwarp();
+                    pass(stage, parity);
+                    if (left > 0) pass(stage, parity);
+                }
+                for (; fine && t < t1; ++t)
+                    if (t >= b0 && t < b1) skip();
             }
             if (!fine) {
                 if (tc::elect()) tc::commit(&bar.gave_up);
