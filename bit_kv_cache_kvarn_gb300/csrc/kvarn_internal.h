@@ -241,6 +241,7 @@ struct PromptArgs {
     // set by the launcher: query heads per kv head, tokens of a copy, rows of a partial slot, whether 32-byte
     // stores are aligned, log2 of a page size that is a power of two (else -1)
     int group, box, slot_rows, wide_out, page_shift;
+    uint32_t group_mul, group_shift;  // division by the group
     float scale, softcap, inv_softcap;
     const void* q;
     int64_t q_token_stride, q_head_stride;

@@ -44,6 +44,11 @@ constexpr float kHalfLift = 7.f;                 // fp16 probabilities are multi
 constexpr int kSerialUnits = 16;                 // of a sequence, whose tiles one lane counts
 constexpr int kJoinRows = 32, kJoinThreads = 256;
 
+// Workspace: partial slots (fp32), two per CTA: slot 0 for the unit that began before the CTA's share, slot 1 for the
+// one that begins in it and goes on after it; then one Join per CTA.  A slot holds o as [32 groups of four
+// channels][rows][4], so that neighbouring rows' threads read and write neighbouring 16 bytes, then m[rows] (log2
+// domain) and l[rows].
+
 struct Join {
     int b, h, u, last;  // the unit that slot 1 begins and the last CTA that holds a part; b = -1: none
 };
@@ -70,6 +75,10 @@ __device__ __forceinline__ Seq load_seq(const PromptArgs& a, int b) {
     s.start = a.kv_starts != nullptr ? max(a.kv_starts[b], 0) : 0;
     return s;
 }
+// f / group for f below 2^31
+__device__ __forceinline__ unsigned token_of(const PromptArgs& a, unsigned f) {
+    return a.group == 1 ? f : __umulhi(f, a.group_mul) >> a.group_shift;
+}
 __device__ __forceinline__ int units_of(const PromptArgs& a, const Seq& s) {
     return (int)(((unsigned)s.n * (unsigned)a.group + kUnit - 1) / kUnit);
 }
@@ -85,9 +94,8 @@ __device__ __forceinline__ Keys keys_of(const PromptArgs& a, const Seq& s, unsig
     if (f1 <= f0) k.hi = k.lo;
     if (a.causal && f1 > f0) {
         const int shift = s.len - s.n;
-        const int p0 = shift + (int)(f0 / (unsigned)a.group), p1 = shift + (int)((f1 - 1) / (unsigned)a.group);
-        k.hi = min(k.hi, p1 + 1);
-        if (a.window > 0) k.lo = max(k.lo, p0 + 1 - a.window);
+        k.hi = min(k.hi, shift + (int)token_of(a, f1 - 1) + 1);
+        if (a.window > 0) k.lo = max(k.lo, shift + (int)token_of(a, f0) + 1 - a.window);
     }
     return k;
 }
@@ -170,6 +178,8 @@ struct Walk {
     }
 };
 
+// the low n bits (none for n <= 0, all for n >= 32)
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -235,10 +245,11 @@ struct Reader {
 };
 
 
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {
-#pragma unroll
+template <typename V>
+__device__ __forceinline__ V warp_scan(V v, int lane) {
+#pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, v, d);
+        const V o = __shfl_up_sync(0xffffffffu, v, d);
         if (lane >= d) v += o;
     }
     return v;
@@ -256,6 +267,7 @@ __device__ __forceinline__ long long seq_cost(const PromptArgs& a, int base, int
     const int n = units_of(a, s);
     long long cost = 0;
     if (n <= kSerialUnits)
+#pragma unroll 1
         for (int u = 0; u < n; ++u) cost += cost_of(a, s, u);
     for (unsigned many = __ballot_sync(0xffffffffu, n > kSerialUnits); many != 0; many &= many - 1) {
         const int k = __ffs(many) - 1;
@@ -266,9 +278,8 @@ __device__ __forceinline__ long long seq_cost(const PromptArgs& a, int base, int
         w.start = __shfl_sync(0xffffffffu, s.start, k);
         const int nw = units_of(a, w);
         long long sum = 0;
-        for (int u = lane; u < nw; u += 32) sum += cost_of(a, w, u);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll 1
+        for (int u = 0; u < nw; u += 32) sum += __reduce_add_sync(0xffffffffu, u + lane < nw ? (unsigned)cost_of(a, w, u + lane) : 0u);
         if (lane == k) cost = sum;
     }
     return cost;
@@ -302,18 +313,19 @@ __device__ __forceinline__ long long plan(const PromptArgs& a, Walk& walk, int w
     const long long want = in_seq - h * per_head;
     long long before = 0;
     int u = 0, o = 0, cost = 0;
+#pragma unroll 1
     for (int u0 = 0; u0 < units; u0 += 32) {
-        const int c = u0 + lane < units ? cost_of(a, s, u0 + lane) : 0;
-        const long long sum = warp_scan(c, lane);
-        const unsigned ends_later = __ballot_sync(0xffffffffu, before + sum > want);
-        if (ends_later != 0) {
-            const int k = __ffs(ends_later) - 1;
+        const unsigned c = u0 + lane < units ? (unsigned)cost_of(a, s, u0 + lane) : 0u;  // (32 of them fit 32 bits)
+        const unsigned all = __reduce_add_sync(0xffffffffu, c);
+        if (before + all > want) {
+            const unsigned sum = warp_scan(c, lane), in = (unsigned)(want - before);
+            const int k = __popc(__ballot_sync(0xffffffffu, sum <= in));
             u = u0 + k;
-            cost = __shfl_sync(0xffffffffu, c, k);
-            o = (int)(want - (before + __shfl_sync(0xffffffffu, sum, k) - cost));
+            cost = (int)__shfl_sync(0xffffffffu, c, k);
+            o = (int)(in - __shfl_sync(0xffffffffu, sum - c, k));
             break;
         }
-        before += __shfl_sync(0xffffffffu, sum, 31);
+        before += all;
     }
     // parts of a unit have kMinPart tiles at least: the boundary moves to the unit's begin or end
     if (o < kMinPart) {
@@ -433,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = p.rows;
             const bool real = r < rows;
             const unsigned f = (unsigned)p.f0 + half * kHalf + r;
-            const int token = (int)(f / (unsigned)a.group), head = p.h * a.group + (int)(f - (unsigned)token * a.group);
+            const int token = (int)token_of(a, f), head = p.h * a.group + (int)(f - (unsigned)token * a.group);
             const int pos = p.shift + token;
             int lo = p.start, hi = p.len;
             if (a.causal) {
@@ -468,8 +480,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (__any_sync(0xffffffffu, lo_in > 0 || hi_in < kTile)) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i)
-                            if (i < lo_in || i >= hi_in) x[i >> 5][i & 31] = 0xff800000u;
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t seen = bits_below(hi_in - 32 * i) & ~bits_below(lo_in - 32 * i);
+                            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[i][k] = (seen & (1u << k)) != 0 ? x[i][k] : 0xff800000u;
+                        }
                     }
                     float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
@@ -544,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 32; ++k) o[k] = 0u;
                     }
                     if (!real) continue;
-                    if (whole && sizeof(O) == 2) {
+                    if (sizeof(O) == 2 && whole) {
                         O* out = static_cast<O*>(a.out) + row * kTile + 32 * i;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
@@ -556,18 +572,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             store32(out + 16 * k, w, a.wide_out);
                         }
-                    } else {
-                        float* out = whole ? static_cast<float*>(a.out) + row * kTile + 32 * i : slot + rr * kTile + 32 * i;
+                    } else if (whole) {
+                        float* out = static_cast<float*>(a.out) + row * kTile + 32 * i;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint32_t w[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float x0 = __uint_as_float(o[8 * k + e]);
-                                w[e] = __float_as_uint(whole ? (l != 0.f ? x0 * inv : 0.f) : x0);
-                            }
+                            for (int e = 0; e < 8; ++e) w[e] = l != 0.f ? __float_as_uint(__uint_as_float(o[8 * k + e]) * inv) : 0u;
                             store32(out + 8 * k, w, a.wide_out);
                         }
+                    } else {
+                        uint4* out = reinterpret_cast<uint4*>(slot) + (size_t)8 * i * a.slot_rows + rr;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) out[(size_t)k * a.slot_rows] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
                 }
             }
@@ -757,34 +774,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int half = warp - kRowWarp;
             uint32_t free_parity = 1;
             bool fine = true;
-            // rows go along the heads of a token and on to the next token's (with one head: along the tokens)
-            const int wrap = a.group > 1 ? a.group : 0x7fffffff, chunk = lane & 15;
-            const int64_t step = a.group > 1 ? a.q_head_stride : a.q_token_stride;
-            const int64_t wrap_step = a.q_token_stride - (int64_t)a.group * a.q_head_stride;
-            const T* const base = static_cast<const T*>(a.q) + 8 * chunk;
+            const int chunk = lane & 15;
             const uint32_t dst = smem_addr(rows_smem + half * kRowBytes) + (chunk >> 3) * kSpan + (lane >> 4) * kTile;
             const uint32_t key = (uint32_t)(chunk & 7) ^ (uint32_t)(lane >> 4);
+            const T* const base = static_cast<const T*>(a.q) + 8 * chunk;
             int rows, h, q0;
-            unsigned f;
+            unsigned f0;
             bool some;
             while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
                 some = p.a0[half] < p.a1[half];
-                f = (unsigned)p.f0 + half * kHalf + (lane >> 4), h = p.h, q0 = p.q0, rows = p.rows - half * kHalf - (lane >> 4);
+                f0 = (unsigned)p.f0 + half * kHalf, h = p.h, q0 = p.q0, rows = p.half_rows(half);
             })) {
                 if (!some) continue;
-                const unsigned token = f / (unsigned)a.group;
-                int g = a.group > 1 ? (int)(f - token * a.group) : 0;
-                const T* src = base + (int64_t)(q0 + (int)token) * a.q_token_stride + ((int64_t)h * a.group + g) * a.q_head_stride;
                 fine = mbar_wait(&bar.q_free[half], free_parity, err);
                 if (!fine) break;
                 free_parity ^= 1;
-#pragma unroll 8
-                for (int r = 0; r < kHalf; r += 2) {
-                    const bool real = r < rows;
-                    cp_async16(dst + r * kTile + ((key ^ (r & 6)) << 4), real ? src : base, real);
-                    src += 2 * step;
-                    g += 2;
-                    if (g >= wrap) g -= wrap, src += wrap_step;
+                for (int r0 = 0; r0 < kHalf; r0 += 32) {
+                    // each lane finds one row's place, then all copy two rows at a time
+                    const unsigned f = f0 + min(r0 + lane, rows - 1), token = token_of(a, f);
+                    const int64_t at = (int64_t)(q0 + (int)token) * a.q_token_stride +
+                                       (int64_t)(h * a.group + (int)(f - token * a.group)) * a.q_head_stride;
+#pragma unroll
+                    for (int r = 0; r < 32; r += 2) {
+                        const T* src = base + __shfl_sync(0xffffffffu, at, r + (lane >> 4));
+                        cp_async16(dst + (r0 + r) * kTile + ((key ^ (r & 6)) << 4), src, r0 + r + (lane >> 4) < rows);
+                    }
                 }
                 cp_async_commit();
                 cp_async_wait<0>();
@@ -857,9 +871,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Parts of the units that several CTAs share, joined: CTA (c, y) takes kJoinRows rows of the unit that begins in the
-// split's CTA c and goes on after it, a warp a row at a time, a lane four channels.
+// split's CTA c and goes on after it.  A warp's lanes take the rows and four of the slots' groups of channels each; the
+// rows are turned in shared memory and written whole.
 template <typename T, typename O>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a) {
+    constexpr int kGroups = kTile / 4 / (kJoinThreads / 32);
+    __shared__ float4 s_out[kJoinRows][kTile / 4 + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -869,36 +886,52 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a)
     if (jn.b < 0) return;
     const Seq s = load_seq(a, jn.b);
     const unsigned f0 = (unsigned)jn.u * kUnit;
-    const int rows = (int)(min(f0 + kUnit, (unsigned)s.n * (unsigned)a.group) - f0);
-    const int past = min(rows, (int)(blockIdx.y + 1) * kJoinRows);
-    for (int r = blockIdx.y * kJoinRows + warp; r < past; r += kJoinThreads / 32) {
-        float m = -CUDART_INF_F, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = c0; c <= jn.last; ++c) {
-            const float* slot = ws.slot(c, c == c0 ? 1 : 0);
-            const float4 po = *reinterpret_cast<const float4*>(slot + r * kTile + 4 * lane);
-            const float pm = slot[a.slot_rows * kTile + r], pl = slot[a.slot_rows * kTile + a.slot_rows + r];
-            const float top = fmaxf(m, pm), ref = top == -CUDART_INF_F ? 0.f : top;
-            const float x = exp2f(m - ref), y = exp2f(pm - ref);
-            m = top;
-            l = fmaf(y, pl, x * l);
-            o.x = fmaf(y, po.x, x * o.x);
-            o.y = fmaf(y, po.y, x * o.y);
-            o.z = fmaf(y, po.z, x * o.z);
-            o.w = fmaf(y, po.w, x * o.w);
+    const int rows = (int)(min(f0 + kUnit, (unsigned)s.n * (unsigned)a.group) - f0) - (int)blockIdx.y * kJoinRows;
+    if (rows <= 0) return;
+    const int r = blockIdx.y * kJoinRows + min(lane, rows - 1);
+    float m = -CUDART_INF_F, l = 0.f;
+    float4 o[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int c = c0; c <= jn.last; ++c) {
+        const float* slot = ws.slot(c, c == c0 ? 1 : 0);
+        float4 po[kGroups];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            po[g] = reinterpret_cast<const float4*>(slot)[(size_t)(warp * kGroups + g) * a.slot_rows + r];
+        const float pm = slot[a.slot_rows * kTile + r], pl = slot[a.slot_rows * kTile + a.slot_rows + r];
+        const float top = fmaxf(m, pm), ref = top == -CUDART_INF_F ? 0.f : top;
+        const float x = exp2f(m - ref), y = exp2f(pm - ref);
+        m = top;
+        l = fmaf(y, pl, x * l);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            o[g].x = fmaf(y, po[g].x, x * o[g].x);
+            o[g].y = fmaf(y, po[g].y, x * o[g].y);
+            o[g].z = fmaf(y, po[g].z, x * o[g].z);
+            o[g].w = fmaf(y, po[g].w, x * o[g].w);
         }
-        const unsigned f = f0 + r;
-        const int token = (int)(f / (unsigned)a.group), head = jn.h * a.group + (int)(f - (unsigned)token * a.group);
-        const int64_t row = (int64_t)(s.q0 + token) * a.Hq + head;
-        const float inv = 1.f / l;
-        o = l != 0.f ? make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+        s_out[lane][warp * kGroups + g] =
+            l != 0.f ? make_float4(o[g].x * inv, o[g].y * inv, o[g].z * inv, o[g].w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (warp == 0 && lane < rows && a.lse != nullptr) {
+        const unsigned f = f0 + r, token = token_of(a, f);
+        a.lse[(int64_t)(s.q0 + (int)token) * a.Hq + jn.h * a.group + (int)(f - token * a.group)] =
+            l != 0.f ? (m + (log2f(l) - (std::is_same<T, __half>::value ? kHalfLift : 0.f))) * 0.69314718055994531f : -CUDART_INF_F;
+    }
+    __syncthreads();
+    for (int i = warp; i < min(rows, kJoinRows); i += kJoinThreads / 32) {
+        const unsigned f = f0 + blockIdx.y * kJoinRows + i, token = token_of(a, f);
+        const int64_t row = (int64_t)(s.q0 + (int)token) * a.Hq + jn.h * a.group + (int)(f - token * a.group);
+        const float4 v = s_out[i][lane];
         if (sizeof(O) == 2)
-            *reinterpret_cast<uint2*>(static_cast<O*>(a.out) + row * kTile + 4 * lane) = make_uint2(pack2(o.x, o.y, T()), pack2(o.z, o.w, T()));
+            *reinterpret_cast<uint2*>(static_cast<O*>(a.out) + row * kTile + 4 * lane) = make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
         else
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kTile + 4 * lane) = o;
-        if (a.lse != nullptr && lane == 0)
-            a.lse[row] = l != 0.f ? (m + (log2f(l) - (std::is_same<T, __half>::value ? kHalfLift : 0.f))) * 0.69314718055994531f : -CUDART_INF_F;
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kTile + 4 * lane) = v;
     }
 }
 
@@ -987,6 +1020,12 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     if (e != cudaSuccess) return e;
     a.group = a.Hq / a.Hkv;
     a.slot_rows = slot_rows(a.T, a.Hq, a.Hkv);
+    // f / group = (f * mul) >> (32 + shift) for f < 2^31: mul = floor(2^(31 + s) / group) + 1, s = ceil(log2 group), is
+    // off by less than 2^s / 2^31 of its quotient's last place times f
+    int log2_group = 0;
+    while ((1 << log2_group) < a.group) ++log2_group;
+    a.group_shift = log2_group > 0 ? log2_group - 1 : 0;
+    a.group_mul = (uint32_t)((1ull << (31 + log2_group)) / (unsigned)a.group + 1);
     a.inv_softcap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     a.box = a.page_size % 128 == 0 ? 128 : a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
