@@ -238,10 +238,11 @@ constexpr int kMaxPromptSeqs = 16384;  // tiles of each sequence in shared memor
 struct PromptArgs {
     int B, T, Hq, Hkv, page_size, max_pages, max_len, window, causal, out_dtype;
     int64_t n_pages;
-    // set by the launcher: query heads per kv head, tokens of a copy, rows of a partial slot, whether 32-byte
-    // stores are aligned, log2 of a page size that is a power of two (else -1)
-    int group, box, slot_rows, wide_out, page_shift;
+    // set by the launcher: query heads per kv head, tokens of a copy, rows of a partial slot, log2 of a page size that
+    // is a power of two (else -1), whether rows come by tiled copies, whether 32-byte stores of the output are aligned
+    int group, box, slot_rows, page_shift, tiled_rows, wide_out;
     uint32_t group_mul, group_shift;  // division by the group
+    uint64_t grid_mul;                // and by the split's CTAs: 2^64 / ctas, rounded up (0: one CTA)
     float scale, softcap, inv_softcap;
     const void* q;
     int64_t q_token_stride, q_head_stride;

@@ -157,19 +157,21 @@ struct Walk {
         const int first = keys.first(), cost = max(keys.past() - first, 1);
         const int o1 = (int)min((long long)cost, o + (end - at));
         p.t0 = first + o, p.t1 = first + o1;
+        // the halves: lanes 0 and 1
+        const Keys k = keys_of(a, s, min(f0 + (lane & 1) * kHalf, past), min(f0 + ((lane & 1) + 1) * kHalf, past));
+        const int a0 = max(k.first(), p.t0), a1 = min(k.past(), p.t1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const Keys k = keys_of(a, s, min(f0 + half * kHalf, past), min(f0 + (half + 1) * kHalf, past));
-            p.a0[half] = max(k.first(), p.t0);
-            p.a1[half] = min(k.past(), p.t1);
+            p.a0[half] = __shfl_sync(0xffffffffu, a0, half);
+            p.a1[half] = __shfl_sync(0xffffffffu, a1, half);
         }
         p.starts = o == 0, p.ends = o1 == cost;
         p.last = 0;
         if (p.starts && !p.ends) {
             // the CTA that takes the unit's last tile; its boundary may have moved to the unit's end
             const long long unit_end = at - o + cost;
-            p.last = (int)((unit_end - 1) / piece);
-            if (unit_end - piece * p.last < kMinPart) --p.last;
+            p.last = blockIdx.x;
+            while (unit_end - piece * (p.last + 1) >= kMinPart) ++p.last;
         }
         at += o1 - o;
         o = 0;
@@ -198,7 +200,9 @@ __device__ __forceinline__ uint32_t pack2(float x, float y, __half) {
     const __half2 h = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 32 bytes, aligned so where wide says it
+// mbar_wait in as few instructions as possible: the kernel has three dozen of these, and with each poll loop unrolled
+// its code was 145 KB, more than the instruction caches hold (a unit's epilogue took 4600 cycles instead of EPI).
+// 32 bytes, in one store where `wide` says that they are aligned
 __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool wide) {
     if (wide) {
         asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
@@ -209,6 +213,34 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool wi
         static_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
     }
 }
+template <bool QUIET = false>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned int* err) {
+    const uint32_t addr = smem_addr(bar);
+    uint32_t began = 0;
+#pragma unroll 1
+    for (uint32_t i = 0; i < (uint32_t)kSpinLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 255) == 0) {
+            if (!QUIET && *reinterpret_cast<volatile unsigned int*>(err)) return false;
+            uint32_t now;
+            asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
+            if (i == 0) began = now;
+            else if (now - began > (uint32_t)kWaitNs) break;
+        }
+    }
+    if (!QUIET) atomicOr(err, kErrTmaTimeout);
+    return false;
+}
+// after a wait that gave up: for a copy or products of this CTA, by time only
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+    wait_for<true>(bar, parity, nullptr);
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -217,6 +249,14 @@ __device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
             smem_addr(dst)),
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
         : "memory");
 }
 
@@ -233,7 +273,7 @@ struct Reader {
     // A whole warp waits for the next piece and copies what it needs by `take`; false: nothing more
     template <typename F>
     __device__ __forceinline__ bool next(const Piece* ring, Barriers& bar, unsigned int* err, int lane, F take) {
-        if (!mbar_wait(&bar.piece_full[slot], parity, err)) return false;
+        if (!wait_for(&bar.piece_full[slot], parity, err)) return false;
         const Piece& p = ring[slot];
         const bool some = p.t1 >= p.t0;
         if (some) take(p);
@@ -255,10 +295,9 @@ __device__ __forceinline__ V warp_scan(V v, int lane) {
     return v;
 }
 // Tiles of a CTA's share, but for the shifts of its boundaries to those of units.
-__device__ __forceinline__ long long piece_of(long long total) {
-    return max(total + gridDim.x > 0xffffffffLL ? (total + gridDim.x - 1) / gridDim.x
-                                                : (long long)((unsigned)(total + gridDim.x - 1) / gridDim.x),
-               (long long)kMinPart);
+__device__ __forceinline__ long long piece_of(const PromptArgs& a, long long total) {
+    // a division by the grid, exact below 2^56
+    return max(gridDim.x == 1 ? total : (long long)__umul64hi((unsigned long long)(total + gridDim.x - 1), a.grid_mul), (long long)kMinPart);
 }
 // Tiles of one kv head's units of sequence base + lane; by a whole warp, a long sequence by all of its lanes.
 __device__ __forceinline__ long long seq_cost(const PromptArgs& a, int base, int lane) {
@@ -284,32 +323,37 @@ __device__ __forceinline__ long long seq_cost(const PromptArgs& a, int base, int
     }
     return cost;
 }
-// Begin (which = 0, with the walk from there) or end of this CTA's share, by one warp.  Up to 32 sequences it finds
-// everything by itself, else the CTA found `total` and the sequences of the share's ends (s_seq, s_in, s_cost).
-__device__ __forceinline__ long long plan(const PromptArgs& a, Walk& walk, int which, long long total, const int* s_seq,
-                                          const long long* s_in, const long long* s_cost, int lane) {
-    long long mine = 0, inc = 0;
-    if (a.B <= 32) {
-        mine = seq_cost(a, 0, lane);
-        inc = warp_scan(mine * a.Hkv, lane);
-        total = __shfl_sync(0xffffffffu, inc, 31);
-    }
-    walk.piece = piece_of(total);
+// Begin (which = 0, with the walk from there) or end of this CTA's share, by one warp, from the sequences' tiles.
+__device__ __forceinline__ void plan(const PromptArgs& a, Walk& walk, int which, const long long* s_cost, int lane) {
+    long long total = 0;
+#pragma unroll 1
+    for (int i = lane; i < a.B; i += 32) total += s_cost[i];
+    total = __shfl_sync(0xffffffffu, warp_scan(total, lane), 31) * a.Hkv;
+    walk.piece = piece_of(a, total);
     long long pos = min(walk.piece * (blockIdx.x + which), total);
     walk.at = pos;
-    if (pos >= total) return pos;
-    int b;
-    long long in_seq, per_head;
-    if (a.B <= 32) {
-        b = __popc(__ballot_sync(0xffffffffu, inc <= pos));
-        in_seq = pos - __shfl_sync(0xffffffffu, inc - mine * a.Hkv, b);
-        per_head = __shfl_sync(0xffffffffu, mine, b);
-    } else {
-        b = s_seq[which], in_seq = s_in[which], per_head = s_cost[b];
+    if (pos >= total) return;
+    int b = 0;
+    long long in_seq = pos, per_head = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const long long mine = b0 + lane < a.B ? s_cost[b0 + lane] : 0;
+        const long long inc = warp_scan(mine, lane) * a.Hkv, all = __shfl_sync(0xffffffffu, inc, 31);
+        if (in_seq < all) {
+            const int k = __popc(__ballot_sync(0xffffffffu, inc <= in_seq));
+            b = b0 + k;
+            per_head = __shfl_sync(0xffffffffu, mine, k);
+            in_seq -= __shfl_sync(0xffffffffu, inc, k) - per_head * a.Hkv;
+            break;
+        }
+        in_seq -= all;
     }
     const Seq s = load_seq(a, b);
     const int units = units_of(a, s);
-    const int h = (in_seq | per_head) >> 32 ? (int)(in_seq / per_head) : (int)((unsigned)in_seq / (unsigned)per_head);
+    int h = 0;  // in_seq / per_head
+#pragma unroll 1
+    for (int i = 1; i < a.Hkv; i += 32)
+        h += __popc(__ballot_sync(0xffffffffu, i + lane < a.Hkv && (i + lane) * per_head <= in_seq));
     const long long want = in_seq - h * per_head;
     long long before = 0;
     int u = 0, o = 0, cost = 0;
@@ -338,18 +382,135 @@ __device__ __forceinline__ long long plan(const PromptArgs& a, Walk& walk, int w
     }
     walk.s = s, walk.h = h, walk.u = u, walk.o = o, walk.units = units;
     walk.at = pos;
-    return pos;
 }
 // lane 0's value, which the compiler then knows to be the same in all lanes
 template <typename V>
 __device__ __forceinline__ V uniform(V v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ void pair_sync() { asm volatile("bar.sync 1, 64;" ::: "memory"); }  // of the planning and the edge warp
 
+// A tile of a thread's row: its 128 scores at t_s become probabilities there, with the running maximum m and sum l; the
+// output at t_o is scaled where the maximum went on by more than kGrow.
+__device__ __forceinline__ void scale_output(uint32_t t_o, float top, float c, bool first, float& m, float& l) {
+    if (!__any_sync(0xffffffffu, (top - m) * c > kGrow)) return;
+    const float scale = top > m ? exp2_fast((m - top) * c) : 1.f;
+    m = top;
+    l *= scale;
+    if (first) return;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        uint32_t o[32];
+        tc::ld32(t_o + 32 * i, o);
+        tc::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * scale);
+        tc::st32(t_o + 32 * i, o);
+    }
+}
+// scores x of 32 columns to packed probabilities, added to sum
+template <typename T>
+__device__ __forceinline__ void probabilities(const uint32_t (&x)[32], uint32_t (&w)[16], float2 c2, float2 ref2, float2 (&sum)[2]) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        float2 v = ffma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, ref2);
+        v.x = exp2_fast(v.x);
+        v.y = exp2_fast(v.y);
+        sum[k & 1] = fadd2(sum[k & 1], v);
+        w[k] = pack2(v.x, v.y, T());
+    }
+}
+__device__ __forceinline__ float max32(const uint32_t (&x)[32], float top) {
+    float mx[4] = {top, top, top, top};
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+    return max3(max3(mx[0], mx[1], mx[2]), mx[3], top);
+}
+// The scores stay in registers, and their scale waits until the maximum is subtracted.  Columns lo .. hi - 1 are seen.
+template <typename T>
+__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int lo, int hi, float c, bool first, float& m, float& l) {
+    constexpr float kLift = std::is_same<T, __half>::value ? kHalfLift : 0.f;
+    uint32_t x[4][32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tc::ld32(t_s + 32 * i, x[i]);
+    tc::wait_ld();
+    if (__any_sync(0xffffffffu, lo > 0 || hi < kTile)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t seen = bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[i][k] = (seen & (1u << k)) != 0 ? x[i][k] : 0xff800000u;
+        }
+    }
+    scale_output(t_o, max3(max3(max32(x[0], m), max32(x[1], m), max32(x[2], m)), max32(x[3], m), m), c, first, m, l);
+    const float ref = (m == -CUDART_INF_F ? 0.f : m * c) - kLift;
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t w[2][16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            probabilities<T>(x[2 * i + k], w[k], make_float2(c, c), make_float2(-ref, -ref), sum);
+            tc::st16(t_s + 32 * i + 16 * k, w[k]);
+        }
+    }
+    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    tc::wait_st();
+}
+// Scores that are capped or biased (d0: position of column 0 less the row's): 32 columns at a time, read twice, and not
+// at all where no row of the warp sees one.
+template <typename T>
+__device__ __forceinline__ void softmax_general(const PromptArgs& a, uint32_t t_s, uint32_t t_o, int lo, int hi, float slope, float d0,
+                                                bool first, float& m, float& l) {
+    constexpr float kLift = std::is_same<T, __half>::value ? kHalfLift : 0.f;
+    uint32_t x[32];
+    float top = m;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t seen = bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
+        if (!__any_sync(0xffffffffu, seen != 0)) continue;
+        tc::ld32(t_s + 32 * i, x);
+        tc::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            float v = __uint_as_float(x[k]) * a.scale;
+            if (a.softcap > 0.f) v = a.softcap * tanhf(v * a.inv_softcap);
+            x[k] = __float_as_uint(fmaf(slope, d0 + (32 * i + k), v) * kLog2e);
+        }
+        if (!__all_sync(0xffffffffu, seen == 0xffffffffu)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = (seen & (1u << k)) != 0 ? x[k] : 0xff800000u;
+        }
+        top = max32(x, top);
+        tc::st32(t_s + 32 * i, x);
+    }
+    scale_output(t_o, top, 1.f, first, m, l);
+    tc::wait_st();
+    const float ref = (m == -CUDART_INF_F ? 0.f : m) - kLift;
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t seen = bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
+        uint32_t w[16];
+        if (__any_sync(0xffffffffu, seen != 0)) {
+            tc::ld32(t_s + 32 * i, x);
+            tc::wait_ld();
+            probabilities<T>(x, w, make_float2(1.f, 1.f), make_float2(-ref, -ref), sum);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = 0u;
+        }
+        tc::st16(t_s + 16 * i, w);  // over scores that were read
+    }
+    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    tc::wait_st();
+}
+
 // T: type of q and the cache; O: type of the output; GEN: scores are capped or biased, or the scale has a sign or
 // size for which the maximum cannot be taken before it.
 template <typename T, typename O, bool GEN>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, PromptArgs a) {
+    prompt_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                        const __grid_constant__ CUtensorMap q_map, PromptArgs a) {
     constexpr bool kIsHalf = std::is_same<T, __half>::value;
     constexpr float kLift = kIsHalf ? kHalfLift : 0.f;
     constexpr uint32_t kIdescS = kIsHalf ? tc::idesc_f16_f32(128, 128) : tc::idesc_as_bf16(tc::idesc_f16_f32(128, 128));
@@ -358,10 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Barriers bar;
     __shared__ Piece s_piece[kPieces];
     __shared__ uint32_t s_tmem;
-    __shared__ long long s_scan[kThreads / 32];
-    __shared__ long long s_end;   // of this CTA's share
-    __shared__ int s_seq[2];      // the sequences in which this CTA's share begins and ends, -1: behind the last tile,
-    __shared__ long long s_in[2];  // and the places in them
+    __shared__ long long s_end;  // of this CTA's share
     uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* rows_smem = dsm;
     uint8_t* ring = dsm + 2 * kRowBytes;
@@ -380,40 +538,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- this CTA's share: the tiles of all units form one stream, cut into equal pieces ----
-    long long total = 0;
-    long long* s_cost = reinterpret_cast<long long*>(ring);  // tiles of a sequence's units, of one kv head
-    if (a.B > 32) {  // else the planning warp finds it by itself
-        for (int base = warp * 32; base < a.B; base += kThreads) {
-            const long long cost = seq_cost(a, base, lane);
-            if (base + lane < a.B) s_cost[base + lane] = cost;
-        }
-        __syncthreads();
-        const int seg = (a.B + kThreads - 1) / kThreads, seg0 = min(tid * seg, a.B), seg1 = min(seg0 + seg, a.B);
-        long long mine = 0;
-        for (int b = seg0; b < seg1; ++b) mine += s_cost[b] * a.Hkv;
-        long long inc = warp_scan(mine, lane);
-        if (lane == 31) s_scan[warp] = inc;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) inc += s_scan[w];
-            total += s_scan[w];
-        }
-        const long long piece = piece_of(total);
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const long long pos = min(piece * (blockIdx.x + which), total);
-            if (pos >= total) {
-                if (tid == 0) s_seq[which] = -1;
-            } else if (pos >= inc - mine && pos < inc) {
-                long long in_seq = pos - (inc - mine);
-                int b = seg0;
-                for (; in_seq >= s_cost[b] * a.Hkv; ++b) in_seq -= s_cost[b] * a.Hkv;
-                s_seq[which] = b;
-                s_in[which] = in_seq;
-            }
-        }
+    // the tiles of all units form one stream, which is cut into equal pieces: first the tiles of each sequence
+    long long* s_cost = reinterpret_cast<long long*>(ring);  // of its units, for one kv head
+#pragma unroll 1
+    for (int base = warp * 32; base < a.B; base += kThreads) {
+        const long long cost = seq_cost(a, base, lane);
+        if (base + lane < a.B) s_cost[base + lane] = cost;
     }
     fence_proxy_async();  // s_cost lies where the copies go
     tc::fence_before();
@@ -456,78 +586,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float slope = GEN && a.slopes != nullptr && real ? a.slopes[head] : 0.f;
             float m = -CUDART_INF_F, l = 0.f;
             const int first = p.first, past = p.past;
+#pragma unroll 1
             for (int t = first; t < past; ++t) {
-                if (!mbar_wait(&bar.s_full[half], s_parity, err)) {
+                if (!wait_for(&bar.s_full[half], s_parity, err)) {
                     fine = false;
                     break;
                 }
                 s_parity ^= 1;
                 tc::fence_after();
                 if ((warp & 3) * 32 < rows) {
-                    uint32_t x[4][32];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tc::ld32(t_s + 32 * i, x[i]);
-                    tc::wait_ld();
                     const int lo_in = lo - t * kTile, hi_in = hi - t * kTile;
-                    if (GEN) {
-                        const float d0 = (float)(t * kTile - pos);
-#pragma unroll
-                        for (int i = 0; i < 128; ++i) {
-                            float v = __uint_as_float(x[i >> 5][i & 31]) * a.scale;
-                            if (a.softcap > 0.f) v = a.softcap * tanhf(v * a.inv_softcap);
-                            x[i >> 5][i & 31] = __float_as_uint(fmaf(slope, d0 + i, v) * kLog2e);
-                        }
-                    }
-                    if (__any_sync(0xffffffffu, lo_in > 0 || hi_in < kTile)) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t seen = bits_below(hi_in - 32 * i) & ~bits_below(lo_in - 32 * i);
-                            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) x[i][k] = (seen & (1u << k)) != 0 ? x[i][k] : 0xff800000u;
-                        }
-                    }
-                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-                    for (int i = 0; i < 128; i += 2)
-                        mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(x[i >> 5][i & 31]), __uint_as_float(x[i >> 5][(i & 31) + 1]));
-                    const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], m);
-                    if (__any_sync(0xffffffffu, (top - m) * c > kGrow)) {
-                        const float scale = top > m ? exp2_fast((m - top) * c) : 1.f;
-                        m = top;
-                        l *= scale;
-                        if (t > first) {
-#pragma unroll 1
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t o[32];
-                                tc::ld32(t_o + 32 * i, o);
-                                tc::wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * scale);
-                                tc::st32(t_o + 32 * i, o);
-                            }
-                        }
-                    }
-                    const float ref = (m == -CUDART_INF_F ? 0.f : m * c) - kLift;
-                    const float2 c2 = make_float2(c, c), ref2 = make_float2(-ref, -ref);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int e = 64 * i + 2 * k;
-                            float2 v = make_float2(__uint_as_float(x[e >> 5][e & 31]), __uint_as_float(x[e >> 5][(e & 31) + 1]));
-                            v = ffma2(v, c2, ref2);
-                            v.x = exp2_fast(v.x);
-                            v.y = exp2_fast(v.y);
-                            sum[k & 1] = fadd2(sum[k & 1], v);
-                            w[k] = pack2(v.x, v.y, T());
-                        }
-                        tc::st32(t_s + 32 * i, w);
-                    }
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    tc::wait_st();
+                    if constexpr (GEN)
+                        softmax_general<T>(a, t_s, t_o, lo_in, hi_in, slope, (float)(t * kTile - pos), t == first, m, l);
+                    else
+                        softmax_tile<T>(t_s, t_o, lo_in, hi_in, c, t == first, m, l);
                 }
                 tc::fence_before();
                 __syncwarp();
@@ -536,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!fine) break;
             const bool any = past > first;
             if (any) {
-                if (!mbar_wait(&bar.o_full[half], o_parity, err)) {
+                if (!wait_for(&bar.o_full[half], o_parity, err)) {
                     fine = false;
                     break;
                 }
@@ -549,43 +621,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rr = half * kHalf + r;
             const float inv = l != 0.f ? 1.f / l : 0.f;
             if ((warp & 3) * 32 < rows) {
-#pragma unroll 1
+                uint32_t o[4][32];
+#pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t o[32];
                     if (any) {
-                        tc::ld32(t_o + 32 * i, o);
-                        tc::wait_ld();
+                        tc::ld32(t_o + 32 * i, o[i]);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = 0u;
+                        for (int k = 0; k < 32; ++k) o[i][k] = 0u;
                     }
-                    if (!real) continue;
-                    if (sizeof(O) == 2 && whole) {
-                        O* out = static_cast<O*>(a.out) + row * kTile + 32 * i;
+                }
+                tc::wait_ld();
+                if (whole) {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < 128; ++k) o[k >> 5][k & 31] = __float_as_uint(__uint_as_float(o[k >> 5][k & 31]) * inv);
+                    if (__any_sync(0xffffffffu, l == 0.f)) {  // no key, or only scores of -inf
+#pragma unroll
+                        for (int k = 0; k < 128; ++k) o[k >> 5][k & 31] = l != 0.f ? o[k >> 5][k & 31] : 0u;
+                    }
+                }
+                if (real && whole) {
+                    if constexpr (sizeof(O) == 2) {
+                        O* out = static_cast<O*>(a.out) + row * kTile;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
                             uint32_t w[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const float x0 = __uint_as_float(o[16 * k + 2 * e]) * inv, x1 = __uint_as_float(o[16 * k + 2 * e + 1]) * inv;
-                                w[e] = pack2(l != 0.f ? x0 : 0.f, l != 0.f ? x1 : 0.f, T());
-                            }
+                            for (int e = 0; e < 8; ++e)
+                                w[e] = pack2(__uint_as_float(o[k >> 1][(k & 1) * 16 + 2 * e]), __uint_as_float(o[k >> 1][(k & 1) * 16 + 2 * e + 1]), T());
                             store32(out + 16 * k, w, a.wide_out);
                         }
-                    } else if (whole) {
-                        float* out = static_cast<float*>(a.out) + row * kTile + 32 * i;
+                    } else {
+                        float* out = static_cast<float*>(a.out) + row * kTile;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 16; ++k) {
                             uint32_t w[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = l != 0.f ? __float_as_uint(__uint_as_float(o[8 * k + e]) * inv) : 0u;
+                            for (int e = 0; e < 8; ++e) w[e] = o[k >> 2][(k & 3) * 8 + e];
                             store32(out + 8 * k, w, a.wide_out);
                         }
-                    } else {
-                        uint4* out = reinterpret_cast<uint4*>(slot) + (size_t)8 * i * a.slot_rows + rr;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) out[(size_t)k * a.slot_rows] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
+                } else if (real) {
+                    uint4* out = reinterpret_cast<uint4*>(slot) + rr;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        out[(size_t)k * a.slot_rows] = make_uint4(o[k >> 3][(k & 7) * 4], o[k >> 3][(k & 7) * 4 + 1], o[k >> 3][(k & 7) * 4 + 2], o[k >> 3][(k & 7) * 4 + 3]);
                 }
             }
             if (real) {
@@ -618,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
                 table = a.page_table + (int64_t)p.b * a.max_pages;
             })) {
+#pragma unroll 1
                 for (int t = t0; t < t1; ++t) {
                     if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
                     // lane i: box i of the tile
@@ -628,13 +709,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool bad = want && (page < 0 || page >= a.n_pages);
                     const unsigned good = __ballot_sync(0xffffffffu, want && !bad), zero = __ballot_sync(0xffffffffu, bad);
                     const uint32_t bytes = (uint32_t)__popc(good) * (uint32_t)a.box * (kTile * 2);
-                    fine = mbar_wait(&bar.empty[stage], parity, err);
+                    fine = wait_for(&bar.empty[stage], parity, err);
                     if (!fine) break;
                     uint8_t* dst = ring + stage * kStageBytes;
                     if (zero != 0) {  // keys and values of pages outside the cache count as zeros
                         if (lane == 0) atomicOr(&g_prompt_page_error, 1u);
                         for (unsigned z = zero; z != 0; z &= z - 1) {
                             const int r0 = (__ffs(z) - 1) * a.box;
+#pragma unroll 1
                             for (int i = lane; i < a.box * 16; i += 32)
                                 *reinterpret_cast<uint4*>(dst + (i & 1) * kSpan + r0 * kTile + (i >> 1) * 16) = make_uint4(0, 0, 0, 0);
                         }
@@ -666,14 +748,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // No copy and no arrival is on its way when the CTA leaves: the ring's stages behind the last tile, in their
             // order, are every other one for the keys and the ones between for the values.
+#pragma unroll 1
             for (int i = values; fine && i < kStages; i += 2) {
-                fine = mbar_wait(&bar.empty[stage], parity, err);
+                fine = wait_for(&bar.empty[stage], parity, err);
                 stage += 2;
                 if (stage >= kStages) stage -= kStages, parity ^= 1;
             }
             if (!fine)
+#pragma unroll 1
                 for (int i = 0; i < kStages; ++i)
-                    if (used >> i & 1) mbar_drain(on_raw >> i & 1 ? &bar.raw[i] : &bar.full[i], last_parity >> i & 1);
+                    if (used >> i & 1) drain(on_raw >> i & 1 ? &bar.raw[i] : &bar.full[i], last_parity >> i & 1);
         } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             // ---- products of a half: while this warp waits for its half's softmax the other half's run ----
             // An MMA's operands are uniform registers.  With one thread in a branch of its own, and operands that the
@@ -694,18 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++st == kStages) st = 0, par ^= 1;
                 };
                 auto my_turn = [&]() {
-                    const bool got = mbar_wait(&bar.turn[half], turn_parity, err);
+                    const bool got = wait_for(&bar.turn[half], turn_parity, err);
                     turn_parity ^= 1;
                     return got;
-                };
-                auto skip = [&]() {  // a tile that only the other half takes
-                    for (int i = 0; fine && i < 2; ++i) {
-                        fine = __all_sync(0xffffffffu, mbar_wait(&bar.full[stage], parity, err));
-                        if (lane == 0) mbar_arrive(&bar.empty[stage]);
-                        pass(stage, parity);
-                    }
-                    fine = __all_sync(0xffffffffu, fine && my_turn());
-                    if (lane == 0) mbar_arrive(&bar.turn[half ^ 1]);
                 };
                 auto scores = [&](uint32_t st) {  // by the elected lane
                     const uint64_t kd = k_desc + st * (kStageBytes >> 4);
@@ -716,31 +791,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc::commit(&bar.s_full[half]);
                 };
-                if (a0 >= a1) a0 = a1 = t1;
-                for (; fine && t < a0; ++t)
-                    if (t >= b0 && t < b1) skip();
-                if (fine && t < a1) {
-                    fine = mbar_wait(&bar.full[stage], parity, err) && mbar_wait(&bar.q_full[half], q_parity, err);
-                    q_parity ^= 1;
-                    if (!__all_sync(0xffffffffu, fine)) break;
-                    tc::fence_after();
-                    const uint32_t st = uniform(stage), last = uniform(a0 + 1 == a1);
-                    if (tc::elect()) {
-                        scores(st);
-                        tc::commit(&bar.empty[st]);
-                        if (last) tc::commit(&bar.q_free[half]);
+#pragma unroll 1
+                for (; t < t1; ++t) {
+                    if (!(t >= a0 && t < a1)) {
+                        if (!(t >= b0 && t < b1)) continue;
+                        // a tile that only the other half takes
+#pragma unroll 1
+                        for (int i = 0; fine && i < 2; ++i) {
+                            fine = __all_sync(0xffffffffu, wait_for(&bar.full[stage], parity, err));
+                            if (lane == 0) mbar_arrive(&bar.empty[stage]);
+                            pass(stage, parity);
+                        }
+                        fine = __all_sync(0xffffffffu, fine && my_turn());
+                        if (!fine) break;
+                        if (lane == 0) mbar_arrive(&bar.turn[half ^ 1]);
+                        continue;
                     }
-                    __syncwarp();
-                    pass(stage, parity);
-                }
-                for (; fine && t < a1; ++t) {
+                    if (t == a0) {
+                        fine = wait_for(&bar.full[stage], parity, err) && wait_for(&bar.q_full[half], q_parity, err);
+                        q_parity ^= 1;
+                        if (!__all_sync(0xffffffffu, fine)) break;
+                        tc::fence_after();
+                        const uint32_t st = uniform(stage), last = uniform(a0 + 1 == a1);
+                        if (tc::elect()) {
+                            scores(st);
+                            tc::commit(&bar.empty[st]);
+                            if (last) tc::commit(&bar.q_free[half]);
+                        }
+                        __syncwarp();
+                        pass(stage, parity);
+                    }
                     // this tile's values, the next one's keys, this half's probabilities, and the other half's products done
                     uint32_t k_stage = stage, k_parity = parity;
                     pass(k_stage, k_parity);
                     const uint32_t vs = uniform(stage), ks = uniform(k_stage), more = uniform(t > a0), left = uniform(a1 - t - 1);
                     const uint64_t vd = v_desc + vs * (kStageBytes >> 4);
-                    fine = mbar_wait(&bar.full[stage], parity, err) && (left == 0 || mbar_wait(&bar.full[k_stage], k_parity, err)) &&
-                           mbar_wait(&bar.p_full[half], p_parity, err) && my_turn();
+                    fine = wait_for(&bar.full[stage], parity, err) && (left == 0 || wait_for(&bar.full[k_stage], k_parity, err)) &&
+                           wait_for(&bar.p_full[half], p_parity, err) && my_turn();
                     p_parity ^= 1;
                     if (!__all_sync(0xffffffffu, fine)) break;
                     tc::fence_after();
@@ -761,13 +848,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pass(stage, parity);
                     if (left > 0) pass(stage, parity);
                 }
-                for (; fine && t < t1; ++t)
-                    if (t >= b0 && t < b1) skip();
             }
             if (!fine) {
                 if (tc::elect()) tc::commit(&bar.gave_up);
                 __syncwarp();
-                mbar_drain(&bar.gave_up, 0);
+                drain(&bar.gave_up, 0);
             }
         } else if (warp == kRowWarp || warp == kRowWarp + 1) {
             // ---- queries of a half: rows of 256 bytes, gathered, chunk i of a row at i ^ (row mod 8) ----
@@ -786,15 +871,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f0 = (unsigned)p.f0 + half * kHalf, h = p.h, q0 = p.q0, rows = p.half_rows(half);
             })) {
                 if (!some) continue;
-                fine = mbar_wait(&bar.q_free[half], free_parity, err);
+                fine = wait_for(&bar.q_free[half], free_parity, err);
                 if (!fine) break;
                 free_parity ^= 1;
+                if (a.tiled_rows) {
+                    // whole tokens' heads; rows behind the unit's last are those of the next tokens and are not used
+                    if (lane < 2) {
+                        if (lane == 0) mbar_expect_tx(&bar.q_full[half], kRowBytes);
+                        __syncwarp(3);
+                        tma_load3(rows_smem + half * kRowBytes + lane * kSpan, &q_map, 64 * lane, h * a.group, q0 + (int)token_of(a, f0), &bar.q_full[half]);
+                    }
+                    __syncwarp();
+                    continue;
+                }
+#pragma unroll 1
                 for (int r0 = 0; r0 < kHalf; r0 += 32) {
                     // each lane finds one row's place, then all copy two rows at a time
                     const unsigned f = f0 + min(r0 + lane, rows - 1), token = token_of(a, f);
                     const int64_t at = (int64_t)(q0 + (int)token) * a.q_token_stride +
                                        (int64_t)(h * a.group + (int)(f - token * a.group)) * a.q_head_stride;
-#pragma unroll
+#pragma unroll 4
                     for (int r = 0; r < 32; r += 2) {
                         const T* src = base + __shfl_sync(0xffffffffu, at, r + (lane >> 4));
                         cp_async16(dst + (r0 + r) * kTile + ((key ^ (r & 6)) << 4), src, r0 + r + (lane >> 4) < rows);
@@ -806,21 +902,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.q_full[half]);
             }
-            if (fine) mbar_wait(&bar.q_free[half], free_parity, err);
-        } else if (warp == kPlanWarp) {
-            // ---- the plan ----
+            if (fine) wait_for(&bar.q_free[half], free_parity, err);
+        } else {
+            // ---- the plan: the share's begin, and by the edge warp its end ----
             Walk walk;
-            walk.at = 0;
             walk.units = 0;
-            plan(a, walk, 0, total, s_seq, s_in, s_cost, lane);
+            plan(a, walk, warp - kPlanWarp, s_cost, lane);
+            if (warp > kPlanWarp && lane == 0) s_end = walk.at;
+            fence_proxy_async();  // s_cost lies where the copies go, which wait for the plan
             pair_sync();
             walk.end = s_end;
+            if (warp == kPlanWarp) {
             uint32_t slot = 0, parity = 1;
             for (bool more = true; more;) {
                 Piece p;
                 more = walk.next(a, p, lane);
                 if (!more) p.t0 = 1, p.t1 = 0;
-                if (!mbar_wait(&bar.piece_empty[slot], parity, err)) break;
+                if (!wait_for(&bar.piece_empty[slot], parity, err)) break;
                 if (lane == 0) {
                     s_piece[slot] = p;
                     mbar_arrive(&bar.piece_full[slot]);
@@ -828,15 +926,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (++slot == kPieces) slot = 0, parity ^= 1;
             }
-        } else {
-            // ---- the end of the share, for the plan; then values at the edges of what a unit sees: rows outside are zeros ----
-            {
-                Walk walk;
-                const long long end = plan(a, walk, 1, total, s_seq, s_in, s_cost, lane);
-                if (lane == 0) s_end = end;
-                fence_proxy_async();  // s_cost lies where the copies go, which wait for the plan
-                pair_sync();
-            }
+            } else {
+            // ---- values at the edges of what a unit sees: rows outside are zeros ----
             uint32_t stage = 1, raw_parity = 0;  // the values' stage; a bit for each
             bool fine = true;
             int t0, t1, a0[2], a1[2], lo, hi;
@@ -844,16 +935,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi;
                 a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
             })) {
+#pragma unroll 1
                 for (int t = t0; t < t1; ++t) {
                     if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
                     if (t * kTile < lo || (t + 1) * kTile > hi) {
-                        fine = mbar_wait(&bar.raw[stage], (raw_parity >> stage) & 1, err);
+                        fine = wait_for(&bar.raw[stage], (raw_parity >> stage) & 1, err);
                         if (!fine) break;
                         raw_parity ^= 1u << stage;
                         uint8_t* v = ring + stage * kStageBytes;
                         const int lo_in = max(lo - t * kTile, 0), hi_in = min(hi - t * kTile, kTile);
+#pragma unroll 1
                         for (int i = lane; i < lo_in * 16; i += 32)
                             *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kSpan + (i >> 4) * kTile + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
                         for (int i = hi_in * 16 + lane; i < kTile * 16; i += 32)
                             *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kSpan + (i >> 4) * kTile + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                         fence_proxy_async();
@@ -863,6 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     stage += 2;
                     if (stage >= kStages) stage -= kStages;
                 }
+            }
             }
         }
     }
@@ -957,7 +1052,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixMergeArgs a) {
 }
 
 struct Kernels {
-    void (*split)(CUtensorMap, CUtensorMap, PromptArgs);
+    void (*split)(CUtensorMap, CUtensorMap, CUtensorMap, PromptArgs);
     void (*join)(PromptArgs);
 };
 template <typename T>
@@ -999,6 +1094,19 @@ cudaError_t cache_map(CUtensorMap* map, const PromptArgs& a, int dtype, const vo
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Queries as channels x heads x tokens, in boxes of 64 channels of a kv head's query heads of 128 rows' tokens.
+cudaError_t rows_map(CUtensorMap* map, const PromptArgs& a, int dtype) {
+    const EncodeTiled encode = encode_tiled();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t sizes[3] = {kTile, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+    const cuuint64_t strides[2] = {a.Hq > 1 ? (cuuint64_t)a.q_head_stride * 2 : 256, a.T > 1 ? (cuuint64_t)a.q_token_stride * 2 : 256};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(kHalf / a.group)}, step[3] = {1, 1, 1};
+    const CUresult r = encode(map, dtype == KVARN_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                              const_cast<void*>(a.q), sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 int slot_rows(int64_t T, int Hq, int Hkv) {
     const int64_t rows = T * (Hq / Hkv);
     return (int)(rows < 1 ? 1 : rows < kUnit ? rows : kUnit);
@@ -1027,16 +1135,20 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     a.group_shift = log2_group > 0 ? log2_group - 1 : 0;
     a.group_mul = (uint32_t)((1ull << (31 + log2_group)) / (unsigned)a.group + 1);
     a.inv_softcap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+    a.wide_out = ((uintptr_t)a.out & 31) == 0;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     a.box = a.page_size % 128 == 0 ? 128 : a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
-    a.wide_out = ((uintptr_t)a.out & 31) == 0 && ((uintptr_t)a.workspace & 31) == 0;
     const float c = a.scale * kLog2e;
     const bool general = a.softcap > 0.f || a.slopes != nullptr || !(c >= 1e-30f && c <= 1e30f);
     const bool wide = a.out_dtype == KVARN_DTYPE_FP32;
     const Kernels k = dtype == KVARN_DTYPE_FP16 ? pick<__half>(general, wide) : pick<__nv_bfloat16>(general, wide);
-    CUtensorMap k_map, v_map;
+    CUtensorMap k_map, v_map, q_map = {};
+    // rows come by tiled copies where 128 of them are whole tokens and the strides are ones that the encoding takes
+    a.tiled_rows = kHalf % a.group == 0 && (a.Hq == 1 || (a.q_head_stride > 0 && a.q_head_stride < (1ll << 38))) &&
+                   (a.T == 1 || (a.q_token_stride > 0 && a.q_token_stride < (1ll << 38)));
     e = cache_map(&k_map, a, dtype, a.k_cache);
     if (e == cudaSuccess) e = cache_map(&v_map, a, dtype, a.v_cache);
+    if (e == cudaSuccess && a.tiled_rows) e = rows_map(&q_map, a, dtype);
     if (e == cudaSuccess) e = set_smem_limit_once(k.split, kSmem, false, dev);
     if (e != cudaSuccess) return e;
     // no more CTAs than parts of kMinPart tiles that the call can have
@@ -1044,7 +1156,8 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     const int64_t parts = units * (((int64_t)a.max_len + 2 * kTile - 1) / kTile);
     const int most = sms < kMaxCtas ? sms : kMaxCtas;
     const int ctas = (int)(parts < 1 ? 1 : parts < most ? parts : most);
-    e = launch_pdl(k.split, dim3(ctas), dim3(kThreads), kSmem, stream, k_map, v_map, a);
+    a.grid_mul = ~0ull / (unsigned)ctas + 1;
+    e = launch_pdl(k.split, dim3(ctas), dim3(kThreads), kSmem, stream, k_map, v_map, q_map, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(k.join, dim3(ctas, (a.slot_rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, stream, a);
 }
