@@ -38,6 +38,7 @@ constexpr int kRowBytes = kHalf * kTile * 2;     // queries of a half
 constexpr int kSmem = 2 * kRowBytes + kStages * kStageBytes + 1024;
 constexpr int kMaxCtas = 160;
 constexpr int kMinPart = 2;                      // tiles of a unit that a CTA takes, at least
+constexpr int kUnitCost = 3;                     // what a unit costs beside its tiles, in tiles
 constexpr int kColS = 0, kColO = 256, kCols = 512;  // tensor memory: scores of the halves, then their outputs
 constexpr float kGrow = 8.f;                     // how far (in powers of two) scores may pass the maximum in use
 constexpr float kHalfLift = 7.f;                 // fp16 probabilities are multiplied by 2^7
@@ -99,11 +100,11 @@ __device__ __forceinline__ Keys keys_of(const PromptArgs& a, const Seq& s, unsig
     }
     return k;
 }
-// Tiles of a unit in the stream of work: at least one, so that a unit without visible keys has its place.
+// A unit's length in the stream of work: kUnitCost, then its tiles.
 __device__ __forceinline__ int cost_of(const PromptArgs& a, const Seq& s, int u) {
     const unsigned f0 = (unsigned)u * kUnit;
     const Keys k = keys_of(a, s, f0, min(f0 + kUnit, (unsigned)s.n * (unsigned)a.group));
-    return max(k.past() - k.first(), 1);
+    return k.past() - k.first() + kUnitCost;
 }
 
 // A CTA's share of one unit, as the planning warp hands it to the others: the tiles [t0, t1), and of them those of
@@ -154,9 +155,9 @@ struct Walk {
         p.rows = (int)(past - f0);
         const Keys keys = keys_of(a, s, f0, past);
         p.lo = keys.lo, p.hi = keys.hi;
-        const int first = keys.first(), cost = max(keys.past() - first, 1);
+        const int first = keys.first(), cost = keys.past() - first + kUnitCost;
         const int o1 = (int)min((long long)cost, o + (end - at));
-        p.t0 = first + o, p.t1 = first + o1;
+        p.t0 = first + max(o - kUnitCost, 0), p.t1 = first + o1 - kUnitCost;
         // the halves: lanes 0 and 1
         const Keys k = keys_of(a, s, min(f0 + (lane & 1) * kHalf, past), min(f0 + ((lane & 1) + 1) * kHalf, past));
         const int a0 = max(k.first(), p.t0), a1 = min(k.past(), p.t1);
@@ -372,7 +373,7 @@ __device__ __forceinline__ void plan(const PromptArgs& a, Walk& walk, int which,
         before += all;
     }
     // parts of a unit have kMinPart tiles at least: the boundary moves to the unit's begin or end
-    if (o < kMinPart) {
+    if (o < kUnitCost + kMinPart) {
         pos -= o;
         o = 0;
     } else if (cost - o < kMinPart) {
