@@ -243,7 +243,8 @@ struct PromptArgs {
     int group, box, slot_rows, page_shift, tiled_rows, wide_out;
     uint32_t group_mul, group_shift;  // division by the group
     uint64_t grid_mul;                // and by the split's CTAs: 2^64 / ctas, rounded up (0: one CTA)
-    float scale, softcap, inv_softcap;
+    float scale, softcap;
+    float score_scale;  // set by the launcher
     const void* q;
     int64_t q_token_stride, q_head_stride;
     const void* k_cache;

@@ -38,7 +38,7 @@ constexpr int kRowBytes = kHalf * kTile * 2;     // queries of a half
 constexpr int kSmem = 2 * kRowBytes + kStages * kStageBytes + 1024;
 constexpr int kMaxCtas = 160;
 constexpr int kMinPart = 2;                      // tiles of a unit that a CTA takes, at least
-constexpr int kUnitCost = 3;                     // what a unit costs beside its tiles, in tiles
+constexpr int kUnitCost = 2;                     // what a unit costs beside its tiles, in tiles
 constexpr int kColS = 0, kColO = 256, kCols = 512;  // tensor memory: scores of the halves, then their outputs
 constexpr float kGrow = 8.f;                     // how far (in powers of two) scores may pass the maximum in use
 constexpr float kHalfLift = 7.f;                 // fp16 probabilities are multiplied by 2^7
@@ -186,6 +186,11 @@ __device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? 0xfffff
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ float max3(float x, float y, float z) {
@@ -426,13 +431,38 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32], float top) {
     return max3(max3(mx[0], mx[1], mx[2]), mx[3], top);
 }
 // The scores stay in registers, and their scale waits until the maximum is subtracted.  Columns lo .. hi - 1 are seen.
-template <typename T>
-__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int lo, int hi, float c, bool first, float& m, float& l) {
+// GEN: the scores are capped and biased first (d0: position of column 0 less the row's), and c is 1.  The cap takes
+// tanh y = 1 - 2 / (e^2y + 1), off by 2^-22 or so: 2^-22 of the cap in a score.  With the library's tanhf a tile took
+// 5.1 us, with this GENT.
+template <typename T, bool GEN>
+__device__ __forceinline__ void softmax_tile(const PromptArgs& a, uint32_t t_s, uint32_t t_o, int lo, int hi, float c, float slope,
+                                             float d0, bool first, float& m, float& l) {
     constexpr float kLift = std::is_same<T, __half>::value ? kHalfLift : 0.f;
     uint32_t x[4][32];
 #pragma unroll
     for (int i = 0; i < 4; ++i) tc::ld32(t_s + 32 * i, x[i]);
     tc::wait_ld();
+    if constexpr (GEN) {
+        const float scale = a.score_scale, cap = a.softcap * kLog2e;
+        if (a.softcap > 0.f) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+                uint32_t &x0 = x[i >> 4][2 * (i & 15)], &x1 = x[i >> 4][2 * (i & 15) + 1];
+                float2 v = fmul2(make_float2(__uint_as_float(x0), __uint_as_float(x1)), make_float2(scale, scale));
+                v = fadd2(make_float2(exp2_fast(v.x), exp2_fast(v.y)), make_float2(1.f, 1.f));
+                v = ffma2(make_float2(rcp_fast(v.x), rcp_fast(v.y)), make_float2(-2.f * cap, -2.f * cap), make_float2(cap, cap));
+                x0 = __float_as_uint(v.x), x1 = __float_as_uint(v.y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) x[i >> 5][i & 31] = __float_as_uint(__uint_as_float(x[i >> 5][i & 31]) * scale);
+        }
+        if (a.slopes != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+                x[i >> 5][i & 31] = __float_as_uint(fmaf(slope, d0 + i, __uint_as_float(x[i >> 5][i & 31])));
+        }
+    }
     if (__any_sync(0xffffffffu, lo > 0 || hi < kTile)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -457,55 +487,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, int lo,
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     tc::wait_st();
 }
-// Scores that are capped or biased (d0: position of column 0 less the row's): 32 columns at a time, read twice, and not
-// at all where no row of the warp sees one.
-template <typename T>
-__device__ __forceinline__ void softmax_general(const PromptArgs& a, uint32_t t_s, uint32_t t_o, int lo, int hi, float slope, float d0,
-                                                bool first, float& m, float& l) {
-    constexpr float kLift = std::is_same<T, __half>::value ? kHalfLift : 0.f;
-    uint32_t x[32];
-    float top = m;
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t seen = bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
-        if (!__any_sync(0xffffffffu, seen != 0)) continue;
-        tc::ld32(t_s + 32 * i, x);
-        tc::wait_ld();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-            float v = __uint_as_float(x[k]) * a.scale;
-            if (a.softcap > 0.f) v = a.softcap * tanhf(v * a.inv_softcap);
-            x[k] = __float_as_uint(fmaf(slope, d0 + (32 * i + k), v) * kLog2e);
-        }
-        if (!__all_sync(0xffffffffu, seen == 0xffffffffu)) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = (seen & (1u << k)) != 0 ? x[k] : 0xff800000u;
-        }
-        top = max32(x, top);
-        tc::st32(t_s + 32 * i, x);
-    }
-    scale_output(t_o, top, 1.f, first, m, l);
-    tc::wait_st();
-    const float ref = (m == -CUDART_INF_F ? 0.f : m) - kLift;
-    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t seen = bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
-        uint32_t w[16];
-        if (__any_sync(0xffffffffu, seen != 0)) {
-            tc::ld32(t_s + 32 * i, x);
-            tc::wait_ld();
-            probabilities<T>(x, w, make_float2(1.f, 1.f), make_float2(-ref, -ref), sum);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = 0u;
-        }
-        tc::st16(t_s + 16 * i, w);  // over scores that were read
-    }
-    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-    tc::wait_st();
-}
-
 // T: type of q and the cache; O: type of the output; GEN: scores are capped or biased, or the scale has a sign or
 // size for which the maximum cannot be taken before it.
 template <typename T, typename O, bool GEN>
@@ -584,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (a.window > 0) lo = max(lo, pos + 1 - a.window);
             }
             if (!real) hi = lo;
-            const float slope = GEN && a.slopes != nullptr && real ? a.slopes[head] : 0.f;
+            const float slope = GEN && a.slopes != nullptr && real ? a.slopes[head] * kLog2e : 0.f;
             float m = -CUDART_INF_F, l = 0.f;
             const int first = p.first, past = p.past;
 #pragma unroll 1
@@ -597,10 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after();
                 if ((warp & 3) * 32 < rows) {
                     const int lo_in = lo - t * kTile, hi_in = hi - t * kTile;
-                    if constexpr (GEN)
-                        softmax_general<T>(a, t_s, t_o, lo_in, hi_in, slope, (float)(t * kTile - pos), t == first, m, l);
-                    else
-                        softmax_tile<T>(t_s, t_o, lo_in, hi_in, c, t == first, m, l);
+                    softmax_tile<T, GEN>(a, t_s, t_o, lo_in, hi_in, c, slope, (float)(t * kTile - pos), t == first, m, l);
                 }
                 tc::fence_before();
                 __syncwarp();
@@ -1135,7 +1113,8 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     while ((1 << log2_group) < a.group) ++log2_group;
     a.group_shift = log2_group > 0 ? log2_group - 1 : 0;
     a.group_mul = (uint32_t)((1ull << (31 + log2_group)) / (unsigned)a.group + 1);
-    a.inv_softcap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
+    // capped scores take e^(2 score / cap), others 2^(score log2 e)
+    a.score_scale = a.softcap > 0.f ? (float)(2.0 * (double)a.scale / (double)a.softcap * (double)kLog2e) : a.scale * kLog2e;
     a.wide_out = ((uintptr_t)a.out & 31) == 0;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     a.box = a.page_size % 128 == 0 ? 128 : a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
