@@ -974,7 +974,6 @@ kvarn_status kvarn_prompt_attention(kvarn_dtype dtype, int B, int T, int Hq, int
     a.max_len = max_pages * page_size;
     a.window = window;
     a.causal = causal;
-    a.out_dtype = (int)dtype;
     a.n_pages = n_pages;
     a.scale = softmax_scale;
     a.softcap = softcap;
@@ -1004,14 +1003,14 @@ namespace {
 
 // Parts of kvarn_prefix_attention's workspace, one after the other.
 struct PrefixWorkspace {
-    size_t prompt, paged, out, lse, total;  // bytes of each (out and lse twice)
+    size_t prompt, paged, out, lse, total;  // bytes of each
     PrefixWorkspace(int B, int Hq, int Hkv) {
         auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
         prompt = kvarn::prompt_attention_workspace_bytes(B, Hq, Hkv);
         paged = kvarn::paged_attention_workspace_bytes(B, Hq, Hkv);
         out = up((size_t)B * Hq * KVARN_HEAD_DIM * sizeof(float));
         lse = up((size_t)B * Hq * sizeof(float));
-        total = prompt + paged + 2 * (out + lse);
+        total = prompt + paged + out + lse;
     }
 };
 
@@ -1069,7 +1068,6 @@ kvarn_status kvarn_prefix_attention(kvarn_dtype dtype, int B, int n_groups, int 
     p.page_size = page_size;
     p.max_pages = max_prefix_pages;
     p.max_len = max_prefix_pages * page_size;
-    p.out_dtype = KVARN_DTYPE_FP32;
     p.n_pages = n_pages;
     p.scale = softmax_scale;
     p.softcap = softcap;
@@ -1105,28 +1103,26 @@ kvarn_status kvarn_prefix_attention(kvarn_dtype dtype, int B, int n_groups, int 
     a.token_stride = token_stride;
     a.page_table = page_table;
     a.kv_lens = kv_lens;
-    kvarn::PrefixMergeArgs m = {};
-    m.B = B;
-    m.Hq = Hq;
-    m.n_groups = n_groups;
-    m.cu = cu_seqs;
-    m.out = out;
-    m.lse = lse;
+    // the sequences' own tokens first; the prefixes' part is joined with that
+    a.workspace = at + need.prompt;
+    if (n_groups == 0) {
+        a.out_dtype = (int)dtype;
+        a.out = out;
+        a.lse = lse;
+    } else {
+        a.out_dtype = KVARN_DTYPE_FP32;
+        a.out = at + need.prompt + need.paged;
+        a.lse = reinterpret_cast<float*>(at + need.prompt + need.paged + need.out);
+    }
+    p.own_out = static_cast<const float*>(a.out);
+    p.own_lse = a.lse;
     p.workspace = at;
-    a.workspace = at += need.prompt;
-    m.prefix_out = reinterpret_cast<float*>(at += need.paged);
-    m.prefix_lse = reinterpret_cast<float*>(at += need.out);
-    m.own_out = reinterpret_cast<float*>(at += need.lse);
-    m.own_lse = reinterpret_cast<float*>(at += need.out);
-    p.out = const_cast<float*>(m.prefix_out);
-    p.lse = const_cast<float*>(m.prefix_lse);
-    a.out = const_cast<float*>(m.own_out);
-    a.lse = const_cast<float*>(m.own_lse);
+    p.out = out;
+    p.lse = lse;
     g_serving_used.store(true);
     g_prompt_used.store(true);
-    cudaError_t e = n_groups > 0 ? kvarn::launch_prompt_attention(p, (int)dtype, (cudaStream_t)stream) : cudaSuccess;
-    if (e == cudaSuccess) e = kvarn::launch_paged_attention(a, (int)dtype, (cudaStream_t)stream);
-    if (e == cudaSuccess) e = kvarn::launch_prefix_merge(m, (int)dtype, (cudaStream_t)stream);
+    cudaError_t e = kvarn::launch_paged_attention(a, (int)dtype, (cudaStream_t)stream);
+    if (e == cudaSuccess && n_groups > 0) e = kvarn::launch_prompt_attention(p, (int)dtype, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
     return ok();
 }

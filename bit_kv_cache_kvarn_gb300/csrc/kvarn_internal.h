@@ -236,7 +236,7 @@ cudaError_t read_and_clear_quantize_error(unsigned int* out);
 // in elements.
 constexpr int kMaxPromptSeqs = 16384;  // tiles of each sequence in shared memory
 struct PromptArgs {
-    int B, T, Hq, Hkv, page_size, max_pages, max_len, window, causal, out_dtype;
+    int B, T, Hq, Hkv, page_size, max_pages, max_len, window, causal;
     int64_t n_pages;
     // set by the launcher: query heads per kv head, tokens of a copy, rows of a partial slot, log2 of a page size that
     // is a power of two (else -1), whether rows come by tiled copies, whether 32-byte stores of the output are aligned
@@ -255,25 +255,14 @@ struct PromptArgs {
     const int32_t* kv_lens;
     const int32_t* kv_starts;
     const float* slopes;
+    const float* own_out;  // a part of each row's result that is joined with this one, and its log-sum-exp, or null:
+    const float* own_lse;  // [T][Hq][128] and [T][Hq]
     void* workspace;
     void* out;
     float* lse;
 };
 size_t prompt_attention_workspace_bytes(int64_t T, int Hq, int Hkv);
 cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream);
-
-// The two parts of kvarn_prefix_attention's rows: [B][Hq][128] and [B][Hq] each.
-struct PrefixMergeArgs {
-    int B, Hq, n_groups;
-    const int32_t* cu;
-    const float* prefix_out;
-    const float* prefix_lse;
-    const float* own_out;
-    const float* own_lse;
-    void* out;
-    float* lse;
-};
-cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, int dtype, cudaStream_t stream);
 cudaError_t read_and_clear_prompt_error(unsigned int* out);
 cudaError_t read_and_clear_prompt_page_error(unsigned int* out);
 

@@ -43,7 +43,8 @@ constexpr int kColS = 0, kColO = 256, kCols = 512;  // tensor memory: scores of 
 constexpr float kGrow = 8.f;                     // how far (in powers of two) scores may pass the maximum in use
 constexpr float kHalfLift = 7.f;                 // fp16 probabilities are multiplied by 2^7
 constexpr int kSerialUnits = 16;                 // of a sequence, whose tiles one lane counts
-constexpr int kJoinRows = 32, kJoinThreads = 256;
+constexpr int kJoinRows = 8, kJoinThreads = 256, kJoinAhead = 5;
+constexpr float kLn2 = 0.69314718055994531f;
 
 // Workspace: partial slots (fp32), two per CTA: slot 0 for the unit that began before the CTA's share, slot 1 for the
 // one that begins in it and goes on after it; then one Join per CTA.  A slot holds o as [32 groups of four
@@ -487,9 +488,18 @@ __device__ __forceinline__ void softmax_tile(const PromptArgs& a, uint32_t t_s, 
     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     tc::wait_st();
 }
-// T: type of q and the cache; O: type of the output; GEN: scores are capped or biased, or the scale has a sign or
+// Two parts of a row by their log-sum-exps x and y: their shares fx and fy of the whole and its log-sum-exp.
+__device__ __forceinline__ float join_lse(float x, float y, float& fx, float& fy) {
+    const float top = fmaxf(x, y), ref = top == -CUDART_INF_F ? 0.f : top;
+    const float wx = exp2f((x - ref) * kLog2e), wy = exp2f((y - ref) * kLog2e), sum = wx + wy;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    fx = wx * inv, fy = wy * inv;
+    return sum != 0.f ? top + log2f(sum) * kLn2 : -CUDART_INF_F;
+}
+
+// T: type of q, the cache and the output; OWN: each row is joined with a part of its own (kvarn_prefix_attention); GEN: scores are capped or biased, or the scale has a sign or
 // size for which the maximum cannot be taken before it.
-template <typename T, typename O, bool GEN>
+template <typename T, bool OWN, bool GEN>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                         const __grid_constant__ CUtensorMap q_map, PromptArgs a) {
@@ -598,7 +608,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t row = (int64_t)(p.q0 + token) * a.Hq + head;
             float* slot = ws.slot(blockIdx.x, p.starts ? 1 : 0);
             const int rr = half * kHalf + r;
-            const float inv = l != 0.f ? 1.f / l : 0.f;
+            float inv = l != 0.f ? 1.f / l : 0.f, lse = l != 0.f ? (m * c + (log2f(l) - kLift)) * kLn2 : -CUDART_INF_F, own = 0.f;
+            if (OWN && real && whole) {
+                float share;
+                lse = join_lse(lse, a.own_lse[row], share, own);
+                inv *= share;
+            }
             if ((warp & 3) * 32 < rows) {
                 uint32_t o[4][32];
 #pragma unroll
@@ -620,25 +635,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (real && whole) {
-                    if constexpr (sizeof(O) == 2) {
-                        O* out = static_cast<O*>(a.out) + row * kTile;
+                    T* out = static_cast<T*>(a.out) + row * kTile;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            uint32_t w[8];
+                    for (int k = 0; k < 8; ++k) {
+                        float v[16];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                w[e] = pack2(__uint_as_float(o[k >> 1][(k & 1) * 16 + 2 * e]), __uint_as_float(o[k >> 1][(k & 1) * 16 + 2 * e + 1]), T());
-                            store32(out + 16 * k, w, a.wide_out);
+                        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[k >> 1][(k & 1) * 16 + e]);
+                        if constexpr (OWN) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float4 w = *reinterpret_cast<const float4*>(a.own_out + row * kTile + 16 * k + 4 * e);
+                                v[4 * e] = fmaf(own, w.x, v[4 * e]), v[4 * e + 1] = fmaf(own, w.y, v[4 * e + 1]);
+                                v[4 * e + 2] = fmaf(own, w.z, v[4 * e + 2]), v[4 * e + 3] = fmaf(own, w.w, v[4 * e + 3]);
+                            }
                         }
-                    } else {
-                        float* out = static_cast<float*>(a.out) + row * kTile;
+                        uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = o[k >> 2][(k & 3) * 8 + e];
-                            store32(out + 8 * k, w, a.wide_out);
-                        }
+                        for (int e = 0; e < 8; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1], T());
+                        store32(out + 16 * k, w, a.wide_out);
                     }
                 } else if (real) {
                     uint4* out = reinterpret_cast<uint4*>(slot) + rr;
@@ -649,8 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (real) {
                 if (whole) {
-                    if (a.lse != nullptr)
-                        a.lse[row] = l != 0.f ? (m * c + (log2f(l) - kLift)) * 0.69314718055994531f : -CUDART_INF_F;
+                    if (a.lse != nullptr) a.lse[row] = lse;
                 } else {
                     slot[a.slot_rows * kTile + rr] = m == -CUDART_INF_F ? m : m * c;
                     slot[a.slot_rows * kTile + a.slot_rows + rr] = l;
@@ -945,89 +958,73 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Parts of the units that several CTAs share, joined: CTA (c, y) takes kJoinRows rows of the unit that begins in the
-// split's CTA c and goes on after it.  A warp's lanes take the rows and four of the slots' groups of channels each; the
-// rows are turned in shared memory and written whole.
-template <typename T, typename O>
+// split's CTA c and goes on after it, and those gridDim.y times as far on, a thread four channels of a row, kJoinAhead
+// parts of it at once.
+template <typename T, bool OWN>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a) {
-    constexpr int kGroups = kTile / 4 / (kJoinThreads / 32);
-    __shared__ float4 s_out[kJoinRows][kTile / 4 + 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    static_assert(kJoinThreads == kJoinRows * kTile / 4, "a thread for each four channels");
+    const int tid = threadIdx.x, in = tid % kJoinRows, g = tid / kJoinRows;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.slot_rows), (int)gridDim.x};
+    if (OWN && blockIdx.x == 0) {  // rows outside the groups have their own part only
+        const int first = min(max(a.cu[0], 0), a.T), past = min(max(a.cu[a.B], first), a.T);
+        const int64_t n = (int64_t)(a.T - (past - first)) * a.Hq * (kTile / 4);
+        for (int64_t i = (int64_t)blockIdx.y * kJoinThreads + tid; i < n; i += (int64_t)gridDim.y * kJoinThreads) {
+            const int64_t skip = (int64_t)first * a.Hq * (kTile / 4), at = i < skip ? i : i + (int64_t)(past - first) * a.Hq * (kTile / 4);
+            const float4 v = reinterpret_cast<const float4*>(a.own_out)[at];
+            reinterpret_cast<uint2*>(a.out)[at] = make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
+            if (a.lse != nullptr && at % (kTile / 4) == 0) a.lse[at / (kTile / 4)] = a.own_lse[at / (kTile / 4)];
+        }
+    }
     const int c0 = blockIdx.x;
     const Join jn = ws.joins()[c0];
     if (jn.b < 0) return;
     const Seq s = load_seq(a, jn.b);
     const unsigned f0 = (unsigned)jn.u * kUnit;
-    const int rows = (int)(min(f0 + kUnit, (unsigned)s.n * (unsigned)a.group) - f0) - (int)blockIdx.y * kJoinRows;
-    if (rows <= 0) return;
-    const int r = blockIdx.y * kJoinRows + min(lane, rows - 1);
-    float m = -CUDART_INF_F, l = 0.f;
-    float4 o[kGroups];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int c = c0; c <= jn.last; ++c) {
-        const float* slot = ws.slot(c, c == c0 ? 1 : 0);
-        float4 po[kGroups];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-            po[g] = reinterpret_cast<const float4*>(slot)[(size_t)(warp * kGroups + g) * a.slot_rows + r];
-        const float pm = slot[a.slot_rows * kTile + r], pl = slot[a.slot_rows * kTile + a.slot_rows + r];
-        const float top = fmaxf(m, pm), ref = top == -CUDART_INF_F ? 0.f : top;
-        const float x = exp2f(m - ref), y = exp2f(pm - ref);
-        m = top;
-        l = fmaf(y, pl, x * l);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            o[g].x = fmaf(y, po[g].x, x * o[g].x);
-            o[g].y = fmaf(y, po[g].y, x * o[g].y);
-            o[g].z = fmaf(y, po[g].z, x * o[g].z);
-            o[g].w = fmaf(y, po[g].w, x * o[g].w);
-        }
-    }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-        s_out[lane][warp * kGroups + g] =
-            l != 0.f ? make_float4(o[g].x * inv, o[g].y * inv, o[g].z * inv, o[g].w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (warp == 0 && lane < rows && a.lse != nullptr) {
+    const int rows = (int)(min(f0 + kUnit, (unsigned)s.n * (unsigned)a.group) - f0);
+#pragma unroll 1
+    for (int r = blockIdx.y * kJoinRows + in; r < rows; r += gridDim.y * kJoinRows) {
         const unsigned f = f0 + r, token = token_of(a, f);
-        a.lse[(int64_t)(s.q0 + (int)token) * a.Hq + jn.h * a.group + (int)(f - token * a.group)] =
-            l != 0.f ? (m + (log2f(l) - (std::is_same<T, __half>::value ? kHalfLift : 0.f))) * 0.69314718055994531f : -CUDART_INF_F;
-    }
-    __syncthreads();
-    for (int i = warp; i < min(rows, kJoinRows); i += kJoinThreads / 32) {
-        const unsigned f = f0 + blockIdx.y * kJoinRows + i, token = token_of(a, f);
         const int64_t row = (int64_t)(s.q0 + (int)token) * a.Hq + jn.h * a.group + (int)(f - token * a.group);
-        const float4 v = s_out[i][lane];
-        if (sizeof(O) == 2)
-            *reinterpret_cast<uint2*>(static_cast<O*>(a.out) + row * kTile + 4 * lane) = make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
-        else
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kTile + 4 * lane) = v;
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        float own_lse = 0.f;
+        if (OWN) w = *reinterpret_cast<const float4*>(a.own_out + row * kTile + 4 * g), own_lse = a.own_lse[row];
+        float m = -CUDART_INF_F, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c <= jn.last; c += kJoinAhead) {
+            float4 po[kJoinAhead];
+            float pm[kJoinAhead], pl[kJoinAhead];
+#pragma unroll
+            for (int i = 0; i < kJoinAhead; ++i) {
+                if (c + i > jn.last) break;
+                const float* slot = ws.slot(c + i, c + i == c0 ? 1 : 0);
+                po[i] = reinterpret_cast<const float4*>(slot)[(size_t)g * a.slot_rows + r];
+                pm[i] = slot[a.slot_rows * kTile + r], pl[i] = slot[a.slot_rows * kTile + a.slot_rows + r];
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinAhead; ++i) {
+                if (c + i > jn.last) break;
+                const float top = fmaxf(m, pm[i]), ref = top == -CUDART_INF_F ? 0.f : top;
+                const float x = exp2f(m - ref), y = exp2f(pm[i] - ref);
+                m = top;
+                l = fmaf(y, pl[i], x * l);
+                o.x = fmaf(y, po[i].x, x * o.x), o.y = fmaf(y, po[i].y, x * o.y);
+                o.z = fmaf(y, po[i].z, x * o.z), o.w = fmaf(y, po[i].w, x * o.w);
+            }
+        }
+        float inv = l != 0.f ? 1.f / l : 0.f, own = 0.f;
+        float lse = l != 0.f ? (m + (log2f(l) - (std::is_same<T, __half>::value ? kHalfLift : 0.f))) * kLn2 : -CUDART_INF_F;
+        if (OWN) {
+            float share;
+            lse = join_lse(lse, own_lse, share, own);
+            inv *= share;
+        }
+        o = l != 0.f ? make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (OWN) o = make_float4(fmaf(own, w.x, o.x), fmaf(own, w.y, o.y), fmaf(own, w.z, o.z), fmaf(own, w.w, o.w));
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * kTile + 4 * g) = make_uint2(pack2(o.x, o.y, T()), pack2(o.z, o.w, T()));
+        if (g == 0 && a.lse != nullptr) a.lse[row] = lse;
     }
-}
-
-// Two parts of every row, each with its log-sum-exp, into one: the prefix's where the row has one.
-template <typename T>
-__global__ void __launch_bounds__(256) prefix_merge_kernel(PrefixMergeArgs a) {
-    const int lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.B * a.Hq) return;
-    const int b = (int)(row / a.Hq);
-    const bool some = b >= a.cu[0] && b < a.cu[a.n_groups];  // rows outside the groups have no prefix
-    const float x = some ? a.prefix_lse[row] : -CUDART_INF_F, y = a.own_lse[row], top = fmaxf(x, y);
-    const float ref = top == -CUDART_INF_F ? 0.f : top;
-    const float wx = exp2f((x - ref) * kLog2e), wy = exp2f((y - ref) * kLog2e), sum = wx + wy;
-    const float4 p = some ? *reinterpret_cast<const float4*>(a.prefix_out + row * kTile + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 o = *reinterpret_cast<const float4*>(a.own_out + row * kTile + 4 * lane);
-    const float inv = sum != 0.f ? 1.f / sum : 0.f, fx = wx * inv, fy = wy * inv;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * kTile + 4 * lane) =
-        make_uint2(pack2(fmaf(fx, p.x, fy * o.x), fmaf(fx, p.y, fy * o.y), T()), pack2(fmaf(fx, p.z, fy * o.z), fmaf(fx, p.w, fy * o.w), T()));
-    if (a.lse != nullptr && lane == 0) a.lse[row] = sum != 0.f ? top + log2f(sum) * 0.69314718055994531f : -CUDART_INF_F;
 }
 
 struct Kernels {
@@ -1035,9 +1032,9 @@ struct Kernels {
     void (*join)(PromptArgs);
 };
 template <typename T>
-Kernels pick(bool general, bool wide) {
-    if (wide) return {general ? prompt_split_kernel<T, float, true> : prompt_split_kernel<T, float, false>, prompt_join_kernel<T, float>};
-    return {general ? prompt_split_kernel<T, T, true> : prompt_split_kernel<T, T, false>, prompt_join_kernel<T, T>};
+Kernels pick(bool general, bool own) {
+    if (own) return {general ? prompt_split_kernel<T, true, true> : prompt_split_kernel<T, true, false>, prompt_join_kernel<T, true>};
+    return {general ? prompt_split_kernel<T, false, true> : prompt_split_kernel<T, false, false>, prompt_join_kernel<T, false>};
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1120,8 +1117,8 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     a.box = a.page_size % 128 == 0 ? 128 : a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
     const float c = a.scale * kLog2e;
     const bool general = a.softcap > 0.f || a.slopes != nullptr || !(c >= 1e-30f && c <= 1e30f);
-    const bool wide = a.out_dtype == KVARN_DTYPE_FP32;
-    const Kernels k = dtype == KVARN_DTYPE_FP16 ? pick<__half>(general, wide) : pick<__nv_bfloat16>(general, wide);
+    const bool own = a.own_out != nullptr;
+    const Kernels k = dtype == KVARN_DTYPE_FP16 ? pick<__half>(general, own) : pick<__nv_bfloat16>(general, own);
     CUtensorMap k_map, v_map, q_map = {};
     // rows come by tiled copies where 128 of them are whole tokens and the strides are ones that the encoding takes
     a.tiled_rows = kHalf % a.group == 0 && (a.Hq == 1 || (a.q_head_stride > 0 && a.q_head_stride < (1ll << 38))) &&
@@ -1139,13 +1136,10 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     a.grid_mul = ~0ull / (unsigned)ctas + 1;
     e = launch_pdl(k.split, dim3(ctas), dim3(kThreads), kSmem, stream, k_map, v_map, q_map, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k.join, dim3(ctas, (a.slot_rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, stream, a);
-}
-
-cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, int dtype, cudaStream_t stream) {
-    const int64_t ctas = ((int64_t)a.B * a.Hq + 7) / 8;
-    return launch_pdl(dtype == KVARN_DTYPE_FP16 ? prefix_merge_kernel<__half> : prefix_merge_kernel<__nv_bfloat16>,
-                      dim3((unsigned)ctas), dim3(256), 0, stream, a);
+    // Few units have many parts each, and a CTA takes only kJoinRows rows of theirs; many units leave at most one with a
+    // few parts to a CTA of the split (152 x 32 CTAs of the join, most with nothing to do, took 3 us more than 152 x 8).
+    const int blocks = (a.slot_rows + kJoinRows - 1) / kJoinRows;
+    return launch_pdl(k.join, dim3(ctas, units > ctas && blocks > 8 ? 8 : blocks), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace kvarn
