@@ -878,8 +878,8 @@ kvarn_status kvarn_quantize_kv(kvarn_dtype x_dtype, int n_tokens, int Hkv, const
     else if (n_tokens > n_pages * page_size)
         return fail(KVARN_ERR_INVALID_ARG, "n_tokens = %d rows without a slot_map; the cache has %lld slots", n_tokens,
                     (long long)(n_pages * page_size));
-    if ((int64_t)n_tokens * Hkv > (1LL << 34))
-        return fail(KVARN_ERR_INVALID_ARG, "n_tokens = %d, Hkv = %d: need n_tokens * Hkv <= 2^34", n_tokens, Hkv);
+    if ((int64_t)n_tokens * Hkv > (1LL << 30))
+        return fail(KVARN_ERR_INVALID_ARG, "n_tokens = %d, Hkv = %d: need n_tokens * Hkv <= 2^30", n_tokens, Hkv);
     kvarn::QuantizeArgs a = {};
     a.n_tokens = n_tokens;
     a.Hkv = Hkv;

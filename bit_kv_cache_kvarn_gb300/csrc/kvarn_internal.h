@@ -217,7 +217,7 @@ cudaError_t read_and_clear_paged_q8_error(unsigned int* out);
 // Keys and values into a paged 8-bit cache: see kvarn_quantize_kv.  Input strides in elements, cache strides in bytes.
 struct QuantizeArgs {
     int n_tokens, Hkv, page_size, n_slots;
-    int64_t n_rows;  // set by the launcher: keys and values, a row of 128 channels each
+    unsigned n_rows;  // set by the launcher: keys and values, a row of 128 channels each
     int page_shift;  // set by the launcher: log2 of a page size that is a power of two, else -1
     const void* k;
     const void* v;

@@ -72,7 +72,8 @@ struct Shape {
     static constexpr int kStage = 2 * kHalf + (Q8 ? 2 * kGroup : 0);          // with the 8-bit ones' exponents
     static constexpr int kThreads = 32 * kWarps, kRing = kStages * kStage;    // bytes of a warp
 };
-constexpr float kHalfLift = 15.f;                      // fp16 probabilities are multiplied by 2^15
+constexpr float kHalfLift = 15.f;                      // fp16 probabilities are multiplied by 2^15,
+constexpr float kGrow = 4.f;                           // over 8-bit caches by 2^11, as scores may pass the maximum by 2^4 there
 constexpr int kJoinWarps = 16;
 constexpr int kAhead = 2;                              // parts that a warp of the join loads at once
 
@@ -119,6 +120,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d = a b
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // (x, y) to 16 bits; x and y become what is left
 __device__ __forceinline__ uint32_t take2(float& x, float& y, __nv_bfloat16) {
@@ -273,12 +281,12 @@ constexpr unsigned kStarts = 2;  //   it begins in this warp's piece
 constexpr unsigned kEnds = 4;    //   it ends with this warp's piece
 constexpr unsigned kHead = 8;    // its first unit began before its piece, ended inside it, and is in its head slot
 
-// E4M3 pairs (the low or the high half of x) to fp16 pairs, exactly
-__device__ __forceinline__ uint32_t half2_of_low(uint32_t x) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+// two E4M3 pairs to fp16 pairs, exactly
+__device__ __forceinline__ void halves_of(uint32_t& low, uint32_t& high, uint32_t x) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+        : "=r"(low), "=r"(high)
+        : "r"(x));
 }
-__device__ __forceinline__ uint32_t half2_of_high(uint32_t x) { return half2_of_low(x >> 16); }
 // 2^e for e of -127..127
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float(e > -127 ? (e + 127) << 23 : 1 << 22); }
 
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(Shape<NT, Q8>::kThreads, 1) paged_split_kernel
     constexpr int kRowBytes = Shape<NT, Q8>::kRowBytes;
     using P = typename std::conditional<Q8, __half, T>::type;  // of the products
     using C = typename std::conditional<Q8, uint8_t, T>::type;  // of the cache
-    constexpr float kLift = std::is_same<P, __half>::value ? kHalfLift : 0.f;  // log2 of the probabilities' factor
+    constexpr float kLift = Q8 ? kHalfLift - kGrow : std::is_same<P, __half>::value ? kHalfLift : 0.f;  // log2 of the probabilities' factor
     constexpr int PIECES = sizeof(O) == 4 && std::is_same<P, __nv_bfloat16>::value ? 3 : 2;  // of a probability
     extern __shared__ __align__(1024) uint8_t dsm[];
     __shared__ long long s_scan[kWarps];
@@ -574,8 +582,9 @@ __global__ void __launch_bounds__(Shape<NT, Q8>::kThreads, 1) paged_split_kernel
                     ldm4(f, kb + k_row * kRowBytes + (((2 * c2 + k_sel) ^ mr) << 4));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t w[4] = {half2_of_low(f[2 * i]), half2_of_low(f[2 * i + 1]), half2_of_high(f[2 * i]),
-                                               half2_of_high(f[2 * i + 1])};
+                        uint32_t w[4];
+                        halves_of(w[0], w[2], f[2 * i]);
+                        halves_of(w[1], w[3], f[2 * i + 1]);
 #pragma unroll
                         for (int e = 0; e < NT; ++e) mma(s[e][i], w, qf[e][2 * c2 + i][0], qf[e][2 * c2 + i][1], P());
                     }
@@ -615,18 +624,28 @@ __global__ void __launch_bounds__(Shape<NT, Q8>::kThreads, 1) paged_split_kernel
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     mx[e][i] = fmaxf(fmaxf(s[e][0][i], s[e][0][i + 2]), m[e][i]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx[e][i] = fmaxf(mx[e][i], __shfl_xor_sync(0xffffffffu, mx[e][i], d));
-                    grew |= mx[e][i] > m[e][i];
-                    if constexpr (Q8) {
+                    if constexpr (Q8) {  // this lane's tokens only: the others' are asked when some score passes its maximum by kGrow
                         mv[e][i] = fmaxf(fmaxf(s[e][0][i] + v_exp[0], s[e][0][i + 2] + v_exp[1]), mo[e][i]);
+                        grew |= mx[e][i] > m[e][i] + kGrow || mv[e][i] > mo[e][i] + kGrow;
+                    } else {
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) mv[e][i] = fmaxf(mv[e][i], __shfl_xor_sync(0xffffffffu, mv[e][i], d));
-                        grew |= mv[e][i] > mo[e][i];
+                        for (int d = 4; d < 32; d <<= 1) mx[e][i] = fmaxf(mx[e][i], __shfl_xor_sync(0xffffffffu, mx[e][i], d));
+                        grew |= mx[e][i] > m[e][i];
                     }
                 }
             }
             if (__any_sync(0xffffffffu, grew)) {
+                if constexpr (Q8) {
+#pragma unroll
+                    for (int e = 0; e < NT; ++e)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) {
+                                mx[e][i] = fmaxf(mx[e][i], __shfl_xor_sync(0xffffffffu, mx[e][i], d));
+                                mv[e][i] = fmaxf(mv[e][i], __shfl_xor_sync(0xffffffffu, mv[e][i], d));
+                            }
+                }
 #pragma unroll
                 for (int e = 0; e < NT; ++e) {
                     float al[2];
@@ -677,8 +696,13 @@ __global__ void __launch_bounds__(Shape<NT, Q8>::kThreads, 1) paged_split_kernel
 #pragma unroll
                 for (int e = 0; e < NT; ++e) {
                     float d[4] = {};
+                    if constexpr (Q8) {
+                        mma_first(d, f, p[e][1][0], p[e][1][1]);
+                        mma(d, f, p[e][0][0], p[e][0][1], P());
+                    } else {
 #pragma unroll
-                    for (int i = PIECES - 1; i >= 0; --i) mma(d, f, p[e][i][0], p[e][i][1], P());  // the small pieces first
+                        for (int i = PIECES - 1; i >= 0; --i) mma(d, f, p[e][i][0], p[e][i][1], P());  // the small pieces first
+                    }
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[e][cc][c] += d[c];
                 }
@@ -693,7 +717,9 @@ __global__ void __launch_bounds__(Shape<NT, Q8>::kThreads, 1) paged_split_kernel
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t x = __byte_perm(g[2 * i], 0, 0x3120), y = __byte_perm(g[2 * i + 1], 0, 0x3120);
-                        const uint32_t f[4] = {half2_of_low(x), half2_of_high(x), half2_of_low(y), half2_of_high(y)};
+                        uint32_t f[4];
+                        halves_of(f[0], f[1], x);
+                        halves_of(f[2], f[3], y);
                         add(2 * c2 + i, f);
                     }
                 }

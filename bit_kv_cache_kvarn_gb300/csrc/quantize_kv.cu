@@ -51,20 +51,21 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_kv_kernel(QuantizeArgs a
     const int lane = threadIdx.x & 31, part = lane & 15;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (2 * kAhead) + (lane >> 4);
+    const unsigned first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * (2 * kAhead) + (lane >> 4), per_token = 2u * a.Hkv;
+    unsigned token = first / per_token, r = first - token * per_token;  // the only division; the other rows go on from there
     float x[kAhead][8];
     int slot[kAhead], kind[kAhead], head[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-        const int64_t row = first + 2 * i;
         slot[i] = -1;
-        if (row < a.n_rows) {
-            const unsigned token = (unsigned)(row / (unsigned)(2 * a.Hkv)), r = (unsigned)(row - (int64_t)token * (2 * a.Hkv));
+        if (first + 2 * i < a.n_rows) {
             kind[i] = r >= (unsigned)a.Hkv;
             head[i] = (int)r - (kind[i] ? a.Hkv : 0);
             slot[i] = a.slot_map != nullptr ? __ldg(a.slot_map + token) : (int)token;
             load8(x[i], static_cast<const T*>(kind[i] ? a.v : a.k) + (int64_t)token * a.kv_token_stride + (int64_t)head[i] * a.kv_head_stride + 8 * part);
         }
+        r += 2;
+        if (r >= per_token) r -= per_token, ++token;
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -101,13 +102,12 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_kv_kernel(QuantizeArgs a
 cudaError_t read_and_clear_quantize_error(unsigned int* out) { return read_and_clear_word(&g_quantize_error, out); }
 
 cudaError_t launch_quantize_kv(QuantizeArgs a, int x_dtype, cudaStream_t stream) {
-    a.n_rows = (int64_t)a.n_tokens * 2 * a.Hkv;
+    a.n_rows = (unsigned)a.n_tokens * 2u * (unsigned)a.Hkv;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
-    const int64_t ctas = (a.n_rows + kWarps * 2 * kAhead - 1) / (kWarps * 2 * kAhead);
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const unsigned ctas = (a.n_rows + kWarps * 2 * kAhead - 1) / (kWarps * 2 * kAhead);
     const auto kern = x_dtype == KVARN_DTYPE_FP32 ? quantize_kv_kernel<float>
                       : x_dtype == KVARN_DTYPE_FP16 ? quantize_kv_kernel<__half> : quantize_kv_kernel<__nv_bfloat16>;
-    return launch_pdl(kern, dim3((unsigned)ctas), dim3(32 * kWarps), 0, stream, a);
+    return launch_pdl(kern, dim3(ctas), dim3(32 * kWarps), 0, stream, a);
 }
 
 }  // namespace kvarn

@@ -528,7 +528,7 @@ kvarn_status kvarn_prefix_attention(kvarn_dtype dtype, int B, int n_groups, int 
  *                 not written; any other slot outside the cache is not written either and sets value 32 of
  *                 kvarn_device_error.  Slots are distinct.
  * n_tokens = 0 is a no-op.  1 <= Hkv <= 65535, page_size >= 1, n_pages * page_size <= 2^31 - 1, n_tokens * Hkv <=
- * 2^34.  One launch. */
+ * 2^30.  One launch. */
 kvarn_status kvarn_quantize_kv(kvarn_dtype x_dtype, int n_tokens, int Hkv, const void* k, const void* v,
                                int64_t kv_token_stride, int64_t kv_head_stride, void* k_cache, void* v_cache,
                                int64_t n_pages, int page_size, int64_t page_stride, int64_t head_stride,
