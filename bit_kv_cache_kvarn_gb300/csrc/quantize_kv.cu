@@ -21,39 +21,42 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kAhead = 4;  // rows that half a warp loads at once
 
-// eight neighbouring channels
-__device__ __forceinline__ void load8(float (&x)[8], const __nv_bfloat16* p) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// eight neighbouring channels, as they lie in memory until they are used
+template <typename T>
+struct Eight {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-}
-__device__ __forceinline__ void load8(float (&x)[8], const __half* p) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
     }
-}
-__device__ __forceinline__ void load8(float (&x)[8], const float* p) {
+    __device__ __forceinline__ void values(float (&x)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                const uint32_t w[4] = {v[i >> 1].x, v[i >> 1].y, v[i >> 1].z, v[i >> 1].w};
+                x[2 * i] = __uint_as_float(w[2 * (i & 1)]), x[2 * i + 1] = __uint_as_float(w[2 * (i & 1) + 1]);
+            } else {
+                const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                if constexpr (std::is_same<T, __half>::value) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+                } else {
+                    x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                }
+            }
+        }
     }
-}
+};
 
 // Rows in the order (token, keys or values, head).
 template <typename T>
-__global__ void __launch_bounds__(32 * kWarps) quantize_kv_kernel(QuantizeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 10) quantize_kv_kernel(QuantizeArgs a) {
     const int lane = threadIdx.x & 31, part = lane & 15;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const unsigned first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * (2 * kAhead) + (lane >> 4), per_token = 2u * a.Hkv;
     unsigned token = first / per_token, r = first - token * per_token;  // the only division; the other rows go on from there
-    float x[kAhead][8];
+    Eight<T> in[kAhead];
     int slot[kAhead], kind[kAhead], head[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -62,16 +65,17 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_kv_kernel(QuantizeArgs a
             kind[i] = r >= (unsigned)a.Hkv;
             head[i] = (int)r - (kind[i] ? a.Hkv : 0);
             slot[i] = a.slot_map != nullptr ? __ldg(a.slot_map + token) : (int)token;
-            load8(x[i], static_cast<const T*>(kind[i] ? a.v : a.k) + (int64_t)token * a.kv_token_stride + (int64_t)head[i] * a.kv_head_stride + 8 * part);
+            in[i].load(static_cast<const T*>(kind[i] ? a.v : a.k) + (int64_t)token * a.kv_token_stride + (int64_t)head[i] * a.kv_head_stride + 8 * part);
         }
         r += 2;
         if (r >= per_token) r -= per_token, ++token;
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-        float top = 0.f;
+        float top = 0.f, x[8];
+        in[i].values(x);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(x[i][c]));
+        for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(x[c]));
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         if (slot[i] < 0 || slot[i] >= a.n_slots) {
@@ -85,8 +89,8 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_kv_kernel(QuantizeArgs a
         uint32_t w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[i][4 * h] * scale, x[i][4 * h + 1] * scale), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[i][4 * h + 2] * scale, x[i][4 * h + 3] * scale), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h] * scale, x[4 * h + 1] * scale), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h + 2] * scale, x[4 * h + 3] * scale), __NV_SATFINITE, __NV_E4M3);
             w[h] = lo | hi << 16;
         }
         const int page = a.page_shift >= 0 ? slot[i] >> a.page_shift : slot[i] / a.page_size, in_page = slot[i] - page * a.page_size;
