@@ -113,7 +113,8 @@ __device__ __forceinline__ int cost_of(const PromptArgs& a, const Seq& s, int u)
 struct Piece {
     int t0, t1;          // t1 < t0: nothing more comes
     int a0[2], a1[2];
-    int lo, hi;          // keys that some row of the unit sees
+    int lo, hi;          // keys that some row of the unit sees,
+    int all_lo, all_hi;  // and those that all of its rows see
     int b, h, u;
     int q0, shift, len, start, f0;  // the sequence's first row of q, the position of its first row, ...
     int rows;            // of the unit
@@ -156,6 +157,11 @@ struct Walk {
         p.rows = (int)(past - f0);
         const Keys keys = keys_of(a, s, f0, past);
         p.lo = keys.lo, p.hi = keys.hi;
+        p.all_lo = s.start, p.all_hi = s.len;
+        if (a.causal) {
+            p.all_hi = min(s.len, p.shift + (int)token_of(a, f0) + 1);
+            if (a.window > 0) p.all_lo = max(s.start, p.shift + (int)token_of(a, past - 1) + 1 - a.window);
+        }
         const int first = keys.first(), cost = keys.past() - first + kUnitCost;
         const int o1 = (int)min((long long)cost, o + (end - at));
         p.t0 = first + max(o - kUnitCost, 0), p.t1 = first + o1 - kUnitCost;
@@ -209,6 +215,17 @@ __device__ __forceinline__ uint32_t pack2(float x, float y, __half) {
 }
 // mbar_wait in as few instructions as possible: the kernel has three dozen of these, and with each poll loop unrolled
 // its code was 145 KB, more than the instruction caches hold (a unit's epilogue took 4600 cycles instead of EPI).
+// sum + 0 x, two 16-bit numbers at a time
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t sum, __nv_bfloat16) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0), "r"(sum));
+    return r;
+}
+__device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t sum, __half) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0), "r"(sum));
+    return r;
+}
 // 32 bytes, in one store where `wide` says that they are aligned
 __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool wide) {
     if (wide) {
@@ -276,7 +293,7 @@ struct Barriers {
 
 // The ring of pieces as one of its readers goes through it.
 struct Reader {
-    uint32_t slot = 0, parity = 0;
+    uint32_t slot = 0, parity = 0, n = 0;  // n: pieces taken
     // A whole warp waits for the next piece and copies what it needs by `take`; false: nothing more
     template <typename F>
     __device__ __forceinline__ bool next(const Piece* ring, Barriers& bar, unsigned int* err, int lane, F take) {
@@ -287,6 +304,7 @@ struct Reader {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.piece_empty[slot]);
         if (++slot == kPieces) slot = 0, parity ^= 1;
+        ++n;
         return some;
     }
 };
@@ -497,6 +515,29 @@ __device__ __forceinline__ float join_lse(float x, float y, float& fx, float& fy
     return sum != 0.f ? top + log2f(sum) * kLn2 : -CUDART_INF_F;
 }
 
+// NaN into the channels of a row's output (or of its part in a slot) in which a value of the tokens [from, past) that the
+// row sees (those in [lo, hi)) is an infinity or a NaN.  Rare: straight from the cache, a token after the other.
+template <typename T>
+__device__ __forceinline__ void odd_channels(const PromptArgs& a, int b, int h, int from, int past, int lo, int hi, T* out,
+                                             float* part, size_t part_stride) {
+    constexpr uint32_t kOdd = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+#pragma unroll 1
+    for (int t = max(from, lo); t < min(past, hi); ++t) {
+        const int entry = a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size;
+        const int page = a.page_table[(int64_t)b * a.max_pages + entry];
+        if (page < 0 || page >= a.n_pages) continue;
+        const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.v_cache) + (int64_t)page * a.page_stride +
+                                                              (int64_t)h * a.head_stride + (int64_t)(t - entry * a.page_size) * a.token_stride);
+#pragma unroll 1
+        for (int c = 0; c < kTile; ++c) {
+            if ((__vcmpgeu2(__ldg(v + c / 2) & 0x7fff7fffu, kOdd) >> (16 * (c & 1)) & 1u) == 0) continue;
+            if (out != nullptr) out[c] = T(CUDART_NAN_F);
+            else part[(c >> 2) * part_stride + (c & 3)] = CUDART_NAN_F;
+        }
+    }
+    __syncwarp();
+}
+
 // T: type of q, the cache and the output; OWN: each row is joined with a part of its own (kvarn_prefix_attention); GEN: scores are capped or biased, or the scale has a sign or
 // size for which the maximum cannot be taken before it.
 template <typename T, bool OWN, bool GEN>
@@ -510,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t dsm_raw[];
     __shared__ Barriers bar;
     __shared__ Piece s_piece[kPieces];
+    __shared__ int2 s_odd[2 * kPieces];  // tiles of a piece in which the edge warp found values that are no numbers
     __shared__ uint32_t s_tmem;
     __shared__ long long s_end;  // of this CTA's share
     uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) & ~(uintptr_t)1023);
@@ -661,6 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         out[(size_t)k * a.slot_rows] = make_uint4(o[k >> 3][(k & 7) * 4], o[k >> 3][(k & 7) * 4 + 1], o[k >> 3][(k & 7) * 4 + 2], o[k >> 3][(k & 7) * 4 + 3]);
                 }
             }
+            const int2 odd = s_odd[(reader.n - 1) % (2 * kPieces)];
+            if (any && odd.y >= odd.x)
+                odd_channels<T>(a, p.b, p.h, max(odd.x, first) * kTile, min(odd.y + 1, past) * kTile, lo, l != 0.f ? hi : lo,
+                                whole ? static_cast<T*>(a.out) + row * kTile : nullptr, slot + 4 * (size_t)rr, 4 * (size_t)a.slot_rows);
             if (real) {
                 if (whole) {
                     if (a.lse != nullptr) a.lse[row] = lse;
@@ -683,10 +729,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool fine = true;
             const int boxes = kTile / a.box;
             uint32_t used = 0, on_raw = 0, last_parity = 0, raw_parity = 0;  // a bit for each stage: its last copy, for the way out
-            int t0, t1, a0[2], a1[2], lo, hi, h;
+            int t0, t1, a0[2], a1[2], lo, hi, all_lo, all_hi, h;
             const int32_t* table;
             while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
-                t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi, h = p.h;
+                t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi, all_lo = p.all_lo, all_hi = p.all_hi, h = p.h;
                 a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
                 table = a.page_table + (int64_t)p.b * a.max_pages;
             })) {
@@ -715,8 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fence_proxy_async();
                         __syncwarp();
                     }
-                    // values with rows that nobody may see go through the edge warp
-                    const bool edge = values && (t * kTile < lo || (t + 1) * kTile > hi);
+                    // values that some row may not see go through the edge warp
+                    const bool edge = values && (t * kTile < all_lo || (t + 1) * kTile > all_hi);
                     uint64_t* b = edge ? &bar.raw[stage] : &bar.full[stage];
                     if (lane == 0) {
                         if (bytes > 0) mbar_expect_tx(b, bytes);
@@ -905,13 +951,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             pair_sync();
             walk.end = s_end;
             if (warp == kPlanWarp) {
-            uint32_t slot = 0, parity = 1;
-            for (bool more = true; more;) {
+            uint32_t slot = 0, parity = 1, n = 0;
+            for (bool more = true; more; ++n) {
                 Piece p;
                 more = walk.next(a, p, lane);
                 if (!more) p.t0 = 1, p.t1 = 0;
                 if (!wait_for(&bar.piece_empty[slot], parity, err)) break;
                 if (lane == 0) {
+                    s_odd[n % (2 * kPieces)] = make_int2(0x7fffffff, -1);
                     s_piece[slot] = p;
                     mbar_arrive(&bar.piece_full[slot]);
                 }
@@ -919,29 +966,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++slot == kPieces) slot = 0, parity ^= 1;
             }
             } else {
-            // ---- values at the edges of what a unit sees: rows outside are zeros ----
+            // ---- values that not every row of the unit sees: those outside what any sees become zeros, and so do infinities
+            // and NaNs (a probability of 0 would not keep them out); rows that do see one get it in their epilogue ----
+            constexpr uint32_t kOdd = kIsHalf ? 0x7c007c00u : 0x7f807f80u;  // exponents of such values
             uint32_t stage = 1, raw_parity = 0;  // the values' stage; a bit for each
             bool fine = true;
-            int t0, t1, a0[2], a1[2], lo, hi;
+            int t0, t1, a0[2], a1[2], lo, hi, all_lo, all_hi;
             while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
-                t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi;
+                t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi, all_lo = p.all_lo, all_hi = p.all_hi;
                 a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
             })) {
 #pragma unroll 1
                 for (int t = t0; t < t1; ++t) {
                     if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
-                    if (t * kTile < lo || (t + 1) * kTile > hi) {
+                    if (t * kTile < all_lo || (t + 1) * kTile > all_hi) {
                         fine = wait_for(&bar.raw[stage], (raw_parity >> stage) & 1, err);
                         if (!fine) break;
                         raw_parity ^= 1u << stage;
                         uint8_t* v = ring + stage * kStageBytes;
                         const int lo_in = max(lo - t * kTile, 0), hi_in = min(hi - t * kTile, kTile);
+                        // a lane takes a 16-byte chunk of every other row
+                        uint8_t* const own = v + ((lane >> 3) & 1) * kSpan + (lane >> 4) * kTile + (lane & 7) * 16;
 #pragma unroll 1
-                        for (int i = lane; i < lo_in * 16; i += 32)
-                            *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kSpan + (i >> 4) * kTile + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int r = lane >> 4; r < lo_in; r += 2) *reinterpret_cast<uint4*>(own + (r - (lane >> 4)) * kTile) = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-                        for (int i = hi_in * 16 + lane; i < kTile * 16; i += 32)
-                            *reinterpret_cast<uint4*>(v + ((i >> 3) & 1) * kSpan + (i >> 4) * kTile + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        for (int r = hi_in + ((hi_in ^ (lane >> 4)) & 1); r < kTile; r += 2)
+                            *reinterpret_cast<uint4*>(own + (r - (lane >> 4)) * kTile) = make_uint4(0, 0, 0, 0);
+                        uint32_t sum[2] = {0, 0};  // of 0 x: a NaN where some x is no number
+                        if (max(lo, t * kTile) < all_lo || min(hi, (t + 1) * kTile) > all_hi) {  // not only at the unit's own edges
+                            __syncwarp();
+#pragma unroll 1
+                            for (int r = 0; r < kTile; r += 16) {
+                                uint4 w[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4*>(own + (r + 2 * i) * kTile);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    sum[0] = add_zero_times(w[i].x, sum[0], T()), sum[1] = add_zero_times(w[i].y, sum[1], T());
+                                    sum[0] = add_zero_times(w[i].z, sum[0], T()), sum[1] = add_zero_times(w[i].w, sum[1], T());
+                                }
+                            }
+                        }
+                        if (__any_sync(0xffffffffu, ((sum[0] | sum[1]) & 0x7fff7fffu) != 0)) {
+#pragma unroll 1
+                            for (int i = lane; i < kTile * 16 * 4; i += 32) {
+                                uint32_t* at = reinterpret_cast<uint32_t*>(v) + i;
+                                *at &= ~__vcmpgeu2(*at & 0x7fff7fffu, kOdd);
+                            }
+                            if (lane == 0) {
+                                int2& odd = s_odd[(reader.n - 1) % (2 * kPieces)];
+                                odd = make_int2(min(odd.x, t), t);
+                            }
+                        }
                         fence_proxy_async();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar.full[stage]);

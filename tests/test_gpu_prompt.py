@@ -172,3 +172,32 @@ def test_many_rows_without_keys_between_others(kv):
     # and inside one sequence, for each head
     c = case(22, [2500, 60], [0, 10], 8, 8, 48, HF, starts=[2000, 0], window=200)
     check(c, *call(kv, c))
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("kw", [dict(), dict(window=100), dict(window=300, starts=[60, 0, 0]), dict(softcap=20.0), dict(causal=False)])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (3, 3), (16, 1)])
+def test_infinite_and_nan_values_reach_only_the_rows_that_see_them(kv, dt, kw, hq, hkv):
+    kw = dict(kw)
+    softcap = kw.pop("softcap", 0.0)
+    c = case(31, [400, 130, 70], [0, 300, 5], hq, hkv, 16, dt, **kw)
+    start = 0 if c["starts"] is None else 60
+    for b, j, h, ch, x in ((0, 70, 0, 3, math.nan), (0, 255, 0, 64, math.inf), (0, 256, hkv - 1, 127, -math.inf), (0, 399, 0, 0, math.nan),
+                           (1, 301, 0, 31, math.nan), (1, 10, hkv - 1, 32, math.inf), (2, 74, 0, 95, math.inf), (2, 6, 0, 96, math.nan)):
+        page = int(c["table"][b, j // 16])
+        if page < c["vc"].shape[0] and (j >= start or b):  # (a window may leave a page unused)
+            c["vc"][page, h, j % 16, ch] = x
+    # keys that a row does not see have no part either
+    c["kc"][int(c["table"][0, 399 // 16]), 0, 399 % 16] = math.nan
+    want = o.prompt_attention(np64(c["q"]), np64(c["kc"]), np64(c["vc"]), c["table"].cpu().numpy(), c["cu"].cpu().numpy(),
+                              c["lens"].cpu().numpy(), SCALE, c["causal"], softcap, None, c["window"],
+                              None if c["starts"] is None else c["starts"].cpu().numpy())[0]
+    out, lse = call(kv, c, softcap=softcap)
+    got = np64(out)
+    if c["causal"]:  # the row with the NaN key is one token's; the others are as without it
+        rows = np.ones(len(got), bool)
+        rows[399] = False
+        assert np.array_equal(np.isfinite(got[rows]), np.isfinite(want[rows]))
+        ok = np.isfinite(want) & rows[:, None, None]
+        assert np.abs(got - want)[ok].max() <= 0.05
+    assert not np.isfinite(got[np.isnan(want)]).any()
