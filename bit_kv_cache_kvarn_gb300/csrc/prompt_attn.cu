@@ -1201,7 +1201,7 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
                    (a.T == 1 || (a.q_token_stride > 0 && a.q_token_stride < (1ll << 38)));
     e = cache_map(&k_map, a, dtype, a.k_cache);
     if (e == cudaSuccess) e = cache_map(&v_map, a, dtype, a.v_cache);
-    if (e == cudaSuccess && a.tiled_rows) e = rows_map(&q_map, a, dtype);
+    if (e == cudaSuccess && a.tiled_rows) a.tiled_rows = rows_map(&q_map, a, dtype) == cudaSuccess;
     if (e == cudaSuccess) e = set_smem_limit_once(k.split, kSmem, false, dev);
     if (e != cudaSuccess) return e;
     // no more CTAs than parts of kMinPart tiles that the call can have

@@ -10,6 +10,9 @@ that times sum p |v|, plus the output's rounding; lse by the score's error and t
 thread's additions (64 and one for each 128 keys), 2^-20 and 2^-22 of itself.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -201,3 +204,205 @@ def test_infinite_and_nan_values_reach_only_the_rows_that_see_them(kv, dt, kw, h
         ok = np.isfinite(want) & rows[:, None, None]
         assert np.abs(got - want)[ok].max() <= 0.05
     assert not np.isfinite(got[np.isnan(want)]).any()
+
+
+@pytest.mark.parametrize("garbage", [math.inf, -math.inf, 6e4, -6e4])
+def test_garbage_of_every_kind_stays_out(kv, garbage):
+    c = case(41, [200, 3, 40], [70, 0, 1000], 8, 2, 48, BF, starts=[11, 0, 300], window=500, garbage=garbage)
+    check(c, *call(kv, c))
+
+
+def test_bad_pages_count_as_zeros_and_are_reported(kv):
+    c = case(42, [200, 60], [100, 0], 4, 2, 16)
+    c["table"][0, 3], c["table"][0, 17], c["table"][1, 2] = -1, c["kc"].shape[0], 2 ** 30
+    out, lse = call(kv, c)
+    assert kv.kvarn_device_error() == 64
+    check(c, out, lse)
+
+
+def test_lengths_past_the_table_and_rows_without_a_place_are_clamped(kv):
+    c = case(43, [50, 20, 9], [0, 30, 0], 4, 2, 16)
+    c["lens"].copy_(i32([10 ** 9, 50, -5]))  # the first is cut to what its table holds, the last to 0
+    c["kc"][~torch.isfinite(c["kc"])] = 0
+    c["vc"][~torch.isfinite(c["vc"])] = 0
+    out, lse = call(kv, c)
+    check(c, out, lse)
+    assert torch.all(out[70:] == 0) and torch.isneginf(lse[70:]).all()
+    kv.kvarn_device_error()  # (the first sequence's last page table entries name no page)
+    # cu_tokens past the rows that there are
+    c = case(44, [50, 20], [0, 30], 4, 2, 16)
+    c["q"] = c["q"][:60].contiguous()
+    out, lse = call(kv, c)
+    c["cu"] = i32([0, 50, 60])
+    check(c, out, lse)
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (10, 2)])
+def test_strided_and_repeated_queries(kv, hq, hkv):
+    c = case(45, [130, 5], [10, 400], hq, hkv, 32)
+    wide = torch.randn(135, hq + 5, 136, device="cuda").to(BF)
+    for q in (wide[:, 2:2 + hq, :128], wide.transpose(0, 1)[:hq].transpose(0, 1)[..., 8:], wide[:1, :hq, :128].expand(135, hq, 128),
+              wide[:, :1, :128].expand(135, hq, 128)):
+        check({**c, "q": q}, *call(kv, {**c, "q": q}))
+
+
+def test_outputs_at_odd_places(kv):
+    # 16-byte but not 32-byte aligned
+    c = case(46, [100, 3], [0, 50], 8, 2)
+    flat = torch.full((103 * 8 * 128 + 8,), FILL, dtype=BF, device="cuda")
+    out = flat[8:].view(103, 8, 128)
+    lse = torch.full((103 * 8 + 1,), FILL, device="cuda")[1:].view(103, 8)
+    check(c, *call(kv, c, out=out, lse=lse))
+    assert torch.all(flat[:8] == FILL)
+
+
+def test_repeats_bit_for_bit_and_ignores_the_workspace(kv):
+    c = case(47, [700, 17, 300, 1], [2000, 0, 9, 5000], 16, 2, 64)
+    n = kv.kvarn_prompt_attention_workspace_size(c["q"].shape[0], 16, 2)
+    a = call(kv, c, ws=torch.zeros(n, dtype=torch.uint8, device="cuda"))
+    b = call(kv, c, ws=torch.full((n,), 127, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    out, _ = call(kv, c, with_lse=False)
+    assert torch.equal(out, a[0])
+
+
+def test_single_tokens_equal_the_decode_attention(kv):
+    lens = [1, 40, 900, 128, 3001]
+    c = case(48, [1] * 5, [n - 1 for n in lens], 8, 2, 32, window=700)
+    out, lse = call(kv, c)
+    ws = torch.empty(kv.kvarn_paged_attention_workspace_size(5, 8, 2), dtype=torch.uint8, device="cuda")
+    want, want_lse = torch.empty(5, 8, 128, device="cuda"), torch.empty(5, 8, device="cuda")
+    kv.kvarn_paged_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], want, SCALE, ws, window=700, lse=want_lse)
+    assert (lse - want_lse).abs().max() <= 1e-4 and (out.float() - want).norm() <= 2.0 ** -8 * want.norm()
+
+
+def test_cache_past_32_bit_offsets(kv):
+    P, n_pages, hkv = 128, 17000, 8  # 2.2e9 elements per cache: the pages in use are the last ones
+    kc, vc = (torch.empty(n_pages, P, hkv, 128, dtype=BF, device="cuda").transpose(1, 2) for _ in range(2))
+    c = case(49, [200, 30], [100, 99], 16, hkv, P, layout="nhd", garbage=0.0)
+    small = c["kc"].shape[0]
+    for big, src in ((kc, c["kc"]), (vc, c["vc"])):
+        big[n_pages - small:] = src
+    want = call(kv, c)
+    far = dict(c, kc=kc, vc=vc, table=torch.where(c["table"] < small, c["table"] + (n_pages - small), c["table"]))
+    got = call(kv, far)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check(c, *got)
+
+
+def test_graphs_share_a_workspace_and_follow_the_lengths(kv):
+    c1, c2 = case(50, [300, 60], [900, 0], 8, 2, 32), case(51, [40, 9, 500], [0, 70, 100], 8, 2, 16)
+    ws = torch.empty(kv.kvarn_prompt_attention_workspace_size(549, 8, 2), dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty_like(c["q"]), torch.empty(c["q"].shape[:2], device="cuda")) for c in (c1, c2)]
+    g1 = _capture(lambda: call(kv, c1, ws=ws, out=outs[0][0], lse=outs[0][1]))
+    g2 = _capture(lambda: call(kv, c2, ws=ws, out=outs[1][0], lse=outs[1][1]))
+    for cu, lens in (([0, 300, 360], [1200, 60]), ([0, 1, 1], [700, 0]), ([5, 300, 340], [300, 41])):
+        c1["cu"].copy_(i32(cu))
+        c1["lens"].copy_(i32(lens))
+        for t in outs[0] + outs[1]:
+            t.fill_(FILL)
+        for _ in range(3):
+            g1.replay()
+            g2.replay()
+        torch.cuda.synchronize()
+        for c, got in ((c1, outs[0]), (c2, outs[1])):
+            want = call(kv, c)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_side_streams_with_their_own_workspaces(kv):
+    cs = [case(52 + i, [200, 10 * i, 99], [1000, 5, 0], 8, 2, 32) for i in range(3)]
+    want = [call(kv, c) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    got = []
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, call(kv, cs[i])))
+    torch.cuda.synchronize()
+    for i, (out, lse) in got:
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_many_sequences(kv):
+    # more than one CTA's warps can count at once, most of them without rows
+    new = [0] * 5000
+    for b in range(0, 5000, 37):
+        new[b] = 1 + b % 5
+    c = case(60, new, [b % 90 if n else 0 for b, n in enumerate(new)], 4, 1, 16)
+    check(c, *call(kv, c))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_cases(kv, seed):
+    rng = np.random.default_rng(1000 + seed)
+    B = int(rng.integers(1, 9))
+    new = [int(x) for x in rng.integers(0, rng.choice([3, 40, 400]), B)]
+    ctx = [int(x) for x in rng.integers(0, rng.choice([2, 200, 3000]), B)]
+    hq, hkv = [(8, 2), (5, 1), (6, 6), (16, 1), (12, 4), (40, 2)][int(rng.integers(6))]
+    causal = bool(rng.random() < 0.8)
+    kw = dict(causal=causal, window=int(rng.integers(1, 700)) if causal and rng.random() < 0.5 else 0,
+              starts=[int(x) for x in rng.integers(-3, 300, B)] if rng.random() < 0.4 else None)
+    softcap = 25.0 if rng.random() < 0.3 else 0.0
+    slopes = 2.0 ** -torch.arange(1, hq + 1, device="cuda", dtype=F32) if causal and rng.random() < 0.3 else None
+    c = case(seed, new, ctx, hq, hkv, int(rng.choice([16, 48, 64, 128, 272])), BF if rng.random() < 0.5 else HF,
+             str(rng.choice(["hnd", "nhd", "both"])), spare_rows=int(rng.integers(0, 5)), **kw)
+    check(c, *call(kv, c, softcap=softcap, slopes=slopes), softcap=softcap, slopes=slopes)
+
+
+def test_python_refusals(kv):
+    c = case(61, [20], [0], 4, 2)
+    for change, match in ((dict(lens=c["lens"].long()), "kv_lens"), (dict(q=c["q"].half()), "k_cache"), (dict(cu=c["cu"][:1]), "cu_tokens"),
+                          (dict(table=c["table"][0]), "page_table"), (dict(q=c["q"].cpu()), "current CUDA"), (dict(lens=i32([20, 3])), "kv_lens"),
+                          (dict(vc=c["vc"].transpose(1, 2)), "v_cache"), (dict(q=c["q"][..., :64]), "q")):
+        with pytest.raises(ValueError, match=match):
+            call(kv, {**c, **change})
+    with pytest.raises(ValueError, match="out"):
+        call(kv, c, out=torch.empty(20, 4, 128, device="cuda"))
+    with pytest.raises(kv.KvarnError, match="workspace"):
+        call(kv, c, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(kv.KvarnError, match="window"):
+        call(kv, {**c, "causal": False, "window": 5})
+
+
+def test_first_calls_of_a_process_may_be_captured(kv):
+    code = """
+import torch, bit_kv_cache_kvarn_gb300 as kv
+kv.load()
+i32 = dict(dtype=torch.int32, device="cuda")
+q = torch.randn(40, 4, 128, device="cuda").to(torch.bfloat16)
+kc, vc = (torch.randn(4, 2, 16, 128, device="cuda").to(torch.bfloat16) for _ in range(2))
+table, cu, lens = torch.arange(4, **i32)[None], torch.tensor([0, 40], **i32), torch.tensor([60], **i32)
+out, lse = torch.empty_like(q), torch.empty(40, 4, device="cuda")
+ws = torch.empty(kv.kvarn_prefix_attention_workspace_size(40, 4, 2), dtype=torch.uint8, device="cuda")
+pre, pre_lse = torch.empty_like(q), torch.empty(40, 4, device="cuda")
+own, none = table.expand(40, 4).contiguous(), torch.full((40,), 9, **i32)
+c8 = [torch.zeros(4, 2, 16, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+e8 = [torch.zeros(4, 2, 16, dtype=torch.int8, device="cuda") for _ in range(2)]
+dec = torch.empty(1, 4, 128, device="cuda")
+flat = [x.transpose(1, 2).reshape(64, 2, 128) for x in (kc, vc)]
+
+def step():
+    kv.kvarn_prompt_attention(q, kc, vc, table, cu, lens, out, 0.1, ws, lse=lse)
+    kv.kvarn_prefix_attention(q, kc, vc, table, lens, cu, own, none, pre, 0.1, ws, lse=pre_lse)
+    kv.kvarn_quantize_kv(*flat, *c8, *e8)
+    kv.kvarn_paged_attention_q8(q[39:], *c8, *e8, table, lens, dec, 0.1, ws)
+
+torch.cuda.synchronize()
+s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+with torch.cuda.stream(s):
+    with torch.cuda.graph(g, stream=s):
+        step()
+g.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in (out, lse, pre, pre_lse, dec)]
+assert all(torch.isfinite(t).all() and t.abs().max() > 0 for t in first)
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, (out, lse, pre, pre_lse, dec))) and kv.kvarn_device_error() == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
