@@ -1048,9 +1048,11 @@ kvarn_status kvarn_prefix_attention(kvarn_dtype dtype, int B, int n_groups, int 
     KV_TRY(check_ptr(q, 16, "q"));
     KV_TRY(check_strides("q", q_token_stride, q_head_stride, 8));
     KV_TRY(check_tiled_cache(k_cache, v_cache, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
-    KV_TRY(check_ptr(prefix_table, 4, "prefix_table"));
-    KV_TRY(check_ptr(prefix_lens, 4, "prefix_lens"));
-    KV_TRY(check_ptr(cu_seqs, 4, "cu_seqs"));
+    if (n_groups > 0) {
+        KV_TRY(check_ptr(prefix_table, 4, "prefix_table"));
+        KV_TRY(check_ptr(prefix_lens, 4, "prefix_lens"));
+        KV_TRY(check_ptr(cu_seqs, 4, "cu_seqs"));
+    }
     KV_TRY(check_ptr(page_table, 4, "page_table"));
     KV_TRY(check_ptr(kv_lens, 4, "kv_lens"));
     KV_TRY(check_ptr(out, 16, "out"));

@@ -499,7 +499,8 @@ size_t kvarn_prefix_attention_workspace_size(int B, int Hq, int Hkv);
  *   dtype, q, cache, softcap, out, lse : as for kvarn_prompt_attention, with T = B.
  *   workspace   : >= kvarn_prefix_attention_workspace_size(B, Hq, Hkv) bytes, 16-byte aligned; needs no clearing.
  *                 Calls that may overlap on the GPU need one each.
- * Sequences without a visible key get zeros and lse -inf.  0 <= B, n_groups <= 16384; B = 0 is a no-op. */
+ * Sequences without a visible key get zeros and lse -inf.  0 <= B, n_groups <= 16384; B = 0 is a no-op, and with
+ * n_groups = 0 the prefixes' arrays may be NULL. */
 kvarn_status kvarn_prefix_attention(kvarn_dtype dtype, int B, int n_groups, int Hq, int Hkv, const void* q,
                                     int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
                                     const void* v_cache, int64_t n_pages, int page_size, int64_t page_stride,

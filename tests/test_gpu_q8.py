@@ -10,6 +10,7 @@ import pytest
 import torch
 
 from oracle import serving as o
+from tests.test_gpu_graph import _capture
 from tests.test_gpu_prompt import BF, F32, HF, SCALE, i32, np64
 
 pytestmark = pytest.mark.gpu
@@ -215,3 +216,101 @@ def test_attention_bad_pages_count_as_zeros_and_are_reported(kv):
     out, lse = call(kv, c)
     assert kv.kvarn_device_error() == 64
     check(c, out, lse)
+
+
+def test_attention_of_written_rows_repeats_and_follows_replays(kv):
+    """A decode loop over 8-bit pages in one graph: write of the step's rows, attention over all so far."""
+    B, hq, hkv, P, steps = 3, 8, 2, 16, 40
+    g = torch.Generator(device="cuda").manual_seed(70)
+    cache = empty_cache(B * 4, hkv, P)
+    table = torch.arange(B * 4, dtype=torch.int32, device="cuda").view(B, 4)
+    rows = torch.randn(2, steps, B, hkv, 128, generator=g, device="cuda").to(BF)
+    k, v, slots, lens = torch.empty_like(rows[0, 0]), torch.empty_like(rows[0, 0]), i32([0] * B), i32([0] * B)
+    q = torch.randn(B, hq, 128, generator=g, device="cuda").to(BF)
+    ws = torch.empty(kv.kvarn_paged_attention_workspace_size(B, hq, hkv), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(B, hq, 128, device="cuda"), torch.empty(B, hq, device="cuda")
+    slots.copy_(table[:, 0] * P)
+
+    def step():
+        kv.kvarn_quantize_kv(k, v, *cache, slot_map=slots)
+        kv.kvarn_paged_attention_q8(q, *cache, table, lens, out, SCALE, ws, lse=lse)
+
+    graph = _capture(step)
+    for t in range(steps):
+        k.copy_(rows[0, t])
+        v.copy_(rows[1, t])
+        slots.copy_(table[:, t // P] * P + t % P)
+        lens.fill_(t + 1)
+        graph.replay()
+    torch.cuda.synchronize()
+    c = dict(q=q, cache=cache, table=table, lens=lens, starts=None, window=0, P=P, dt=BF)
+    check(c, out, lse)
+    again, again_lse = call(kv, c)
+    assert torch.equal(out, again) and torch.equal(lse, again_lse)
+    # what an 8-bit cache costs against the rows themselves: a value and a key are off by up to 2^-4 of each element
+    dense_k, dense_v = (x.double().permute(1, 2, 0, 3).cpu().numpy() for x in rows)
+    s = np.einsum("bhgc,bhtc->bhgt", np64(q).reshape(B, hkv, hq // hkv, 128), dense_k) * SCALE
+    p = np.exp(s - s.max(-1, keepdims=True))
+    want = np.einsum("bhgt,bhtc->bhgc", p / p.sum(-1, keepdims=True), dense_v).reshape(B, hq, 128)
+    assert np.linalg.norm(np64(out) - want) <= 2.0 ** -4 * np.linalg.norm(want)
+
+
+def test_attention_cache_past_32_bit_offsets(kv):
+    P, n_pages, hkv = 128, 17500, 16  # 4.6e9 bytes per cache: the pages in use are the last ones
+    c = case(71, [300, 129], 32, hkv, P, layout="nhd")
+    small = c["cache"][0].shape[0]
+    far = empty_cache(n_pages, hkv, P, "nhd", code=0)
+    for big, src in zip(far, c["cache"]):
+        (big.view(torch.uint8) if big.dtype == E4 else big)[n_pages - small:] = src.view(torch.uint8) if src.dtype == E4 else src
+    want = call(kv, c)
+    table = torch.where(c["table"] < small, c["table"] + (n_pages - small), c["table"])
+    got = call(kv, dict(c, cache=far, table=table))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    x = torch.randn(3, hkv, 128, device="cuda").to(BF)
+    slots = n_pages * P - 1 - 5 * torch.arange(3, device="cuda", dtype=torch.int32)
+    kv.kvarn_quantize_kv(x, x, *far, slot_map=slots)
+    s = slots.long()
+    want_code, want_e = o.quantize_row(np64(x))
+    assert np.array_equal(np64(far[0][s // P, :, s % P]), want_code) and np.array_equal(far[3][s // P, :, s % P].cpu().numpy(), want_e)
+
+
+def test_attention_repeats_and_side_streams(kv):
+    cs = [case(72 + i, [3000, 10 * i, 999], 8, 2, P=32, wide=i == 1) for i in range(3)]
+    want = [call(kv, c) for c in cs]
+    torch.cuda.synchronize()
+    got = []
+    for i, s in enumerate([torch.cuda.Stream() for _ in cs] * 3):
+        with torch.cuda.stream(s):
+            got.append((i % 3, call(kv, cs[i % 3])))
+    torch.cuda.synchronize()
+    for i, (out, lse) in got:
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_rows_of_minus_infinity_and_strided_queries(kv):
+    c = case(75, [200, 3], 8, 2)
+    wide = torch.randn(2, 13, 136, device="cuda").to(BF)
+    c["q"] = wide[:, 2:10, :128]
+    check(c, *call(kv, c))
+    c["q"] = torch.full((2, 8, 128), -math.inf, dtype=BF, device="cuda")
+    out, lse = call(kv, c)
+    assert not torch.isfinite(lse).any()  # infinities of both signs in every score
+
+
+def test_python_refusals(kv):
+    c = case(76, [20], 4, 2)
+    kc, vc, ke, ve = c["cache"]
+    for cache, match in (((kc.view(torch.uint8), vc, ke, ve), "k_cache"), ((kc, vc, ke.int(), ve), "k_exp"), ((kc, vc, ke, ve[:1]), "v_exp"),
+                         ((kc, vc.transpose(1, 2), ke, ve), "v_cache")):
+        with pytest.raises(ValueError, match=match):
+            call(kv, {**c, "cache": cache})
+        x = torch.ones(2, 2, 128, dtype=BF, device="cuda")
+        with pytest.raises(ValueError, match=match):
+            kv.kvarn_quantize_kv(x, x, *cache)
+    x = torch.ones(2, 2, 128, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="heads"):
+        kv.kvarn_quantize_kv(x[:, :1], x[:, :1], *c["cache"])
+    with pytest.raises(ValueError, match="strides"):
+        kv.kvarn_quantize_kv(x, x.expand(2, 2, 128).transpose(0, 1).contiguous().transpose(0, 1), *c["cache"])
+    with pytest.raises(kv.KvarnError, match="workspace"):
+        call(kv, c, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
