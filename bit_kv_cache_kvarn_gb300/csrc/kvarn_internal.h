@@ -239,8 +239,8 @@ struct PromptArgs {
     int B, T, Hq, Hkv, page_size, max_pages, max_len, window, causal;
     int64_t n_pages;
     // set by the launcher: query heads per kv head, tokens of a copy, rows of a partial slot, log2 of a page size that
-    // is a power of two (else -1), whether rows come by tiled copies, whether 32-byte stores of the output are aligned
-    int group, box, slot_rows, page_shift, tiled_rows, wide_out;
+    // is a power of two (else -1), whether rows come and go by tiled copies
+    int group, box, slot_rows, page_shift, tiled_rows, tiled_out;
     uint32_t group_mul, group_shift;  // division by the group
     uint64_t grid_mul;                // and by the split's CTAs: 2^64 / ctas, rounded up (0: one CTA)
     float scale, softcap;

@@ -31,11 +31,12 @@ constexpr int kMmaWarp = 10;                     //   products of a half (and 11
 constexpr int kRowWarp = 12;                     //   queries of a half (and 13),
 constexpr int kPlanWarp = 14;                    //   the plan, and (15) values at the edges of what a unit sees
 constexpr int kPieces = 4, kReaders = 15;        // the planning warp's ring, and the warps that read it
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kStageBytes = kTile * kTile * 2;   // keys or values of a tile
 constexpr int kSpan = kStageBytes / 2;           // 64 channels of it
 constexpr int kRowBytes = kHalf * kTile * 2;     // queries of a half
-constexpr int kSmem = 2 * kRowBytes + kStages * kStageBytes + 1024;
+constexpr int kTurnBytes = 32 * 128;              // where a softmax warp lays out 32 rows of 64 channels for a tiled store
+constexpr int kSmem = 2 * kRowBytes + kStages * kStageBytes + 8 * kTurnBytes + 1024;
 constexpr int kMaxCtas = 160;
 constexpr int kMinPart = 2;                      // tiles of a unit that a CTA takes, at least
 constexpr int kUnitCost = 2;                     // what a unit costs beside its tiles, in tiles
@@ -226,17 +227,6 @@ __device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t sum, __h
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0), "r"(sum));
     return r;
 }
-// 32 bytes, in one store where `wide` says that they are aligned
-__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8], bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                     "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                     : "memory");
-    } else {
-        static_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-        static_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
-    }
-}
 template <bool QUIET = false>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned int* err) {
     const uint32_t addr = smem_addr(bar);
@@ -283,6 +273,16 @@ __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
         : "memory");
 }
+
+__device__ __forceinline__ void tma_store3(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0), "r"(c1),
+                 "r"(c2), "r"(smem_addr(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// this thread's stores have read their shared memory, or are done
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 struct Barriers {
     uint64_t full[kStages], raw[kStages], empty[kStages];
@@ -543,7 +543,7 @@ __device__ __forceinline__ void odd_channels(const PromptArgs& a, int b, int h, 
 template <typename T, bool OWN, bool GEN>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                        const __grid_constant__ CUtensorMap q_map, PromptArgs a) {
+                        const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map, PromptArgs a) {
     constexpr bool kIsHalf = std::is_same<T, __half>::value;
     constexpr float kLift = kIsHalf ? kHalfLift : 0.f;
     constexpr uint32_t kIdescS = kIsHalf ? tc::idesc_f16_f32(128, 128) : tc::idesc_as_bf16(tc::idesc_f16_f32(128, 128));
@@ -592,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---- softmax: a thread has a row of its half ----
         const int half = warp >> 2, r = tid & 127;
+        uint8_t* const turn = ring + kStages * kStageBytes + warp * kTurnBytes;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t t_s = tmem + lanes + kColS + half * kTile, t_o = tmem + lanes + kColO + half * kTile;
         uint32_t s_parity = 0, o_parity = 0;
@@ -657,56 +658,75 @@ __global__ void __launch_bounds__(kThreads, 1)
                 inv *= share;
             }
             if ((warp & 3) * 32 < rows) {
-                uint32_t o[4][32];
-#pragma unroll
+                const bool tiled = whole && a.tiled_out && rows >= ((warp & 3) + 1) * 32;  // all of the warp's rows
+                T* const out = static_cast<T*>(a.out) + row * kTile;
+                const bool zero = whole && __any_sync(0xffffffffu, l == 0.f);  // no key, or only scores of -inf
+                const float by = whole ? inv : 1.f;
+                // (rolled: code that runs once a unit costs its fetching)
+#pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
+                    uint32_t o[32];
                     if (any) {
-                        tc::ld32(t_o + 32 * i, o[i]);
+                        tc::ld32(t_o + 32 * i, o);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[i][k] = 0u;
+                        for (int k = 0; k < 32; ++k) o[k] = 0u;
                     }
-                }
-                tc::wait_ld();
-                if (whole) {
-#pragma unroll
-                    for (int k = 0; k < 128; ++k) o[k >> 5][k & 31] = __float_as_uint(__uint_as_float(o[k >> 5][k & 31]) * inv);
-                    if (__any_sync(0xffffffffu, l == 0.f)) {  // no key, or only scores of -inf
-#pragma unroll
-                        for (int k = 0; k < 128; ++k) o[k >> 5][k & 31] = l != 0.f ? o[k >> 5][k & 31] : 0u;
+                    tc::wait_ld();
+                    if (tiled && (i & 1) == 0) {  // the warp's 4 KB are free again
+                        if (lane == 0) bulk_wait_read();
+                        __syncwarp();
                     }
-                }
-                if (real && whole) {
-                    T* out = static_cast<T*>(a.out) + row * kTile;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float v[16];
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * by);
+                    if (zero) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[k >> 1][(k & 1) * 16 + e]);
-                        if constexpr (OWN) {
+                        for (int k = 0; k < 32; ++k) o[k] = l != 0.f ? o[k] : 0u;
+                    }
+                    if (OWN && real && whole) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float4 w = *reinterpret_cast<const float4*>(a.own_out + row * kTile + 16 * k + 4 * e);
-                                v[4 * e] = fmaf(own, w.x, v[4 * e]), v[4 * e + 1] = fmaf(own, w.y, v[4 * e + 1]);
-                                v[4 * e + 2] = fmaf(own, w.z, v[4 * e + 2]), v[4 * e + 3] = fmaf(own, w.w, v[4 * e + 3]);
-                            }
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 w = *reinterpret_cast<const float4*>(a.own_out + row * kTile + 32 * i + 4 * k);
+                            o[4 * k] = __float_as_uint(fmaf(own, w.x, __uint_as_float(o[4 * k])));
+                            o[4 * k + 1] = __float_as_uint(fmaf(own, w.y, __uint_as_float(o[4 * k + 1])));
+                            o[4 * k + 2] = __float_as_uint(fmaf(own, w.z, __uint_as_float(o[4 * k + 2])));
+                            o[4 * k + 3] = __float_as_uint(fmaf(own, w.w, __uint_as_float(o[4 * k + 3])));
                         }
-                        uint32_t w[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1], T());
-                        store32(out + 16 * k, w, a.wide_out);
                     }
-                } else if (real) {
-                    uint4* out = reinterpret_cast<uint4*>(slot) + rr;
+                    if (!whole) {
+                        if (real) {
+                            uint4* part = reinterpret_cast<uint4*>(slot) + (size_t)8 * i * a.slot_rows + rr;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        out[(size_t)k * a.slot_rows] = make_uint4(o[k >> 3][(k & 7) * 4], o[k >> 3][(k & 7) * 4 + 1], o[k >> 3][(k & 7) * 4 + 2], o[k >> 3][(k & 7) * 4 + 3]);
+                            for (int k = 0; k < 8; ++k) part[(size_t)k * a.slot_rows] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
+                        continue;
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) w[k] = pack2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]), T());
+                    if (tiled) {
+                        uint8_t* const mine = turn + lane * 128;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(mine + (((4 * (i & 1) + k) ^ (lane & 7)) << 4)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                        if ((i & 1) == 1) {
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) tma_store3(&o_map, turn, 32 * (i - 1), head, p.q0 + token);
+                        }
+                    } else if (real) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(out + 32 * i)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    }
                 }
             }
             const int2 odd = s_odd[(reader.n - 1) % (2 * kPieces)];
-            if (any && odd.y >= odd.x)
+            if (any && odd.y >= odd.x) {
+                if (lane == 0) bulk_wait_all();
+                __syncwarp();
                 odd_channels<T>(a, p.b, p.h, max(odd.x, first) * kTile, min(odd.y + 1, past) * kTile, lo, l != 0.f ? hi : lo,
                                 whole ? static_cast<T*>(a.out) + row * kTile : nullptr, slot + 4 * (size_t)rr, 4 * (size_t)a.slot_rows);
+            }
             if (real) {
                 if (whole) {
                     if (a.lse != nullptr) a.lse[row] = lse;
@@ -718,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tid == 0 && p.starts && !p.ends) ws.joins()[blockIdx.x] = Join{p.b, p.h, p.u, p.last};
             tc::fence_before();
         }
+        if (lane == 0) bulk_wait_all();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         Reader reader;
@@ -1104,7 +1125,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a)
 }
 
 struct Kernels {
-    void (*split)(CUtensorMap, CUtensorMap, CUtensorMap, PromptArgs);
+    void (*split)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PromptArgs);
     void (*join)(PromptArgs);
 };
 template <typename T>
@@ -1146,15 +1167,18 @@ cudaError_t cache_map(CUtensorMap* map, const PromptArgs& a, int dtype, const vo
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Queries as channels x heads x tokens, in boxes of 64 channels of a kv head's query heads of 128 rows' tokens.
-cudaError_t rows_map(CUtensorMap* map, const PromptArgs& a, int dtype) {
+// Rows of queries or outputs as channels x heads x tokens, in boxes of 64 channels of `rows` rows: of a kv head's query
+// heads and as many tokens as that makes, or of some of the heads.
+cudaError_t rows_map(CUtensorMap* map, const PromptArgs& a, int dtype, const void* base, int64_t token_stride, int64_t head_stride,
+                     int rows) {
     const EncodeTiled encode = encode_tiled();
     if (encode == nullptr) return cudaErrorNotSupported;
     const cuuint64_t sizes[3] = {kTile, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
-    const cuuint64_t strides[2] = {a.Hq > 1 ? (cuuint64_t)a.q_head_stride * 2 : 256, a.T > 1 ? (cuuint64_t)a.q_token_stride * 2 : 256};
-    const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(kHalf / a.group)}, step[3] = {1, 1, 1};
+    const cuuint64_t strides[2] = {a.Hq > 1 ? (cuuint64_t)head_stride * 2 : 256, a.T > 1 ? (cuuint64_t)token_stride * 2 : 256};
+    const int heads = a.group < rows ? a.group : rows;
+    const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)(rows / heads)}, step[3] = {1, 1, 1};
     const CUresult r = encode(map, dtype == KVARN_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                              const_cast<void*>(a.q), sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              const_cast<void*>(base), sizes, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -1188,20 +1212,21 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     a.group_mul = (uint32_t)((1ull << (31 + log2_group)) / (unsigned)a.group + 1);
     // capped scores take e^(2 score / cap), others 2^(score log2 e)
     a.score_scale = a.softcap > 0.f ? (float)(2.0 * (double)a.scale / (double)a.softcap * (double)kLog2e) : a.scale * kLog2e;
-    a.wide_out = ((uintptr_t)a.out & 31) == 0;
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     a.box = a.page_size % 128 == 0 ? 128 : a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
     const float c = a.scale * kLog2e;
     const bool general = a.softcap > 0.f || a.slopes != nullptr || !(c >= 1e-30f && c <= 1e30f);
     const bool own = a.own_out != nullptr;
     const Kernels k = dtype == KVARN_DTYPE_FP16 ? pick<__half>(general, own) : pick<__nv_bfloat16>(general, own);
-    CUtensorMap k_map, v_map, q_map = {};
+    CUtensorMap k_map, v_map, q_map = {}, o_map = {};
     // rows come by tiled copies where 128 of them are whole tokens and the strides are ones that the encoding takes
     a.tiled_rows = kHalf % a.group == 0 && (a.Hq == 1 || (a.q_head_stride > 0 && a.q_head_stride < (1ll << 38))) &&
                    (a.T == 1 || (a.q_token_stride > 0 && a.q_token_stride < (1ll << 38)));
     e = cache_map(&k_map, a, dtype, a.k_cache);
     if (e == cudaSuccess) e = cache_map(&v_map, a, dtype, a.v_cache);
-    if (e == cudaSuccess && a.tiled_rows) a.tiled_rows = rows_map(&q_map, a, dtype) == cudaSuccess;
+    a.tiled_out = e == cudaSuccess && kHalf % a.group == 0 && rows_map(&o_map, a, dtype, a.out, (int64_t)a.Hq * kTile, kTile, 32) == cudaSuccess;
+    if (e == cudaSuccess && a.tiled_rows)
+        a.tiled_rows = rows_map(&q_map, a, dtype, a.q, a.q_token_stride, a.q_head_stride, kHalf) == cudaSuccess;
     if (e == cudaSuccess) e = set_smem_limit_once(k.split, kSmem, false, dev);
     if (e != cudaSuccess) return e;
     // no more CTAs than parts of kMinPart tiles that the call can have
@@ -1210,7 +1235,7 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     const int most = sms < kMaxCtas ? sms : kMaxCtas;
     const int ctas = (int)(parts < 1 ? 1 : parts < most ? parts : most);
     a.grid_mul = ~0ull / (unsigned)ctas + 1;
-    e = launch_pdl(k.split, dim3(ctas), dim3(kThreads), kSmem, stream, k_map, v_map, q_map, a);
+    e = launch_pdl(k.split, dim3(ctas), dim3(kThreads), kSmem, stream, k_map, v_map, q_map, o_map, a);
     if (e != cudaSuccess) return e;
     // Few units have many parts each, and a CTA takes only kJoinRows rows of theirs; many units leave at most one with a
     // few parts to a CTA of the split (152 x 32 CTAs of the join, most with nothing to do, took 3 us more than 152 x 8).
