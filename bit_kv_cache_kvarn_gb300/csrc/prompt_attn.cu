@@ -458,6 +458,22 @@ __device__ __forceinline__ void softmax_tile(const PromptArgs& a, uint32_t t_s, 
                                              float d0, bool first, float& m, float& l) {
     constexpr float kLift = std::is_same<T, __half>::value ? kHalfLift : 0.f;
     uint32_t x[4][32];
+    const bool partial = __any_sync(0xffffffffu, lo > 0 || hi < kTile);
+    if (!GEN && partial) {
+        // hidden scores become -inf in tensor memory, 32 columns at a time: unrolled over the registers below, these
+        // instructions, which a unit runs once or twice, cost their fetching (a masked tile took twice a whole one's time)
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t seen = bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+            tc::ld32(t_s + 32 * i, x[0]);
+            tc::wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[0][k] = (seen & (1u << k)) != 0 ? x[0][k] : 0xff800000u;
+            tc::st32(t_s + 32 * i, x[0]);
+        }
+        tc::wait_st();
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) tc::ld32(t_s + 32 * i, x[i]);
     tc::wait_ld();
@@ -482,7 +498,7 @@ __device__ __forceinline__ void softmax_tile(const PromptArgs& a, uint32_t t_s, 
                 x[i >> 5][i & 31] = __float_as_uint(fmaf(slope, d0 + i, __uint_as_float(x[i >> 5][i & 31])));
         }
     }
-    if (__any_sync(0xffffffffu, lo > 0 || hi < kTile)) {
+    if (GEN && partial) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t seen = bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
