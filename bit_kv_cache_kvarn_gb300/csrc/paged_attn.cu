@@ -297,6 +297,10 @@ __device__ __forceinline__ float power_of_two(int e) { return __int_as_float(e >
 // 2^-39 of its largest element); keys' exponents scale the scores.  Values' exponents go into the probabilities:
 // with their own maximum m' = max(s + e), 2^(s + e - m') is at most 1 for fp16, while l keeps 2^(s - m), and the
 // factor 2^(m' - m) joins them at the end of a unit.
+// Half the bytes but as many products: instruction issue is near HBM as a bound (505 instructions a warp and group,
+// 55% of the issue slots).  So maxima are shared between lanes only when one has grown by 2^kGrow, and a channel's order
+// inside a product is the one that the bytes have.  Measured: 16 sequences of 32k tokens, 32 over 8 heads, 189 us
+// (5.7 TB/s; with a maximum per group and its shuffles 237); 200 of 1 to 1200 tokens 75 to 77 us by the lengths drawn.
 // CLUSTER: a thread-block cluster takes one unit, its CTAs equal parts of it, and the parts are joined
 // through the cluster's shared memory: no second launch.
 template <typename T, typename O, int NT, bool CAP, bool CLUSTER, bool Q8>

@@ -6,6 +6,34 @@
 // over the visible keys j: start <= j, and p_i - window < j <= p_i when causal, else j < L.  One pass over the
 // keys: with (m, l, o) of the keys so far, a tile's scores give m' = max(m, max s), and l and o are scaled by
 // e^{m - m'} before its probabilities are added.
+//
+// What bounds it: 4 * 128 operations for each (row, key), 8.4 M for a tile of 128 rows x 128 keys, against 64 KB of keys
+// and values for 256 rows: the tensor cores, or HBM where few rows meet many keys.  So:
+//   - the rows of a kv head, (token, query head) pairs, are taken 256 at a time (a unit), whatever the heads per kv head,
+//     as two halves of 128 rows = 128 lanes of tensor memory.  Scores (fp32, 128 columns), the probabilities over them (16
+//     bit, 64 columns) and the output (fp32, 128 columns) of both halves fill the 512 columns, and a tile's keys and values
+//     are read from shared memory for both;
+//   - while one half's softmax runs, the other half's P V and next Q K^T do.  The two halves' products take turns: left to
+//     themselves they interleaved, both halves finished late and then waited together (1503 us for 2000 rows behind 60k
+//     keys, with turns 1341);
+//   - a warp for each job: products of a half, copies of keys, of values, queries of a half, the plan, the edges; eight
+//     warps of softmax with a row a thread, so that no maximum or sum crosses a thread;
+//   - the maximum in use may lag by 2^8: then nothing is scaled, which the output (in tensor memory) mostly spares;
+//   - the tiles of all units form one stream that is cut into equal shares, one per SM, whatever the lengths; a unit counts
+//     as kUnitCost tiles more than it has (without that 24 packed prompts of 1 to 2000 tokens took 384 us, with it 254).
+//     Units that several CTAs share leave partial sums, joined by a second launch;
+//   - pages come by tiled copies with the 128-byte swizzle that the products want, in the largest boxes that pages allow.
+// A tile of 256 rows takes 3200 cycles, 2048 of them at the tensor cores' full rate: what is left is one half's chain,
+// scores -> softmax (1200 cycles) -> P V -> Q K^T (1400 with their latency) and the hand-overs between them.  Not kept: the
+// probabilities handed over in two parts, turns passed on before a half's Q K^T, spinning waits, and sixteen softmax warps
+// with half a row each, whose registers did not suffice.
+// Rounding: products are exact in fp32 but for their sums; scores, maxima, sums and outputs are fp32.  Probabilities enter
+// P V rounded to the cache's type, as the operand has to be: off by half a step each, at random, so that an output of
+// many keys is off by as much as by its own rounding.  l keeps them unrounded.  fp16 ones are multiplied by 2^7, so that
+// with the maximum's lag of 2^8 they use the range of fp16 (p below 2^-21 of the largest lose digits, those below 2^-31 go).
+//
+// Measured (us): 2000 rows behind 60k keys, 32 over 8 heads, 1300 (1540 TFLOP/s, 79% of cuBLAS's burst); a 16k prompt 1440
+// (1530); 24 prompts of 1 to 2000 tokens 253 (870); one token 10.
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -31,15 +59,16 @@ constexpr int kMmaWarp = 10;                     //   products of a half (and 11
 constexpr int kRowWarp = 12;                     //   queries of a half (and 13),
 constexpr int kPlanWarp = 14;                    //   the plan, and (15) values at the edges of what a unit sees
 constexpr int kPieces = 4, kReaders = 15;        // the planning warp's ring, and the warps that read it
-constexpr int kStages = 4;
+constexpr int kStages = 4;                       // tiles of keys or values on their way (a fifth one gained nothing)
 constexpr int kStageBytes = kTile * kTile * 2;   // keys or values of a tile
 constexpr int kSpan = kStageBytes / 2;           // 64 channels of it
 constexpr int kRowBytes = kHalf * kTile * 2;     // queries of a half
-constexpr int kTurnBytes = 32 * 128;              // where a softmax warp lays out 32 rows of 64 channels for a tiled store
+constexpr int kTurnBytes = 32 * 128;             // where a softmax warp lays out 32 rows of 64 channels for a tiled store
 constexpr int kSmem = 2 * kRowBytes + kStages * kStageBytes + 8 * kTurnBytes + 1024;
 constexpr int kMaxCtas = 160;
-constexpr int kMinPart = 2;                      // tiles of a unit that a CTA takes, at least
-constexpr int kUnitCost = 2;                     // what a unit costs beside its tiles, in tiles
+constexpr int kMinPart = 2;                      // tiles of a unit that a CTA takes, at least (8 drafts: 2 24, 4 30 us)
+constexpr int kUnitCost = 2;                     // what a unit costs beside its tiles, in tiles (24 packed prompts: 0 384,
+                                                 // 2 252, 4 261, 5 265 us)
 constexpr int kColS = 0, kColO = 256, kCols = 512;  // tensor memory: scores of the halves, then their outputs
 constexpr float kGrow = 8.f;                     // how far (in powers of two) scores may pass the maximum in use
 constexpr float kHalfLift = 7.f;                 // fp16 probabilities are multiplied by 2^7
@@ -47,16 +76,15 @@ constexpr int kSerialUnits = 16;                 // of a sequence, whose tiles o
 constexpr int kJoinRows = 8, kJoinThreads = 256, kJoinAhead = 5;
 constexpr float kLn2 = 0.69314718055994531f;
 
-// Workspace: partial slots (fp32), two per CTA: slot 0 for the unit that began before the CTA's share, slot 1 for the
-// one that begins in it and goes on after it; then one Join per CTA.  A slot holds o as [32 groups of four
-// channels][rows][4], so that neighbouring rows' threads read and write neighbouring 16 bytes, then m[rows] (log2
-// domain) and l[rows].
-
 struct Join {
     int b, h, u, last;  // the unit that slot 1 begins and the last CTA that holds a part; b = -1: none
 };
 __host__ __device__ constexpr size_t slot_floats(int rows) { return ((size_t)rows * (kTile + 2) + 7) & ~(size_t)7; }
 
+// Workspace: partial slots (fp32), two per CTA: slot 0 for the unit that began before the CTA's share, slot 1 for the
+// one that begins in it and goes on after it; then one Join per CTA.  A slot holds o as [32 groups of four
+// channels][rows][4], so that neighbouring rows' threads read and write neighbouring 16 bytes, then m[rows] (log2
+// domain) and l[rows].
 struct Workspace {
     float* base;
     size_t stride;
@@ -214,8 +242,6 @@ __device__ __forceinline__ uint32_t pack2(float x, float y, __half) {
     const __half2 h = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// mbar_wait in as few instructions as possible: the kernel has three dozen of these, and with each poll loop unrolled
-// its code was 145 KB, more than the instruction caches hold (a unit's epilogue took 4600 cycles instead of EPI).
 // sum + 0 x, two 16-bit numbers at a time
 __device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t sum, __nv_bfloat16) {
     uint32_t r;
@@ -227,6 +253,8 @@ __device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t sum, __h
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0), "r"(sum));
     return r;
 }
+// mbar_wait in as few instructions as possible: the kernel has three dozen of these, and with each poll loop unrolled
+// its code was 145 KB, with this 80 KB (24 packed prompts 437 and 431 us).  QUIET: by time only, without an error word.
 template <bool QUIET = false>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned int* err) {
     const uint32_t addr = smem_addr(bar);
@@ -308,7 +336,6 @@ struct Reader {
         return some;
     }
 };
-
 
 template <typename V>
 __device__ __forceinline__ V warp_scan(V v, int lane) {
@@ -451,8 +478,8 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32], float top) {
 }
 // The scores stay in registers, and their scale waits until the maximum is subtracted.  Columns lo .. hi - 1 are seen.
 // GEN: the scores are capped and biased first (d0: position of column 0 less the row's), and c is 1.  The cap takes
-// tanh y = 1 - 2 / (e^2y + 1), off by 2^-22 or so: 2^-22 of the cap in a score.  With the library's tanhf a tile took
-// 5.1 us, with this GENT.
+// tanh y = 1 - 2 / (e^2y + 1), off by 2^-22 or so: 2^-22 of the cap in a score.  With the library's tanhf
+// a capped 4k prompt took 361 us, with this 211.
 template <typename T, bool GEN>
 __device__ __forceinline__ void softmax_tile(const PromptArgs& a, uint32_t t_s, uint32_t t_o, int lo, int hi, float c, float slope,
                                              float d0, bool first, float& m, float& l) {
@@ -988,81 +1015,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             pair_sync();
             walk.end = s_end;
             if (warp == kPlanWarp) {
-            uint32_t slot = 0, parity = 1, n = 0;
-            for (bool more = true; more; ++n) {
-                Piece p;
-                more = walk.next(a, p, lane);
-                if (!more) p.t0 = 1, p.t1 = 0;
-                if (!wait_for(&bar.piece_empty[slot], parity, err)) break;
-                if (lane == 0) {
-                    s_odd[n % (2 * kPieces)] = make_int2(0x7fffffff, -1);
-                    s_piece[slot] = p;
-                    mbar_arrive(&bar.piece_full[slot]);
+                uint32_t slot = 0, parity = 1, n = 0;
+                for (bool more = true; more; ++n) {
+                    Piece p;
+                    more = walk.next(a, p, lane);
+                    if (!more) p.t0 = 1, p.t1 = 0;
+                    if (!wait_for(&bar.piece_empty[slot], parity, err)) break;
+                    if (lane == 0) {
+                        s_odd[n % (2 * kPieces)] = make_int2(0x7fffffff, -1);
+                        s_piece[slot] = p;
+                        mbar_arrive(&bar.piece_full[slot]);
+                    }
+                    __syncwarp();
+                    if (++slot == kPieces) slot = 0, parity ^= 1;
                 }
-                __syncwarp();
-                if (++slot == kPieces) slot = 0, parity ^= 1;
-            }
             } else {
-            // ---- values that not every row of the unit sees: those outside what any sees become zeros, and so do infinities
-            // and NaNs (a probability of 0 would not keep them out); rows that do see one get it in their epilogue ----
-            constexpr uint32_t kOdd = kIsHalf ? 0x7c007c00u : 0x7f807f80u;  // exponents of such values
-            uint32_t stage = 1, raw_parity = 0;  // the values' stage; a bit for each
-            bool fine = true;
-            int t0, t1, a0[2], a1[2], lo, hi, all_lo, all_hi;
-            while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
-                t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi, all_lo = p.all_lo, all_hi = p.all_hi;
-                a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
-            })) {
+                // ---- values that not every row of the unit sees: those outside what any sees become zeros, and so do infinities
+                // and NaNs (a probability of 0 would not keep them out); rows that do see one get it in their epilogue ----
+                constexpr uint32_t kOdd = kIsHalf ? 0x7c007c00u : 0x7f807f80u;  // exponents of such values
+                uint32_t stage = 1, raw_parity = 0;  // the values' stage; a bit for each
+                bool fine = true;
+                int t0, t1, a0[2], a1[2], lo, hi, all_lo, all_hi;
+                while (fine && reader.next(s_piece, bar, err, lane, [&](const Piece& p) {
+                    t0 = p.t0, t1 = p.t1, lo = p.lo, hi = p.hi, all_lo = p.all_lo, all_hi = p.all_hi;
+                    a0[0] = p.a0[0], a0[1] = p.a0[1], a1[0] = p.a1[0], a1[1] = p.a1[1];
+                })) {
 #pragma unroll 1
-                for (int t = t0; t < t1; ++t) {
-                    if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
-                    if (t * kTile < all_lo || (t + 1) * kTile > all_hi) {
-                        fine = wait_for(&bar.raw[stage], (raw_parity >> stage) & 1, err);
-                        if (!fine) break;
-                        raw_parity ^= 1u << stage;
-                        uint8_t* v = ring + stage * kStageBytes;
-                        const int lo_in = max(lo - t * kTile, 0), hi_in = min(hi - t * kTile, kTile);
-                        // a lane takes a 16-byte chunk of every other row
-                        uint8_t* const own = v + ((lane >> 3) & 1) * kSpan + (lane >> 4) * kTile + (lane & 7) * 16;
+                    for (int t = t0; t < t1; ++t) {
+                        if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
+                        if (t * kTile < all_lo || (t + 1) * kTile > all_hi) {
+                            fine = wait_for(&bar.raw[stage], (raw_parity >> stage) & 1, err);
+                            if (!fine) break;
+                            raw_parity ^= 1u << stage;
+                            uint8_t* v = ring + stage * kStageBytes;
+                            const int lo_in = max(lo - t * kTile, 0), hi_in = min(hi - t * kTile, kTile);
+                            // a lane takes a 16-byte chunk of every other row
+                            uint8_t* const own = v + ((lane >> 3) & 1) * kSpan + (lane >> 4) * kTile + (lane & 7) * 16;
 #pragma unroll 1
-                        for (int r = lane >> 4; r < lo_in; r += 2) *reinterpret_cast<uint4*>(own + (r - (lane >> 4)) * kTile) = make_uint4(0, 0, 0, 0);
+                            for (int r = lane >> 4; r < lo_in; r += 2) *reinterpret_cast<uint4*>(own + (r - (lane >> 4)) * kTile) = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-                        for (int r = hi_in + ((hi_in ^ (lane >> 4)) & 1); r < kTile; r += 2)
-                            *reinterpret_cast<uint4*>(own + (r - (lane >> 4)) * kTile) = make_uint4(0, 0, 0, 0);
-                        uint32_t sum[2] = {0, 0};  // of 0 x: a NaN where some x is no number
-                        if (max(lo, t * kTile) < all_lo || min(hi, (t + 1) * kTile) > all_hi) {  // not only at the unit's own edges
-                            __syncwarp();
+                            for (int r = hi_in + ((hi_in ^ (lane >> 4)) & 1); r < kTile; r += 2)
+                                *reinterpret_cast<uint4*>(own + (r - (lane >> 4)) * kTile) = make_uint4(0, 0, 0, 0);
+                            uint32_t sum[2] = {0, 0};  // of 0 x: a NaN where some x is no number
+                            if (max(lo, t * kTile) < all_lo || min(hi, (t + 1) * kTile) > all_hi) {  // not only at the unit's own edges
+                                __syncwarp();
 #pragma unroll 1
-                            for (int r = 0; r < kTile; r += 16) {
-                                uint4 w[8];
+                                for (int r = 0; r < kTile; r += 16) {
+                                    uint4 w[8];
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4*>(own + (r + 2 * i) * kTile);
+                                    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4*>(own + (r + 2 * i) * kTile);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    sum[0] = add_zero_times(w[i].x, sum[0], T()), sum[1] = add_zero_times(w[i].y, sum[1], T());
-                                    sum[0] = add_zero_times(w[i].z, sum[0], T()), sum[1] = add_zero_times(w[i].w, sum[1], T());
+                                    for (int i = 0; i < 8; ++i) {
+                                        sum[0] = add_zero_times(w[i].x, sum[0], T()), sum[1] = add_zero_times(w[i].y, sum[1], T());
+                                        sum[0] = add_zero_times(w[i].z, sum[0], T()), sum[1] = add_zero_times(w[i].w, sum[1], T());
+                                    }
                                 }
                             }
-                        }
-                        if (__any_sync(0xffffffffu, ((sum[0] | sum[1]) & 0x7fff7fffu) != 0)) {
+                            if (__any_sync(0xffffffffu, ((sum[0] | sum[1]) & 0x7fff7fffu) != 0)) {
 #pragma unroll 1
-                            for (int i = lane; i < kTile * 16 * 4; i += 32) {
-                                uint32_t* at = reinterpret_cast<uint32_t*>(v) + i;
-                                *at &= ~__vcmpgeu2(*at & 0x7fff7fffu, kOdd);
+                                for (int i = lane; i < kTile * 16 * 4; i += 32) {
+                                    uint32_t* at = reinterpret_cast<uint32_t*>(v) + i;
+                                    *at &= ~__vcmpgeu2(*at & 0x7fff7fffu, kOdd);
+                                }
+                                if (lane == 0) {
+                                    int2& odd = s_odd[(reader.n - 1) % (2 * kPieces)];
+                                    odd = make_int2(min(odd.x, t), t);
+                                }
                             }
-                            if (lane == 0) {
-                                int2& odd = s_odd[(reader.n - 1) % (2 * kPieces)];
-                                odd = make_int2(min(odd.x, t), t);
-                            }
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar.full[stage]);
                         }
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.full[stage]);
+                        stage += 2;
+                        if (stage >= kStages) stage -= kStages;
                     }
-                    stage += 2;
-                    if (stage >= kStages) stage -= kStages;
                 }
-            }
             }
         }
     }

@@ -5,7 +5,11 @@
 // that one rounding, and the same inputs give the same codes everywhere.
 //
 // What bounds it: 256 bytes read and 129 written per row (16-bit inputs): HBM.  Half a warp takes a row, 16 bytes a
-// lane, and has kAhead rows in flight.
+// lane, so that the maximum takes four shuffles and a store is 8 bytes a lane of one row, and has kAhead rows in flight;
+// they stay packed until they are used (unpacked at the load they took 26.4 us below, kept packed 20.4).  A warp does its
+// rows and ends: a grid of resident CTAs that loops took 27.8 us.
+//
+// Measured: 16384 tokens of 8 heads, bf16, 101 MB: 20.4 us (4.9 TB/s; kAhead 2: 21.9); 64 tokens 2.9 us.
 #include <type_traits>
 
 #include "kvarn_common.cuh"

