@@ -914,7 +914,7 @@ static kvarn_status check_prompt_shape(int64_t T, int Hq, int Hkv) {
 
 // What kvarn_prompt_attention and kvarn_prefix_attention ask of the cache: the strides of a tiled copy.
 static kvarn_status check_tiled_cache(const void* k, const void* v, int64_t n_pages, int Hkv, int page_size, int64_t page_stride,
-                                      int64_t head_stride, int64_t token_stride, int multiple = 8) {
+                                      int64_t head_stride, int64_t token_stride) {
     if (page_size < 16 || page_size % 16 != 0)
         return fail(KVARN_ERR_INVALID_ARG, "page_size = %d; need a positive multiple of 16", page_size);
     KV_TRY(check_cache(k, v, n_pages, Hkv, page_size, page_stride, head_stride, token_stride));
@@ -972,7 +972,7 @@ kvarn_status kvarn_prompt_attention(kvarn_dtype dtype, int B, int T, int Hq, int
     a.page_size = page_size;
     a.max_pages = max_pages;
     a.max_len = max_pages * page_size;
-    a.window = window;
+    a.window = window < a.max_len ? window : 0;  // (a wider one hides nothing, and position + 1 - window keeps to 32 bits)
     a.causal = causal;
     a.n_pages = n_pages;
     a.scale = softmax_scale;

@@ -617,6 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // the tiles of all units form one stream, which is cut into equal pieces: first the tiles of each sequence
     long long* s_cost = reinterpret_cast<long long*>(ring);  // of its units, for one kv head
+    static_assert(kMaxPromptSeqs * sizeof(long long) <= (size_t)kStages * kStageBytes, "all sequences' tiles lie in the ring");
 #pragma unroll 1
     for (int base = warp * 32; base < a.B; base += kThreads) {
         const long long cost = seq_cost(a, base, lane);

@@ -334,6 +334,23 @@ def test_many_sequences(kv):
     check(c, *call(kv, c))
 
 
+def test_as_many_sequences_as_a_call_takes(kv):
+    new = [0] * 16384
+    for b in (0, 1, 31, 8191, 8192, 16383):
+        new[b] = 1 + b % 3
+    c = case(62, new, [b % 50 if n else 0 for b, n in enumerate(new)], 4, 2, 16)
+    check(c, *call(kv, c))
+
+
+@pytest.mark.parametrize("window", [0, 1, 40, 2 ** 31 - 1])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_more_rows_than_tokens(kv, window, softcap):
+    # rows before position 0 see nothing; the widest window there is hides nothing from the others
+    c = case(63, [300, 70, 9], [0, 0, 0], 8, 2, 32)
+    c["lens"], c["window"] = i32([170, 1, 0]), window
+    check(c, *call(kv, c, softcap=softcap), softcap=softcap)
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random_cases(kv, seed):
     rng = np.random.default_rng(1000 + seed)
