@@ -1,6 +1,8 @@
 """Steps of a small server that use the calls together: tables, norm and rotation with the cache write, attention of the
 step's packed rows; and the same sequences behind a shared prefix, and over 8-bit pages."""
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -98,3 +100,36 @@ def test_answers_behind_a_prompt_that_they_share(kv):
             want, want_lse, *_ = o.prefix_attention(np64(q), np64(kc), np64(vc), prompt.cpu().numpy(), [n], [0, B], own.cpu().numpy(),
                                                     [i + 1] * B, SCALE)
             assert np.abs(np64(out) - want).max() <= 2.0 ** -6 * 4 and np.abs(np64(lse) - want_lse).max() <= 1e-3
+
+
+def test_the_example_of_the_documentation_runs(kv):
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        code = next(b for b in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "kvarn_prompt_attention" in b)
+    B, Hq, Hkv, P, T = 2, 4, 2, 16, 25
+    g = torch.Generator(device="cuda").manual_seed(83)
+    q_out, out_rows = torch.randn(T, Hq, 128, generator=g, device="cuda").to(BF), torch.zeros(T, Hq, 128, dtype=BF, device="cuda")
+    k_cache, v_cache = (torch.randn(8, Hkv, P, 128, generator=g, device="cuda").to(BF) for _ in range(2))
+    k_rows, v_rows = (torch.randn(T, Hkv, 128, generator=g, device="cuda").to(BF) for _ in range(2))
+    k8, v8 = (torch.zeros(8, Hkv, P, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    ke, ve = (torch.zeros(8, Hkv, P, dtype=torch.int8, device="cuda") for _ in range(2))
+    names = dict(kv=kv, torch=torch, B=B, Hq=Hq, Hkv=Hkv, T=T, q_out=q_out, out_rows=out_rows, k_cache=k_cache, v_cache=v_cache,
+                 page_table=i32([[3, 0], [1, 2]]), cu_tokens=i32([0, 20, 25]), lens=i32([20, 30]), q_last=q_out[[19, 24]],
+                 prefix_table=i32([[5, 6, 7]]), prefix_lens=i32([41]), cu_seqs=i32([0, 2]),
+                 out=torch.zeros(B, Hq, 128, dtype=BF, device="cuda"), k_rows=k_rows, v_rows=v_rows, k8=k8, v8=v8, ke=ke, ve=ve,
+                 slots=i32([(3, 0)[i // P] * P + i % P for i in range(20)] + [P * 2 + 9 + i for i in range(5)]))
+    parts = code.partition("# k8, v8")
+    exec(compile(parts[0], "README.md", "exec"), names)
+    torch.cuda.synchronize()
+    prefix_out = np64(names["out"])
+    exec(compile(parts[1] + parts[2], "README.md", "exec"), names)
+    torch.cuda.synchronize()
+    table, lens = names["page_table"].cpu().numpy(), [20, 30]
+    want, _, mass = o.prompt_attention(np64(q_out), np64(k_cache), np64(v_cache), table, [0, 20, 25], lens, SCALE)[:3]
+    # probabilities and the output rounded once each to bf16, and 2^-8 for all that is fp32
+    assert np.all(np.abs(np64(out_rows) - want) <= 2.0 ** -8 * (2 * mass + np.abs(want)))
+    want, _, mass = o.prefix_attention(np64(names["q_last"]), np64(k_cache), np64(v_cache), names["prefix_table"].cpu().numpy(), [41], [0, 2],
+                                       table, lens, SCALE)[:3]
+    assert np.all(np.abs(prefix_out - want) <= 2.0 ** -8 * (2 * mass + np.abs(want)))
+    codes = [np64(c.float()) * 2.0 ** np64(e.float())[..., None] for c, e in ((k8, ke), (v8, ve))]
+    want, _, mass = o.paged_attention(np64(names["q_last"]), *codes, table, lens, SCALE)[:3]
+    assert np.all(np.abs(np64(names["out"]) - want) <= 2.0 ** -8 * (mass + np.abs(want)))
