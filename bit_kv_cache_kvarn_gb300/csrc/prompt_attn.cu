@@ -35,6 +35,7 @@
 // Measured (us): 2000 rows behind 60k keys, 32 over 8 heads, 1300 (1540 TFLOP/s, 79% of cuBLAS's burst); a 16k prompt 1440
 // (1530); 24 prompts of 1 to 2000 tokens 253 (870); one token 10.
 #include <cuda.h>
+#include <float.h>
 #include <math_constants.h>
 
 #include <type_traits>
@@ -581,8 +582,8 @@ __device__ __forceinline__ void odd_channels(const PromptArgs& a, int b, int h, 
     __syncwarp();
 }
 
-// T: type of q, the cache and the output; OWN: each row is joined with a part of its own (kvarn_prefix_attention); GEN: scores are capped or biased, or the scale has a sign or
-// size for which the maximum cannot be taken before it.
+// T: type of q, the cache and the output; OWN: each row is joined with a part of its own (kvarn_prefix_attention); GEN:
+// scores are capped or biased, or the scale has a sign or size for which the maximum cannot be taken before it.
 template <typename T, bool OWN, bool GEN>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
@@ -1255,7 +1256,9 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     a.group_shift = log2_group > 0 ? log2_group - 1 : 0;
     a.group_mul = (uint32_t)((1ull << (31 + log2_group)) / (unsigned)a.group + 1);
     // capped scores take e^(2 score / cap), others 2^(score log2 e)
-    a.score_scale = a.softcap > 0.f ? (float)(2.0 * (double)a.scale / (double)a.softcap * (double)kLog2e) : a.scale * kLog2e;
+    // (kept finite, as infinity times a score of 0 would be NaN)
+    const double score_scale = (a.softcap > 0.f ? 2.0 * (double)a.scale / (double)a.softcap : (double)a.scale) * (double)kLog2e;
+    a.score_scale = (float)(score_scale > FLT_MAX ? FLT_MAX : score_scale < -FLT_MAX ? -FLT_MAX : score_scale);
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     a.box = a.page_size % 128 == 0 ? 128 : a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
     const float c = a.scale * kLog2e;

@@ -351,6 +351,25 @@ def test_more_rows_than_tokens(kv, window, softcap):
     check(c, *call(kv, c, softcap=softcap), softcap=softcap)
 
 
+@pytest.mark.parametrize("scale,softcap", [(0.0, 30.0), (-SCALE, 30.0), (SCALE, 0.02), (30 * SCALE, 5.0), (3e38, 2.0 ** -126)])
+def test_capped_scores_beside_hidden_garbage(kv, scale, softcap):
+    # hidden keys hold NaN or infinities; scores of 0, of either sign, far past the cap; a scale over the cap past fp32
+    for garbage in (float("nan"), float("inf")):
+        c = case(64, [150, 3], [61, 0], 8, 2, 16, garbage=garbage, starts=[17, 0])
+        if scale > 1:
+            c["q"].zero_()
+        check(c, *call(kv, c, scale=scale, softcap=softcap), scale=scale, softcap=softcap)
+
+
+def test_a_capped_row_with_a_nan_score_is_nan(kv):
+    c = case(65, [200], [0], 4, 1, 16)
+    page, slot = int(c["table"][0, 100 // 16]), 100 % 16
+    c["kc"][page, 0, slot, 3] = float("nan")
+    out, lse = call(kv, c, softcap=30.0)
+    assert torch.isnan(out[100:]).all() and torch.isnan(lse[100:]).all()
+    assert torch.isfinite(out[:100]).all() and torch.isfinite(lse[:100]).all()
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random_cases(kv, seed):
     rng = np.random.default_rng(1000 + seed)
