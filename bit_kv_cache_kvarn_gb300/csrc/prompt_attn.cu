@@ -77,8 +77,11 @@ constexpr int kSerialUnits = 16;                 // of a sequence, whose tiles o
 constexpr int kJoinRows = 8, kJoinThreads = 256, kJoinAhead = 5;
 constexpr float kLn2 = 0.69314718055994531f;
 
-struct Join {
-    int b, h, u, last;  // the unit that slot 1 begins and the last CTA that holds a part; b = -1: none
+struct alignas(16) Join {
+    int last;       // the last CTA that holds a part of the unit that slot 1 begins; -1: none
+    int h, u;       // the unit,
+    int q0, n;      // and its sequence's rows (from here they come a round trip to L2 earlier)
+    int unused[3];
 };
 __host__ __device__ constexpr size_t slot_floats(int rows) { return ((size_t)rows * (kTile + 2) + 7) & ~(size_t)7; }
 
@@ -630,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after();
     const uint32_t tmem = s_tmem;
     const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.slot_rows), (int)gridDim.x};
-    if (tid == 0) ws.joins()[blockIdx.x].b = -1;
+    if (tid == 0) ws.joins()[blockIdx.x].last = -1;
     unsigned int* const err = &g_prompt_error;
 
     if (warp < 8) {
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     slot[a.slot_rows * kTile + a.slot_rows + rr] = l;
                 }
             }
-            if (tid == 0 && p.starts && !p.ends) ws.joins()[blockIdx.x] = Join{p.b, p.h, p.u, p.last};
+            if (tid == 0 && p.starts && !p.ends) ws.joins()[blockIdx.x] = Join{p.last, p.h, p.u, p.q0, p.len - p.shift, {}};
             tc::fence_before();
         }
         if (lane == 0) bulk_wait_all();
@@ -1121,14 +1124,13 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a)
     }
     const int c0 = blockIdx.x;
     const Join jn = ws.joins()[c0];
-    if (jn.b < 0) return;
-    const Seq s = load_seq(a, jn.b);
+    if (jn.last < 0) return;
     const unsigned f0 = (unsigned)jn.u * kUnit;
-    const int rows = (int)(min(f0 + kUnit, (unsigned)s.n * (unsigned)a.group) - f0);
+    const int rows = (int)(min(f0 + kUnit, (unsigned)jn.n * (unsigned)a.group) - f0);
 #pragma unroll 1
     for (int r = blockIdx.y * kJoinRows + in; r < rows; r += gridDim.y * kJoinRows) {
         const unsigned f = f0 + r, token = token_of(a, f);
-        const int64_t row = (int64_t)(s.q0 + (int)token) * a.Hq + jn.h * a.group + (int)(f - token * a.group);
+        const int64_t row = (int64_t)(jn.q0 + (int)token) * a.Hq + jn.h * a.group + (int)(f - token * a.group);
         float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
         float own_lse = 0.f;
         if (OWN) w = *reinterpret_cast<const float4*>(a.own_out + row * kTile + 4 * g), own_lse = a.own_lse[row];
