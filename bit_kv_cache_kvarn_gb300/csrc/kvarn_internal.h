@@ -241,6 +241,7 @@ struct PromptArgs {
     // set by the launcher: query heads per kv head, tokens of a copy, rows of a partial slot, log2 of a page size that
     // is a power of two (else -1), whether rows come and go by tiled copies
     int group, box, slot_rows, page_shift, tiled_rows, tiled_out;
+    int ctas;                     // of the split
     uint32_t group_mul, group_shift;  // division by the group
     uint64_t grid_mul;                // and by the split's CTAs: 2^64 / ctas, rounded up (0: one CTA)
     float scale, softcap;

@@ -74,7 +74,7 @@ constexpr int kColS = 0, kColO = 256, kCols = 512;  // tensor memory: scores of 
 constexpr float kGrow = 8.f;                     // how far (in powers of two) scores may pass the maximum in use
 constexpr float kHalfLift = 7.f;                 // fp16 probabilities are multiplied by 2^7
 constexpr int kSerialUnits = 16;                 // of a sequence, whose tiles one lane counts
-constexpr int kJoinRows = 8, kJoinThreads = 256, kJoinAhead = 5;
+constexpr int kJoinRows = 8, kJoinThreads = 256, kJoinAhead = 5, kJoinGrid = 8;
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct alignas(16) Join {
@@ -86,7 +86,7 @@ struct alignas(16) Join {
 __host__ __device__ constexpr size_t slot_floats(int rows) { return ((size_t)rows * (kTile + 2) + 7) & ~(size_t)7; }
 
 // Workspace: partial slots (fp32), two per CTA: slot 0 for the unit that began before the CTA's share, slot 1 for the
-// one that begins in it and goes on after it; then one Join per CTA.  A slot holds o as [32 groups of four
+// one that begins in it and goes on after it; then one Join per CTA, and their `last` once more.  A slot holds o as [32 groups of four
 // channels][rows][4], so that neighbouring rows' threads read and write neighbouring 16 bytes, then m[rows] (log2
 // domain) and l[rows].
 struct Workspace {
@@ -95,6 +95,7 @@ struct Workspace {
     int ctas;
     __device__ __forceinline__ float* slot(int cta, int which) const { return base + (2 * (size_t)cta + which) * stride; }
     __device__ __forceinline__ Join* joins() const { return reinterpret_cast<Join*>(slot(ctas, 0)); }
+    __device__ __forceinline__ int* lasts() const { return reinterpret_cast<int*>(joins() + ctas); }  // theirs again, side by side
 };
 
 // A sequence: its rows of q, its length and its first visible key.
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after();
     const uint32_t tmem = s_tmem;
     const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.slot_rows), (int)gridDim.x};
-    if (tid == 0) ws.joins()[blockIdx.x].last = -1;
+    if (tid == 0) ws.joins()[blockIdx.x].last = -1, ws.lasts()[blockIdx.x] = -1;
     unsigned int* const err = &g_prompt_error;
 
     if (warp < 8) {
@@ -783,7 +784,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     slot[a.slot_rows * kTile + a.slot_rows + rr] = l;
                 }
             }
-            if (tid == 0 && p.starts && !p.ends) ws.joins()[blockIdx.x] = Join{p.last, p.h, p.u, p.q0, p.len - p.shift, {}};
+            if (tid == 0 && p.starts && !p.ends) {
+                ws.joins()[blockIdx.x] = Join{p.last, p.h, p.u, p.q0, p.len - p.shift, {}};
+                ws.lasts()[blockIdx.x] = p.last;
+            }
             tc::fence_before();
         }
         if (lane == 0) bulk_wait_all();
@@ -1105,30 +1109,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Parts of the units that several CTAs share, joined: CTA (c, y) takes kJoinRows rows of the unit that begins in the
 // split's CTA c and goes on after it, and those gridDim.y times as far on, a thread four channels of a row, kJoinAhead
 // parts of it at once.
-template <typename T, bool OWN>
+// DIRECT: a CTA takes kJoinRows rows of the unit that one CTA of the split left.  Where that makes more than kJoinGrid rows
+// of CTAs, of which most would have nothing to do, each looks up all units first and takes its share of their rows: 128
+// sequences behind one prefix 105.8 us (with 32 direct rows 109.3), 8 drafts behind 100 keys, with nothing to join, 12.9 (20
+// direct rows: 14.1; kJoinGrid 4: 12.0, but 24 packed prompts then 252.9 instead of 251.1); 4 sequences, 2 direct rows: 21.5
+// (looked up 22.1).
+__host__ __device__ constexpr int join_blocks(int slot_rows) { return (slot_rows + kJoinRows - 1) / kJoinRows; }
+template <typename T, bool OWN, bool DIRECT>
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a) {
     static_assert(kJoinThreads == kJoinRows * kTile / 4, "a thread for each four channels");
     const int tid = threadIdx.x, in = tid % kJoinRows, g = tid / kJoinRows;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.slot_rows), (int)gridDim.x};
-    if (OWN && blockIdx.x == 0) {  // rows outside the groups have their own part only
+    const Workspace ws = {static_cast<float*>(a.workspace), slot_floats(a.slot_rows), a.ctas};
+    if (OWN) {  // rows outside the groups have their own part only
         const int first = min(max(a.cu[0], 0), a.T), past = min(max(a.cu[a.B], first), a.T);
         const int64_t n = (int64_t)(a.T - (past - first)) * a.Hq * (kTile / 4);
-        for (int64_t i = (int64_t)blockIdx.y * kJoinThreads + tid; i < n; i += (int64_t)gridDim.y * kJoinThreads) {
+        const int64_t step = (int64_t)gridDim.x * gridDim.y * kJoinThreads;
+        for (int64_t i = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * kJoinThreads + tid; i < n; i += step) {
             const int64_t skip = (int64_t)first * a.Hq * (kTile / 4), at = i < skip ? i : i + (int64_t)(past - first) * a.Hq * (kTile / 4);
             const float4 v = reinterpret_cast<const float4*>(a.own_out)[at];
             reinterpret_cast<uint2*>(a.out)[at] = make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
             if (a.lse != nullptr && at % (kTile / 4) == 0) a.lse[at / (kTile / 4)] = a.own_lse[at / (kTile / 4)];
         }
     }
-    const int c0 = blockIdx.x;
-    const Join jn = ws.joins()[c0];
-    if (jn.last < 0) return;
-    const unsigned f0 = (unsigned)jn.u * kUnit;
-    const int rows = (int)(min(f0 + kUnit, (unsigned)jn.n * (unsigned)a.group) - f0);
-#pragma unroll 1
-    for (int r = blockIdx.y * kJoinRows + in; r < rows; r += gridDim.y * kJoinRows) {
+    auto join = [&](const Join& jn, int c0, int block) {
+        const int r = block * kJoinRows + in;
+        const unsigned f0 = (unsigned)jn.u * kUnit;
+        if (r >= (int)(min(f0 + kUnit, (unsigned)jn.n * (unsigned)a.group) - f0)) return;
         const unsigned f = f0 + r, token = token_of(a, f);
         const int64_t row = (int64_t)(jn.q0 + (int)token) * a.Hq + jn.h * a.group + (int)(f - token * a.group);
         float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1168,6 +1176,34 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a)
         if (OWN) o = make_float4(fmaf(own, w.x, o.x), fmaf(own, w.y, o.y), fmaf(own, w.z, o.z), fmaf(own, w.w, o.w));
         *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * kTile + 4 * g) = make_uint2(pack2(o.x, o.y, T()), pack2(o.z, o.w, T()));
         if (g == 0 && a.lse != nullptr) a.lse[row] = lse;
+    };
+    if constexpr (DIRECT) {
+        const int c0 = blockIdx.x;
+        const Join jn = ws.joins()[c0];
+        if (jn.last >= 0) join(jn, c0, blockIdx.y);
+    } else {
+        // the CTAs that left a unit, in the same order for all
+        __shared__ int s_cta[kMaxCtas], s_n[kJoinThreads / 32];
+        static_assert(kJoinThreads >= kMaxCtas, "a thread for each CTA of the split");
+        const bool mine = tid < a.ctas && ws.lasts()[tid] >= 0;
+        const unsigned found = __ballot_sync(0xffffffffu, mine);
+        if (tid % 32 == 0) s_n[tid / 32] = __popc(found);
+        __syncthreads();
+        int joins = 0, at = __popc(found & bits_below(tid % 32));
+#pragma unroll
+        for (int i = 0; i < kJoinThreads / 32; ++i) {
+            if (i < tid / 32) at += s_n[i];
+            joins += s_n[i];
+        }
+        if (mine) s_cta[at] = tid;
+        __syncthreads();
+        const int items = joins * join_blocks(a.slot_rows);
+#pragma unroll 1
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+            const int block = item / joins, c0 = s_cta[item - block * joins];
+            const Join jn = ws.joins()[c0];
+            join(jn, c0, block);
+        }
     }
 }
 
@@ -1175,10 +1211,14 @@ struct Kernels {
     void (*split)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PromptArgs);
     void (*join)(PromptArgs);
 };
+template <typename T, bool OWN>
+Kernels pick(bool general, bool direct) {
+    return {general ? prompt_split_kernel<T, OWN, true> : prompt_split_kernel<T, OWN, false>,
+            direct ? prompt_join_kernel<T, OWN, true> : prompt_join_kernel<T, OWN, false>};
+}
 template <typename T>
-Kernels pick(bool general, bool own) {
-    if (own) return {general ? prompt_split_kernel<T, true, true> : prompt_split_kernel<T, true, false>, prompt_join_kernel<T, true>};
-    return {general ? prompt_split_kernel<T, false, true> : prompt_split_kernel<T, false, false>, prompt_join_kernel<T, false>};
+Kernels pick(bool general, bool own, bool direct) {
+    return own ? pick<T, true>(general, direct) : pick<T, false>(general, direct);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1238,7 +1278,7 @@ int slot_rows(int64_t T, int Hq, int Hkv) {
 }  // namespace
 
 size_t prompt_attention_workspace_bytes(int64_t T, int Hq, int Hkv) {
-    const size_t bytes = 2 * kMaxCtas * slot_floats(slot_rows(T, Hq, Hkv)) * sizeof(float) + kMaxCtas * sizeof(Join);
+    const size_t bytes = 2 * kMaxCtas * slot_floats(slot_rows(T, Hq, Hkv)) * sizeof(float) + kMaxCtas * (sizeof(Join) + sizeof(int));
     return (bytes + 255) & ~(size_t)255;
 }
 
@@ -1266,7 +1306,8 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     const float c = a.scale * kLog2e;
     const bool general = a.softcap > 0.f || a.slopes != nullptr || !(c >= 1e-30f && c <= 1e30f);
     const bool own = a.own_out != nullptr;
-    const Kernels k = dtype == KVARN_DTYPE_FP16 ? pick<__half>(general, own) : pick<__nv_bfloat16>(general, own);
+    const bool direct = join_blocks(a.slot_rows) <= kJoinGrid;
+    const Kernels k = dtype == KVARN_DTYPE_FP16 ? pick<__half>(general, own, direct) : pick<__nv_bfloat16>(general, own, direct);
     CUtensorMap k_map, v_map, q_map = {}, o_map = {};
     // rows come by tiled copies where 128 of them are whole tokens and the strides are ones that the encoding takes
     a.tiled_rows = kHalf % a.group == 0 && (a.Hq == 1 || (a.q_head_stride > 0 && a.q_head_stride < (1ll << 38))) &&
@@ -1284,12 +1325,11 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     const int most = sms < kMaxCtas ? sms : kMaxCtas;
     const int ctas = (int)(parts < 1 ? 1 : parts < most ? parts : most);
     a.grid_mul = ~0ull / (unsigned)ctas + 1;
+    a.ctas = ctas;
     e = launch_pdl(k.split, dim3(ctas), dim3(kThreads), kSmem, stream, k_map, v_map, q_map, o_map, a);
     if (e != cudaSuccess) return e;
-    // Few units have many parts each, and a CTA takes only kJoinRows rows of theirs; many units leave at most one with a
-    // few parts to a CTA of the split (152 x 32 CTAs of the join, most with nothing to do, took 3 us more than 152 x 8).
-    const int blocks = (a.slot_rows + kJoinRows - 1) / kJoinRows;
-    return launch_pdl(k.join, dim3(ctas, units > ctas && blocks > 8 ? 8 : blocks), dim3(kJoinThreads), 0, stream, a);
+    if (direct) return launch_pdl(k.join, dim3(ctas, join_blocks(a.slot_rows)), dim3(kJoinThreads), 0, stream, a);
+    return launch_pdl(k.join, dim3(ctas * kJoinGrid), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace kvarn
