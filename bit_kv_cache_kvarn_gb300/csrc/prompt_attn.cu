@@ -32,8 +32,9 @@
 // many keys is off by as much as by its own rounding.  l keeps them unrounded.  fp16 ones are multiplied by 2^7, so that
 // with the maximum's lag of 2^8 they use the range of fp16 (p below 2^-21 of the largest lose digits, those below 2^-31 go).
 //
-// Measured (us): 2000 rows behind 60k keys, 32 over 8 heads, 1300 (1540 TFLOP/s, 79% of cuBLAS's burst); a 16k prompt 1440
-// (1530); 24 prompts of 1 to 2000 tokens 253 (870); one token 10.
+// Measured (us): 2000 rows behind 60k keys, 32 over 8 heads, 1300 in short runs (1540 TFLOP/s, 79% of cuBLAS's burst) and
+// 1530 in long ones, whose clocks the power cap lowers (76% of cuBLAS's sustained rate); a 16k prompt 1440 and 1530; 24
+// prompts of 1 to 2000 tokens 252 (870 TFLOP/s); one token 10.
 #include <cuda.h>
 #include <float.h>
 #include <math_constants.h>
