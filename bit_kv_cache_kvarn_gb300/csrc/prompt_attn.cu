@@ -482,11 +482,31 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32], float top) {
     for (int k = 0; k < 32; k += 2) mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
     return max3(max3(mx[0], mx[1], mx[2]), mx[3], top);
 }
+// cap tanh(s / cap), in the log2 domain.  Up to |y| = |s / cap| = 1/4 it is s (1 + z P(z)), z = y^2: P is the polynomial of
+// degree 2 whose 1 + z P(z) has the least relative error against tanh(y) / y there (3e-9, by Remez exchange), so that
+// such a score is off by its roundings, whatever the cap, and is s itself under a large one.  Beyond that it takes
+// tanh y = 1 - 2 / (e^2y + 1), off by 2^-22 or so, 2^-20 of the score at most (near 0 it would be all of a score that is
+// small against the cap).  A warp takes the polynomial for a whole tile, and where some score of it is larger the tile
+// again, choosing for each score: a 4k prompt under a cap of 50 takes 169 us (by the second formula alone 214, with the
+// library's tanhf 361), under one of 5, where every tile is taken again, 293.  A polynomial up to 1/2 takes a degree more:
+// 181 and 301; a warp that leaves the polynomial out after such tiles 181 and 253.
+constexpr float kNear = 0.0625f;  // of z
+__device__ __forceinline__ float2 cap_near(const PromptArgs& a, float2 x, float2& y, float2& z) {
+    y = fmul2(x, make_float2(a.cap_scale, a.cap_scale));
+    z = fmul2(y, y);
+    float2 p = ffma2(z, make_float2(a.near[3], a.near[3]), make_float2(a.near[2], a.near[2]));
+    p = ffma2(p, z, make_float2(a.near[1], a.near[1]));
+    p = ffma2(p, z, make_float2(a.near[0], a.near[0]));
+    return fmul2(x, p);
+}
+__device__ __forceinline__ float2 cap_far(const PromptArgs& a, float2 y) {
+    const float2 e = fmul2(y, make_float2(2.f * kLog2e, 2.f * kLog2e));
+    const float2 d = fadd2(make_float2(exp2_fast(e.x), exp2_fast(e.y)), make_float2(1.f, 1.f));
+    return ffma2(make_float2(rcp_fast(d.x), rcp_fast(d.y)), make_float2(-2.f * a.cap, -2.f * a.cap), make_float2(a.cap, a.cap));
+}
 // The scores stay in registers, and their scale waits until the maximum is subtracted.  Columns lo .. hi - 1 are seen.
-// GEN: the scores are capped and biased first (d0: position of column 0 less the row's), and c is 1.  The cap takes
-// tanh y = 1 - 2 / (e^2y + 1), off by 2^-22 or so: 2^-22 of the cap in a score.  With the library's tanhf
-// a capped 4k prompt took 361 us, with this 211.
-template <typename T, bool GEN>
+// GEN: the scores are scaled, capped (CAP) and biased first (d0: position of column 0 less the row's), and c is 1.
+template <typename T, bool GEN, bool CAP>
 __device__ __forceinline__ void softmax_tile(const PromptArgs& a, uint32_t t_s, uint32_t t_o, int lo, int hi, float c, float slope,
                                              float d0, bool first, float& m, float& l) {
     constexpr float kLift = std::is_same<T, __half>::value ? kHalfLift : 0.f;
@@ -511,15 +531,36 @@ __device__ __forceinline__ void softmax_tile(const PromptArgs& a, uint32_t t_s, 
     for (int i = 0; i < 4; ++i) tc::ld32(t_s + 32 * i, x[i]);
     tc::wait_ld();
     if constexpr (GEN) {
-        const float scale = a.score_scale, cap = a.softcap * kLog2e;
-        if (a.softcap > 0.f) {
+        const float scale = a.score_scale;
+        if constexpr (CAP) {
+            float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 64; ++i) {
                 uint32_t &x0 = x[i >> 4][2 * (i & 15)], &x1 = x[i >> 4][2 * (i & 15) + 1];
-                float2 v = fmul2(make_float2(__uint_as_float(x0), __uint_as_float(x1)), make_float2(scale, scale));
-                v = fadd2(make_float2(exp2_fast(v.x), exp2_fast(v.y)), make_float2(1.f, 1.f));
-                v = ffma2(make_float2(rcp_fast(v.x), rcp_fast(v.y)), make_float2(-2.f * cap, -2.f * cap), make_float2(cap, cap));
+                float2 y, z;
+                const float2 v = cap_near(a, make_float2(__uint_as_float(x0), __uint_as_float(x1)), y, z);
+                top[i & 3] = max3(top[i & 3], z.x, z.y);
                 x0 = __float_as_uint(v.x), x1 = __float_as_uint(v.y);
+            }
+            if (__any_sync(0xffffffffu, fmaxf(max3(top[0], top[1], top[2]), top[3]) > kNear)) {
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    tc::ld32(t_s + 32 * i, x[0]);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float2 y, z;
+                        const float2 near = cap_near(a, make_float2(__uint_as_float(x[0][k]), __uint_as_float(x[0][k + 1])), y, z);
+                        const float2 far = cap_far(a, y);
+                        x[0][k] = __float_as_uint(z.x <= kNear ? near.x : far.x);
+                        x[0][k + 1] = __float_as_uint(z.y <= kNear ? near.y : far.y);
+                    }
+                    tc::st32(t_s + 32 * i, x[0]);
+                }
+                tc::wait_st();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tc::ld32(t_s + 32 * i, x[i]);
+                tc::wait_ld();
             }
         } else {
 #pragma unroll
@@ -588,8 +629,9 @@ __device__ __forceinline__ void odd_channels(const PromptArgs& a, int b, int h, 
 }
 
 // T: type of q, the cache and the output; OWN: each row is joined with a part of its own (kvarn_prefix_attention); GEN:
-// scores are capped or biased, or the scale has a sign or size for which the maximum cannot be taken before it.
-template <typename T, bool OWN, bool GEN>
+// scores are capped or biased, or the scale has a sign or size for which the maximum cannot be taken before it; CAP: they
+// are capped (with both in one kernel a biased 4k prompt took 173 us for 166).
+template <typename T, bool OWN, bool GEN, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_split_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                         const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map, PromptArgs a) {
@@ -681,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after();
                 if ((warp & 3) * 32 < rows) {
                     const int lo_in = lo - t * kTile, hi_in = hi - t * kTile;
-                    softmax_tile<T, GEN>(a, t_s, t_o, lo_in, hi_in, c, slope, (float)(t * kTile - pos), t == first, m, l);
+                    softmax_tile<T, GEN, CAP>(a, t_s, t_o, lo_in, hi_in, c, slope, (float)(t * kTile - pos), t == first, m, l);
                 }
                 tc::fence_before();
                 __syncwarp();
@@ -1213,13 +1255,13 @@ struct Kernels {
     void (*join)(PromptArgs);
 };
 template <typename T, bool OWN>
-Kernels pick(bool general, bool direct) {
-    return {general ? prompt_split_kernel<T, OWN, true> : prompt_split_kernel<T, OWN, false>,
+Kernels pick(bool general, bool capped, bool direct) {
+    return {capped ? prompt_split_kernel<T, OWN, true, true> : general ? prompt_split_kernel<T, OWN, true, false> : prompt_split_kernel<T, OWN, false, false>,
             direct ? prompt_join_kernel<T, OWN, true> : prompt_join_kernel<T, OWN, false>};
 }
 template <typename T>
-Kernels pick(bool general, bool own, bool direct) {
-    return own ? pick<T, true>(general, direct) : pick<T, false>(general, direct);
+Kernels pick(bool general, bool capped, bool own, bool direct) {
+    return own ? pick<T, true>(general, capped, direct) : pick<T, false>(general, capped, direct);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1298,17 +1340,24 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     while ((1 << log2_group) < a.group) ++log2_group;
     a.group_shift = log2_group > 0 ? log2_group - 1 : 0;
     a.group_mul = (uint32_t)((1ull << (31 + log2_group)) / (unsigned)a.group + 1);
-    // capped scores take e^(2 score / cap), others 2^(score log2 e)
-    // (kept finite, as infinity times a score of 0 would be NaN)
-    const double score_scale = (a.softcap > 0.f ? 2.0 * (double)a.scale / (double)a.softcap : (double)a.scale) * (double)kLog2e;
-    a.score_scale = (float)(score_scale > FLT_MAX ? FLT_MAX : score_scale < -FLT_MAX ? -FLT_MAX : score_scale);
+    // Scores are taken in the log2 domain.  Factors are kept finite (infinity times a score of 0 would be NaN), and twice
+    // the cap too: one past 1.17e38 counts as that, which a score notices only if it is nearly as large.
+    const auto finite = [](double x, double most) { return (float)(x > most ? most : x < -most ? -most : x); };
+    const double scale = (double)a.scale * (double)kLog2e;
+    a.score_scale = finite(scale, FLT_MAX);
+    if (a.softcap > 0.f) {
+        constexpr double kTanh[4] = {1.0, -0.333332400882, 0.133242366306, -0.0514300288342};  // 1 + z P(z) of cap_near
+        a.cap = finite((double)a.softcap * (double)kLog2e, FLT_MAX / 2);
+        a.cap_scale = finite(scale / (double)a.cap, FLT_MAX);
+        for (int i = 0; i < 4; ++i) a.near[i] = finite(scale * kTanh[i], FLT_MAX);
+    }
     a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz((unsigned)a.page_size) : -1;
     a.box = a.page_size % 128 == 0 ? 128 : a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
     const float c = a.scale * kLog2e;
     const bool general = a.softcap > 0.f || a.slopes != nullptr || !(c >= 1e-30f && c <= 1e30f);
     const bool own = a.own_out != nullptr;
     const bool direct = join_blocks(a.slot_rows) <= kJoinGrid;
-    const Kernels k = dtype == KVARN_DTYPE_FP16 ? pick<__half>(general, own, direct) : pick<__nv_bfloat16>(general, own, direct);
+    const Kernels k = dtype == KVARN_DTYPE_FP16 ? pick<__half>(general, a.softcap > 0.f, own, direct) : pick<__nv_bfloat16>(general, a.softcap > 0.f, own, direct);
     CUtensorMap k_map, v_map, q_map = {}, o_map = {};
     // rows come by tiled copies where 128 of them are whole tokens and the strides are ones that the encoding takes
     a.tiled_rows = kHalf % a.group == 0 && (a.Hq == 1 || (a.q_head_stride > 0 && a.q_head_stride < (1ll << 38))) &&
