@@ -136,6 +136,15 @@ __device__ __forceinline__ Keys keys_of(const PromptArgs& a, const Seq& s, unsig
     }
     return k;
 }
+// Keys that all of these rows see, of a sequence whose first row has the position `shift`.
+__device__ __forceinline__ Keys common_keys(const PromptArgs& a, int start, int len, int shift, unsigned f0, unsigned f1) {
+    Keys k = {start, len};
+    if (a.causal) {
+        k.hi = min(len, shift + (int)token_of(a, f0) + 1);
+        if (a.window > 0) k.lo = max(start, shift + (int)token_of(a, f1 - 1) + 1 - a.window);
+    }
+    return k;
+}
 // A unit's length in the stream of work: kUnitCost, then its tiles.
 __device__ __forceinline__ int cost_of(const PromptArgs& a, const Seq& s, int u) {
     const unsigned f0 = (unsigned)u * kUnit;
@@ -192,11 +201,8 @@ struct Walk {
         p.rows = (int)(past - f0);
         const Keys keys = keys_of(a, s, f0, past);
         p.lo = keys.lo, p.hi = keys.hi;
-        p.all_lo = s.start, p.all_hi = s.len;
-        if (a.causal) {
-            p.all_hi = min(s.len, p.shift + (int)token_of(a, f0) + 1);
-            if (a.window > 0) p.all_lo = max(s.start, p.shift + (int)token_of(a, past - 1) + 1 - a.window);
-        }
+        const Keys all = common_keys(a, s.start, s.len, p.shift, f0, past);
+        p.all_lo = all.lo, p.all_hi = all.hi;
         const int first = keys.first(), cost = keys.past() - first + kUnitCost;
         const int o1 = (int)min((long long)cost, o + (end - at));
         p.t0 = first + max(o - kUnitCost, 0), p.t1 = first + o1 - kUnitCost;
@@ -605,24 +611,32 @@ __device__ __forceinline__ float join_lse(float x, float y, float& fx, float& fy
     return sum != 0.f ? top + log2f(sum) * kLn2 : -CUDART_INF_F;
 }
 
-// NaN into the channels of a row's output (or of its part in a slot) in which a value of the tokens [from, past) that the
-// row sees (those in [lo, hi)) is an infinity or a NaN.  Rare: straight from the cache, a token after the other.
+// The infinities and NaNs among the values of the tokens [from, past), which a row sees, in tiles that not all rows see
+// whole (the others' were in the products), added to its output or to its part in a slot: its probabilities are positive,
+// whatever they round to.  Rare: straight from the cache, a token after the other.
 template <typename T>
-__device__ __forceinline__ void odd_channels(const PromptArgs& a, int b, int h, int from, int past, int lo, int hi, T* out,
-                                             float* part, size_t part_stride) {
-    constexpr uint32_t kOdd = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+__device__ __forceinline__ void add_odd(const PromptArgs& a, int b, int h, int from, int past, Keys all, T* out, float* part,
+                                        size_t part_stride) {
+    constexpr uint32_t kOdd = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;  // such a value's exponent
 #pragma unroll 1
-    for (int t = max(from, lo); t < min(past, hi); ++t) {
+    for (int t = from; t < past; ++t) {
+        const int tile = t / kTile * kTile;
+        if (tile >= all.lo && tile + kTile <= all.hi) {
+            t = all.hi / kTile * kTile - 1;
+            continue;
+        }
         const int entry = a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size;
         const int page = a.page_table[(int64_t)b * a.max_pages + entry];
         if (page < 0 || page >= a.n_pages) continue;
-        const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.v_cache) + (int64_t)page * a.page_stride +
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(static_cast<const T*>(a.v_cache) + (int64_t)page * a.page_stride +
                                                               (int64_t)h * a.head_stride + (int64_t)(t - entry * a.page_size) * a.token_stride);
 #pragma unroll 1
         for (int c = 0; c < kTile; ++c) {
-            if ((__vcmpgeu2(__ldg(v + c / 2) & 0x7fff7fffu, kOdd) >> (16 * (c & 1)) & 1u) == 0) continue;
-            if (out != nullptr) out[c] = T(CUDART_NAN_F);
-            else part[(c >> 2) * part_stride + (c & 3)] = CUDART_NAN_F;
+            const uint32_t bits = __ldg(v + c), size = bits & 0x7fffu;
+            if (size < kOdd) continue;
+            const float x = size > kOdd ? CUDART_NAN_F : bits != size ? -CUDART_INF_F : CUDART_INF_F;
+            if (out != nullptr) out[c] = T((float)__ldcg(out + c) + x);
+            else part[(c >> 2) * part_stride + (c & 3)] += x;
         }
     }
     __syncwarp();
@@ -816,8 +830,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (any && odd.y >= odd.x) {
                 if (lane == 0) bulk_wait_all();
                 __syncwarp();
-                odd_channels<T>(a, p.b, p.h, max(odd.x, first) * kTile, min(odd.y + 1, past) * kTile, lo, l != 0.f ? hi : lo,
-                                whole ? static_cast<T*>(a.out) + row * kTile : nullptr, slot + 4 * (size_t)rr, 4 * (size_t)a.slot_rows);
+                const unsigned unit = (unsigned)p.f0, unit_past = min(unit + kUnit, (unsigned)(p.len - p.shift) * (unsigned)a.group);
+                add_odd<T>(a, p.b, p.h, max(max(odd.x, first) * kTile, lo), l != 0.f ? min(min(odd.y + 1, past) * kTile, hi) : lo,
+                           common_keys(a, p.start, p.len, p.shift, unit, unit_past), whole ? static_cast<T*>(a.out) + row * kTile : nullptr,
+                           slot + 4 * (size_t)rr, 4 * (size_t)a.slot_rows);
             }
             if (real) {
                 if (whole) {

@@ -468,11 +468,12 @@ size_t kvarn_prompt_attention_workspace_size(int64_t T, int Hq, int Hkv);
  *                 the sequences are left as they were.
  *   workspace   : >= kvarn_prompt_attention_workspace_size(T, Hq, Hkv) bytes, 16-byte aligned; needs no
  *                 clearing.  Calls that may overlap on the GPU need one each.
- * Rows without a visible key (and rows whose scores are all -inf) get zeros and lse -inf.  Probabilities are
- * rounded to dtype for the product with the values (scores, maxima, sums and outputs are fp32 until the output's
- * own rounding); lse is not affected.  0 <= B <= 16384, Hq a positive multiple of Hkv, Hq <= 65535, T * Hq / Hkv
- * <= 2^31 - 1024, 1 <= max_pages, max_pages * page_size <= 2^31 - 256.  B = 0 and T = 0 are no-ops.  A split and
- * a join kernel. */
+ * Rows without a visible key (and rows whose scores are all -inf) get zeros and lse -inf.  An infinite value that
+ * a row sees makes its channel infinite, NaN beside the other infinity or a NaN (or where its probability rounds to
+ * 0); the other channels are as without it.  Probabilities are rounded to dtype for the product with the values
+ * (scores, maxima, sums and outputs are fp32 until the output's own rounding); lse is not affected.
+ * 0 <= B <= 16384, Hq a positive multiple of Hkv, Hq <= 65535, T * Hq / Hkv <= 2^31 - 1024, 1 <= max_pages,
+ * max_pages * page_size <= 2^31 - 256.  B = 0 and T = 0 are no-ops.  A split and a join kernel. */
 kvarn_status kvarn_prompt_attention(kvarn_dtype dtype, int B, int T, int Hq, int Hkv, const void* q,
                                     int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
                                     const void* v_cache, int64_t n_pages, int page_size, int64_t page_stride,
