@@ -245,7 +245,8 @@ struct PromptArgs {
     uint32_t group_mul, group_shift;  // division by the group
     uint64_t grid_mul;                // and by the split's CTAs: 2^64 / ctas, rounded up (0: one CTA)
     float scale, softcap;
-    float score_scale, cap, cap_scale, near[4];  // set by the launcher: of scores in the log2 domain, and for capped ones (cap_near)
+    // set by the launcher: of scores in the log2 domain, for capped ones (cap_near), of the maxima in partial slots
+    float score_scale, cap, cap_scale, near[4], join_scale;
     const void* q;
     int64_t q_token_stride, q_head_stride;
     const void* k_cache;

@@ -73,6 +73,7 @@ constexpr int kUnitCost = 2;                     // what a unit costs beside its
                                                  // 2 252, 4 261, 5 265 us)
 constexpr int kColS = 0, kColO = 256, kCols = 512;  // tensor memory: scores of the halves, then their outputs
 constexpr float kGrow = 8.f;                     // how far (in powers of two) scores may pass the maximum in use
+constexpr float kLarge = 1048576.f;              // log2 domain; see softmax_tile
 constexpr float kHalfLift = 7.f;                 // fp16 probabilities are multiplied by 2^7
 constexpr int kSerialUnits = 16;                 // of a sequence, whose tiles one lane counts
 constexpr int kJoinRows = 8, kJoinThreads = 256, kJoinAhead = 5, kJoinGrid = 8;
@@ -88,8 +89,8 @@ __host__ __device__ constexpr size_t slot_floats(int rows) { return ((size_t)row
 
 // Workspace: partial slots (fp32), two per CTA: slot 0 for the unit that began before the CTA's share, slot 1 for the
 // one that begins in it and goes on after it; then one Join per CTA, and their `last` once more.  A slot holds o as [32 groups of four
-// channels][rows][4], so that neighbouring rows' threads read and write neighbouring 16 bytes, then m[rows] (log2
-// domain) and l[rows].
+// channels][rows][4], so that neighbouring rows' threads read and write neighbouring 16 bytes, then m[rows] (before
+// the scale) and l[rows].
 struct Workspace {
     float* base;
     size_t stride;
@@ -455,7 +456,6 @@ __device__ __forceinline__ void pair_sync() { asm volatile("bar.sync 1, 64;" :::
 // A tile of a thread's row: its 128 scores at t_s become probabilities there, with the running maximum m and sum l; the
 // output at t_o is scaled where the maximum went on by more than kGrow.
 __device__ __forceinline__ void scale_output(uint32_t t_o, float top, float c, bool first, float& m, float& l) {
-    if (!__any_sync(0xffffffffu, (top - m) * c > kGrow)) return;
     const float scale = top > m ? exp2_fast((m - top) * c) : 1.f;
     m = top;
     l *= scale;
@@ -512,23 +512,28 @@ __device__ __forceinline__ float2 cap_far(const PromptArgs& a, float2 y) {
 }
 // The scores stay in registers, and their scale waits until the maximum is subtracted.  Columns lo .. hi - 1 are seen.
 // GEN: the scores are scaled, capped (CAP) and biased first (d0: position of column 0 less the row's), and c is 1.
+// x c - m c takes m c rounded: off by half a step of m c, which no longer matters to the row's sums, but a probability of
+// more than 2^16 is no fp16 number, and past 2^31 even fp32 has no room.  So a maximum past 2^20 becomes the row's base
+// (`based`: some row of the warp has one), which is subtracted from the scores first; m lies beside it.
 template <typename T, bool GEN, bool CAP>
 __device__ __forceinline__ void softmax_tile(const PromptArgs& a, uint32_t t_s, uint32_t t_o, int lo, int hi, float c, float slope,
-                                             float d0, bool first, float& m, float& l) {
+                                             float d0, bool first, float& m, float& l, float& base, bool& based) {
     constexpr float kLift = std::is_same<T, __half>::value ? kHalfLift : 0.f;
     uint32_t x[4][32];
     const bool partial = __any_sync(0xffffffffu, lo > 0 || hi < kTile);
-    if (!GEN && partial) {
+    float less = base;
+again:
+    if (!GEN && (partial || based)) {
         // hidden scores become -inf in tensor memory, 32 columns at a time: unrolled over the registers below, these
         // instructions, which a unit runs once or twice, cost their fetching (a masked tile took twice a whole one's time)
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
             const uint32_t seen = bits_below(hi - 32 * i) & ~bits_below(lo - 32 * i);
-            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu) && !based) continue;
             tc::ld32(t_s + 32 * i, x[0]);
             tc::wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[0][k] = (seen & (1u << k)) != 0 ? x[0][k] : 0xff800000u;
+            for (int k = 0; k < 32; ++k) x[0][k] = (seen & (1u << k)) != 0 ? __float_as_uint(__uint_as_float(x[0][k]) - less) : 0xff800000u;
             tc::st32(t_s + 32 * i, x[0]);
         }
         tc::wait_st();
@@ -587,8 +592,20 @@ __device__ __forceinline__ void softmax_tile(const PromptArgs& a, uint32_t t_s, 
             for (int k = 0; k < 32; ++k) x[i][k] = (seen & (1u << k)) != 0 ? x[i][k] : 0xff800000u;
         }
     }
-    scale_output(t_o, max3(max3(max32(x[0], m), max32(x[1], m), max32(x[2], m)), max32(x[3], m), m), c, first, m, l);
-    const float ref = (m == -CUDART_INF_F ? 0.f : m * c) - kLift;
+    const float top = max3(max3(max32(x[0], m), max32(x[1], m), max32(x[2], m)), max32(x[3], m), m);
+    if (__any_sync(0xffffffffu, (top - m) * c > kGrow)) {
+        // a large maximum becomes the base, and the tile is taken again without it
+        const bool large = !GEN && fabsf(top * c) > kLarge && top != -CUDART_INF_F;
+        if (!GEN && __any_sync(0xffffffffu, large)) {
+            less = large ? top : 0.f;
+            base += less, m -= less;
+            based = true;
+            goto again;
+        }
+        scale_output(t_o, top, c, first, m, l);
+    }
+    // (GEN's scores are rounded as much as their maximum; a lift that is lost to a large one makes probabilities smaller)
+    const float ref = GEN ? __fsub_ru(m == -CUDART_INF_F ? 0.f : m, kLift) : (m == -CUDART_INF_F ? 0.f : m * c) - kLift;
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -725,7 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!real) hi = lo;
             const float slope = GEN && a.slopes != nullptr && real ? a.slopes[head] * kLog2e : 0.f;
-            float m = -CUDART_INF_F, l = 0.f;
+            float m = -CUDART_INF_F, l = 0.f, base = 0.f;
+            bool based = false;
             const int first = p.first, past = p.past;
 #pragma unroll 1
             for (int t = first; t < past; ++t) {
@@ -737,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after();
                 if ((warp & 3) * 32 < rows) {
                     const int lo_in = lo - t * kTile, hi_in = hi - t * kTile;
-                    softmax_tile<T, GEN, CAP>(a, t_s, t_o, lo_in, hi_in, c, slope, (float)(t * kTile - pos), t == first, m, l);
+                    softmax_tile<T, GEN, CAP>(a, t_s, t_o, lo_in, hi_in, c, slope, (float)(t * kTile - pos), t == first, m, l, base, based);
                 }
                 tc::fence_before();
                 __syncwarp();
@@ -757,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t row = (int64_t)(p.q0 + token) * a.Hq + head;
             float* slot = ws.slot(blockIdx.x, p.starts ? 1 : 0);
             const int rr = half * kHalf + r;
-            float inv = l != 0.f ? 1.f / l : 0.f, lse = l != 0.f ? (m * c + (log2f(l) - kLift)) * kLn2 : -CUDART_INF_F, own = 0.f;
+            float inv = l != 0.f ? 1.f / l : 0.f, lse = l != 0.f ? ((m + base) * c + (log2f(l) - kLift)) * kLn2 : -CUDART_INF_F, own = 0.f;
             if (OWN && real && whole) {
                 float share;
                 lse = join_lse(lse, a.own_lse[row], share, own);
@@ -839,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (whole) {
                     if (a.lse != nullptr) a.lse[row] = lse;
                 } else {
-                    slot[a.slot_rows * kTile + rr] = m == -CUDART_INF_F ? m : m * c;
+                    slot[a.slot_rows * kTile + rr] = m + base;
                     slot[a.slot_rows * kTile + a.slot_rows + rr] = l;
                 }
             }
@@ -1217,7 +1235,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a)
             for (int i = 0; i < kJoinAhead; ++i) {
                 if (c + i > jn.last) break;
                 const float top = fmaxf(m, pm[i]), ref = top == -CUDART_INF_F ? 0.f : top;
-                const float x = exp2f(m - ref), y = exp2f(pm[i] - ref);
+                const float x = exp2f((m - ref) * a.join_scale), y = exp2f((pm[i] - ref) * a.join_scale);
                 m = top;
                 l = fmaf(y, pl[i], x * l);
                 o.x = fmaf(y, po[i].x, x * o.x), o.y = fmaf(y, po[i].y, x * o.y);
@@ -1225,7 +1243,7 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(PromptArgs a)
             }
         }
         float inv = l != 0.f ? 1.f / l : 0.f, own = 0.f;
-        float lse = l != 0.f ? (m + (log2f(l) - (std::is_same<T, __half>::value ? kHalfLift : 0.f))) * kLn2 : -CUDART_INF_F;
+        float lse = l != 0.f ? (m * a.join_scale + (log2f(l) - (std::is_same<T, __half>::value ? kHalfLift : 0.f))) * kLn2 : -CUDART_INF_F;
         if (OWN) {
             float share;
             lse = join_lse(lse, own_lse, share, own);
@@ -1371,6 +1389,7 @@ cudaError_t launch_prompt_attention(PromptArgs a, int dtype, cudaStream_t stream
     a.box = a.page_size % 128 == 0 ? 128 : a.page_size % 64 == 0 ? 64 : a.page_size % 32 == 0 ? 32 : 16;
     const float c = a.scale * kLog2e;
     const bool general = a.softcap > 0.f || a.slopes != nullptr || !(c >= 1e-30f && c <= 1e30f);
+    a.join_scale = general ? 1.f : c;
     const bool own = a.own_out != nullptr;
     const bool direct = join_blocks(a.slot_rows) <= kJoinGrid;
     const Kernels k = dtype == KVARN_DTYPE_FP16 ? pick<__half>(general, a.softcap > 0.f, own, direct) : pick<__nv_bfloat16>(general, a.softcap > 0.f, own, direct);
