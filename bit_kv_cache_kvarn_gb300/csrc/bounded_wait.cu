@@ -5,30 +5,36 @@
 // and the kernel ends normally, so the CUDA context stays usable and the host learns of the
 // failure through kvarn_device_error.  This kernel exercises that path without any fault: thread 0
 // arms an mbarrier for 16 bytes of transfer that no copy will ever deliver (nothing is issued), so
-// the phase never completes and the wait gives up after the requested limit.  No memory outside
-// the block's own shared memory is touched besides the error word.
+// the phase never completes and the wait gives up after the requested limit: first a whole warp's
+// wait, whose lanes have different limits and still have to end together, then a thread's.  The
+// error word is set only if both gave up.  No memory outside the block's own shared memory is touched besides it.
 #include "kvarn_common.cuh"
 #include "kvarn_internal.h"
 
 namespace kvarn {
 
-// Set by the self-check kernel when its wait gives up (always, unless the word was already set).
+// Set by the self-check kernel when its waits give up (always).
 __device__ unsigned int g_selftest_error = 0;
 
 namespace {
 
 __global__ void __launch_bounds__(32) bounded_wait_kernel(uint64_t limit_ns) {
     __shared__ __align__(8) uint64_t bar;
+    __shared__ unsigned int gave_up[2];
     if (threadIdx.x == 0) {
+        gave_up[0] = gave_up[1] = 0;
         mbar_init(&bar, 1);
         fence_mbar_init();
-    }
-    __syncwarp();
-    if (threadIdx.x == 0) {
         // one arrival (the barrier's whole count) with 16 bytes of pending transfer: the phase
         // stays open because no bulk copy is ever issued against it
         mbar_expect_tx(&bar, 16);
-        mbar_wait_for(&bar, 0, &g_selftest_error, limit_ns);
+    }
+    __syncwarp();
+    const bool done = mbar_wait_warp(&bar, 0, &gave_up[0], (uint32_t)(limit_ns * (32 + threadIdx.x) / 32));
+    const unsigned int ended = __ballot_sync(0xffffffffu, !done);  // (lanes that had ended alone would not meet here)
+    if (threadIdx.x == 0) {
+        mbar_wait_for(&bar, 0, &gave_up[1], limit_ns);
+        if (ended == 0xffffffffu && gave_up[0] != 0 && gave_up[1] != 0) atomicOr(&g_selftest_error, kErrTmaTimeout);
     }
 }
 

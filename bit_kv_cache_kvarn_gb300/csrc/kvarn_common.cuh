@@ -136,6 +136,32 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
     return mbar_wait_for(bar, parity, err_word, kWaitNs);
 }
 
+// mbar_wait_for by a whole warp, with one answer for its lanes: as soon as one of them gives up, all do (a lane that went
+// on alone would wait for the others in its next warp-wide instruction).  In as few instructions as possible.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned int* err_word, uint32_t limit_ns) {
+    const uint32_t addr = smem_addr(bar);
+    uint32_t began = 0;
+#pragma unroll 1
+    for (uint32_t i = 0; i < (uint32_t)kSpinLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, done)) return true;
+        if ((i & 255) == 0) {
+            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile unsigned int*>(err_word))) return false;
+            uint32_t now;
+            asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
+            if (i == 0) began = now;
+            if (__any_sync(0xffffffffu, now - began > limit_ns)) break;
+        }
+    }
+    atomicOr(err_word, kErrTmaTimeout);
+    return false;
+}
+
 // After a give-up: wait (bounded by time only) for a copy this CTA issued, so it never exits with a
 // bulk copy still writing into its shared memory.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {

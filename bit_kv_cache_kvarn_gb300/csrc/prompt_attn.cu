@@ -266,10 +266,15 @@ __device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t sum, __h
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0), "r"(sum));
     return r;
 }
-// mbar_wait in as few instructions as possible: the kernel has three dozen of these, and with each poll loop unrolled
-// its code was 145 KB, with this 80 KB (24 packed prompts 437 and 431 us).  QUIET: by time only, without an error word.
-template <bool QUIET = false>
+// The waits are in as few instructions as possible: the kernel has three dozen of these, and with each poll loop unrolled
+// its code was 145 KB, with these 80 KB (24 packed prompts 437 and 431 us).
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned int* err) {
+    return mbar_wait_warp(bar, parity, err, (uint32_t)kWaitNs);
+}
+// The same with an answer of each lane's own, for a warp that asks for several before it votes.  QUIET: by time only,
+// without an error word.
+template <bool QUIET = false>
+__device__ __forceinline__ bool lane_wait_for(uint64_t* bar, uint32_t parity, unsigned int* err) {
     const uint32_t addr = smem_addr(bar);
     uint32_t began = 0;
 #pragma unroll 1
@@ -294,7 +299,7 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigne
 }
 // after a wait that gave up: for a copy or products of this CTA, by time only
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
-    wait_for<true>(bar, parity, nullptr);
+    lane_wait_for<true>(bar, parity, nullptr);
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -966,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++st == kStages) st = 0, par ^= 1;
                 };
                 auto my_turn = [&]() {
-                    const bool got = wait_for(&bar.turn[half], turn_parity, err);
+                    const bool got = lane_wait_for(&bar.turn[half], turn_parity, err);
                     turn_parity ^= 1;
                     return got;
                 };
@@ -986,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // a tile that only the other half takes
 #pragma unroll 1
                         for (int i = 0; fine && i < 2; ++i) {
-                            fine = __all_sync(0xffffffffu, wait_for(&bar.full[stage], parity, err));
+                            fine = __all_sync(0xffffffffu, lane_wait_for(&bar.full[stage], parity, err));
                             if (lane == 0) mbar_arrive(&bar.empty[stage]);
                             pass(stage, parity);
                         }
@@ -996,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         continue;
                     }
                     if (t == a0) {
-                        fine = wait_for(&bar.full[stage], parity, err) && wait_for(&bar.q_full[half], q_parity, err);
+                        fine = lane_wait_for(&bar.full[stage], parity, err) && lane_wait_for(&bar.q_full[half], q_parity, err);
                         q_parity ^= 1;
                         if (!__all_sync(0xffffffffu, fine)) break;
                         tc::fence_after();
@@ -1014,8 +1019,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pass(k_stage, k_parity);
                     const uint32_t vs = uniform(stage), ks = uniform(k_stage), more = uniform(t > a0), left = uniform(a1 - t - 1);
                     const uint64_t vd = v_desc + vs * (kStageBytes >> 4);
-                    fine = wait_for(&bar.full[stage], parity, err) && (left == 0 || wait_for(&bar.full[k_stage], k_parity, err)) &&
-                           wait_for(&bar.p_full[half], p_parity, err) && my_turn();
+                    fine = lane_wait_for(&bar.full[stage], parity, err) && (left == 0 || lane_wait_for(&bar.full[k_stage], k_parity, err)) &&
+                           lane_wait_for(&bar.p_full[half], p_parity, err) && my_turn();
                     p_parity ^= 1;
                     if (!__all_sync(0xffffffffu, fine)) break;
                     tc::fence_after();

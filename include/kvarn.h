@@ -567,9 +567,9 @@ kvarn_status kvarn_paged_attention_q8(kvarn_dtype dtype, int B, int Hq, int Hkv,
 kvarn_status kvarn_device_error(uint32_t* code_out);
 
 /* Self-check of the bounded device waits (a library diagnostic; the pages have no counterpart).
- * Enqueues one small kernel whose mbarrier wait cannot complete (it expects 16 bytes that no copy
- * delivers) and therefore gives up after limit_us microseconds (1..1000000): the kernel sets bit 4
- * of the device error word and ends normally.  A following kvarn_device_error returns
+ * Enqueues one small kernel whose mbarrier waits, a warp's and then a thread's, cannot complete (they
+ * expect 16 bytes that no copy delivers) and therefore give up after limit_us microseconds (1..1000000)
+ * each: the kernel sets bit 4 of the device error word and ends normally.  A following kvarn_device_error returns
  * KVARN_ERR_TIMEOUT with bit 4 set, and the device stays usable.  No fault, trap or hang is
  * involved; this is how the failure path of every bounded wait in the library is tested.
  * Errors: KVARN_ERR_INVALID_ARG for limit_us outside 1..1000000. */
