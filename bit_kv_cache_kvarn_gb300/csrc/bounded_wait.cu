@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(32) bounded_wait_kernel(uint64_t limit_ns) {
         mbar_expect_tx(&bar, 16);
     }
     __syncwarp();
-    const bool done = mbar_wait_warp(&bar, 0, &gave_up[0], (uint32_t)(limit_ns * (32 + threadIdx.x) / 32));
+    const bool done = mbar_wait_warp(&bar, 0, &gave_up[0], (uint32_t)(limit_ns / 1000 * (32 + threadIdx.x) / 32));
     const unsigned int ended = __ballot_sync(0xffffffffu, !done);  // (lanes that had ended alone would not meet here)
     if (threadIdx.x == 0) {
         mbar_wait_for(&bar, 0, &gave_up[1], limit_ns);

@@ -138,11 +138,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
 
 // mbar_wait_for by a whole warp, with one answer for its lanes: as soon as one of them gives up, all do (a lane that went
 // on alone would wait for the others in its next warp-wide instruction).  In as few instructions as possible.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned int* err_word, uint32_t limit_ns) {
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned int* err_word, uint32_t limit_us) {
     const uint32_t addr = smem_addr(bar);
     uint32_t began = 0;
 #pragma unroll 1
-    for (uint32_t i = 0; i < (uint32_t)kSpinLimit; ++i) {
+    for (uint32_t i = 0; i < 0xffffffffu; ++i) {  // (a limit may be longer than kSpinLimit polls)
         uint32_t done;
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
@@ -152,10 +152,9 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
         if (__all_sync(0xffffffffu, done)) return true;
         if ((i & 255) == 0) {
             if (__any_sync(0xffffffffu, *reinterpret_cast<volatile unsigned int*>(err_word))) return false;
-            uint32_t now;
-            asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
+            const uint32_t now = (uint32_t)(global_ns() >> 10);  // 1.024 us
             if (i == 0) began = now;
-            if (__any_sync(0xffffffffu, now - began > limit_ns)) break;
+            if (__any_sync(0xffffffffu, now - began > limit_us)) break;
         }
     }
     atomicOr(err_word, kErrTmaTimeout);

@@ -267,9 +267,15 @@ __device__ __forceinline__ uint32_t add_zero_times(uint32_t x, uint32_t sum, __h
     return r;
 }
 // The waits are in as few instructions as possible: the kernel has three dozen of these, and with each poll loop unrolled
-// its code was 145 KB, with these 80 KB (24 packed prompts 437 and 431 us).
+// its code was 145 KB, with these 80 KB (24 packed prompts 437 and 431 us).  A wait for a step of a tile has a second.  One
+// that may last for a whole unit has kUnitUs, twice what 2^31 keys take (2 us for 128); it ends with the first of the
+// others that gives up.
+constexpr uint32_t kUnitUs = 64u << 20;
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned int* err) {
-    return mbar_wait_warp(bar, parity, err, (uint32_t)kWaitNs);
+    return mbar_wait_warp(bar, parity, err, (uint32_t)(kWaitNs / 1000));
+}
+__device__ __forceinline__ bool wait_unit(uint64_t* bar, uint32_t parity, unsigned int* err) {
+    return mbar_wait_warp(bar, parity, err, kUnitUs);
 }
 // The same with an answer of each lane's own, for a warp that asks for several before it votes.  QUIET: by time only,
 // without an error word.
@@ -343,7 +349,7 @@ struct Reader {
     // A whole warp waits for the next piece and copies what it needs by `take`; false: nothing more
     template <typename F>
     __device__ __forceinline__ bool next(const Piece* ring, Barriers& bar, unsigned int* err, int lane, F take) {
-        if (!wait_for(&bar.piece_full[slot], parity, err)) return false;
+        if (!wait_unit(&bar.piece_full[slot], parity, err)) return false;
         const Piece& p = ring[slot];
         const bool some = p.t1 >= p.t0;
         if (some) take(p);
@@ -1064,7 +1070,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f0 = (unsigned)p.f0 + half * kHalf, h = p.h, q0 = p.q0, rows = p.half_rows(half);
             })) {
                 if (!some) continue;
-                fine = wait_for(&bar.q_free[half], free_parity, err);
+                fine = wait_unit(&bar.q_free[half], free_parity, err);
                 if (!fine) break;
                 free_parity ^= 1;
                 if (a.tiled_rows) {
@@ -1095,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.q_full[half]);
             }
-            if (fine) wait_for(&bar.q_free[half], free_parity, err);
+            if (fine) wait_unit(&bar.q_free[half], free_parity, err);
         } else {
             // ---- the plan: the share's begin, and by the edge warp its end ----
             Walk walk;
@@ -1111,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     Piece p;
                     more = walk.next(a, p, lane);
                     if (!more) p.t0 = 1, p.t1 = 0;
-                    if (!wait_for(&bar.piece_empty[slot], parity, err)) break;
+                    if (!wait_unit(&bar.piece_empty[slot], parity, err)) break;
                     if (lane == 0) {
                         s_odd[n % (2 * kPieces)] = make_int2(0x7fffffff, -1);
                         s_piece[slot] = p;
@@ -1135,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int t = t0; t < t1; ++t) {
                         if (!((t >= a0[0] && t < a1[0]) || (t >= a0[1] && t < a1[1]))) continue;
                         if (t * kTile < all_lo || (t + 1) * kTile > all_hi) {
-                            fine = wait_for(&bar.raw[stage], (raw_parity >> stage) & 1, err);
+                            fine = wait_unit(&bar.raw[stage], (raw_parity >> stage) & 1, err);
                             if (!fine) break;
                             raw_parity ^= 1u << stage;
                             uint8_t* v = ring + stage * kStageBytes;

@@ -31,7 +31,7 @@ def test_a_warps_wait_votes_on_both_ends():
 
 def test_only_votes_follow_the_waits_of_lanes():
     text = source("prompt_attn.cu")
-    assert "mbar_wait_warp(" in body(text, "bool wait_for(")
+    assert "mbar_wait_warp(" in body(text, "bool wait_for(") and "mbar_wait_warp(" in body(text, "bool wait_unit(")
     lines = text.splitlines()
     for i, line in enumerate(lines):
         if "lane_wait_for" not in line or "bool lane_wait_for(" in line:
