@@ -444,7 +444,8 @@ def kvarn_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, cu_se
     (cu_seqs [n_groups + 1] int32) share the prefix_lens[g] tokens in the pages of row g of prefix_table
     [n_groups, max_prefix_pages] int32; kv_lens [B] int32 own tokens, the query's among them, in the pages of
     page_table [B, max_pages] int32; out [B, Hq, 128] of q's type; workspace:
-    kvarn_prefix_attention_workspace_size bytes; lse [B, Hq] float32 receives the log-sum-exp."""
+    kvarn_prefix_attention_workspace_size bytes; lse [B, Hq] float32 receives the log-sum-exp.  The prefix's
+    probabilities are rounded to q's type for the product with the values, as in kvarn_prompt_attention."""
     _call(_native().prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, cu_seqs, page_table, kv_lens, out,
                                      softmax_scale, workspace, softcap, lse, _raw(stream)))
 

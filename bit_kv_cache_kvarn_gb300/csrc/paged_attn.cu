@@ -293,15 +293,15 @@ __device__ __forceinline__ float power_of_two(int e) { return __int_as_float(e >
 // T: type of q and the cache; O: type of the output; NT: eights of query heads in a unit; CAP: scores are
 // capped.
 // Q8: the cache holds E4M3 values c and an exponent e for each token and head, x = c 2^e.  The products take c as
-// fp16, exactly, and queries as fp16 with a power of two of their own (so that a bf16 query keeps its digits over
-// 2^-39 of its largest element); keys' exponents scale the scores.  Values' exponents go into the probabilities:
-// with their own maximum m' = max(s + e), 2^(s + e - m') is at most 1 for fp16, while l keeps 2^(s - m), and the
-// factor 2^(m' - m) joins them at the end of a unit.
+// fp16, exactly, and queries as fp16 with a power of two of their own (so that a bf16 query keeps its eight digits down to
+// 2^-31 of its largest element, and the last of them goes at 2^-39); keys' exponents scale the scores.  Values' exponents
+// go into the probabilities: with their own maximum m' = max(s + e), 2^(s + e - m') is at most 1 for fp16, while l keeps
+// 2^(s - m), and the factor 2^(m' - m) joins them at the end of a unit.
 // Half the bytes but as many products: instruction issue is near HBM as a bound (505 instructions a warp and group,
 // 55% of the issue slots).  So maxima are shared between lanes only when one has grown by 2^kGrow, and a channel's order
 // inside a product is the one that the bytes have.  Measured: 16 sequences of 32k tokens, 32 over 8 heads, 189 us
-// (5.7 TB/s; with a maximum per group and its shuffles 237); 200 of 1 to 1200 tokens 75 to 77 us by the lengths drawn.  (16 warps a CTA in 128
-// registers: 182 and 79.)
+// (5.7 TB/s; with a maximum per group and its shuffles 237); 200 of 1 to 1200 tokens 75 to 77 us by the
+// lengths drawn.  (16 warps a CTA in 128 registers: 182 and 79.)
 // CLUSTER: a thread-block cluster takes one unit, its CTAs equal parts of it, and the parts are joined
 // through the cluster's shared memory: no second launch.
 template <typename T, typename O, int NT, bool CAP, bool CLUSTER, bool Q8>

@@ -23,18 +23,21 @@
 //     as kUnitCost tiles more than it has (without that 24 packed prompts of 1 to 2000 tokens took 384 us, with it 254).
 //     Units that several CTAs share leave partial sums, joined by a second launch;
 //   - pages come by tiled copies with the 128-byte swizzle that the products want, in the largest boxes that pages allow.
-// A tile of 256 rows takes 3200 cycles, 2048 of them at the tensor cores' full rate: what is left is one half's chain,
-// scores -> softmax (1200 cycles) -> P V -> Q K^T (1400 with their latency) and the hand-overs between them.  Not kept: the
+// A tile of 256 rows takes 3070 to 3250 cycles, 2048 of them at the tensor cores' full rate (63 to 67%): what is left is one
+// half's chain, scores -> softmax (1200 cycles) -> P V -> Q K^T (1400 with their latency) and the hand-overs between them.
+// The softmax threads' 200 registers do not quite hold a tile's row: 56 to 80 bytes a thread are spilled.  Not kept: the
 // probabilities handed over in two parts, turns passed on before a half's Q K^T, spinning waits, and sixteen softmax warps
 // with half a row each, whose registers did not suffice.
 // Rounding: products are exact in fp32 but for their sums; scores, maxima, sums and outputs are fp32.  Probabilities enter
 // P V rounded to the cache's type, as the operand has to be: off by half a step each, at random, so that an output of
-// many keys is off by as much as by its own rounding.  l keeps them unrounded.  fp16 ones are multiplied by 2^7, so that
+// many keys is off by as much as by its own rounding (kvarn_paged_attention, which HBM bounds, takes two or three operands
+// for a probability; here a second one would cost half as many products again).  l keeps them unrounded.  fp16 ones are multiplied by 2^7, so that
 // with the maximum's lag of 2^8 they use the range of fp16 (p below 2^-21 of the largest lose digits, those below 2^-31 go).
 //
-// Measured (us): 2000 rows behind 60k keys, 32 over 8 heads, 1300 in short runs (1540 TFLOP/s, 79% of cuBLAS's burst) and
-// 1530 in long ones, whose clocks the power cap lowers (76% of cuBLAS's sustained rate); a 16k prompt 1440 and 1530; 24
-// prompts of 1 to 2000 tokens 252 (870 TFLOP/s); one token 10.
+// Measured (us): 2000 rows behind 60k keys, 32 over 8 heads, 1300 to 1380 in short runs (1450 to 1540 TFLOP/s, 75 to 79% of
+// cuBLAS's burst) and 1520 in long ones, whose clocks the power cap lowers (76% of cuBLAS's sustained rate, 68% of its burst);
+// a 16k prompt 1455 and 1490 (78% of the burst, 86% of the sustained rate); 24 prompts of 1 to 2000 tokens 258 (850 TFLOP/s);
+// one token 10.
 #include <cuda.h>
 #include <float.h>
 #include <math_constants.h>

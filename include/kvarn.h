@@ -491,8 +491,10 @@ size_t kvarn_prefix_attention_workspace_size(int B, int Hq, int Hkv);
  * tokens, both in one paged 16-bit cache: a system prompt, several answers to one question, a beam's common part.
  * Sequences cu_seqs[g] .. cu_seqs[g + 1] - 1 share the prefix g of prefix_lens[g] tokens in the pages of row g of
  * prefix_table, which is read once for all of them (and once for each 256 query heads of a kv head); sequence b's
- * own kv_lens[b] tokens, the query's among them, lie in the pages of row b of page_table.  The result is
- * kvarn_paged_attention's over the prefix's tokens followed by the sequence's own.
+ * own kv_lens[b] tokens, the query's among them, lie in the pages of row b of page_table.  The result is that of
+ * kvarn_paged_attention over the prefix's tokens followed by the sequence's own, but for two roundings: the prefix's
+ * probabilities are rounded to dtype for the product with the values (there they are not), as in
+ * kvarn_prompt_attention, and out is of dtype.
  *   cu_seqs     : [n_groups + 1] int32, non-decreasing, clamped to 0..B; sequences outside the groups have no
  *                 prefix.  prefix_lens : [n_groups] int32, kv_lens : [B] int32, clamped to what their tables
  *                 hold; 0 is allowed in both.
